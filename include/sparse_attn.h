@@ -14,6 +14,14 @@
  *   sparse_attn_diff         per step: diff against the previous step and an LRU slot
  *                            cache; reports hits, misses (with their slots), evictions.
  *
+ * Growing the cache and verifying drafted tokens:
+ *
+ *   sparse_attn_append_kv     new tokens: keys rotated to their positions and stored with the
+ *                             values in the pages, queries rotated, key box kept current.
+ *   sparse_attn_tree_decode   attention of a tree of drafted tokens over the context (all of
+ *                             it or a selection) and over the drafts each query may see.
+ *   sparse_attn_commit_drafts the accepted drafts' K/V moved to the end of the context.
+ *
  * Conventions shared by every call
  * --------------------------------
  *  * All tensor pointers are DEVICE pointers into memory the caller owns.  The library
@@ -88,9 +96,15 @@ enum {
                                             completion, a selection published by another
                                             CTA) gave up after about a second */
     SPARSE_ATTN_ERR_SLOT = 1u << 4,      /* LRU state holds an id outside [-1, nb) */
-    SPARSE_ATTN_ERR_CAPACITY = 1u << 5   /* a per-CTA work list overflowed (the host's
+    SPARSE_ATTN_ERR_CAPACITY = 1u << 5,  /* a per-CTA work list overflowed (the host's
                                             launch limits exclude it; a set bit is a bug) */
+    SPARSE_ATTN_ERR_LENGTH = 1u << 6     /* seq_lens, cu_rows, path or path_len outside the
+                                            range its call allows */
 };
+
+/* Which channels a rotation turns together (sparse_attn_append_kv): with R rotary channels,
+ * pair i is (i, i + R/2) or (2i, 2i + 1). */
+enum { SPARSE_ATTN_ROTATE_HALVES = 1, SPARSE_ATTN_ROTATE_PAIRS = 2 };
 
 /* Problem description.  Passed by pointer, read during the call, never retained.
  * Field names follow the sparse-attention config of 从HiSparse到QSA的移植实战 §3.1
@@ -351,6 +365,98 @@ int sparse_attn_decode_slots_io(const sparse_attn_params* p, const void* q, void
                                 const void* host_v_pages, const int32_t* block_table,
                                 const int32_t* miss_ids, const int32_t* miss_slot, const int32_t* counts,
                                 float* out, void* ws, size_t ws_bytes, sparse_attn_stream stream);
+
+/* ---- Growing the cache, and verifying drafted tokens -------------------------------
+ * The three calls below have no counterpart in the pages; they give this library's paged
+ * cache its writer (the metadata stays current as the context grows, SGLang page §2.2) and
+ * its speculative-decoding step.  One loop iteration of a user's program:
+ *   append_kv(drafts at seq_lens)  ->  [select]  ->  tree_decode  ->  the user accepts a path
+ *   ->  commit_drafts(path)  ->  seq_lens = new_lens.
+ *
+ * Conventions of these calls, beyond the ones at the top:
+ *  * p->n_tokens is the longest context, p->capacity_tokens (n_tokens when 0) the tokens a
+ *    sequence's block_table row has pages for; drafts live behind the context, so the
+ *    capacity covers them too.  p->num_queries = Q drafts per sequence (0 or 1: one).  Any
+ *    K/V dtype and selection kind is allowed with Q > 1 here.
+ *  * seq_lens: device int32 [B], the tokens cached per sequence before the call, in
+ *    [0, n_tokens] (append_kv: [0, capacity]).  NULL: the same for all sequences
+ *    (n_tokens, or for append_kv n_tokens minus the rows of a sequence).  -1 marks an
+ *    inactive sequence of a padded batch: nothing of it is read or written, its output
+ *    rows stay as they were.  Any other value sets SPARSE_ATTN_ERR_LENGTH and is treated
+ *    as inactive.
+ *  * No call reads anything from the device on the host: a step can be captured into a CUDA
+ *    graph and replayed as the contexts grow.
+ *  * Two sequences may share context pages.  The pages that append_kv and commit_drafts
+ *    write must belong to one sequence. */
+
+/* Append new tokens to the paged cache: rotate queries and keys to their positions, store
+ * keys and values, and (when kmin / kmax are given) keep the Quest box of the touched
+ * blocks current, in one launch.
+ *   Rows: q_new [rows, Hq, D], k_new, v_new [rows, Hkv, D] in q_dtype; row r of a tensor
+ *   starts at element r * its row stride (in elements, a multiple of 16 bytes, at least its
+ *   heads * D; the three may be slices of one projection's output).  cu_rows, device int32
+ *   [B + 1], ascending: sequence b owns rows cu_rows[b] .. cu_rows[b + 1] - 1 (seq_lens is
+ *   then required); rows outside [cu_rows[0], cu_rows[B]) are left alone.  cu_rows == NULL:
+ *   num_rows / B rows each.
+ *   Row i of sequence b becomes token t = seq_lens[b] + i, in page
+ *   block_table[b][t / block_size] at t % block_size; its position is positions[row]
+ *   (device int32 [rows]; drafts of one tree depth share a position) or t when positions
+ *   is NULL.
+ *   Rotation by angle_i = position * inv_freq[i] (device double [rotary_dim / 2], radians
+ *   per position): (x_a, x_b) -> (x_a cos - x_b sin, x_b cos + x_a sin) on the first
+ *   rotary_dim channels (a multiple of 16, <= D; 0: no rotation, inv_freq may be NULL),
+ *   paired as `pairing` says.  Angles are reduced to one turn exactly (64-bit fixed
+ *   point), the rotation is fp32, rounded once to the stored type.
+ *   q_out [rows, Hq, D] in q_dtype, contiguous; it may be q_new itself when q_new is
+ *   contiguous.  q_new and q_out may both be NULL.
+ *   kmin / kmax: both or neither; the rows of blocks that got tokens become the box of all
+ *   their tokens, bit for bit what sparse_attn_append_meta computes.  (Block means need
+ *   sparse_attn_append_meta.)  Leave them NULL for drafts. */
+int sparse_attn_append_kv(const sparse_attn_params* p, int32_t num_rows, const int32_t* cu_rows,
+                          const int32_t* seq_lens, const int32_t* positions, int32_t rotary_dim,
+                          int32_t pairing, const double* inv_freq, const void* q_new, int64_t q_stride,
+                          const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,
+                          void* q_out, void* k_pages, void* v_pages, const int32_t* block_table,
+                          void* kmin, void* kmax, void* ws, size_t ws_bytes, sparse_attn_stream stream);
+
+/* Workspace of sparse_attn_tree_decode for this problem (it also serves
+ * sparse_attn_append_kv and sparse_attn_commit_drafts, which use its first 256 bytes);
+ * independent of n_tokens, so one workspace serves a growing context. */
+int sparse_attn_tree_workspace_size(const sparse_attn_params* p, size_t* bytes);
+
+/* Attention of Q drafted tokens per sequence over the cached context and each other:
+ *   out[b][i][h] = sum over visible t of softmax_t(softmax_scale * q[b][i][h] . k_t) * v_t,
+ * exactly.  q, out [B, Q, Hq, D]; draft j of sequence b is token seq_lens[b] + j of the
+ * pages (put there by sparse_attn_append_kv).  Every query sees the context tokens, or with
+ * sel_ids [B, Hkv, sel_stride] / sel_count [B, Hkv] (as written by sparse_attn_select for
+ * the context; both or neither) those of its KV head's selected blocks; and draft j iff bit
+ * j % 32 of word j / 32 of tree_mask[b][i] is set (device 32-bit words
+ * [B, Q, ceil(Q / 32)]; bits past Q are ignored).  tree_mask == NULL: drafts 0 .. i, a chain.
+ * A query that sees nothing gets a zero row.
+ * Context tokens must be finite; a draft's K and V may hold anything (infinities and NaN
+ * too) as long as the queries that see it are meant to: they reach no other query's row.
+ * Memory behind the drafts is never read into a result.
+ * Q <= 1024, else UNSUPPORTED.  The result does not depend on the launch's timing. */
+int sparse_attn_tree_decode(const sparse_attn_params* p, const void* q, const void* k_pages,
+                            const void* v_pages, const int32_t* block_table, const int32_t* seq_lens,
+                            const int32_t* sel_ids, const int32_t* sel_count, const uint32_t* tree_mask,
+                            float* out, void* ws, size_t ws_bytes, sparse_attn_stream stream);
+
+/* Move accepted drafts to the end of the context: for i < path_len[b], token
+ * seq_lens[b] + i gets the K and V of token seq_lens[b] + path[b][i] (all KV heads), as if
+ * all were read before any is written; new_lens[b] = seq_lens[b] + path_len[b].
+ * path: device int32 [B, path_stride], strictly ascending draft numbers in [0, Q) (a path of a
+ * tree whose parents come before their children); path_len: device int32 [B] in
+ * [0, path_stride].  A path that breaks this sets SPARSE_ATTN_ERR_LENGTH; nothing of that
+ * sequence moves and new_lens[b] = seq_lens[b].  new_lens [B] must not overlap seq_lens; an
+ * inactive sequence keeps -1.
+ * kmin / kmax: both or neither; the touched blocks' rows become the box of their tokens
+ * below new_lens[b], as in sparse_attn_append_kv.
+ * On return the drafts that were not accepted are undefined. */
+int sparse_attn_commit_drafts(const sparse_attn_params* p, const int32_t* seq_lens, const int32_t* path,
+                              int32_t path_stride, const int32_t* path_len, void* k_pages, void* v_pages,
+                              const int32_t* block_table, void* kmin, void* kmax, int32_t* new_lens,
+                              void* ws, size_t ws_bytes, sparse_attn_stream stream);
 
 /* Synchronise `stream`, copy the device error word to *flags (SPARSE_ATTN_ERR_* bits)
  * and clear it.  Returns SPARSE_ATTN_DEVICE_BOUNDS when any bit was set. */

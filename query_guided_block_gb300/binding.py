@@ -19,7 +19,8 @@ LIB_PATH = os.path.join(_HERE, "libsparse_attn.so")
 OK, INVALID_ARG, UNSUPPORTED, CUDA_ERROR, DEVICE_BOUNDS = range(5)
 F32, BF16 = 0, 1
 SCORE_QUEST, SCORE_MEAN = 0, 1
-ERR_PAGE, ERR_SEL_ID, ERR_SEL_COUNT, ERR_TIMEOUT, ERR_SLOT, ERR_CAPACITY = 1, 2, 4, 8, 16, 32
+ERR_PAGE, ERR_SEL_ID, ERR_SEL_COUNT, ERR_TIMEOUT, ERR_SLOT, ERR_CAPACITY, ERR_LENGTH = 1, 2, 4, 8, 16, 32, 64
+ROTATE_HALVES, ROTATE_PAIRS = 1, 2
 
 
 class SparseAttnError(RuntimeError):
@@ -82,7 +83,7 @@ def lib():
                                "(query_guided_block_gb300.build.build())")
         L = C.CDLL(LIB_PATH)
         P = C.POINTER(sparse_attn_params)
-        vp, sz, i32, u32p = C.c_void_p, C.c_size_t, C.c_int32, C.POINTER(C.c_uint32)
+        vp, sz, i32, i64, u32p = C.c_void_p, C.c_size_t, C.c_int32, C.c_int64, C.POINTER(C.c_uint32)
         sigs = {
             "sparse_attn_status_string": ([C.c_int], C.c_char_p),
             "sparse_attn_num_blocks": ([P], C.c_int32),
@@ -110,6 +111,11 @@ def lib():
             "sparse_attn_decode_slots": ([P, vp, vp, vp, i32, vp, vp, vp, vp, vp, sz, vp], C.c_int),
             "sparse_attn_decode_slots_io": ([P, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz,
                                              vp], C.c_int),
+            "sparse_attn_append_kv": ([P, i32, vp, vp, vp, i32, i32, vp, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp,
+                                       vp, vp, vp, sz, vp], C.c_int),
+            "sparse_attn_tree_workspace_size": ([P, C.POINTER(C.c_size_t)], C.c_int),
+            "sparse_attn_tree_decode": ([P, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp], C.c_int),
+            "sparse_attn_commit_drafts": ([P, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp], C.c_int),
         }
         for name, (args, res) in sigs.items():
             fn = getattr(L, name)
@@ -128,7 +134,8 @@ def exported_symbols():
             "sparse_attn_slot_map", "sparse_attn_load_misses", "sparse_attn_decode_slots",
             "sparse_attn_append_meta", "sparse_attn_step", "sparse_attn_step_launches",
             "sparse_attn_select_noalloc_device_error", "sparse_attn_workspace_set_wait_limit",
-            "sparse_attn_decode_slots_io", "sparse_attn_diff_slots"]
+            "sparse_attn_decode_slots_io", "sparse_attn_diff_slots", "sparse_attn_append_kv",
+            "sparse_attn_tree_workspace_size", "sparse_attn_tree_decode", "sparse_attn_commit_drafts"]
 
 
 def _status_string(status: int) -> str:
@@ -347,3 +354,137 @@ def sparse_attn_get_device_error(ws, stream=None) -> int:
     if st not in (OK, DEVICE_BOUNDS):
         raise SparseAttnError("sparse_attn_get_device_error", st)
     return int(flags.value)
+
+
+# ------------------------------- growing the cache, verifying drafted tokens --
+
+def _device_ptr(t: Optional[torch.Tensor], device: torch.device, what: str, shape=None, dtype=None):
+    """Pointer of a contiguous tensor on `device`, of that shape and dtype where given; None
+    stays None."""
+    if t is None:
+        return None
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{what}: expected a CUDA tensor on {device}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous tensor")
+    if dtype is not None and t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _rows_ptr(t: torch.Tensor, device: torch.device, what: str, heads: int, dim: int, dtype):
+    """Pointer and row stride of [rows, heads, dim] whose rows may be strided."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{what}: expected [rows, {heads}, {dim}], got {tuple(t.shape)}")
+    if t.device != device or not t.is_cuda or t.dtype != dtype:
+        raise ValueError(f"{what}: expected a {dtype} CUDA tensor on {device}")
+    s0, s1, s2 = t.stride()
+    if t.shape[0] > 0 and (s2 != 1 or (heads > 1 and s1 != dim)):
+        raise ValueError(f"{what}: the heads of a row must be contiguous")
+    return t.data_ptr(), max(s0, heads * dim) if t.shape[0] <= 1 else s0
+
+
+def _torch_dtypes(p):
+    of = {BF16: torch.bfloat16, F32: torch.float32}
+    return of[p.q_dtype], of[p.kv_dtype]
+
+
+def _cache_ptrs(p, device, k_pages, v_pages, block_table, kmin=None, kmax=None):
+    """Pointers of the page pools, the page table and the key box, their shapes checked."""
+    kvt = _torch_dtypes(p)[1]
+    pool = (p.num_pages, p.num_kv_heads, p.block_size, p.head_dim)
+    nb_cap = meta_rows(p)[0]
+    box = (p.batch, p.num_kv_heads, nb_cap, p.head_dim)
+    return (_device_ptr(k_pages, device, "k_pages", pool, kvt), _device_ptr(v_pages, device, "v_pages", pool, kvt),
+            _device_ptr(block_table, device, "block_table", (p.batch, nb_cap), torch.int32),
+            _device_ptr(kmin, device, "kmin", box, kvt), _device_ptr(kmax, device, "kmax", box, kvt))
+
+
+def _launch_on(device: torch.device, fn: str, stream, *args) -> None:
+    """Calls `fn` with the device of its tensors current, on `stream` or that device's
+    current stream."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    s = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+    if torch.cuda.current_device() == device.index:
+        status = getattr(lib(), fn)(*args, s)
+    else:
+        with torch.cuda.device(device):
+            status = getattr(lib(), fn)(*args, s)
+    if status != OK:
+        raise SparseAttnError(fn, status)
+
+
+def sparse_attn_append_kv(p, q_new, k_new, v_new, inv_freq, q_out, k_pages, v_pages, block_table, ws,
+                          cu_rows=None, seq_lens=None, positions=None, pairing=ROTATE_HALVES, kmin=None,
+                          kmax=None, stream=None) -> None:
+    """Append rows of new tokens to the cache: q_new [rows, Hq, D] (or None), k_new and v_new
+    [rows, Hkv, D], rows possibly strided (slices of one projection); inv_freq float64
+    [rotary_dim / 2] or None for no rotation; q_out [rows, Hq, D]."""
+    dev, (qt, _) = k_new.device, _torch_dtypes(p)
+    rows, hkv, dim = k_new.shape[0], p.num_kv_heads, p.head_dim
+    k, ks = _rows_ptr(k_new, dev, "k_new", hkv, dim, qt)
+    v, vs = _rows_ptr(v_new, dev, "v_new", hkv, dim, qt)
+    q, qs = (None, 0) if q_new is None else _rows_ptr(q_new, dev, "q_new", p.num_q_heads, dim, qt)
+    if v_new.shape[0] != rows or (q_new is not None and q_new.shape[0] != rows):
+        raise ValueError("q_new, k_new and v_new must have the same number of rows")
+    kp, vp, bt, lo, hi = _cache_ptrs(p, dev, k_pages, v_pages, block_table, kmin, kmax)
+    i32 = torch.int32
+    if inv_freq is not None and inv_freq.dim() != 1:
+        raise ValueError("inv_freq: expected [rotary_dim / 2]")
+    _launch_on(dev, "sparse_attn_append_kv", stream, C.byref(p), rows,
+               _device_ptr(cu_rows, dev, "cu_rows", (p.batch + 1,), i32),
+               _device_ptr(seq_lens, dev, "seq_lens", (p.batch,), i32),
+               _device_ptr(positions, dev, "positions", (rows,), i32),
+               0 if inv_freq is None else 2 * inv_freq.shape[0], int(pairing),
+               _device_ptr(inv_freq, dev, "inv_freq", None, torch.float64), q, qs, k, ks, v, vs,
+               _device_ptr(q_out, dev, "q_out", (rows, p.num_q_heads, dim), qt), kp, vp, bt, lo, hi,
+               _device_ptr(ws, dev, "ws"), ws.numel() * ws.element_size())
+
+
+def sparse_attn_tree_workspace_size(p: sparse_attn_params) -> int:
+    n = C.c_size_t(0)
+    _check("sparse_attn_tree_workspace_size", lib().sparse_attn_tree_workspace_size(C.byref(p), C.byref(n)))
+    return int(n.value)
+
+
+def sparse_attn_tree_decode(p, q, k_pages, v_pages, block_table, out, ws, seq_lens=None, sel_ids=None,
+                            sel_count=None, tree_mask=None, stream=None) -> None:
+    """Attention of Q = max(1, p.num_queries) drafts per sequence; q and out [B, Q, Hq, D] (or
+    [B, Hq, D] for one), tree_mask 32-bit words [B, Q, ceil(Q / 32)]."""
+    dev, (qt, _) = q.device, _torch_dtypes(p)
+    n = max(1, p.num_queries)
+    shape = (p.batch, n, p.num_q_heads, p.head_dim)
+    if n == 1 and q.dim() == 3:
+        shape = (p.batch, p.num_q_heads, p.head_dim)
+    kp, vp, bt, _, _ = _cache_ptrs(p, dev, k_pages, v_pages, block_table)
+    i32 = torch.int32
+    sel = None
+    if sel_ids is not None:        # the stride does not depend on the number of queries
+        one = sparse_attn_params.from_buffer_copy(p)
+        one.num_queries = 1
+        sel = (p.batch, p.num_kv_heads, sparse_attn_sel_stride(one))
+    _launch_on(dev, "sparse_attn_tree_decode", stream, C.byref(p), _device_ptr(q, dev, "q", shape, qt), kp, vp, bt,
+               _device_ptr(seq_lens, dev, "seq_lens", (p.batch,), i32), _device_ptr(sel_ids, dev, "sel_ids", sel, i32),
+               _device_ptr(sel_count, dev, "sel_count", (p.batch, p.num_kv_heads), i32),
+               _device_ptr(tree_mask, dev, "tree_mask", (p.batch, n, -(-n // 32)), (torch.int32, torch.uint32)),
+               _device_ptr(out, dev, "out", shape, torch.float32), _device_ptr(ws, dev, "ws"),
+               ws.numel() * ws.element_size())
+
+
+def sparse_attn_commit_drafts(p, path, path_len, k_pages, v_pages, block_table, new_lens, ws, seq_lens=None,
+                              kmin=None, kmax=None, stream=None) -> None:
+    """Move the accepted drafts path [B, stride] (path_len [B] of them) to the end of the
+    context; new_lens [B] gets the new lengths."""
+    dev, i32 = path.device, torch.int32
+    if path.dim() != 2:
+        raise ValueError("path: expected [B, stride]")
+    kp, vp, bt, lo, hi = _cache_ptrs(p, dev, k_pages, v_pages, block_table, kmin, kmax)
+    _launch_on(dev, "sparse_attn_commit_drafts", stream, C.byref(p),
+               _device_ptr(seq_lens, dev, "seq_lens", (p.batch,), i32),
+               _device_ptr(path, dev, "path", (p.batch, path.shape[1]), i32), path.shape[1],
+               _device_ptr(path_len, dev, "path_len", (p.batch,), i32), kp, vp, bt, lo, hi,
+               _device_ptr(new_lens, dev, "new_lens", (p.batch,), i32), _device_ptr(ws, dev, "ws"),
+               ws.numel() * ws.element_size())

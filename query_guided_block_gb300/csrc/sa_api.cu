@@ -14,8 +14,10 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-// 0 on success, else a status code; fills g.
-int make_geometry(const sparse_attn_params* p, Geometry* g)
+// 0 on success, else a status code; fills g.  `drafts`: the queries are a draft tree
+// (sparse_attn_tree_decode and its companions), which any K/V dtype and selection kind may
+// have; otherwise several queries share the selection that one launch computes.
+int make_geometry(const sparse_attn_params* p, Geometry* g, bool drafts = false)
 {
     if (!p || !g) return SPARSE_ATTN_INVALID_ARG;
     memset(g, 0, sizeof *g);
@@ -39,7 +41,7 @@ int make_geometry(const sparse_attn_params* p, Geometry* g)
     const int bs = p->block_size;
     if (bs != 8 && bs != 16 && bs != 32 && bs != 64 && bs != 128) return SPARSE_ATTN_UNSUPPORTED;
     const bool kv_bf16 = p->kv_dtype == SPARSE_ATTN_BF16;
-    if (!decode_supported(p->head_dim, kv_bf16, bs, G)) return SPARSE_ATTN_UNSUPPORTED;
+    if (!drafts && !decode_supported(p->head_dim, kv_bf16, bs, G)) return SPARSE_ATTN_UNSUPPORTED;
 
     g->B = p->batch;
     g->Hq = p->num_q_heads;
@@ -64,7 +66,7 @@ int make_geometry(const sparse_attn_params* p, Geometry* g)
     g->topk = p->topk;
     g->n_reserve = p->num_reserve;
     g->Q = p->num_queries > 1 ? p->num_queries : 1;
-    if (g->Q > 1 && (p->two_level != 0 || !kv_bf16)) return SPARSE_ATTN_UNSUPPORTED;
+    if (!drafts && g->Q > 1 && (p->two_level != 0 || !kv_bf16)) return SPARSE_ATTN_UNSUPPORTED;
     if ((long long)g->Q * G > (1 << 20)) return SPARSE_ATTN_UNSUPPORTED;
     const int k_max = p->topk < g->n_cand ? p->topk : g->n_cand;
     const int r_max = p->num_reserve < g->n_cand ? p->num_reserve : g->n_cand;
@@ -568,6 +570,137 @@ int sparse_attn_decode_slots_io(const sparse_attn_params* p, const void* q, void
     const SlotIo io{hk, hv, miss_ids, miss_slot, counts};
     return status_of(launch_decode(g, L, static_cast<char*>(ws), q, pool_k, pool_v, block_table, sel_ids, sel_count,
                                    out, sel_slot, cache_slots, reinterpret_cast<cudaStream_t>(stream), nullptr, &io));
+}
+
+// ---- growing the cache, draft trees --------------------------------------------
+static int draft_geometry(const sparse_attn_params* p, Geometry* g)
+{
+    const int st = make_geometry(p, g, true);
+    if (st) return st;
+    // page x KV head indexes are 32-bit
+    if ((long long)g->num_pages * g->Hkv > INT32_MAX) return SPARSE_ATTN_UNSUPPORTED;
+    if (g->nb_cap > kMaxCandidates) return SPARSE_ATTN_UNSUPPORTED;
+    return SPARSE_ATTN_OK;
+}
+
+static long long capacity_of(const sparse_attn_params* p)
+{
+    return p->capacity_tokens > 0 ? p->capacity_tokens : p->n_tokens;
+}
+
+int sparse_attn_append_kv(const sparse_attn_params* p, int32_t num_rows, const int32_t* cu_rows,
+                          const int32_t* seq_lens, const int32_t* positions, int32_t rotary_dim,
+                          int32_t pairing, const double* inv_freq, const void* q_new, int64_t q_stride,
+                          const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,
+                          void* q_out, void* k_pages, void* v_pages, const int32_t* block_table,
+                          void* kmin, void* kmax, void* ws, size_t ws_bytes, sparse_attn_stream stream)
+{
+    Geometry g;
+    int st = draft_geometry(p, &g);
+    if (st) return st;
+    if (!ws || !aligned(ws, 256) || ws_bytes < 256) return SPARSE_ATTN_INVALID_ARG;
+    if (num_rows < 0 || rotary_dim < 0 || rotary_dim > g.D || rotary_dim % 16 != 0) return SPARSE_ATTN_INVALID_ARG;
+    if (rotary_dim > 0 && ((pairing != SPARSE_ATTN_ROTATE_HALVES && pairing != SPARSE_ATTN_ROTATE_PAIRS) ||
+                           !inv_freq || !aligned(inv_freq, 8)))
+        return SPARSE_ATTN_INVALID_ARG;
+    if (cu_rows && !seq_lens) return SPARSE_ATTN_INVALID_ARG;
+    if (!aligned(cu_rows, 4) || !aligned(seq_lens, 4) || !aligned(positions, 4)) return SPARSE_ATTN_INVALID_ARG;
+    if ((q_new == nullptr) != (q_out == nullptr) || (kmin == nullptr) != (kmax == nullptr)) return SPARSE_ATTN_INVALID_ARG;
+    if (g.B == 0 || num_rows == 0) return SPARSE_ATTN_OK;
+    const int per_seq = num_rows / g.B;
+    if (!cu_rows && num_rows % g.B != 0) return SPARSE_ATTN_INVALID_ARG;
+    if (!seq_lens && per_seq > g.N) return SPARSE_ATTN_INVALID_ARG;
+    if (g.num_pages < 1 || g.nb_cap < 1) return SPARSE_ATTN_INVALID_ARG;
+    if (!k_new || !v_new || !k_pages || !v_pages || !block_table) return SPARSE_ATTN_INVALID_ARG;
+    const void* ptrs[] = {q_new, k_new, v_new, q_out, k_pages, v_pages, kmin, kmax};
+    for (const void* ptr : ptrs)
+        if (!aligned(ptr, 16)) return SPARSE_ATTN_INVALID_ARG;
+    if (!aligned(block_table, 4)) return SPARSE_ATTN_INVALID_ARG;
+    const int64_t unit = g.q_bf16 ? 8 : 4;   // elements in 16 bytes
+    const int64_t kv_row = int64_t(g.Hkv) * g.D, q_row = int64_t(g.Hq) * g.D;
+    if (k_stride < kv_row || v_stride < kv_row || k_stride % unit || v_stride % unit) return SPARSE_ATTN_INVALID_ARG;
+    if (q_new && (q_stride < q_row || q_stride % unit)) return SPARSE_ATTN_INVALID_ARG;
+    if (q_new == q_out && q_new && q_stride != q_row) return SPARSE_ATTN_INVALID_ARG;
+    AppendCall c{};
+    c.num_rows = num_rows;
+    c.cu_rows = cu_rows;
+    c.seq_lens = seq_lens;
+    c.uniform_len = g.N - per_seq;
+    c.positions = positions;
+    c.rotary_dim = rotary_dim;
+    c.pairing = pairing;
+    c.inv_freq = inv_freq;
+    c.q_new = q_new;
+    c.k_new = k_new;
+    c.v_new = v_new;
+    c.q_stride = q_stride;
+    c.k_stride = k_stride;
+    c.v_stride = v_stride;
+    c.q_out = q_out;
+    c.k_pages = k_pages;
+    c.v_pages = v_pages;
+    c.block_table = block_table;
+    c.kmin = kmin;
+    c.kmax = kmax;
+    c.capacity = int(capacity_of(p));
+    return status_of(launch_append(g, c, static_cast<uint32_t*>(ws), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int sparse_attn_tree_workspace_size(const sparse_attn_params* p, size_t* bytes)
+{
+    if (!bytes) return SPARSE_ATTN_INVALID_ARG;
+    Geometry g;
+    const int st = draft_geometry(p, &g);
+    if (st) return st;
+    if (g.Q > kTreeMaxDrafts) return SPARSE_ATTN_UNSUPPORTED;
+    *bytes = tree_layout(g).total;
+    return SPARSE_ATTN_OK;
+}
+
+int sparse_attn_tree_decode(const sparse_attn_params* p, const void* q, const void* k_pages,
+                            const void* v_pages, const int32_t* block_table, const int32_t* seq_lens,
+                            const int32_t* sel_ids, const int32_t* sel_count, const uint32_t* tree_mask,
+                            float* out, void* ws, size_t ws_bytes, sparse_attn_stream stream)
+{
+    Geometry g;
+    const int st = draft_geometry(p, &g);
+    if (st) return st;
+    if (g.Q > kTreeMaxDrafts) return SPARSE_ATTN_UNSUPPORTED;
+    if (!ws || !aligned(ws, 256) || ws_bytes < tree_layout(g).total) return SPARSE_ATTN_INVALID_ARG;
+    if ((sel_ids == nullptr) != (sel_count == nullptr)) return SPARSE_ATTN_INVALID_ARG;
+    if (capacity_of(p) < (long long)g.N + g.Q) return SPARSE_ATTN_INVALID_ARG;   // the drafts' pages
+    if (g.B == 0) return SPARSE_ATTN_OK;
+    if (g.num_pages < 1 || !q || !out || !k_pages || !v_pages || !block_table) return SPARSE_ATTN_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) ||
+        !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(sel_ids, 4) || !aligned(sel_count, 4) ||
+        !aligned(tree_mask, 4))
+        return SPARSE_ATTN_INVALID_ARG;
+    const TreeCall c{q, k_pages, v_pages, block_table, seq_lens, sel_ids, sel_count, tree_mask, out};
+    return status_of(launch_tree(g, c, static_cast<char*>(ws), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int sparse_attn_commit_drafts(const sparse_attn_params* p, const int32_t* seq_lens, const int32_t* path,
+                              int32_t path_stride, const int32_t* path_len, void* k_pages, void* v_pages,
+                              const int32_t* block_table, void* kmin, void* kmax, int32_t* new_lens,
+                              void* ws, size_t ws_bytes, sparse_attn_stream stream)
+{
+    Geometry g;
+    const int st = draft_geometry(p, &g);
+    if (st) return st;
+    if (g.Q > kTreeMaxDrafts) return SPARSE_ATTN_UNSUPPORTED;
+    if (!ws || !aligned(ws, 256) || ws_bytes < 256) return SPARSE_ATTN_INVALID_ARG;
+    if (path_stride < 0 || (kmin == nullptr) != (kmax == nullptr)) return SPARSE_ATTN_INVALID_ARG;
+    if (capacity_of(p) < (long long)g.N + g.Q) return SPARSE_ATTN_INVALID_ARG;
+    if (g.B == 0) return SPARSE_ATTN_OK;
+    if (!path_len || !new_lens || !aligned(path_len, 4) || !aligned(new_lens, 4) || !aligned(seq_lens, 4))
+        return SPARSE_ATTN_INVALID_ARG;
+    if (g.num_pages < 1 || !path || !k_pages || !v_pages || !block_table) return SPARSE_ATTN_INVALID_ARG;
+    if (!aligned(path, 4) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(block_table, 4) ||
+        !aligned(kmin, 16) || !aligned(kmax, 16))
+        return SPARSE_ATTN_INVALID_ARG;
+    if (seq_lens && new_lens < seq_lens + g.B && seq_lens < new_lens + g.B) return SPARSE_ATTN_INVALID_ARG;
+    return status_of(launch_commit(g, seq_lens, path, path_stride, path_len, k_pages, v_pages, block_table, kmin, kmax,
+                                   new_lens, static_cast<uint32_t*>(ws), reinterpret_cast<cudaStream_t>(stream)));
 }
 
 // ---- selection for callers that cannot allocate device memory ---------------

@@ -148,6 +148,43 @@ cudaError_t launch_step_d64(const Geometry& g, const WorkspaceLayout& L, char* w
                             const int32_t* block_table, int32_t* sel_ids, int32_t* sel_count, float* out,
                             cudaStream_t s);
 
+// Growing the cache (sa_append.cu).  Arguments as the C calls, validated.
+struct AppendCall {
+    int num_rows;
+    const int32_t* cu_rows;      // null: num_rows / B rows a sequence
+    const int32_t* seq_lens;     // null: uniform_len
+    int uniform_len;
+    const int32_t* positions;    // null: the token's index
+    int rotary_dim, pairing;
+    const double* inv_freq;
+    const void *q_new, *k_new, *v_new;
+    long long q_stride, k_stride, v_stride;   // elements
+    void *q_out, *k_pages, *v_pages;
+    const int32_t* block_table;
+    void *kmin, *kmax;
+    int capacity;                // tokens a sequence has pages for
+};
+cudaError_t launch_append(const Geometry& g, const AppendCall& c, uint32_t* err, cudaStream_t s);
+cudaError_t launch_commit(const Geometry& g, const int32_t* seq_lens, const int32_t* path, int path_stride,
+                          const int32_t* path_len, void* k_pages, void* v_pages, const int32_t* block_table,
+                          void* kmin, void* kmax, int32_t* new_lens, uint32_t* err, cudaStream_t s);
+
+// Draft-tree attention (sa_tree.cu).  Workspace: header, one arrival counter per (unit, row
+// group), then the partial results of units that several CTAs share.
+struct TreeLayout {
+    size_t counters, part_m, part_l, part_o, total;
+};
+TreeLayout tree_layout(const Geometry& g);
+constexpr int kTreeMaxDrafts = 1024;
+struct TreeCall {
+    const void* q;
+    const void *k_pages, *v_pages;
+    const int32_t *block_table, *seq_lens, *sel_ids, *sel_count;
+    const uint32_t* mask;
+    float* out;
+};
+cudaError_t launch_tree(const Geometry& g, const TreeCall& c, char* ws, cudaStream_t s);
+
 cudaError_t launch_diff(const Geometry& g, int step, const int32_t* sel_ids,
                         const int32_t* sel_count, const int32_t* prev_ids,
                         const int32_t* prev_count, int cache_slots, int32_t* slot_block,

@@ -1,0 +1,590 @@
+// Attention of a tree of drafted tokens over a paged cache: Q queries per sequence, each over
+// the context (all of it or its KV head's selected blocks) and over the drafts its mask names.
+//
+// This file: the kernel for every type combination on warp-level matrix instructions, and
+// the launcher.  Per 64-token tile of the unit's list (sa_tree.cuh) and warp of 16 query
+// rows: S = Q K^T, the softmax with a running maximum and sum on the accumulator fragments,
+// O += P V with the score fragments as the A operand.
+//   bf16 K/V: mma.m16n8k16, fp32 accumulation.  P goes in as bf16 hi + lo (16 bits: the output
+//     is fp32, one bf16 would leave an error of 2^-9 in every weight), an fp32 query as three
+//     bf16 parts (24 bits).
+//   fp32 K/V: mma.m16n8k8 on tf32 parts, x = hi + lo rounded to nearest (22 bits), the three
+//     products that matter.  The channel (token) order inside a k-step is permuted alike on
+//     both sides, so that a thread's two elements are neighbours in memory.
+// Four warps: 4 x 16 rows over the same tokens, or with at most 16 rows 4 x 16 tokens over the
+// same rows, their (m, l, o) joined at the item's end.
+#include "sa_tree.cuh"
+
+namespace sa {
+namespace {
+
+constexpr int kTrThreads = 128;
+constexpr int kTrTile = 64;
+constexpr int kTrEntries = 1024;     // list entries resolved at a time
+
+__device__ __forceinline__ void mma_tf32_1688(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t to_tf32(float x)
+{
+    uint32_t r;
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo)
+{
+    hi = to_tf32(x);
+    lo = to_tf32(x - __uint_as_float(hi));
+}
+
+template <int D, bool KB>
+struct TrShape {
+    static constexpr int ROW = D * (KB ? 2 : 4);            // bytes of a token row
+    static constexpr int CPR = ROW / 16;                    // 16-byte chunks
+    static constexpr int TENSOR = kTrTile * ROW;
+    static constexpr int STAGE = 2 * TENSOR;
+    static constexpr int STAGES = STAGE > 32768 ? 2 : 3;    // 64 to 96 KB of tiles (fp32, D = 128: 128 KB)
+    static constexpr int Q_ROW = D + 8;                     // floats of a query row (fp32 K/V)
+    // Chunk c of token row r.  bf16: 128-byte groups, c ^ (r mod 8) (ldmatrix reads 8 rows).
+    // fp32: a fragment load touches 4 rows x 2 chunks; f takes 4 values over rows 0-3 and
+    // 4-7 (keys) and over the even and the odd rows (values).
+    static __device__ __forceinline__ uint32_t at(int r, int c)
+    {
+        if constexpr (KB) {
+            return uint32_t((c >> 3) * (kTrTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+        } else {
+            const int f = (r ^ (r >> 2)) & 3;
+            return uint32_t(r * ROW + ((c ^ (f << 1)) << 4));
+        }
+    }
+};
+
+template <int D, bool KB, int NQ, int RW>
+__global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
+{
+    using SH = TrShape<D, KB>;
+    constexpr int TW = 4 / RW;                // warps that split a tile's tokens
+    constexpr int NT = 8 / TW;                // 8-token groups per warp
+    constexpr int DT = D / 8;
+    constexpr int ROWS = 16 * RW;
+    constexpr int CPT = kTrTile * SH::CPR / kTrThreads;     // chunks a thread copies per tensor
+
+    extern __shared__ __align__(128) unsigned char smem_raw[];
+    __shared__ int2 s_ent[kTrEntries];
+    __shared__ uint32_t s_any[kTreeMaxDrafts / 32];         // drafts that some query sees
+    __shared__ long long s_scan[kTrThreads / 32 + 2];
+    __shared__ int s_last;
+    __shared__ uint32_t s_bad[2];
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g4 = lane >> 2, t4 = lane & 3;
+    const int wr = RW == 1 ? 0 : warp, wt = RW == 1 ? warp : 0;    // the warp's rows / tokens
+    unsigned char* smem = smem_raw + ((128u - (smem_u32(smem_raw) & 127u)) & 127u);
+    const uint32_t base = smem_u32(smem);
+    float* s_q = reinterpret_cast<float*>(smem + SH::STAGES * SH::STAGE);   // fp32 K/V: [ROWS][Q_ROW]
+
+    allow_dependents_early();
+    grid_dependency_wait();   // queries, pages and lengths may come from the previous kernel
+
+    const TreePart part = tree_part<kTrThreads>(a, s_scan);
+    const bool dense = a.sel_ids == nullptr;
+    long long lo = part.lo, start = part.start;
+    int item = part.item;
+
+    while (lo < part.hi) {
+        const int u = item / a.row_groups, rg = item - u * a.row_groups;
+        const int b = u / a.Hkv, kvh = u - b * a.Hkv;
+        const TreeUnit un = tree_unit(a, u);
+        const int tiles = tree_tiles(a, un);
+        if (tiles == 0) {
+            ++item;
+            continue;
+        }
+        const int t0 = int(lo - start), t1 = int(min((long long)tiles, part.hi - start));
+        const int row0 = rg * ROWS;                          // first unit row of the item
+        const uint32_t* mask_b = a.mask != nullptr ? a.mask + (long long)b * a.Q * a.mask_words : nullptr;
+
+        __syncthreads();                                     // the previous item is done with shared memory
+        for (int w = tid; w < a.mask_words; w += kTrThreads) {
+            uint32_t m = 0u;
+            if (mask_b == nullptr) m = ~0u;
+            else
+                for (int i = 0; i < a.Q; ++i) m |= mask_b[(long long)i * a.mask_words + w];
+            s_any[w] = m;
+        }
+
+        // ---- the queries: A fragments in registers, or fp32 rows in shared memory -------
+        const int r_lo = row0 + wr * 16 + g4, r_hi = r_lo + 8;
+        uint32_t qa[KB ? NQ : 1][KB ? D / 16 : 1][4];
+        if constexpr (KB) {
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+                for (int hc = 0; hc < 4; ++hc) {             // a0, a1: k 0-7 of rows lo, hi; a2, a3: k 8-15
+                    const int r = (hc & 1) ? r_hi : r_lo;
+                    float f0 = 0.f, f1 = 0.f;
+                    if (r < a.R) {
+                        const size_t at = size_t(tree_out_row(a, b, kvh, r)) * D + ks * 16 + (hc >> 1) * 8 + 2 * t4;
+                        f0 = load_q(a.q, at, a.q_bf16 != 0);
+                        f1 = load_q(a.q, at + 1, a.q_bf16 != 0);
+                    }
+#pragma unroll
+                    for (int part_q = 0; part_q < NQ; ++part_q) {
+                        const uint32_t w = pack_bf16x2(f0, f1);
+                        qa[part_q][ks][hc] = w;
+                        f0 -= bf16_lo(w);
+                        f1 -= bf16_hi(w);
+                    }
+                }
+        } else {
+            for (int i = tid; i < ROWS * D; i += kTrThreads) {
+                const int rr = i / D, d = i - rr * D;
+                s_q[rr * SH::Q_ROW + d] =
+                    row0 + rr < a.R ? load_q(a.q, size_t(tree_out_row(a, b, kvh, row0 + rr)) * D + d, a.q_bf16 != 0) : 0.f;
+            }
+        }
+
+        float acc[DT][4];
+#pragma unroll
+        for (int j = 0; j < DT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+        float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+
+        const int step = ((kTrEntries - 1) << a.bs_shift) / kTrTile;      // tiles whose entries fit s_ent
+        for (int ca = t0; ca < t1; ca += step) {
+            const int cb = min(t1, ca + step);
+            const int e0 = (ca * kTrTile) >> a.bs_shift;
+            const int e1 = min(un.n_entries, ((cb * kTrTile - 1) >> a.bs_shift) + 1);
+            __syncthreads();
+            for (int e = e0 + tid; e < e1; e += kTrThreads) s_ent[e - e0] = tree_entry(a, u, un, e);
+            __syncthreads();
+
+            // 1: context token, 2: draft that some query sees, 0: neither
+            auto token_kind = [&](int gi, int& draft) -> int {
+                const int e = gi >> a.bs_shift;
+                if (e >= e1) return 0;
+                const int2 en = s_ent[e - e0];
+                const int tok = en.y + (gi & (a.bs - 1));
+                draft = tok - un.len;
+                if (en.x < 0) return 0;
+                if (draft < 0) return (dense || e < un.n_ctx) ? 1 : 0;
+                if (draft >= a.Q || !(dense || e >= un.n_ctx)) return 0;
+                return ((s_any[draft >> 5] >> (draft & 31)) & 1u) ? 2 : 0;
+            };
+            auto sees = [&](int r, int draft) -> bool {      // unit row r, a draft in [0, Q)
+                if (r >= a.R) return false;
+                const int t = r / a.G;
+                if (mask_b == nullptr) return draft <= t;
+                return (__ldg(mask_b + (long long)t * a.mask_words + (draft >> 5)) >> (draft & 31)) & 1u;
+            };
+            const char* kp = static_cast<const char*>(a.k_pages);
+            const char* vp = static_cast<const char*>(a.v_pages);
+            const int cp_c = tid % SH::CPR, cp_r = tid / SH::CPR;
+            auto issue_tile = [&](int tile, int st) {
+                const uint32_t kd = base + uint32_t(st) * SH::STAGE, vd = kd + SH::TENSOR;
+#pragma unroll
+                for (int i = 0; i < CPT; ++i) {
+                    const int tr = cp_r + i * (kTrThreads / SH::CPR);
+                    const int gi = tile * kTrTile + tr;
+                    int draft;
+                    const bool ok = token_kind(gi, draft) != 0;
+                    const size_t off =
+                        ok ? (size_t(s_ent[(gi >> a.bs_shift) - e0].x) * a.bs + (gi & (a.bs - 1))) * SH::ROW + cp_c * 16 : 0;
+                    cp_async_16_zfill(kd + SH::at(tr, cp_c), kp + off, ok ? 16u : 0u);
+                    cp_async_16_zfill(vd + SH::at(tr, cp_c), vp + off, ok ? 16u : 0u);
+                }
+            };
+#pragma unroll
+            for (int kk = 0; kk < SH::STAGES - 1; ++kk) {
+                if (ca + kk < cb) issue_tile(ca + kk, kk);
+                cp_async_commit();
+            }
+
+            for (int tile = ca; tile < cb; ++tile) {
+                const int k = tile - ca;
+                cp_async_wait_group<SH::STAGES - 2>();
+                __syncthreads();          // tile k is staged; stage k - 1 is free
+                if (tile + SH::STAGES - 1 < cb) issue_tile(tile + SH::STAGES - 1, (k + SH::STAGES - 1) % SH::STAGES);
+                cp_async_commit();
+                unsigned char* stage = smem + (k % SH::STAGES) * SH::STAGE;
+                const uint32_t kst = base + uint32_t(k % SH::STAGES) * SH::STAGE, vst = kst + SH::TENSOR;
+
+                // does the tile hold anything but context tokens, and drafts?
+                bool whole = true, drafts = false;
+                for (int p = tile * kTrTile; p < (tile + 1) * kTrTile; p += min(a.bs, kTrTile)) {
+                    const int e = p >> a.bs_shift;
+                    if (e >= e1) {
+                        whole = false;
+                        break;
+                    }
+                    const int2 en = s_ent[e - e0];
+                    const int end = en.y + a.bs;
+                    if (en.x < 0 || end > un.len || !(dense || e < un.n_ctx)) whole = false;
+                    if (en.x >= 0 && end > un.len && (dense || e >= un.n_ctx)) drafts = true;
+                }
+                // A draft's V may hold infinities or NaN that other queries must not meet as
+                // 0 * inf: such rows are taken out of the product and added where they are seen.
+                uint32_t bad0 = 0u, bad1 = 0u;
+                if (drafts) {
+                    if (tid < 2) s_bad[tid] = 0u;
+                    __syncthreads();
+                    for (int i = tid; i < kTrTile * SH::CPR; i += kTrThreads) {
+                        const int tr = i / SH::CPR;
+                        const uint4 v = *reinterpret_cast<const uint4*>(stage + SH::TENSOR + SH::at(tr, i - tr * SH::CPR));
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                        bool odd = false;
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            odd |= (w[x] & 0x7f800000u) == 0x7f800000u;
+                            if constexpr (KB) odd |= (w[x] & 0x7f80u) == 0x7f80u;
+                        }
+                        if (odd) atomicOr(&s_bad[tr >> 5], 1u << (tr & 31));
+                    }
+                    __syncthreads();
+                    bad0 = s_bad[0];
+                    bad1 = s_bad[1];
+                    if (bad0 | bad1) {
+                        for (int i = tid; i < kTrTile * SH::CPR; i += kTrThreads) {
+                            const int tr = i / SH::CPR;
+                            if (((tr < 32 ? bad0 : bad1) >> (tr & 31)) & 1u)
+                                *reinterpret_cast<uint4*>(stage + SH::TENSOR + SH::at(tr, i - tr * SH::CPR)) =
+                                    make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        __syncthreads();
+                    }
+                }
+
+                // ---- S = Q K^T ------------------------------------------------------
+                float c[NT][4];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) c[nt][0] = c[nt][1] = c[nt][2] = c[nt][3] = 0.f;
+                const int tok0 = wt * NT * 8;                // the warp's first token of the tile
+                if constexpr (KB) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int kp2 = 0; kp2 < D / 32; ++kp2) {
+                            uint32_t b0, b1, b2, b3;
+                            ldsm_x4(kst + SH::at(tok0 + nt * 8 + (lane & 7), kp2 * 4 + (lane >> 3)), b0, b1, b2, b3);
+#pragma unroll
+                            for (int pq = NQ - 1; pq >= 0; --pq) {
+                                mma_bf16_16816(c[nt], qa[pq][2 * kp2][0], qa[pq][2 * kp2][1], qa[pq][2 * kp2][2],
+                                               qa[pq][2 * kp2][3], b0, b1);
+                                mma_bf16_16816(c[nt], qa[pq][2 * kp2 + 1][0], qa[pq][2 * kp2 + 1][1],
+                                               qa[pq][2 * kp2 + 1][2], qa[pq][2 * kp2 + 1][3], b2, b3);
+                            }
+                        }
+                } else {
+#pragma unroll 2
+                    for (int ks = 0; ks < D / 8; ++ks) {
+                        const float* q0 = s_q + (wr * 16 + g4) * SH::Q_ROW + ks * 8 + 2 * t4;
+                        const float2 x = *reinterpret_cast<const float2*>(q0);
+                        const float2 y = *reinterpret_cast<const float2*>(q0 + 8 * SH::Q_ROW);
+                        uint32_t ah[4], al[4];
+                        split_tf32(x.x, ah[0], al[0]);
+                        split_tf32(y.x, ah[1], al[1]);
+                        split_tf32(x.y, ah[2], al[2]);
+                        split_tf32(y.y, ah[3], al[3]);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const int tr = tok0 + nt * 8 + g4;
+                            const float2 kf = *reinterpret_cast<const float2*>(stage + SH::at(tr, ks * 2 + (t4 >> 1)) + (t4 & 1) * 8);
+                            uint32_t bh0, bl0, bh1, bl1;
+                            split_tf32(kf.x, bh0, bl0);
+                            split_tf32(kf.y, bh1, bl1);
+                            mma_tf32_1688(c[nt], al, bh0, bh1);
+                            mma_tf32_1688(c[nt], ah, bl0, bl1);
+                            mma_tf32_1688(c[nt], ah, bh0, bh1);
+                        }
+                    }
+                }
+                // ---- scale, mask, running maximum and sum ---------------------------------
+                float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        bool ok0 = true, ok1 = true;
+                        if (!whole) {
+                            int draft;
+                            const int kind = token_kind(tile * kTrTile + tok0 + nt * 8 + 2 * t4 + e, draft);
+                            ok0 = kind == 1 || (kind == 2 && sees(r_lo, draft));
+                            ok1 = kind == 1 || (kind == 2 && sees(r_hi, draft));
+                        }
+                        c[nt][e] = ok0 ? c[nt][e] * a.scale_log2 : -INFINITY;
+                        c[nt][e + 2] = ok1 ? c[nt][e + 2] * a.scale_log2 : -INFINITY;
+                        mx[0] = fmaxf(mx[0], c[nt][e]);
+                        mx[1] = fmaxf(mx[1], c[nt][e + 2]);
+                    }
+                float alpha[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    mx[h] = fmaxf(mx[h], __shfl_xor_sync(kFullMask, mx[h], 1));
+                    mx[h] = fmaxf(mx[h], __shfl_xor_sync(kFullMask, mx[h], 2));
+                    const float m_new = fmaxf(m_run[h], mx[h]);
+                    alpha[h] = (m_run[h] == -INFINITY) ? 0.f : fast_exp2(m_run[h] - m_new);
+                    m_run[h] = m_new;
+                }
+                float psum[2] = {0.f, 0.f};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int h = e >> 1;
+                        c[nt][e] = (c[nt][e] == -INFINITY) ? 0.f : fast_exp2(c[nt][e] - m_run[h]);
+                        psum[h] += c[nt][e];
+                    }
+                l_run[0] = fmaf(l_run[0], alpha[0], psum[0]);
+                l_run[1] = fmaf(l_run[1], alpha[1], psum[1]);
+#pragma unroll
+                for (int j = 0; j < DT; ++j) {
+                    acc[j][0] *= alpha[0];
+                    acc[j][1] *= alpha[0];
+                    acc[j][2] *= alpha[1];
+                    acc[j][3] *= alpha[1];
+                }
+                // ---- O += P V ---------------------------------------------------------
+                if constexpr (KB) {
+#pragma unroll
+                    for (int kk = 0; kk < NT / 2; ++kk) {
+                        const float* p0 = c[2 * kk];
+                        const float* p1 = c[2 * kk + 1];
+                        const uint32_t h0 = pack_bf16x2(p0[0], p0[1]), h1 = pack_bf16x2(p0[2], p0[3]);
+                        const uint32_t h2 = pack_bf16x2(p1[0], p1[1]), h3 = pack_bf16x2(p1[2], p1[3]);
+                        const uint32_t l0 = pack_bf16x2(p0[0] - bf16_lo(h0), p0[1] - bf16_hi(h0));
+                        const uint32_t l1 = pack_bf16x2(p0[2] - bf16_lo(h1), p0[3] - bf16_hi(h1));
+                        const uint32_t l2 = pack_bf16x2(p1[0] - bf16_lo(h2), p1[1] - bf16_hi(h2));
+                        const uint32_t l3 = pack_bf16x2(p1[2] - bf16_lo(h3), p1[3] - bf16_hi(h3));
+#pragma unroll
+                        for (int jp = 0; jp < DT; jp += 2) {
+                            const int mtx = lane >> 3;
+                            uint32_t v0, v1, v2, v3;
+                            ldsm_x4_trans(vst + SH::at(tok0 + kk * 16 + (mtx & 1) * 8 + (lane & 7), jp + (mtx >> 1)), v0, v1,
+                                          v2, v3);
+                            mma_bf16_16816(acc[jp], l0, l1, l2, l3, v0, v1);
+                            mma_bf16_16816(acc[jp], h0, h1, h2, h3, v0, v1);
+                            mma_bf16_16816(acc[jp + 1], l0, l1, l2, l3, v2, v3);
+                            mma_bf16_16816(acc[jp + 1], h0, h1, h2, h3, v2, v3);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        uint32_t ah[4], al[4];               // k index t4 <-> token 2 t4, t4 + 4 <-> 2 t4 + 1
+                        split_tf32(c[nt][0], ah[0], al[0]);
+                        split_tf32(c[nt][2], ah[1], al[1]);
+                        split_tf32(c[nt][1], ah[2], al[2]);
+                        split_tf32(c[nt][3], ah[3], al[3]);
+                        const int tr = tok0 + nt * 8 + 2 * t4;
+                        const unsigned char* vs = stage + SH::TENSOR;
+#pragma unroll
+                        for (int j = 0; j < DT; ++j) {
+                            const int ch = j * 2 + (g4 >> 2), by = (g4 & 3) * 4;
+                            const float v0 = *reinterpret_cast<const float*>(vs + SH::at(tr, ch) + by);
+                            const float v1 = *reinterpret_cast<const float*>(vs + SH::at(tr + 1, ch) + by);
+                            uint32_t bh0, bl0, bh1, bl1;
+                            split_tf32(v0, bh0, bl0);
+                            split_tf32(v1, bh1, bl1);
+                            mma_tf32_1688(acc[j], al, bh0, bh1);
+                            mma_tf32_1688(acc[j], ah, bl0, bl1);
+                            mma_tf32_1688(acc[j], ah, bh0, bh1);
+                        }
+                    }
+                }
+                if (bad0 | bad1) {                           // rows taken out above
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) {
+                            const int tr = tok0 + nt * 8 + x;
+                            if (!(((tr < 32 ? bad0 : bad1) >> (tr & 31)) & 1u)) continue;
+                            const float p0 = __shfl_sync(kFullMask, c[nt][x & 1], (lane & ~3) | (x >> 1));
+                            const float p1 = __shfl_sync(kFullMask, c[nt][2 + (x & 1)], (lane & ~3) | (x >> 1));
+                            const int gi = tile * kTrTile + tr;
+                            const size_t at = (size_t(s_ent[(gi >> a.bs_shift) - e0].x) * a.bs + (gi & (a.bs - 1))) * D;
+#pragma unroll
+                            for (int j = 0; j < DT; ++j)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const float v = load_q(a.v_pages, at + j * 8 + 2 * t4 + e, KB);
+                                    if (p0 != 0.f) acc[j][e] = fmaf(p0, v, acc[j][e]);
+                                    if (p1 != 0.f) acc[j][2 + e] = fmaf(p1, v, acc[j][2 + e]);
+                                }
+                        }
+                }
+            }
+            cp_async_wait_group<0>();
+        }
+
+        // ---- the part's (m, l, o): the output itself, or a partial ---------------------
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            l_run[h] += __shfl_xor_sync(kFullMask, l_run[h], 1);
+            l_run[h] += __shfl_xor_sync(kFullMask, l_run[h], 2);
+        }
+        const bool complete = t0 == 0 && t1 == tiles;
+        const long long slot = (long long)tree_slot(blockIdx.x, part.per, start) * a.item_rows;
+        if constexpr (TW == 1) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = h ? r_hi : r_lo, rr = r - row0;
+                if (r >= a.R) continue;
+                const float inv = complete ? (l_run[h] == 0.f ? 0.f : 1.f / l_run[h]) : 1.f;
+                float* dst = (complete ? a.out + tree_out_row(a, b, kvh, r) * D : a.part_o + (slot + rr) * D) + 2 * t4;
+#pragma unroll
+                for (int j = 0; j < DT; ++j)
+                    *reinterpret_cast<float2*>(dst + j * 8) = make_float2(acc[j][2 * h] * inv, acc[j][2 * h + 1] * inv);
+                if (!complete && t4 == 0) {
+                    a.part_m[slot + rr] = m_run[h];
+                    a.part_l[slot + rr] = l_run[h];
+                }
+            }
+        } else {
+            // the four warps' token shares of the same 16 rows, through the freed stages
+            float* x_o = reinterpret_cast<float*>(smem);                 // [TW][16][D + 4]
+            float* x_m = x_o + TW * 16 * (D + 4);                        // [TW][16]
+            float* x_l = x_m + TW * 16;
+            __syncthreads();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int rr = g4 + 8 * h;
+                float* dst = x_o + (wt * 16 + rr) * (D + 4) + 2 * t4;
+#pragma unroll
+                for (int j = 0; j < DT; ++j) *reinterpret_cast<float2*>(dst + j * 8) = make_float2(acc[j][2 * h], acc[j][2 * h + 1]);
+                if (t4 == 0) {
+                    x_m[wt * 16 + rr] = m_run[h];
+                    x_l[wt * 16 + rr] = l_run[h];
+                }
+            }
+            __syncthreads();
+            for (int i = tid; i < 16 * (D / 4); i += kTrThreads) {
+                const int rr = i / (D / 4), d = (i - rr * (D / 4)) * 4;
+                if (row0 + rr >= a.R) continue;
+                float M = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < TW; ++w) M = fmaxf(M, x_m[w * 16 + rr]);
+                float den = 0.f;
+                float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < TW; ++w) {
+                    const float mw = x_m[w * 16 + rr];
+                    if (mw == -INFINITY) continue;
+                    const float wgt = fast_exp2(mw - M);
+                    den = fmaf(x_l[w * 16 + rr], wgt, den);
+                    const float4 o = *reinterpret_cast<const float4*>(x_o + (w * 16 + rr) * (D + 4) + d);
+                    num.x = fmaf(o.x, wgt, num.x);
+                    num.y = fmaf(o.y, wgt, num.y);
+                    num.z = fmaf(o.z, wgt, num.z);
+                    num.w = fmaf(o.w, wgt, num.w);
+                }
+                const float inv = complete ? (den == 0.f ? 0.f : 1.f / den) : 1.f;
+                float* dst = complete ? a.out + tree_out_row(a, b, kvh, row0 + rr) * D : a.part_o + (slot + rr) * D;
+                *reinterpret_cast<float4*>(dst + d) = make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
+                if (!complete && d == 0) {
+                    a.part_m[slot + rr] = M;
+                    a.part_l[slot + rr] = den;
+                }
+            }
+        }
+        if (!complete) tree_arrive_and_merge<kTrThreads>(a, item, start, tiles, part.per, &s_last);
+        lo = start + t1;
+        if (t1 == tiles) {
+            start += tiles;
+            ++item;
+        }
+    }
+}
+
+template <int D, bool KB, int NQ, int RW>
+cudaError_t launch_tree_t(TreeArgs a, cudaStream_t s)
+{
+    using SH = TrShape<D, KB>;
+    const size_t smem = 128 + size_t(SH::STAGES) * SH::STAGE + (KB ? 0 : size_t(16 * RW) * SH::Q_ROW * 4);
+    static std::atomic<unsigned long long> configured{0};   // devices set up
+    const cudaError_t cfg = once_per_device(configured, [&]() -> cudaError_t {
+        return cudaFuncSetAttribute(tree_kernel<D, KB, NQ, RW>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    });
+    if (cfg != cudaSuccess) return cfg;
+    a.tile = kTrTile;
+    a.item_rows = 16 * RW;
+    a.row_groups = (a.R + a.item_rows - 1) / a.item_rows;
+    a.min_per = 4;
+    int ctas = num_sms() * (2 * (smem + 10 * 1024) <= size_t(kSmemPerSm) ? 2 : 1);
+    if (ctas > kTreeMaxCtas) ctas = kTreeMaxCtas;
+    return launch_after_previous(tree_kernel<D, KB, NQ, RW>, dim3(unsigned(ctas)), dim3(kTrThreads), smem, s, a);
+}
+
+template <int D, bool KB, int NQ>
+cudaError_t launch_tree_rows(const TreeArgs& a, cudaStream_t s)
+{
+    return a.R <= 16 ? launch_tree_t<D, KB, NQ, 1>(a, s) : launch_tree_t<D, KB, NQ, 4>(a, s);
+}
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+}  // namespace
+
+TreeLayout tree_layout(const Geometry& g)
+{
+    TreeLayout L{};
+    const int R = g.Q * g.G;
+    const size_t rows = R <= 16 ? 16 : (R <= 64 ? 64 : (R <= 128 ? 128 : kTreeMaxRows));   // of an item, in any kernel
+    const size_t slots = 2 * size_t(kTreeMaxCtas);
+    L.counters = 256;
+    L.part_m = align256(L.counters + size_t(g.units()) * ((R + 15) / 16) * sizeof(uint32_t));
+    L.part_l = align256(L.part_m + slots * rows * sizeof(float));
+    L.part_o = align256(L.part_l + slots * rows * sizeof(float));
+    L.total = align256(L.part_o + slots * rows * g.D * sizeof(float));
+    return L;
+}
+
+cudaError_t launch_tree(const Geometry& g, const TreeCall& c, char* ws, cudaStream_t s)
+{
+    const TreeLayout L = tree_layout(g);
+    TreeArgs a{};
+    a.q = c.q;
+    a.q_bf16 = g.q_bf16;
+    a.k_pages = c.k_pages;
+    a.v_pages = c.v_pages;
+    a.block_table = c.block_table;
+    a.seq_lens = c.seq_lens;
+    a.sel_ids = c.sel_ids;
+    a.sel_count = c.sel_count;
+    a.mask = c.mask;
+    a.out = c.out;
+    a.B = g.B;
+    a.Hq = g.Hq;
+    a.Hkv = g.Hkv;
+    a.G = g.G;
+    a.Q = g.Q;
+    a.R = g.Q * g.G;
+    a.D = g.D;
+    a.N = g.N;
+    a.bs = g.bs;
+    a.bs_shift = 0;
+    while ((1 << a.bs_shift) < g.bs) ++a.bs_shift;
+    a.nb = g.nb;
+    a.nb_cap = g.nb_cap;
+    a.num_pages = g.num_pages;
+    a.sel_stride = g.sel_stride;
+    a.mask_words = (g.Q + 31) / 32;
+    a.scale_log2 = g.scale_log2;
+    a.part_m = reinterpret_cast<float*>(ws + L.part_m);
+    a.part_l = reinterpret_cast<float*>(ws + L.part_l);
+    a.part_o = reinterpret_cast<float*>(ws + L.part_o);
+    a.counters = reinterpret_cast<uint32_t*>(ws + L.counters);
+    a.err = reinterpret_cast<uint32_t*>(ws);
+    if (g.kv_bf16) {
+        if (g.q_bf16) return g.D == 128 ? launch_tree_rows<128, true, 1>(a, s) : launch_tree_rows<64, true, 1>(a, s);
+        return g.D == 128 ? launch_tree_rows<128, true, 3>(a, s) : launch_tree_rows<64, true, 3>(a, s);
+    }
+    return g.D == 128 ? launch_tree_rows<128, false, 1>(a, s) : launch_tree_rows<64, false, 1>(a, s);
+}
+
+}  // namespace sa

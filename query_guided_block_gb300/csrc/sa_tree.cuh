@@ -1,0 +1,231 @@
+// Shared by the draft-tree attention kernels: the token list of a (sequence, KV head) unit,
+// how its tiles are dealt to CTAs, and the merge of units that several CTAs share.
+//
+// A unit's keys are a list of entries of one block each: the context's blocks (or the
+// selected ones), then the blocks that hold drafts.  Without a selection both are the blocks
+// 0 .. of the sequence and a block may hold context and drafts.  Entry e covers list
+// positions e * bs .. e * bs + bs - 1; tiles of T positions are cut from the list.
+//
+// Work split: the tiles of all items (unit, row group) form one line, cut into equal parts of
+// `per` tiles, one per CTA, whatever the contexts' lengths are (they are only known on the
+// device).  An item that lies in one part is finished there; one that several parts share
+// leaves (m, l, o) per part in the workspace, and the CTA that arrives last adds them up in
+// the parts' order, so the result does not depend on timing.
+#pragma once
+
+#include "sa_common.cuh"
+#include "sa_internal.h"
+
+namespace sa {
+
+constexpr int kTreeMaxCtas = 304;    // partial slots: two per CTA (the item a part begins in, the one it ends in)
+constexpr int kTreeMaxRows = 256;    // query rows of an item at most
+
+struct TreeArgs {
+    const void* q;
+    int q_bf16;
+    const void *k_pages, *v_pages;
+    const int32_t *block_table, *seq_lens, *sel_ids, *sel_count;
+    const uint32_t* mask;      // [B, Q, mask_words], null: a chain
+    float* out;
+    int B, Hq, Hkv, G, Q, R, D, N, bs, bs_shift, nb, nb_cap, num_pages, sel_stride, mask_words;
+    int row_groups;            // items per unit
+    int item_rows;             // query rows of an item at most
+    int tile;                  // list positions per tile
+    int min_per;               // tiles of a part at least
+    float scale_log2;
+    float *part_m, *part_l, *part_o;   // [2 * CTA + which][item_rows] ([D])
+    uint32_t *counters, *err;
+};
+
+// The list of a unit.
+struct TreeUnit {
+    int len;          // context tokens; -1: inactive
+    int n_ctx;        // entries of the context (selection), or of everything without a selection
+    int n_entries;
+    int draft_blk;    // with a selection: the block of entry n_ctx
+};
+
+__device__ __forceinline__ TreeUnit tree_unit(const TreeArgs& a, int u)
+{
+    TreeUnit t;
+    const int b = u / a.Hkv;
+    t.len = a.seq_lens != nullptr ? a.seq_lens[b] : a.N;
+    t.n_ctx = t.n_entries = t.draft_blk = 0;
+    if (t.len < 0 || t.len > a.N) {
+        if (t.len != -1) raise_error(a.err, SPARSE_ATTN_ERR_LENGTH);
+        t.len = -1;
+        return t;
+    }
+    const int last = (t.len + a.Q - 1) >> a.bs_shift;       // the last block with a draft
+    if (a.sel_ids == nullptr) {
+        t.n_ctx = t.n_entries = last + 1;
+        return t;
+    }
+    int count = a.sel_count[u];
+    if (count < 0 || count > a.sel_stride) {
+        raise_error(a.err, SPARSE_ATTN_ERR_SEL_COUNT);
+        count = count < 0 ? 0 : a.sel_stride;
+    }
+    t.n_ctx = count;
+    t.draft_blk = t.len >> a.bs_shift;
+    t.n_entries = count + last - t.draft_blk + 1;
+    return t;
+}
+
+__device__ __forceinline__ int tree_tiles(const TreeArgs& a, const TreeUnit& t)
+{
+    if (t.len < 0) return 0;
+    const long long n = a.sel_ids == nullptr ? t.len + a.Q : (long long)t.n_entries << a.bs_shift;
+    return int((n + a.tile - 1) / a.tile);
+}
+
+// Entry e of the list: the page's tile index (page * Hkv + KV head; -1 when there is none)
+// and its first token.
+__device__ __forceinline__ int2 tree_entry(const TreeArgs& a, int u, const TreeUnit& t, int e)
+{
+    const int b = u / a.Hkv, kvh = u - b * a.Hkv;
+    int j = e;
+    if (a.sel_ids != nullptr) {
+        if (e < t.n_ctx) {
+            j = a.sel_ids[(long long)u * a.sel_stride + e];
+            if (j < 0 || j >= a.nb) {
+                raise_error(a.err, SPARSE_ATTN_ERR_SEL_ID);
+                return make_int2(-1, 0);
+            }
+            if ((j << a.bs_shift) >= t.len) return make_int2(-1, 0);   // behind this sequence's context
+        } else {
+            j = t.draft_blk + e - t.n_ctx;
+        }
+    }
+    const int page = a.block_table[(long long)b * a.nb_cap + j];
+    if (page < 0 || page >= a.num_pages) {
+        raise_error(a.err, SPARSE_ATTN_ERR_PAGE);
+        return make_int2(-1, 0);
+    }
+    return make_int2(page * a.Hkv + kvh, j << a.bs_shift);
+}
+
+// This CTA's part [lo, hi) of the line of tiles and the item that holds tile lo, found by all
+// threads (NT of them, a multiple of 32).
+struct TreePart {
+    long long lo, hi;     // tiles of the line
+    long long start;      // first tile of `item`
+    int item;
+    int per;              // tiles of a part
+};
+
+template <int NT>
+__device__ TreePart tree_part(const TreeArgs& a, long long* s_scan /* [NT / 32 + 2] shared */)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int units = a.B * a.Hkv;
+    // thread t owns units [t * ch, (t + 1) * ch)
+    const int ch = (units + NT - 1) / NT;
+    const int u0 = min(units, tid * ch), u1 = min(units, u0 + ch);
+    long long mine = 0;
+    for (int u = u0; u < u1; ++u) mine += tree_tiles(a, tree_unit(a, u));
+    mine *= a.row_groups;
+    long long incl = mine;
+#pragma unroll
+    for (int off = 1; off < kWarp; off <<= 1) {
+        const long long t = __shfl_up_sync(kFullMask, incl, off);
+        if (lane >= off) incl += t;
+    }
+    if (lane == 31) s_scan[warp] = incl;
+    __syncthreads();
+    long long before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+        if (w < warp) before += s_scan[w];
+        total += s_scan[w];
+    }
+    before += incl - mine;
+    TreePart p;
+    const long long share = (total + gridDim.x - 1) / gridDim.x;
+    p.per = int(share < a.min_per ? a.min_per : share);
+    p.lo = min(total, (long long)blockIdx.x * p.per);
+    p.hi = min(total, p.lo + p.per);
+    if (p.lo < p.hi && mine > 0 && p.lo >= before && p.lo < before + mine) {
+        long long at = before;
+        for (int u = u0; u < u1; ++u) {
+            const int t = tree_tiles(a, tree_unit(a, u));
+            const long long all = (long long)t * a.row_groups;
+            if (p.lo < at + all) {
+                const int rg = int((p.lo - at) / t);
+                s_scan[NT / 32] = (long long)u * a.row_groups + rg;
+                s_scan[NT / 32 + 1] = at + (long long)rg * t;
+                break;
+            }
+            at += all;
+        }
+    }
+    __syncthreads();
+    p.item = int(s_scan[NT / 32]);
+    p.start = s_scan[NT / 32 + 1];
+    return p;
+}
+
+// The output row of an item's query row r (query r / G, head r % G of the KV head's group).
+__device__ __forceinline__ long long tree_out_row(const TreeArgs& a, int b, int kvh, int r)
+{
+    const int t = r / a.G, g = r - t * a.G;
+    return ((long long)b * a.Q + t) * a.Hq + kvh * a.G + g;
+}
+
+// Partial slot of CTA `cta` for an item that starts at tile `start`: 0 when the item began in
+// an earlier part, 1 when it begins in this one (and goes on in the next).
+__device__ __forceinline__ int tree_slot(int cta, int per, long long start)
+{
+    return 2 * cta + (start < (long long)cta * per ? 0 : 1);
+}
+
+// Called by every thread once the CTA's (m, l, o) of a shared item is written: counts the
+// arrival; the last one merges the parts c0 .. c1 and writes the output rows.
+template <int NT>
+__device__ void tree_arrive_and_merge(const TreeArgs& a, int item, long long start, int tiles, int per, int* s_last)
+{
+    const int tid = threadIdx.x;
+    const int c0 = int(start / per), c1 = int((start + tiles - 1) / per);
+    __syncthreads();
+    if (tid == 0) {
+        const uint32_t before = atomic_add_acq_rel_u32(&a.counters[item], 1u);
+        *s_last = before + 1u == uint32_t(c1 - c0 + 1);
+        if (*s_last) a.counters[item] = 0u;
+    }
+    __syncthreads();
+    const bool last = *s_last != 0;
+    __syncthreads();
+    if (!last) return;
+    const int u = item / a.row_groups, rg = item - u * a.row_groups;
+    const int b = u / a.Hkv, kvh = u - b * a.Hkv;
+    const int rows = min(a.item_rows, a.R - rg * a.item_rows);
+    const int vec = a.D / 4;
+    for (int i = tid; i < rows * vec; i += NT) {
+        const int r = i / vec, d = (i - r * vec) * 4;
+        float M = -INFINITY, den = 0.f;
+        float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int c = c0; c <= c1; ++c) {
+            const long long at = (long long)tree_slot(c, per, start) * a.item_rows + r;
+            const float m = __ldcg(a.part_m + at), l = __ldcg(a.part_l + at);
+            const float4 o = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * a.D + d));
+            if (m == -INFINITY) continue;                   // this part saw nothing
+            const float m_new = fmaxf(M, m);
+            const float w0 = M == -INFINITY ? 0.f : fast_exp2(M - m_new), w1 = fast_exp2(m - m_new);
+            M = m_new;
+            den = fmaf(den, w0, l * w1);
+            num.x = fmaf(o.x, w1, num.x * w0);
+            num.y = fmaf(o.y, w1, num.y * w0);
+            num.z = fmaf(o.z, w1, num.z * w0);
+            num.w = fmaf(o.w, w1, num.w * w0);
+        }
+        // l > 0 where something was seen; NaN sums give NaN rows
+        const float inv = den == 0.f ? 0.f : 1.f / den;
+        if (den == 0.f) num = make_float4(0.f, 0.f, 0.f, 0.f);
+        *reinterpret_cast<float4*>(a.out + tree_out_row(a, b, kvh, rg * a.item_rows + r) * a.D + d) =
+            make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
+    }
+}
+
+}  // namespace sa

@@ -188,3 +188,50 @@ class SlotPool:
                                       self.sel_slot, d.sel_count, host_k_pages, host_v_pages, block_table,
                                       c.lists["miss_ids"], c.lists["miss_slot"], c.counts,
                                       d.out if out is None else out, d.ws, stream)
+
+
+class DraftDecoder:
+    """Speculative decoding over a paged cache: puts drafted tokens behind every sequence's
+    context, attends a tree of them over the context and each other, and moves the accepted
+    path to the context's end.  Owns the context lengths, the output and the workspace; the
+    page pools, the page table (and its key box) belong to the caller.  No call waits for
+    the device, so a step can be captured into a CUDA graph."""
+
+    def __init__(self, params: B.sparse_attn_params, seq_lens: torch.Tensor):
+        p = params
+        self.p = p
+        self.device = seq_lens.device
+        self.Q = max(1, p.num_queries)
+        self.seq_lens = seq_lens
+        self.new_lens = torch.empty_like(seq_lens)
+        self.out = torch.empty(p.batch, self.Q, p.num_q_heads, p.head_dim, dtype=torch.float32, device=self.device)
+        with torch.cuda.device(self.device):
+            self.ws = torch.empty(B.sparse_attn_tree_workspace_size(p), dtype=torch.uint8, device=self.device)
+            B.sparse_attn_workspace_init(self.ws)
+
+    def append(self, q_new, k_new, v_new, inv_freq, q_out, k_pages, v_pages, block_table, cu_rows=None,
+               positions=None, pairing=B.ROTATE_HALVES, kmin=None, kmax=None, stream=None):
+        """Tokens behind the contexts (drafts, or with ``kmin`` / ``kmax`` tokens that the
+        selection's key box covers); the lengths stay as they are."""
+        B.sparse_attn_append_kv(self.p, q_new, k_new, v_new, inv_freq, q_out, k_pages, v_pages, block_table, self.ws,
+                                cu_rows, self.seq_lens, positions, pairing, kmin, kmax, stream)
+
+    def decode(self, q, k_pages, v_pages, block_table, tree_mask=None, sel_ids=None, sel_count=None, stream=None):
+        """Attention of the drafts [B, Q, Hq, D]; returns the output tensor."""
+        B.sparse_attn_tree_decode(self.p, q, k_pages, v_pages, block_table, self.out.view(q.shape), self.ws,
+                                  self.seq_lens, sel_ids, sel_count, tree_mask, stream)
+        return self.out
+
+    def commit(self, path, path_len, k_pages, v_pages, block_table, kmin=None, kmax=None, stream=None):
+        """The accepted drafts join the context; ``seq_lens`` holds the new lengths after it."""
+        B.sparse_attn_commit_drafts(self.p, path, path_len, k_pages, v_pages, block_table, self.new_lens, self.ws,
+                                    self.seq_lens, kmin, kmax, stream)
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        elif not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
+        with torch.cuda.stream(stream):
+            self.seq_lens.copy_(self.new_lens)
+
+    def device_error(self, stream=None) -> int:
+        return B.sparse_attn_get_device_error(self.ws, stream)
