@@ -5,12 +5,15 @@
 // the launcher.  Per 64-token tile of the unit's list (sa_tree.cuh) and warp of 16 query
 // rows: S = Q K^T, the softmax with a running maximum and sum on the accumulator fragments,
 // O += P V with the score fragments as the A operand.
-//   bf16 K/V: mma.m16n8k16, fp32 accumulation.  P goes in as bf16 hi + lo (16 bits: the output
-//     is fp32, one bf16 would leave an error of 2^-9 in every weight), an fp32 query as three
-//     bf16 parts (24 bits).
+//   bf16 K/V: mma.m16n8k16, fp32 accumulation.  P goes in as three bf16 parts cut off its 24
+//     bits, which add up to it exactly (two would leave 2^-18 in every weight, more than an
+//     fp32 softmax's own error), an fp32 query likewise.
 //   fp32 K/V: mma.m16n8k8 on tf32 parts, x = hi + lo rounded to nearest (22 bits), the three
 //     products that matter.  The channel (token) order inside a k-step is permuted alike on
 //     both sides, so that a thread's two elements are neighbours in memory.
+// The matrix unit rounds its running sum toward zero at every step, so a long chain drifts
+// (measured: 1e-5 of the output after 8K tokens).  A tile's product is therefore summed from
+// zero and joins the running O by one fused multiply-add, which carries the rescaling too.
 // Four warps: 4 x 16 rows over the same tokens, or with at most 16 rows 4 x 16 tokens over the
 // same rows, their (m, l, o) joined at the item's end.
 #include "sa_tree.cuh"
@@ -42,6 +45,16 @@ __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo)
 {
     hi = to_tf32(x);
     lo = to_tf32(x - __uint_as_float(hi));
+}
+
+// A pair of fp32 cut to bf16 (the upper halves of the words; the first in the low half), the
+// remainders left behind: three cuts hold the 24 bits of an fp32 exactly.
+__device__ __forceinline__ uint32_t cut_bf16x2(float& x, float& y)
+{
+    const uint32_t ux = __float_as_uint(x), uy = __float_as_uint(y);
+    x -= __uint_as_float(ux & 0xffff0000u);
+    y -= __uint_as_float(uy & 0xffff0000u);
+    return __byte_perm(ux, uy, 0x7632);
 }
 
 template <int D, bool KB>
@@ -137,10 +150,7 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
                     }
 #pragma unroll
                     for (int part_q = 0; part_q < NQ; ++part_q) {
-                        const uint32_t w = pack_bf16x2(f0, f1);
-                        qa[part_q][ks][hc] = w;
-                        f0 -= bf16_lo(w);
-                        f1 -= bf16_hi(w);
+                        qa[part_q][ks][hc] = cut_bf16x2(f0, f1);
                     }
                 }
         } else {
@@ -281,6 +291,9 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
                             }
                         }
                 } else {
+                    float cs[NT][4];                         // the small products, apart
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) cs[nt][0] = cs[nt][1] = cs[nt][2] = cs[nt][3] = 0.f;
 #pragma unroll 2
                     for (int ks = 0; ks < D / 8; ++ks) {
                         const float* q0 = s_q + (wr * 16 + g4) * SH::Q_ROW + ks * 8 + 2 * t4;
@@ -298,11 +311,15 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
                             uint32_t bh0, bl0, bh1, bl1;
                             split_tf32(kf.x, bh0, bl0);
                             split_tf32(kf.y, bh1, bl1);
-                            mma_tf32_1688(c[nt], al, bh0, bh1);
-                            mma_tf32_1688(c[nt], ah, bl0, bl1);
+                            mma_tf32_1688(cs[nt], al, bh0, bh1);
+                            mma_tf32_1688(cs[nt], ah, bl0, bl1);
                             mma_tf32_1688(c[nt], ah, bh0, bh1);
                         }
                     }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) c[nt][e] += cs[nt][e];
                 }
                 // ---- scale, mask, running maximum and sum ---------------------------------
                 float mx[2] = {-INFINITY, -INFINITY};
@@ -317,8 +334,8 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
                             ok0 = kind == 1 || (kind == 2 && sees(r_lo, draft));
                             ok1 = kind == 1 || (kind == 2 && sees(r_hi, draft));
                         }
-                        c[nt][e] = ok0 ? c[nt][e] * a.scale_log2 : -INFINITY;
-                        c[nt][e + 2] = ok1 ? c[nt][e + 2] * a.scale_log2 : -INFINITY;
+                        c[nt][e] = ok0 ? c[nt][e] : -INFINITY;
+                        c[nt][e + 2] = ok1 ? c[nt][e + 2] : -INFINITY;
                         mx[0] = fmaxf(mx[0], c[nt][e]);
                         mx[1] = fmaxf(mx[1], c[nt][e + 2]);
                     }
@@ -327,7 +344,7 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
                 for (int h = 0; h < 2; ++h) {
                     mx[h] = fmaxf(mx[h], __shfl_xor_sync(kFullMask, mx[h], 1));
                     mx[h] = fmaxf(mx[h], __shfl_xor_sync(kFullMask, mx[h], 2));
-                    const float m_new = fmaxf(m_run[h], mx[h]);
+                    const float m_new = fmaxf(m_run[h], mx[h] * a.scale_log2);
                     alpha[h] = (m_run[h] == -INFINITY) ? 0.f : fast_exp2(m_run[h] - m_new);
                     m_run[h] = m_new;
                 }
@@ -337,64 +354,73 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int h = e >> 1;
-                        c[nt][e] = (c[nt][e] == -INFINITY) ? 0.f : fast_exp2(c[nt][e] - m_run[h]);
+                        c[nt][e] = (c[nt][e] == -INFINITY) ? 0.f : fast_exp2(fmaf(c[nt][e], a.scale_log2, -m_run[h]));
                         psum[h] += c[nt][e];
                     }
                 l_run[0] = fmaf(l_run[0], alpha[0], psum[0]);
                 l_run[1] = fmaf(l_run[1], alpha[1], psum[1]);
-#pragma unroll
-                for (int j = 0; j < DT; ++j) {
-                    acc[j][0] *= alpha[0];
-                    acc[j][1] *= alpha[0];
-                    acc[j][2] *= alpha[1];
-                    acc[j][3] *= alpha[1];
-                }
-                // ---- O += P V ---------------------------------------------------------
+                // ---- O = alpha O + P V ---------------------------------------------------
+                auto join = [&](float (&o)[4], const float (&x)[4]) {
+                    o[0] = fmaf(o[0], alpha[0], x[0]);
+                    o[1] = fmaf(o[1], alpha[0], x[1]);
+                    o[2] = fmaf(o[2], alpha[1], x[2]);
+                    o[3] = fmaf(o[3], alpha[1], x[3]);
+                };
                 if constexpr (KB) {
+                    uint32_t pa[3][NT / 2][4];               // parts of P as A fragments, 16 tokens each
 #pragma unroll
-                    for (int kk = 0; kk < NT / 2; ++kk) {
-                        const float* p0 = c[2 * kk];
-                        const float* p1 = c[2 * kk + 1];
-                        const uint32_t h0 = pack_bf16x2(p0[0], p0[1]), h1 = pack_bf16x2(p0[2], p0[3]);
-                        const uint32_t h2 = pack_bf16x2(p1[0], p1[1]), h3 = pack_bf16x2(p1[2], p1[3]);
-                        const uint32_t l0 = pack_bf16x2(p0[0] - bf16_lo(h0), p0[1] - bf16_hi(h0));
-                        const uint32_t l1 = pack_bf16x2(p0[2] - bf16_lo(h1), p0[3] - bf16_hi(h1));
-                        const uint32_t l2 = pack_bf16x2(p1[0] - bf16_lo(h2), p1[1] - bf16_hi(h2));
-                        const uint32_t l3 = pack_bf16x2(p1[2] - bf16_lo(h3), p1[3] - bf16_hi(h3));
+                    for (int kk = 0; kk < NT / 2; ++kk)
 #pragma unroll
-                        for (int jp = 0; jp < DT; jp += 2) {
-                            const int mtx = lane >> 3;
+                        for (int x = 0; x < 4; ++x) {
+                            float p0 = c[2 * kk + (x >> 1)][2 * (x & 1)], p1 = c[2 * kk + (x >> 1)][2 * (x & 1) + 1];
+#pragma unroll
+                            for (int pp = 0; pp < 3; ++pp) pa[pp][kk][x] = cut_bf16x2(p0, p1);
+                        }
+#pragma unroll
+                    for (int jp = 0; jp < DT; jp += 2) {
+                        const int mtx = lane >> 3;
+                        float x0[4] = {0.f, 0.f, 0.f, 0.f}, x1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int kk = 0; kk < NT / 2; ++kk) {
                             uint32_t v0, v1, v2, v3;
                             ldsm_x4_trans(vst + SH::at(tok0 + kk * 16 + (mtx & 1) * 8 + (lane & 7), jp + (mtx >> 1)), v0, v1,
                                           v2, v3);
-                            mma_bf16_16816(acc[jp], l0, l1, l2, l3, v0, v1);
-                            mma_bf16_16816(acc[jp], h0, h1, h2, h3, v0, v1);
-                            mma_bf16_16816(acc[jp + 1], l0, l1, l2, l3, v2, v3);
-                            mma_bf16_16816(acc[jp + 1], h0, h1, h2, h3, v2, v3);
+#pragma unroll
+                            for (int pp = 2; pp >= 0; --pp) {
+                                mma_bf16_16816(x0, pa[pp][kk][0], pa[pp][kk][1], pa[pp][kk][2], pa[pp][kk][3], v0, v1);
+                                mma_bf16_16816(x1, pa[pp][kk][0], pa[pp][kk][1], pa[pp][kk][2], pa[pp][kk][3], v2, v3);
+                            }
                         }
+                        join(acc[jp], x0);
+                        join(acc[jp + 1], x1);
                     }
                 } else {
+                    uint32_t ah[NT][4], al[NT][4];           // k index t4 <-> token 2 t4, t4 + 4 <-> 2 t4 + 1
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        uint32_t ah[4], al[4];               // k index t4 <-> token 2 t4, t4 + 4 <-> 2 t4 + 1
-                        split_tf32(c[nt][0], ah[0], al[0]);
-                        split_tf32(c[nt][2], ah[1], al[1]);
-                        split_tf32(c[nt][1], ah[2], al[2]);
-                        split_tf32(c[nt][3], ah[3], al[3]);
-                        const int tr = tok0 + nt * 8 + 2 * t4;
-                        const unsigned char* vs = stage + SH::TENSOR;
+                        split_tf32(c[nt][0], ah[nt][0], al[nt][0]);
+                        split_tf32(c[nt][2], ah[nt][1], al[nt][1]);
+                        split_tf32(c[nt][1], ah[nt][2], al[nt][2]);
+                        split_tf32(c[nt][3], ah[nt][3], al[nt][3]);
+                    }
+                    const unsigned char* vs = stage + SH::TENSOR;
 #pragma unroll
-                        for (int j = 0; j < DT; ++j) {
-                            const int ch = j * 2 + (g4 >> 2), by = (g4 & 3) * 4;
+                    for (int j = 0; j < DT; ++j) {
+                        const int ch = j * 2 + (g4 >> 2), by = (g4 & 3) * 4;
+                        float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const int tr = tok0 + nt * 8 + 2 * t4;
                             const float v0 = *reinterpret_cast<const float*>(vs + SH::at(tr, ch) + by);
                             const float v1 = *reinterpret_cast<const float*>(vs + SH::at(tr + 1, ch) + by);
                             uint32_t bh0, bl0, bh1, bl1;
                             split_tf32(v0, bh0, bl0);
                             split_tf32(v1, bh1, bl1);
-                            mma_tf32_1688(acc[j], al, bh0, bh1);
-                            mma_tf32_1688(acc[j], ah, bl0, bl1);
-                            mma_tf32_1688(acc[j], ah, bh0, bh1);
+                            mma_tf32_1688(x, al[nt], bh0, bh1);
+                            mma_tf32_1688(x, ah[nt], bl0, bl1);
+                            mma_tf32_1688(x, ah[nt], bh0, bh1);
                         }
+                        join(acc[j], x);
                     }
                 }
                 if (bad0 | bad1) {                           // rows taken out above
@@ -581,6 +607,7 @@ cudaError_t launch_tree(const Geometry& g, const TreeCall& c, char* ws, cudaStre
     a.counters = reinterpret_cast<uint32_t*>(ws + L.counters);
     a.err = reinterpret_cast<uint32_t*>(ws);
     if (g.kv_bf16) {
+        if (g.q_bf16 && a.R > 16) return launch_tree_tc(a, s);
         if (g.q_bf16) return g.D == 128 ? launch_tree_rows<128, true, 1>(a, s) : launch_tree_rows<64, true, 1>(a, s);
         return g.D == 128 ? launch_tree_rows<128, true, 3>(a, s) : launch_tree_rows<64, true, 3>(a, s);
     }

@@ -180,22 +180,29 @@ __device__ __forceinline__ int tree_slot(int cta, int per, long long start)
     return 2 * cta + (start < (long long)cta * per ? 0 : 1);
 }
 
-// Called by every thread once the CTA's (m, l, o) of a shared item is written: counts the
+// Barrier of the first NT threads of the CTA (barrier 2 is theirs).
+template <int NT>
+__device__ __forceinline__ void tree_sync()
+{
+    asm volatile("bar.sync 2, %0;" ::"n"(NT) : "memory");
+}
+
+// Called by the CTA's first NT threads once its (m, l, o) of a shared item is written: counts the
 // arrival; the last one merges the parts c0 .. c1 and writes the output rows.
 template <int NT>
 __device__ void tree_arrive_and_merge(const TreeArgs& a, int item, long long start, int tiles, int per, int* s_last)
 {
     const int tid = threadIdx.x;
     const int c0 = int(start / per), c1 = int((start + tiles - 1) / per);
-    __syncthreads();
+    tree_sync<NT>();
     if (tid == 0) {
         const uint32_t before = atomic_add_acq_rel_u32(&a.counters[item], 1u);
         *s_last = before + 1u == uint32_t(c1 - c0 + 1);
         if (*s_last) a.counters[item] = 0u;
     }
-    __syncthreads();
+    tree_sync<NT>();
     const bool last = *s_last != 0;
-    __syncthreads();
+    tree_sync<NT>();
     if (!last) return;
     const int u = item / a.row_groups, rg = item - u * a.row_groups;
     const int b = u / a.Hkv, kvh = u - b * a.Hkv;
@@ -227,5 +234,8 @@ __device__ void tree_arrive_and_merge(const TreeArgs& a, int item, long long sta
             make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
     }
 }
+
+// The tensor-core kernel (sa_tree_tc.cu): bf16 queries and K/V.
+cudaError_t launch_tree_tc(TreeArgs a, cudaStream_t s);
 
 }  // namespace sa
