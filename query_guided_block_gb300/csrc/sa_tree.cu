@@ -518,7 +518,9 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
                 }
             }
         }
-        if (!complete) tree_arrive_and_merge<kTrThreads>(a, item, start, tiles, part.per, &s_last);
+        if (!complete)
+            tree_arrive_and_merge<kTrThreads>(a, item, start, tiles, part.per, &s_last, reinterpret_cast<float*>(smem),
+                                              SH::STAGES * SH::STAGE / 4);
         lo = start + t1;
         if (t1 == tiles) {
             start += tiles;

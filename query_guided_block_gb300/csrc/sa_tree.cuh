@@ -184,54 +184,83 @@ __device__ __forceinline__ int tree_slot(int cta, int per, long long start)
 template <int NT>
 __device__ __forceinline__ void tree_sync()
 {
+    __syncwarp();
     asm volatile("bar.sync 2, %0;" ::"n"(NT) : "memory");
 }
 
 // Called by the CTA's first NT threads once its (m, l, o) of a shared item is written: counts the
-// arrival; the last one merges the parts c0 .. c1 and writes the output rows.
+// arrival; the last one merges the parts c0 .. c1 and writes the output rows.  `s_w`: floats of
+// shared memory free for use (at least as many as CTAs in the grid).
+//   Two steps, so that no load waits for another one's result: a warp per row takes the parts'
+// maxima and sums (lane = part) and leaves the parts' weights in shared memory, then a thread
+// per four channels adds up its parts.
 template <int NT>
-__device__ void tree_arrive_and_merge(const TreeArgs& a, int item, long long start, int tiles, int per, int* s_last)
+__device__ void tree_arrive_and_merge(const TreeArgs& a, int item, long long start, int tiles, int per, int* s_last,
+                                      float* s_w, int n_w)
 {
-    const int tid = threadIdx.x;
-    const int c0 = int(start / per), c1 = int((start + tiles - 1) / per);
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int c0 = int(start / per), np = int((start + tiles - 1) / per) - c0 + 1;
     tree_sync<NT>();
     if (tid == 0) {
         const uint32_t before = atomic_add_acq_rel_u32(&a.counters[item], 1u);
-        *s_last = before + 1u == uint32_t(c1 - c0 + 1);
+        *s_last = before + 1u == uint32_t(np);
         if (*s_last) a.counters[item] = 0u;
     }
     tree_sync<NT>();
     const bool last = *s_last != 0;
-    tree_sync<NT>();
-    if (!last) return;
-    const int u = item / a.row_groups, rg = item - u * a.row_groups;
+    if (!last) return;                                      // the next item's barriers keep s_last
+    const int u = item / a.row_groups, row0 = (item - u * a.row_groups) * a.item_rows;
     const int b = u / a.Hkv, kvh = u - b * a.Hkv;
-    const int rows = min(a.item_rows, a.R - rg * a.item_rows);
-    const int vec = a.D / 4;
-    for (int i = tid; i < rows * vec; i += NT) {
-        const int r = i / vec, d = (i - r * vec) * 4;
-        float M = -INFINITY, den = 0.f;
-        float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int c = c0; c <= c1; ++c) {
-            const long long at = (long long)tree_slot(c, per, start) * a.item_rows + r;
-            const float m = __ldcg(a.part_m + at), l = __ldcg(a.part_l + at);
-            const float4 o = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * a.D + d));
-            if (m == -INFINITY) continue;                   // this part saw nothing
-            const float m_new = fmaxf(M, m);
-            const float w0 = M == -INFINITY ? 0.f : fast_exp2(M - m_new), w1 = fast_exp2(m - m_new);
-            M = m_new;
-            den = fmaf(den, w0, l * w1);
-            num.x = fmaf(o.x, w1, num.x * w0);
-            num.y = fmaf(o.y, w1, num.y * w0);
-            num.z = fmaf(o.z, w1, num.z * w0);
-            num.w = fmaf(o.w, w1, num.w * w0);
+    const int rows = min(a.item_rows, a.R - row0);
+    const int vec = a.D / 4, batch = min(rows, n_w / np);
+    for (int r0 = 0; r0 < rows; r0 += batch) {
+        const int n = min(batch, rows - r0);
+        for (int r = tid >> 5; r < n; r += NT / 32) {
+            float M = -INFINITY;
+            for (int c = lane; c < np; c += 32)
+                M = fmaxf(M, __ldcg(a.part_m + (long long)tree_slot(c0 + c, per, start) * a.item_rows + r0 + r));
+#pragma unroll
+            for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, x));
+            float den = 0.f;
+            for (int c = lane; c < np; c += 32) {
+                const long long at = (long long)tree_slot(c0 + c, per, start) * a.item_rows + r0 + r;
+                const float m = __ldcg(a.part_m + at);
+                const float w = m == -INFINITY ? 0.f : fast_exp2(m - M);   // a part that saw nothing has no weight
+                s_w[r * np + c] = w;
+                den = fmaf(w, __ldcg(a.part_l + at), den);
+            }
+#pragma unroll
+            for (int x = 16; x > 0; x >>= 1) den += __shfl_xor_sync(kFullMask, den, x);
+            __syncwarp();
+            const float inv = den == 0.f ? 0.f : 1.f / den;
+            for (int c = lane; c < np; c += 32) s_w[r * np + c] *= inv;
         }
-        // l > 0 where something was seen; NaN sums give NaN rows
-        const float inv = den == 0.f ? 0.f : 1.f / den;
-        if (den == 0.f) num = make_float4(0.f, 0.f, 0.f, 0.f);
-        *reinterpret_cast<float4*>(a.out + tree_out_row(a, b, kvh, rg * a.item_rows + r) * a.D + d) =
-            make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
+        tree_sync<NT>();
+        for (int i = tid; i < n * vec; i += NT) {
+            const int r = i / vec, d = (i - r * vec) * 4;
+            float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int c = 0; c < np; c += 4) {
+                float4 o[4];
+                float w[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    w[x] = c + x < np ? s_w[r * np + c + x] : 0.f;
+                    o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (w[x] != 0.f)
+                        o[x] = __ldcg(reinterpret_cast<const float4*>(
+                            a.part_o + ((long long)tree_slot(c0 + c + x, per, start) * a.item_rows + r0 + r) * a.D + d));
+                }
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    num.x = fmaf(o[x].x, w[x], num.x);
+                    num.y = fmaf(o[x].y, w[x], num.y);
+                    num.z = fmaf(o[x].z, w[x], num.z);
+                    num.w = fmaf(o[x].w, w[x], num.w);
+                }
+            }
+            *reinterpret_cast<float4*>(a.out + tree_out_row(a, b, kvh, row0 + r0 + r) * a.D + d) = num;
+        }
+        tree_sync<NT>();
     }
 }
 

@@ -7,13 +7,14 @@
 // at the item's end), with two row tiles each slot keeps one of them and both use every K/V
 // tile.  While one slot's softmax runs, the other's products keep the tensor core busy.
 //
-// Roles (12 warps):
-//   warp 8      resolves the list's entries 32 at a time and brings K and V by TMA, one box
+// Roles (20 warps):
+//   warps 0-7, 8-15  the slots' softmax: two threads own a query row, each half of its tokens
+//               and half of its channels.  They read S, take the maximum, write P, then add the
+//               finished O tile to their channels in registers.
+//   warp 16     resolves the list's entries 32 at a time and brings K and V by TMA, one box
 //               of 64 channels x one block per entry and channel half, into a ring of K and
 //               V units that it refills as the products release them;
-//   warps 9, 10 one thread each: S = Q K^T, then O = P V for one slot (tcgen05.mma);
-//   warps 0-3, 4-7  the slots' softmax: a thread owns one query row.  Reads S, takes the
-//               maximum, writes P, then adds the finished O tile to its row in registers.
+//   warps 17, 18  one thread each: S = Q K^T, then O = P V for one slot (tcgen05.mma).
 //
 // Precision.  The output is fp32, so P goes into the product as three bf16 parts that hold
 // its 24 bits exactly: two of them overwrite S in tensor memory (A operands there), the third
@@ -35,9 +36,9 @@
 namespace sa {
 namespace {
 
-constexpr int kTcThreads = 384;
+constexpr int kTcSoft = 512;           // softmax threads, 256 a slot
+constexpr int kTcThreads = kTcSoft + 128;
 constexpr int kTcTile = 128;
-constexpr int kTcInfo = 8;           // tiles whose entries are remembered (more than the ring holds)
 constexpr int kNoToken = INT32_MIN;
 
 template <int D, int RT>
@@ -47,12 +48,14 @@ struct TcShape {
     static constexpr int UNIT = HALVES * HALF;              // K or V of a tile
     static constexpr int Q_TILE = HALVES * HALF;
     static constexpr int P_TILE = 2 * HALF;                 // 128 rows x 128 tokens
-    static constexpr int UNITS = D == 128 ? (RT == 1 ? 4 : 3) : 8;
+    static constexpr int UNITS = D == 128 ? (RT == 1 ? 4 : 3) : 7;
+    // Tiles whose entries are remembered.  The producer is at most UNITS / 2 tiles past the
+    // oldest tile whose V is still in the ring.
+    static constexpr int INFO = UNITS / 2 + 2;
     static constexpr int OFF_P = RT * Q_TILE;
     static constexpr int OFF_RING = OFF_P + 2 * P_TILE;
-    static constexpr size_t SMEM = 1024 + size_t(OFF_RING) + size_t(UNITS) * UNIT;
-    static_assert(SMEM <= 227 * 1024 - 2000, "dynamic and static shared memory of one CTA");
-    static_assert(size_t(UNITS) * UNIT >= size_t(kTcTile) * D * 4, "the joined rows go through the ring");
+    static constexpr int OFF_SHARED = OFF_RING + UNITS * UNIT;
+    static_assert(2 * P_TILE + size_t(UNITS) * UNIT >= size_t(RT) * 128 * D * 4, "the rows leave through this memory");
 };
 
 __device__ __forceinline__ void bar_sync(int id, int threads)
@@ -82,6 +85,16 @@ __device__ __forceinline__ void umma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, u
         : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16])
 {
     asm volatile(
@@ -90,6 +103,43 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
           "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
+}
+
+// Two fp32 operations in one instruction (each rounded as usual).
+union F2 {
+    unsigned long long u;
+    float2 f;
+};
+__device__ __forceinline__ F2 make_f2(float x, float y)
+{
+    F2 r;
+    r.f = make_float2(x, y);
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
+{
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.u) : "l"(a.u), "l"(b.u), "l"(c.u));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b)
+{
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(a.u), "l"(b.u));
+    return r;
+}
+__device__ __forceinline__ F2 sub2(F2 a, F2 b)
+{
+    F2 r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(a.u), "l"(b.u));
+    return r;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
 __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr)
@@ -101,12 +151,19 @@ __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr)
 
 // A pair of fp32 cut to bf16 (the upper halves of the words; the first in the low half), the
 // remainders left behind.
-__device__ __forceinline__ uint32_t cut_bf16x2(float& x, float& y)
+__device__ __forceinline__ uint32_t cut_bf16x2(F2& p)
 {
-    const uint32_t ux = __float_as_uint(x), uy = __float_as_uint(y);
-    x -= __uint_as_float(ux & 0xffff0000u);
-    y -= __uint_as_float(uy & 0xffff0000u);
+    const uint32_t ux = __float_as_uint(p.f.x), uy = __float_as_uint(p.f.y);
+    p = sub2(p, make_f2(__uint_as_float(ux & 0xffff0000u), __uint_as_float(uy & 0xffff0000u)));
     return __byte_perm(ux, uy, 0x7632);
+}
+
+// The smallest bf16 not below x, as an fp32's bits (NaN may become anything).
+__device__ __forceinline__ uint32_t round_up_bf16(float x)
+{
+    const uint32_t u = __float_as_uint(x);
+    // toward zero is up for negative values; positive ones go up unless they are exact
+    return (u & 0x80000000u) ? u & 0xffff0000u : (u + (x < INFINITY ? 0xffffu : 0u)) & 0xffff0000u;
 }
 
 // Bits d0 .. d0 + 7 of a draft mask (bit j of word j / 32), those in [0, limit).
@@ -128,20 +185,31 @@ __device__ __forceinline__ uint32_t mask_bits8(const uint32_t* words, int d0, in
     return v & 0xffu;
 }
 
-// Register shares: the CTA starts with 12 warps x 168; the softmax threads hold an output row.
-constexpr int kTcRegsFew = 88, kTcRegsMany = 208;
-static_assert(kTcRegsFew * 128 + kTcRegsMany * 256 <= 168 * kTcThreads, "no more registers than the launch got");
+// Register shares: the CTA starts with 20 warps x 96; the softmax threads hold half an output
+// row.
+constexpr int kTcRegsFew = 64, kTcRegsMany = 104;
+static_assert(kTcRegsFew * 128 + kTcRegsMany * kTcSoft <= 96 * kTcThreads, "no more registers than the launch got");
 
+template <int D, int RT>
 struct TcShared {
-    uint64_t full[8], empty[8], s_full[2], o_full[2], p_ready[2];
+    using SH = TcShape<D, RT>;
+    uint64_t full[SH::UNITS], empty[SH::UNITS], s_full[2], o_full[2], p_ready[2];
+    long long scan[kTcThreads / 32 + 2];
+    int2 entry[SH::INFO][16];
+    int masked[SH::INFO];
+    uint32_t bad[2][4];                         // by slot, or by the tile's parity where both slots share a tile
+    uint32_t any[kTreeMaxDrafts / 32];
+    uint16_t top[2][2][128];                    // half rows' maxima (slot, half, row), bf16 rounded up
     uint32_t tmem;
     int dead;                                   // a bounded wait ran out: no more waiting
     int last;
-    uint32_t bad[2][4];
-    uint32_t any[kTreeMaxDrafts / 32];
-    int2 entry[kTcInfo][16];
-    int masked[kTcInfo];
 };
+template <int D, int RT>
+constexpr size_t tc_smem()
+{
+    static_assert(1024 + TcShape<D, RT>::OFF_SHARED + sizeof(TcShared<D, RT>) <= 227 * 1024, "shared memory of a CTA");
+    return 1024 + TcShape<D, RT>::OFF_SHARED + sizeof(TcShared<D, RT>);
+}
 
 // One item's share of this CTA's part: tiles [t0, t1) of the item's list.
 struct TcSegment {
@@ -189,13 +257,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     constexpr int SLOT_STEP = RT == 1 ? 2 : 1;                     // tiles between a slot's tiles
 
     extern __shared__ __align__(128) unsigned char smem_raw[];
-    __shared__ __align__(8) TcShared sh;
-    __shared__ long long s_scan[kTcThreads / 32 + 2];
-
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;                  // swizzle atoms: 1024-byte aligned
     unsigned char* smem = smem_raw + (base - raw);
+    TcShared<D, RT>& sh = *reinterpret_cast<TcShared<D, RT>*>(smem + SH::OFF_SHARED);
 
     allow_dependents_early();
     if (warp == 0) {
@@ -203,21 +269,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tmem_relinquish();
     }
     if (tid == 0) {
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < SH::UNITS; ++i) {
             mbar_init(&sh.full[i], 1);
             mbar_init(&sh.empty[i], RT);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&sh.s_full[s], 1);
             mbar_init(&sh.o_full[s], 1);
-            mbar_init(&sh.p_ready[s], 128);
+            mbar_init(&sh.p_ready[s], kTcSoft / 2);
         }
         sh.dead = 0;
         fence_mbar_init();
     }
     grid_dependency_wait();   // queries, pages and lengths may come from the previous kernel
     tc_fence_before_sync();
-    const TreePart part = tree_part<kTcThreads>(a, s_scan);        // synchronises the CTA
+    const TreePart part = tree_part<kTcThreads>(a, sh.scan);        // synchronises the CTA
     tc_fence_after_sync();
     const uint32_t tmem = sh.tmem;
     const bool dense = a.sel_ids == nullptr;
@@ -234,7 +300,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
     };
 
-    if (warp >= 8) {
+    if (warp >= 16) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTcRegsFew));
         uint32_t unit0 = 0;                                        // ring units used by earlier segments
         uint32_t tile0 = 0;                                        // tiles of earlier segments
@@ -242,7 +308,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         while (tc_next(a, part, lo, start, item, g)) {
             const int ntl = g.t1 - g.t0;
             bar_sync(1, kTcThreads);                               // queries staged, the ring is free
-            if (warp == 8) {
+            if (warp == 16) {
                 // ---- producer ---------------------------------------------------------
                 const int n_e = a.bs >= kTcTile ? 1 : kTcTile >> a.bs_shift;   // entries of a tile
                 const int per_batch = 32 / n_e;                    // tiles whose entries one batch holds
@@ -267,7 +333,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     const bool partly = mine && (!ok || en.y + a.bs > g.un.len || !(dense || e < g.un.n_ctx));
                     const uint32_t n_ok = __popc(__ballot_sync(kFullMask, ok));
                     const bool any_partly = __any_sync(kFullMask, partly);
-                    const uint32_t info = (tile0 + i) % kTcInfo;
+                    const uint32_t info = (tile0 + i) % SH::INFO;
                     if (mine) sh.entry[info][lane] = make_int2(en.x, ok ? en.y : kNoToken);
                     if (lane == 0) sh.masked[info] = any_partly;
                     __syncwarp();
@@ -286,9 +352,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         }
                     }
                 }
-            } else if (warp <= 10) {
+            } else if (warp <= 18) {
                 // ---- issuer of slot s ----------------------------------------------------
-                const int s = warp - 9;
+                const int s = warp - 17;
                 uint32_t done = mine0;
                 if (lane == 0) {
                     const uint64_t q_desc = smem_desc_sw128(base + (RT == 2 ? s * SH::Q_TILE : 0), 16, 1024);
@@ -323,7 +389,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         for (int pp = 1; pp >= 0; --pp)
 #pragma unroll
                             for (int k = 0; k < kTcTile / 16; ++k)
-                                umma_bf16_ta(o_tm, s_tm + (k >> 1) * 32 + pp * 16 + (k & 1) * 8,
+                                umma_bf16_ta(o_tm, s_tm + k * 16 + pp * 8,
                                              vd + uint32_t((k * 16 * 128) >> 4), IDESC_O, 1u);
                         umma_commit(&sh.empty[vs]);
                         umma_commit(&sh.o_full[s]);
@@ -337,10 +403,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTcRegsMany));
-        const int s = warp >> 2;                                   // slot
-        const int row = tid & 127;                                 // row of the slot's tile
+        constexpr int DH = D / 2;                                  // channels of a thread
+        const int s = warp >> 3;                                   // slot
+        const int h = (warp >> 2) & 1;                             // which tokens and channels
+        const int row = 32 * (warp & 3) + lane;                    // row of the slot's tile
         const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
         const uint32_t s_tm = tmem + S_COL + s * 128 + lanes, o_tm = tmem + O_COL + s * 128 + lanes;
+        const int pair_bar = 5 + 4 * s + (warp & 3);               // the two warps that share rows
         const float scale = a.scale_log2;
         uint32_t tile0 = 0, done = 0, unit0 = 0;
         while (tc_next(a, part, lo, start, item, g)) {
@@ -349,7 +418,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // ---- the item's queries, and the drafts that some query sees ----------------
             {
                 constexpr int CPR = D / 8;                         // 16-byte chunks of a row
-                for (int i = tid; i < RT * 128 * CPR; i += 256) {
+                for (int i = tid; i < RT * 128 * CPR; i += kTcSoft) {
                     const int r = i / CPR, c = i - r * CPR;
                     uint4 v = make_uint4(0u, 0u, 0u, 0u);
                     if (g.row0 + r < a.R)
@@ -358,40 +427,36 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     *reinterpret_cast<uint4*>(smem + (r >> 7) * SH::Q_TILE + (c >> 3) * SH::HALF + (r & 127) * 128 +
                                               (((c & 7) ^ (r & 7)) << 4)) = v;
                 }
-                fence_proxy_async_smem();
                 const long long list = dense ? g.un.len : (long long)g.un.n_ctx << a.bs_shift;
                 if ((long long)g.t1 * kTcTile > list) {            // this part meets drafts
-                    for (int w = tid; w < a.mask_words; w += 256) {
-                        uint32_t m = 0u;
-                        if (mask_b == nullptr) m = ~0u;
-                        else
-                            for (int i = 0; i < a.Q; ++i) m |= mask_b[(long long)i * a.mask_words + w];
-                        sh.any[w] = m;
+                    if (tid < a.mask_words) sh.any[tid] = mask_b == nullptr ? ~0u : 0u;
+                    if (mask_b != nullptr) {
+                        tree_sync<kTcSoft>();
+                        for (int i = tid; i < a.Q * a.mask_words; i += kTcSoft) atomicOr(&sh.any[i % a.mask_words], mask_b[i]);
                     }
                 }
+                fence_proxy_async_smem();                          // before TMA and the tensor core use this memory
             }
             bar_sync(1, kTcThreads);
 
             const int r_unit = g.row0 + (RT == 2 ? s * 128 : 0) + row;
-            const bool live = g.row0 + (RT == 2 ? s * 128 : 0) + 32 * (warp & 3) < a.R;    // of this warp's rows, any
+            const bool live = g.row0 + (RT == 2 ? s * 128 : 0) + 32 * (warp & 3) < a.R;    // any of this warp's rows
             const int q_row = r_unit < a.R ? r_unit / a.G : 0;
-            float acc[D];
+            F2 acc[DH / 2];
 #pragma unroll
-            for (int d = 0; d < D; ++d) acc[d] = 0.f;
+            for (int d = 0; d < DH / 2; ++d) acc[d] = make_f2(0.f, 0.f);
             float m_run = -INFINITY, l_run = 0.f;
 
             for (int i = RT == 1 ? s : 0; i < ntl; i += SLOT_STEP, ++done) {
                 wait(&sh.s_full[s], done & 1u);
                 __syncwarp();
                 tc_fence_after_sync();
-                const uint32_t info = (tile0 + i) % kTcInfo;
-                const bool masked = sh.masked[info] != 0;
-                uint32_t mk[4] = {~0u, ~0u, ~0u, ~0u};             // tokens that this row sees
-                uint32_t bad[4] = {0u, 0u, 0u, 0u};
-                if (masked) {
-                    // which tokens the row sees; V rows of tokens that nobody sees are zeroed (their
-                    // memory may hold anything), and so are drafts with infinities or NaN, which
-                    // are added below where they are seen
+                const uint32_t info = (tile0 + i) % SH::INFO;
+                bool odd_drafts = false;
+                if (sh.masked[info] != 0) {
+                    // Scores of tokens that the row does not see become -infinity.  V rows of tokens
+                    // that nobody sees are zeroed (their memory may hold anything), and so are drafts
+                    // with infinities or NaN, which are added below where they are seen.
                     const int e0 = ((g.t0 + i) * kTcTile) >> a.bs_shift;
                     auto tokens8 = [&](int g8, const uint32_t* words, int limit) -> uint32_t {
                         const int le = (g8 * 8) >> a.bs_shift;
@@ -400,207 +465,239 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         const int tok = first + ((g8 * 8) & (a.bs - 1));
                         const bool ctx = dense || e0 + le < g.un.n_ctx;
                         uint32_t bits = 0u;
-                        if (ctx) {
-                            const int n = min(8, max(0, g.un.len - tok));
-                            bits = (1u << n) - 1u;
-                        }
+                        if (ctx) bits = (1u << min(8, max(0, g.un.len - tok))) - 1u;
                         if (dense || !ctx) bits |= mask_bits8(words, tok - g.un.len, limit);
                         return bits;
                     };
-                    const uint32_t* words = mask_b != nullptr ? mask_b + (long long)q_row * a.mask_words : nullptr;
-                    const int limit = r_unit < a.R ? (mask_b != nullptr ? a.Q : q_row + 1) : 0;
+                    if (live) {
+                        const uint32_t* words = mask_b != nullptr ? mask_b + (long long)q_row * a.mask_words : nullptr;
+                        const int limit = r_unit < a.R ? (mask_b != nullptr ? a.Q : q_row + 1) : 0;
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            const uint32_t mk = tokens8(8 * h + 2 * c, words, limit) | tokens8(8 * h + 2 * c + 1, words, limit) << 8;
+                            uint32_t v[16];
+                            __syncwarp();
+                            tmem_ld16(s_tm + 64 * h + 16 * c, v);
+                            tmem_wait_ld();
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        mk[w] = 0u;
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) mk[w] |= tokens8(4 * w + x, words, limit) << (8 * x);
+                            for (int j = 0; j < 16; ++j)
+                                if (!((mk >> j) & 1u)) v[j] = 0xff800000u;
+                            tmem_st16(s_tm + 64 * h + 16 * c, v);
+                        }
+                        tmem_wait_st();
                     }
                     const uint32_t vn = unit0 + 2 * i + 1, vs = vn % SH::UNITS;
                     wait(&sh.full[vs], (vn / SH::UNITS) & 1u);
-                    const int tok_row = row;                       // this thread looks after token `row`
-                    uint32_t* s_bad = sh.bad[RT == 1 ? s : 0];
-                    const int bar_id = RT == 1 ? 3 + s : 2, bar_n = RT == 1 ? 128 : 256;
-                    constexpr int CH0 = SH::HALVES * 8 / RT;       // 16-byte chunks of the row, shared by the warpgroups
-                    const int c0 = RT == 1 ? 0 : s * CH0;
-                    unsigned char* vrow = smem + SH::OFF_RING + vs * SH::UNIT + tok_row * 128;
-                    if (tid < 4 || (RT == 1 && s == 1 && row < 4)) s_bad[row] = 0u;
-                    const bool seen = (tokens8(tok_row >> 3, sh.any, a.Q) >> (tok_row & 7)) & 1u;
-                    const int first = sh.entry[info][tok_row >> a.bs_shift].y;
-                    const bool draft = first != kNoToken && first + (tok_row & (a.bs - 1)) >= g.un.len;
+                    // this thread looks after token `row`, together with the others that have it
+                    constexpr int CHUNKS = SH::HALVES * 8 / (2 * RT);
+                    const int c0 = (RT == 1 ? h : 2 * s + h) * CHUNKS;
+                    uint32_t* s_bad = sh.bad[RT == 1 ? s : i & 1];
+                    const int bar_id = RT == 1 ? 3 + s : 2, bar_n = RT == 1 ? 256 : 512;
+                    unsigned char* vrow = smem + SH::OFF_RING + vs * SH::UNIT + row * 128;
+                    if ((RT == 1 || s == 0) && h == 0 && row < 4) s_bad[row] = 0u;
+                    const bool seen = (tokens8(row >> 3, sh.any, a.Q) >> (row & 7)) & 1u;
+                    const int first = sh.entry[info][row >> a.bs_shift].y;
+                    const bool draft = first != kNoToken && first + (row & (a.bs - 1)) >= g.un.len;
+                    tc_fence_before_sync();
                     bar_sync(bar_id, bar_n);
                     if (seen && draft) {
                         bool odd = false;
-                        for (int c = c0; c < c0 + CH0; ++c) {
+                        for (int c = c0; c < c0 + CHUNKS; ++c) {
                             const uint4 v = *reinterpret_cast<const uint4*>(vrow + (c >> 3) * SH::HALF + (c & 7) * 16);
                             const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                             for (int x = 0; x < 4; ++x)
                                 odd |= (w4[x] & 0x7f800000u) == 0x7f800000u || (w4[x] & 0x7f80u) == 0x7f80u;
                         }
-                        if (odd) atomicOr(&s_bad[tok_row >> 5], 1u << (tok_row & 31));
+                        if (odd) atomicOr(&s_bad[row >> 5], 1u << (row & 31));
                     }
                     bar_sync(bar_id, bar_n);
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) bad[w] = s_bad[w];
-                    if (!seen || ((bad[tok_row >> 5] >> (tok_row & 31)) & 1u)) {
-                        for (int c = c0; c < c0 + CH0; ++c)
+                    odd_drafts = (s_bad[0] | s_bad[1] | s_bad[2] | s_bad[3]) != 0u;
+                    if (!seen || ((s_bad[row >> 5] >> (row & 31)) & 1u)) {
+                        for (int c = c0; c < c0 + CHUNKS; ++c)
                             *reinterpret_cast<uint4*>(vrow + (c >> 3) * SH::HALF + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
                         fence_proxy_async_smem();
                     }
-                    if (RT == 2) bar_sync(bar_id, bar_n);
+                    bar_sync(bar_id, bar_n);                       // s_bad is read, every V row is ready
+                    tc_fence_after_sync();
                 }
-                float alpha = 1.f, psum = 0.f;
-                __syncwarp();
+                float alpha = 1.f;
                 if (live) {
-                    // ---- the maximum ---------------------------------------------------------
-                    float mx = -INFINITY;
+                    // ---- the maximum: of half a row, then of both halves ----------------------
+                    float x0 = -INFINITY, x1 = -INFINITY;
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        uint32_t v[32];
-                        tmem_ld32(s_tm + 32 * c, v);
+                        uint32_t v[16];
+                        tmem_ld16(s_tm + 64 * h + 16 * c, v);
                         tmem_wait_ld();
-                        if (masked) {
 #pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (!((mk[c] >> j) & 1u)) v[j] = 0xff800000u;
+                        for (int j = 0; j < 16; j += 4) {
+                            x0 = max3(x0, __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+                            x1 = max3(x1, __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
                         }
-                        float x0 = -INFINITY, x1 = -INFINITY;
-#pragma unroll
-                        for (int j = 0; j < 32; j += 2) {
-                            x0 = fmaxf(x0, __uint_as_float(v[j]));
-                            x1 = fmaxf(x1, __uint_as_float(v[j + 1]));
-                        }
-                        mx = fmaxf(mx, fmaxf(x0, x1));
                     }
-                    const float m_new = fmaxf(m_run, mx * scale);
+                    // Any reference near the maximum will do, as long as the row's two threads use
+                    // the same one: they exchange it as bf16, rounded up.
+                    const uint32_t top = round_up_bf16(fmaxf(x0, x1) * scale);
+                    sh.top[s][h][row] = uint16_t(top >> 16);
+                    bar_sync(pair_bar, 64);
+                    const float other = __uint_as_float(uint32_t(sh.top[s][1 - h][row]) << 16);
+                    const float m_new = fmaxf(m_run, fmaxf(__uint_as_float(top), other));
                     alpha = m_run == -INFINITY ? 0.f : fast_exp2(m_run - m_new);
                     m_run = m_new;
                     const float m_sub = m_new == -INFINITY ? 0.f : m_new;      // nothing seen yet: every weight is 0
-                    if (masked && (bad[0] | bad[1] | bad[2] | bad[3])) {
+                    l_run *= alpha;
+                    if (odd_drafts) {
+                        const uint32_t* s_bad = sh.bad[RT == 1 ? s : i & 1];
 #pragma unroll
-                        for (int d = 0; d < D; ++d) acc[d] *= alpha;
-                        l_run *= alpha;
+                        for (int d = 0; d < DH / 2; ++d) acc[d] = make_f2(acc[d].f.x * alpha, acc[d].f.y * alpha);
                         alpha = 1.f;
 #pragma unroll 1
                         for (int j = 0; j < kTcTile; ++j) {
-                            if (!((bad[j >> 5] >> (j & 31)) & 1u)) continue;
+                            if (!((s_bad[j >> 5] >> (j & 31)) & 1u)) continue;
                             const float sj = __uint_as_float(tmem_ld1(s_tm + j));
                             tmem_wait_ld();
-                            const float p = (mk[j >> 5] >> (j & 31)) & 1u ? fast_exp2(fmaf(sj, scale, -m_sub)) : 0.f;
-                            const int2 en = sh.entry[info][j >> a.bs_shift];
+                            const float p = fast_exp2(fmaf(sj, scale, -m_sub));
                             const uint4* vg = reinterpret_cast<const uint4*>(
-                                static_cast<const uint16_t*>(a.v_pages) + (size_t(en.x) * a.bs + (j & (a.bs - 1))) * D);
+                                static_cast<const uint16_t*>(a.v_pages) +
+                                (size_t(sh.entry[info][j >> a.bs_shift].x) * a.bs + (j & (a.bs - 1))) * D + h * DH);
                             if (p != 0.f) {
 #pragma unroll
-                                for (int c = 0; c < D / 8; ++c) {
+                                for (int c = 0; c < DH / 8; ++c) {
                                     float f[8];
                                     unpack16<true>(__ldg(vg + c), f);
 #pragma unroll
-                                    for (int x = 0; x < 8; ++x) acc[8 * c + x] = fmaf(p, f[x], acc[8 * c + x]);
+                                    for (int x = 0; x < 4; ++x)
+                                        acc[4 * c + x] = fma2(make_f2(p, p), make_f2(f[2 * x], f[2 * x + 1]), acc[4 * c + x]);
                                 }
                             }
                             __syncwarp();
                         }
+                        tc_fence_before_sync();
+                        bar_sync(pair_bar, 64);                    // both have read the row's scores
+                        tc_fence_after_sync();
                     }
-                    // ---- the weights, in three bf16 parts ----------------------------------------
-                    unsigned char* p_row = smem + SH::OFF_P + s * SH::P_TILE + row * 128;
-                    float sums[4] = {0.f, 0.f, 0.f, 0.f};
+                    // ---- the weights, in three bf16 parts, over the scores' own columns -----------
+                    unsigned char* p_row = smem + SH::OFF_P + s * SH::P_TILE + h * SH::HALF + row * 128;
+                    const F2 scale2 = make_f2(scale, scale), m2 = make_f2(-m_sub, -m_sub);
+                    F2 sum_a = make_f2(0.f, 0.f), sum_b = make_f2(0.f, 0.f);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        uint32_t v[32];
-                        tmem_ld32(s_tm + 32 * c, v);
+                        uint32_t v[16];
+                        tmem_ld16(s_tm + 64 * h + 16 * c, v);
                         tmem_wait_ld();
-                        uint32_t hi[16], mid[16], small[16];
+                        uint32_t hm[16], small[8];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            float p0 = fast_exp2(fmaf(__uint_as_float(v[2 * j]), scale, -m_sub));
-                            float p1 = fast_exp2(fmaf(__uint_as_float(v[2 * j + 1]), scale, -m_sub));
-                            if (masked) {
-                                if (!((mk[c] >> (2 * j)) & 1u)) p0 = 0.f;
-                                if (!((mk[c] >> (2 * j + 1)) & 1u)) p1 = 0.f;
-                            }
-                            sums[j & 1] += p0;
-                            sums[2 + (j & 1)] += p1;
-                            hi[j] = cut_bf16x2(p0, p1);
-                            mid[j] = cut_bf16x2(p0, p1);
-                            small[j] = cut_bf16x2(p0, p1);
+                        for (int j = 0; j < 8; ++j) {
+                            F2 p = fma2(make_f2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), scale2, m2);
+                            p = make_f2(fast_exp2(p.f.x), fast_exp2(p.f.y));
+                            if (j & 1) sum_b = add2(sum_b, p);
+                            else sum_a = add2(sum_a, p);
+                            hm[j] = cut_bf16x2(p);
+                            hm[8 + j] = cut_bf16x2(p);
+                            small[j] = __byte_perm(__float_as_uint(p.f.x), __float_as_uint(p.f.y), 0x7632);
                         }
-                        tmem_st16(s_tm + 32 * c, hi);
-                        tmem_st16(s_tm + 32 * c + 16, mid);
+                        tmem_st16(s_tm + 64 * h + 16 * c, hm);
 #pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            *reinterpret_cast<uint4*>(p_row + (c >> 1) * SH::HALF + (((((c & 1) << 2) + x) ^ (row & 7)) << 4)) =
+                        for (int x = 0; x < 2; ++x)
+                            *reinterpret_cast<uint4*>(p_row + (((2 * c + x) ^ (row & 7)) << 4)) =
                                 make_uint4(small[4 * x], small[4 * x + 1], small[4 * x + 2], small[4 * x + 3]);
                     }
-                    psum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+                    const F2 sum = add2(sum_a, sum_b);
+                    l_run += sum.f.x + sum.f.y;
                     tmem_wait_st();
                     fence_proxy_async_smem();
                 }
                 tc_fence_before_sync();
                 mbar_arrive(&sh.p_ready[s]);
-                l_run = fmaf(l_run, alpha, psum);
                 wait(&sh.o_full[s], done & 1u);
                 __syncwarp();
                 tc_fence_after_sync();
                 if (live) {
+                    const F2 alpha2 = make_f2(alpha, alpha);
 #pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t v[32];
-                        tmem_ld32(o_tm + 32 * c, v);
+                    for (int c = 0; c < DH / 16; ++c) {
+                        uint32_t v[16];
+                        tmem_ld16(o_tm + h * DH + 16 * c, v);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) acc[32 * c + j] = fmaf(acc[32 * c + j], alpha, __uint_as_float(v[j]));
+                        for (int j = 0; j < 8; ++j)
+                            acc[8 * c + j] = fma2(acc[8 * c + j], alpha2,
+                                                  make_f2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])));
                     }
                     tc_fence_before_sync();
                 }
             }
 
             // ---- the part's (m, l, o): the output itself, or a partial -------------------------
+            // The halves' sums meet through the query tiles, the rows leave through the P tiles and the
+            // ring (all idle now): with one row tile the odd tiles' rows join the even tiles' on the
+            // way; then whole rows go out, a warp 512 bytes at a time.
             const bool complete = g.t0 == 0 && g.t1 == g.tiles;
-            if (RT == 1) {
-                // the odd tiles' rows join the even tiles' through the ring, which is idle now
-                float4* x = reinterpret_cast<float4*>(smem + SH::OFF_RING) + row * (D / 4);
-                float2* x_ml = reinterpret_cast<float2*>(smem + SH::OFF_P);
-                bar_sync(2, 256);
-                if (s == 1 && live) {
+            constexpr int V4 = D / 4;
+            float2* x_ml = reinterpret_cast<float2*>(smem);                    // [slot][half][row]
+            float4* x_rows = reinterpret_cast<float4*>(smem + SH::OFF_P);
+            const int x_row = RT == 2 ? s * 128 + row : row;
+            auto cell = [&](int r, int c) -> float4& { return x_rows[r * V4 + ((c + r) & (V4 - 1))]; };
+            tree_sync<kTcSoft>();
+            x_ml[(2 * s + h) * 128 + row] = make_float2(m_run, l_run);
+            if (RT == 1 && s == 1 && live) {
 #pragma unroll
-                    for (int c = 0; c < D / 4; ++c)
-                        x[(c + lane) & (D / 4 - 1)] = make_float4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]);
-                    x_ml[row] = make_float2(m_run, l_run);
-                }
-                bar_sync(2, 256);
-                if (s == 0 && live) {
-                    const float m1 = x_ml[row].x, m_new = fmaxf(m_run, m1);
-                    const float w0 = m_run == -INFINITY ? 0.f : fast_exp2(m_run - m_new);
-                    const float w1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - m_new);
-                    l_run = l_run * w0 + x_ml[row].y * w1;
-                    m_run = m_new;
-#pragma unroll
-                    for (int c = 0; c < D / 4; ++c) {
-                        const float4 o = x[(c + lane) & (D / 4 - 1)];
-                        acc[4 * c] = fmaf(acc[4 * c], w0, o.x * w1);
-                        acc[4 * c + 1] = fmaf(acc[4 * c + 1], w0, o.y * w1);
-                        acc[4 * c + 2] = fmaf(acc[4 * c + 2], w0, o.z * w1);
-                        acc[4 * c + 3] = fmaf(acc[4 * c + 3], w0, o.w * w1);
-                    }
-                }
+                for (int c = 0; c < DH / 4; ++c)
+                    cell(x_row, h * (DH / 4) + c) =
+                        make_float4(acc[2 * c].f.x, acc[2 * c].f.y, acc[2 * c + 1].f.x, acc[2 * c + 1].f.y);
             }
-            if ((RT == 2 || s == 0) && r_unit < a.R) {
-                const int rr = r_unit - g.row0;
-                const long long slot = (long long)tree_slot(blockIdx.x, part.per, g.start) * a.item_rows + rr;
-                const float inv = complete ? (l_run == 0.f ? 0.f : 1.f / l_run) : 1.f;
-                float* dst = complete ? a.out + tree_out_row(a, g.b, g.kvh, r_unit) * D : a.part_o + slot * D;
-#pragma unroll
-                for (int d = 0; d < D; d += 4)
-                    *reinterpret_cast<float4*>(dst + d) =
-                        make_float4(acc[d] * inv, acc[d + 1] * inv, acc[d + 2] * inv, acc[d + 3] * inv);
-                if (!complete) {
+            tree_sync<kTcSoft>();
+            if ((RT == 2 || s == 0) && live) {
+                l_run += x_ml[(2 * s + 1 - h) * 128 + row].y;
+                float w0 = 1.f, w1 = 0.f;
+                if (RT == 1) {
+                    const float2 ml = x_ml[256 + row];
+                    const float m_new = fmaxf(m_run, ml.x);
+                    w0 = m_run == -INFINITY ? 0.f : fast_exp2(m_run - m_new);
+                    w1 = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - m_new);
+                    l_run = l_run * w0 + (ml.y + x_ml[384 + row].y) * w1;
+                    m_run = m_new;
+                }
+                if (complete) {
+                    const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+                    w0 *= inv;
+                    w1 *= inv;
+                } else if (h == 0 && r_unit < a.R) {
+                    const long long slot =
+                        (long long)tree_slot(blockIdx.x, part.per, g.start) * a.item_rows + r_unit - g.row0;
                     a.part_m[slot] = m_run;
                     a.part_l[slot] = l_run;
                 }
+#pragma unroll
+                for (int c = 0; c < DH / 4; ++c) {
+                    float4& x = cell(x_row, h * (DH / 4) + c);
+                    float4 o = make_float4(acc[2 * c].f.x * w0, acc[2 * c].f.y * w0, acc[2 * c + 1].f.x * w0,
+                                           acc[2 * c + 1].f.y * w0);
+                    if (RT == 1) {
+                        const float4 y = x;
+                        o = make_float4(fmaf(y.x, w1, o.x), fmaf(y.y, w1, o.y), fmaf(y.z, w1, o.z), fmaf(y.w, w1, o.w));
+                    }
+                    x = o;
+                }
             }
-            if (!complete) tree_arrive_and_merge<256>(a, g.item, g.start, g.tiles, part.per, &sh.last);
-            else bar_sync(2, 256);                                 // queries and ring are free for the next item
+            tree_sync<kTcSoft>();
+            {
+                const int rows = min(a.item_rows, a.R - g.row0);
+                float4* part_rows = reinterpret_cast<float4*>(a.part_o) +
+                                    (long long)tree_slot(blockIdx.x, part.per, g.start) * a.item_rows * V4;
+                for (int i = tid; i < rows * V4; i += kTcSoft) {
+                    const int r = i / V4, c = i % V4;
+                    float4* dst = complete ? reinterpret_cast<float4*>(a.out) + tree_out_row(a, g.b, g.kvh, g.row0 + r) * V4
+                                           : part_rows + (long long)r * V4;
+                    dst[c] = cell(r, c);
+                }
+            }
+            if (!complete)
+                tree_arrive_and_merge<kTcSoft>(a, g.item, g.start, g.tiles, part.per, &sh.last,
+                                               reinterpret_cast<float*>(smem + SH::OFF_P),
+                                               (2 * SH::P_TILE + SH::UNITS * SH::UNIT) / 4);
+            tree_sync<kTcSoft>();                                  // this memory is free for the next item
             unit0 += 2 * ntl;
             tile0 += ntl;
         }
@@ -648,7 +745,7 @@ cudaError_t launch_tc_t(const TreeArgs& a, cudaStream_t s)
     static std::atomic<unsigned long long> configured{0};   // devices set up
     const cudaError_t cfg = once_per_device(configured, [&]() -> cudaError_t {
         return cudaFuncSetAttribute(tree_tc_kernel<D, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    int(TcShape<D, RT>::SMEM));
+                                    int(tc_smem<D, RT>()));
     });
     if (cfg != cudaSuccess) return cfg;
     CUtensorMap kmap, vmap;
@@ -658,7 +755,7 @@ cudaError_t launch_tc_t(const TreeArgs& a, cudaStream_t s)
     e = encode_tree_map(&vmap, a.v_pages, D, a.bs, tiles);
     if (e != cudaSuccess) return e;
     const int ctas = num_sms() < kTreeMaxCtas ? num_sms() : kTreeMaxCtas;
-    return launch_after_previous(tree_tc_kernel<D, RT>, dim3(unsigned(ctas)), dim3(kTcThreads), TcShape<D, RT>::SMEM, s, a,
+    return launch_after_previous(tree_tc_kernel<D, RT>, dim3(unsigned(ctas)), dim3(kTcThreads), tc_smem<D, RT>(), s, a,
                                  kmap, vmap);
 }
 
