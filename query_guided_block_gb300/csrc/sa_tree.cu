@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
     extern __shared__ __align__(128) unsigned char smem_raw[];
     __shared__ int2 s_ent[kTrEntries];
     __shared__ uint32_t s_any[kTreeMaxDrafts / 32];         // drafts that some query sees
-    __shared__ long long s_scan[kTrThreads / 32 + 2];
+    __shared__ long long s_scan[kTreeScan<kTrThreads>];
     __shared__ int s_last;
     __shared__ uint32_t s_bad[2];
 
@@ -543,6 +543,7 @@ cudaError_t launch_tree_t(TreeArgs a, cudaStream_t s)
     a.item_rows = 16 * RW;
     a.row_groups = (a.R + a.item_rows - 1) / a.item_rows;
     a.min_per = 4;
+    a.whole_slack = 8;
     int ctas = num_sms() * (2 * (smem + 10 * 1024) <= size_t(kSmemPerSm) ? 2 : 1);
     if (ctas > kTreeMaxCtas) ctas = kTreeMaxCtas;
     return launch_after_previous(tree_kernel<D, KB, NQ, RW>, dim3(unsigned(ctas)), dim3(kTrThreads), smem, s, a);
@@ -562,7 +563,7 @@ TreeLayout tree_layout(const Geometry& g)
 {
     TreeLayout L{};
     const int R = g.Q * g.G;
-    const size_t rows = R <= 16 ? 16 : (R <= 64 ? 64 : (R <= 128 ? 128 : kTreeMaxRows));   // of an item, in any kernel
+    const size_t rows = size_t(tree_item_rows(R));
     const size_t slots = 2 * size_t(kTreeMaxCtas);
     L.counters = 256;
     L.part_m = align256(L.counters + size_t(g.units()) * ((R + 15) / 16) * sizeof(uint32_t));

@@ -19,7 +19,14 @@
 namespace sa {
 
 constexpr int kTreeMaxCtas = 304;    // partial slots: two per CTA (the item a part begins in, the one it ends in)
-constexpr int kTreeMaxRows = 256;    // query rows of an item at most
+constexpr int kTreeMaxRows = 128;    // query rows of an item at most
+
+// Query rows of an item, in any kernel at most.
+inline int tree_item_rows(int R) { return R <= 16 ? 16 : (R <= 64 ? 64 : kTreeMaxRows); }
+
+// Words of shared memory that tree_part needs.
+template <int NT>
+constexpr int kTreeScan = 3 * (NT / 32) + 2;
 
 struct TreeArgs {
     const void* q;
@@ -33,6 +40,7 @@ struct TreeArgs {
     int item_rows;             // query rows of an item at most
     int tile;                  // list positions per tile
     int min_per;               // tiles of a part at least
+    int whole_slack;           // tiles that a part may grow by so that it holds whole items
     float scale_log2;
     float *part_m, *part_l, *part_o;   // [2 * CTA + which][item_rows] ([D])
     uint32_t *counters, *err;
@@ -116,15 +124,22 @@ struct TreePart {
 };
 
 template <int NT>
-__device__ TreePart tree_part(const TreeArgs& a, long long* s_scan /* [NT / 32 + 2] shared */)
+__device__ TreePart tree_part(const TreeArgs& a, long long* s_scan /* [kTreeScan<NT>] shared */)
 {
+    constexpr int W = NT / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int units = a.B * a.Hkv;
     // thread t owns units [t * ch, (t + 1) * ch)
     const int ch = (units + NT - 1) / NT;
     const int u0 = min(units, tid * ch), u1 = min(units, u0 + ch);
     long long mine = 0;
-    for (int u = u0; u < u1; ++u) mine += tree_tiles(a, tree_unit(a, u));
+    int most = 0, least = INT32_MAX;                         // tiles of an active item
+    for (int u = u0; u < u1; ++u) {
+        const int t = tree_tiles(a, tree_unit(a, u));
+        mine += t;
+        most = max(most, t);
+        if (t > 0) least = min(least, t);
+    }
     mine *= a.row_groups;
     long long incl = mine;
 #pragma unroll
@@ -132,18 +147,31 @@ __device__ TreePart tree_part(const TreeArgs& a, long long* s_scan /* [NT / 32 +
         const long long t = __shfl_up_sync(kFullMask, incl, off);
         if (lane >= off) incl += t;
     }
-    if (lane == 31) s_scan[warp] = incl;
+    most = __reduce_max_sync(kFullMask, most);
+    least = __reduce_min_sync(kFullMask, least);
+    if (lane == 31) {
+        s_scan[warp] = incl;
+        s_scan[W + warp] = most;
+        s_scan[2 * W + warp] = least;
+    }
     __syncthreads();
     long long before = 0, total = 0;
 #pragma unroll
-    for (int w = 0; w < NT / 32; ++w) {
+    for (int w = 0; w < W; ++w) {
         if (w < warp) before += s_scan[w];
         total += s_scan[w];
+        most = max(most, int(s_scan[W + w]));
+        least = min(least, int(s_scan[2 * W + w]));
     }
     before += incl - mine;
     TreePart p;
     const long long share = (total + gridDim.x - 1) / gridDim.x;
     p.per = int(share < a.min_per ? a.min_per : share);
+    if (most == least && most > 0) {
+        // equal items: parts of whole items leave nothing to merge, if they are not much longer
+        const int whole = (p.per + most - 1) / most * most;
+        if (whole - p.per <= a.whole_slack) p.per = whole;
+    }
     p.lo = min(total, (long long)blockIdx.x * p.per);
     p.hi = min(total, p.lo + p.per);
     if (p.lo < p.hi && mine > 0 && p.lo >= before && p.lo < before + mine) {
@@ -153,16 +181,17 @@ __device__ TreePart tree_part(const TreeArgs& a, long long* s_scan /* [NT / 32 +
             const long long all = (long long)t * a.row_groups;
             if (p.lo < at + all) {
                 const int rg = int((p.lo - at) / t);
-                s_scan[NT / 32] = (long long)u * a.row_groups + rg;
-                s_scan[NT / 32 + 1] = at + (long long)rg * t;
+                s_scan[3 * W] = (long long)u * a.row_groups + rg;
+                s_scan[3 * W + 1] = at + (long long)rg * t;
                 break;
             }
             at += all;
         }
     }
     __syncthreads();
-    p.item = int(s_scan[NT / 32]);
-    p.start = s_scan[NT / 32 + 1];
+    p.item = int(s_scan[3 * W]);
+    p.start = s_scan[3 * W + 1];
+    __syncthreads();                                         // s_scan may be used for something else
     return p;
 }
 

@@ -1,19 +1,19 @@
 // Draft-tree attention on the fifth-generation tensor cores (bf16 queries and K/V).
 //
-// A CTA holds one or two tiles of 128 query rows of a (sequence, KV head) unit and walks the
-// unit's list (sa_tree.cuh) in tiles of 128 tokens.  Two slots work side by side, each with a
-// score tile and an output tile in tensor memory (all 512 columns) and a warpgroup of its own:
-// with one row tile the slots take the even and the odd token tiles (their results are joined
-// at the item's end), with two row tiles each slot keeps one of them and both use every K/V
-// tile.  While one slot's softmax runs, the other's products keep the tensor core busy.
+// A CTA holds up to 128 query rows of a (sequence, KV head) unit and walks the unit's list
+// (sa_tree.cuh) in tiles of 128 tokens; more rows are further items over the same keys, which
+// the L2 then holds.  Two slots take the even and the odd tiles, each with a score tile and an
+// output tile in tensor memory (all 512 columns) and a softmax warpgroup pair of its own, so
+// that one slot's products run while the other's softmax does.
 //
 // Roles (20 warps):
-//   warps 0-7, 8-15  the slots' softmax: two threads own a query row, each half of its tokens
-//               and half of its channels.  They read S, take the maximum, write P, then add the
-//               finished O tile to their channels in registers.
+//   warps 0-7, 8-15  the slots' softmax: two threads of a slot own a query row, each half of the
+//               tile's tokens.  They read S, take the maximum, write P.  All four threads of a
+//               row then add every finished O tile, a quarter of the channels each, to the
+//               row's running O in registers (half as many registers as an O per slot).
 //   warp 16     resolves the list's entries 32 at a time and brings K and V by TMA, one box
 //               of 64 channels x one block per entry and channel half, into a ring of K and
-//               V units that it refills as the products release them;
+//               V units that it refills as the products release them, into the next item;
 //   warps 17, 18  one thread each: S = Q K^T, then O = P V for one slot (tcgen05.mma).
 //
 // Precision.  The output is fp32, so P goes into the product as three bf16 parts that hold
@@ -23,10 +23,9 @@
 // every tile and the rows add it up in registers by one FMA, which carries the softmax's
 // rescaling as well.
 //
-// Per 128 tokens and row tile the tensor core does 4 x 128 x 128 x D multiply-adds (one for S,
-// three for P V), about 2050 cycles at D = 128; the 64 KB of K and V arrive in about 2800
-// cycles at the SM's share of the HBM bandwidth, so one row tile is bound by memory and
-// two row tiles by the tensor core.
+// Per 128 tokens the tensor core does 4 x 128 x 128 x D multiply-adds (one part for S, three
+// for P V), about 2050 cycles at D = 128; the 64 KB of K and V arrive in about 2800 cycles
+// at the SM's share of the HBM bandwidth.
 #include "sa_tcgen05.cuh"
 #include "sa_tree.cuh"
 
@@ -41,21 +40,21 @@ constexpr int kTcThreads = kTcSoft + 128;
 constexpr int kTcTile = 128;
 constexpr int kNoToken = INT32_MIN;
 
-template <int D, int RT>
+template <int D>
 struct TcShape {
     static constexpr int HALVES = D / 64;
     static constexpr int HALF = kTcTile * 128;              // 128 rows x 64 bf16
     static constexpr int UNIT = HALVES * HALF;              // K or V of a tile
     static constexpr int Q_TILE = HALVES * HALF;
     static constexpr int P_TILE = 2 * HALF;                 // 128 rows x 128 tokens
-    static constexpr int UNITS = D == 128 ? (RT == 1 ? 4 : 3) : 7;
-    // Tiles whose entries are remembered.  The producer is at most UNITS / 2 tiles past the
-    // oldest tile whose V is still in the ring.
-    static constexpr int INFO = UNITS / 2 + 2;
-    static constexpr int OFF_P = RT * Q_TILE;
+    static constexpr int UNITS = D == 128 ? 4 : 7;
+    // Tiles whose entries are remembered: while a tile's O is not yet added up, the V two tiles on
+    // is still in the ring, and the producer is at most (UNITS + 1) / 2 tiles past that one.
+    static constexpr int INFO = (UNITS + 1) / 2 + 4;
+    static constexpr int OFF_P = Q_TILE;
     static constexpr int OFF_RING = OFF_P + 2 * P_TILE;
     static constexpr int OFF_SHARED = OFF_RING + UNITS * UNIT;
-    static_assert(2 * P_TILE + size_t(UNITS) * UNIT >= size_t(RT) * 128 * D * 4, "the rows leave through this memory");
+    static_assert(2 * P_TILE >= 128 * D * 4, "the rows leave through the P tiles");
 };
 
 __device__ __forceinline__ void bar_sync(int id, int threads)
@@ -105,6 +104,16 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         : "memory");
 }
 
+// Waits for the loads in flight; the registers are named so that nothing uses them earlier.
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+
 // Two fp32 operations in one instruction (each rounded as usual).
 union F2 {
     unsigned long long u;
@@ -120,6 +129,12 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
 {
     F2 r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.u) : "l"(a.u), "l"(b.u), "l"(c.u));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b)
+{
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(a.u), "l"(b.u));
     return r;
 }
 __device__ __forceinline__ F2 add2(F2 a, F2 b)
@@ -139,13 +154,6 @@ __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr)
-{
-    uint32_t r;
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
     return r;
 }
 
@@ -185,30 +193,32 @@ __device__ __forceinline__ uint32_t mask_bits8(const uint32_t* words, int d0, in
     return v & 0xffu;
 }
 
-// Register shares: the CTA starts with 20 warps x 96; the softmax threads hold half an output
-// row.
+// Register shares: the CTA starts with 20 warps x 96; the softmax threads hold a quarter of an
+// output row and half of a tile's scores.
 constexpr int kTcRegsFew = 64, kTcRegsMany = 104;
 static_assert(kTcRegsFew * 128 + kTcRegsMany * kTcSoft <= 96 * kTcThreads, "no more registers than the launch got");
 
-template <int D, int RT>
+template <int D>
 struct TcShared {
-    using SH = TcShape<D, RT>;
-    uint64_t full[SH::UNITS], empty[SH::UNITS], s_full[2], o_full[2], p_ready[2];
-    long long scan[kTcThreads / 32 + 2];
-    int2 entry[SH::INFO][16];
+    using SH = TcShape<D>;
+    uint64_t full[SH::UNITS], empty[SH::UNITS], s_full[2], o_full[2], p_ready[2], o_read[2];
+    union {
+        long long scan[kTreeScan<kTcThreads>];
+        uint16_t top[2][2][2][128];             // half rows' maxima (slot, tile parity, half, row), bf16 rounded up
+    };
+    int token[SH::INFO][16];                    // first token of each entry of a tile
     int masked[SH::INFO];
-    uint32_t bad[2][4];                         // by slot, or by the tile's parity where both slots share a tile
+    uint32_t odd[SH::INFO][4];                  // drafts of a tile whose V holds infinities or NaN
     uint32_t any[kTreeMaxDrafts / 32];
-    uint16_t top[2][2][128];                    // half rows' maxima (slot, half, row), bf16 rounded up
     uint32_t tmem;
     int dead;                                   // a bounded wait ran out: no more waiting
     int last;
 };
-template <int D, int RT>
+template <int D>
 constexpr size_t tc_smem()
 {
-    static_assert(1024 + TcShape<D, RT>::OFF_SHARED + sizeof(TcShared<D, RT>) <= 227 * 1024, "shared memory of a CTA");
-    return 1024 + TcShape<D, RT>::OFF_SHARED + sizeof(TcShared<D, RT>);
+    static_assert(TcShape<D>::OFF_SHARED + sizeof(TcShared<D>) <= 227 * 1024, "shared memory of a CTA");
+    return TcShape<D>::OFF_SHARED + sizeof(TcShared<D>);
 }
 
 // One item's share of this CTA's part: tiles [t0, t1) of the item's list.
@@ -246,22 +256,23 @@ __device__ __forceinline__ bool tc_next(const TreeArgs& a, const TreePart& part,
     return false;
 }
 
-template <int D, int RT>
+template <int D>
 __global__ void __launch_bounds__(kTcThreads, 1)
     tree_tc_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap)
 {
-    using SH = TcShape<D, RT>;
+    using SH = TcShape<D>;
     constexpr uint32_t TMEM_COLS = 512, S_COL = 0, O_COL = 256;    // slot s at + 128 s
     constexpr uint32_t IDESC_S = idesc_bf16_f32(128, kTcTile, false);
     constexpr uint32_t IDESC_O = idesc_bf16_f32(128, D, true);
-    constexpr int SLOT_STEP = RT == 1 ? 2 : 1;                     // tiles between a slot's tiles
 
-    extern __shared__ __align__(128) unsigned char smem_raw[];
+    extern __shared__ __align__(1024) unsigned char smem[];        // swizzle atoms: 1024-byte aligned
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t raw = smem_u32(smem_raw);
-    const uint32_t base = (raw + 1023u) & ~1023u;                  // swizzle atoms: 1024-byte aligned
-    unsigned char* smem = smem_raw + (base - raw);
-    TcShared<D, RT>& sh = *reinterpret_cast<TcShared<D, RT>*>(smem + SH::OFF_SHARED);
+    const uint32_t base = smem_u32(smem);
+    TcShared<D>& sh = *reinterpret_cast<TcShared<D>*>(smem + SH::OFF_SHARED);
+    if ((base & 1023u) != 0u) {                                    // the alignment above is not kept: no result
+        if (tid == 0) raise_error(a.err, SPARSE_ATTN_ERR_CAPACITY);
+        return;
+    }
 
     allow_dependents_early();
     if (warp == 0) {
@@ -271,19 +282,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < SH::UNITS; ++i) {
             mbar_init(&sh.full[i], 1);
-            mbar_init(&sh.empty[i], RT);
+            mbar_init(&sh.empty[i], 1);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&sh.s_full[s], 1);
             mbar_init(&sh.o_full[s], 1);
             mbar_init(&sh.p_ready[s], kTcSoft / 2);
+            mbar_init(&sh.o_read[s], kTcSoft / 2);
         }
         sh.dead = 0;
         fence_mbar_init();
     }
     grid_dependency_wait();   // queries, pages and lengths may come from the previous kernel
     tc_fence_before_sync();
-    const TreePart part = tree_part<kTcThreads>(a, sh.scan);        // synchronises the CTA
+    const TreePart part = tree_part<kTcThreads>(a, sh.scan);       // synchronises the CTA
     tc_fence_after_sync();
     const uint32_t tmem = sh.tmem;
     const bool dense = a.sel_ids == nullptr;
@@ -304,10 +316,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTcRegsFew));
         uint32_t unit0 = 0;                                        // ring units used by earlier segments
         uint32_t tile0 = 0;                                        // tiles of earlier segments
-        uint32_t mine0 = 0;                                        // tiles of this issuer's slot, likewise
+        uint32_t done = 0;                                         // tiles of this issuer's slot so far
         while (tc_next(a, part, lo, start, item, g)) {
             const int ntl = g.t1 - g.t0;
-            bar_sync(1, kTcThreads);                               // queries staged, the ring is free
             if (warp == 16) {
                 // ---- producer ---------------------------------------------------------
                 const int n_e = a.bs >= kTcTile ? 1 : kTcTile >> a.bs_shift;   // entries of a tile
@@ -334,7 +345,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     const uint32_t n_ok = __popc(__ballot_sync(kFullMask, ok));
                     const bool any_partly = __any_sync(kFullMask, partly);
                     const uint32_t info = (tile0 + i) % SH::INFO;
-                    if (mine) sh.entry[info][lane] = make_int2(en.x, ok ? en.y : kNoToken);
+                    if (mine) sh.token[info][lane] = ok ? en.y : kNoToken;
                     if (lane == 0) sh.masked[info] = any_partly;
                     __syncwarp();
 #pragma unroll
@@ -355,14 +366,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             } else if (warp <= 18) {
                 // ---- issuer of slot s ----------------------------------------------------
                 const int s = warp - 17;
-                uint32_t done = mine0;
+                bar_sync(1, kTcSoft + 64);                         // queries staged
                 if (lane == 0) {
-                    const uint64_t q_desc = smem_desc_sw128(base + (RT == 2 ? s * SH::Q_TILE : 0), 16, 1024);
+                    const uint64_t q_desc = smem_desc_sw128(base, 16, 1024);
                     const uint64_t p_desc = smem_desc_sw128(base + SH::OFF_P + s * SH::P_TILE, 16, 1024);
                     const uint64_t k_desc0 = smem_desc_sw128(base + SH::OFF_RING, 16, 1024);
                     const uint64_t v_desc0 = smem_desc_sw128(base + SH::OFF_RING, SH::HALF, 1024);
                     const uint32_t s_tm = tmem + S_COL + s * 128, o_tm = tmem + O_COL + s * 128;
-                    for (int i = RT == 1 ? s : 0; i < ntl; i += SLOT_STEP, ++done) {
+                    for (int i = s; i < ntl; i += 2, ++done) {
                         const uint32_t kn = unit0 + 2 * i, ks = kn % SH::UNITS;
                         const uint32_t vn = kn + 1, vs = vn % SH::UNITS;
                         wait(&sh.full[ks], (kn / SH::UNITS) & 1u);
@@ -377,6 +388,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         umma_commit(&sh.s_full[s]);
                         umma_commit(&sh.empty[ks]);
                         wait(&sh.full[vs], (vn / SH::UNITS) & 1u);
+                        if (done > 0) wait(&sh.o_read[s], (done - 1) & 1u);      // the other slot's threads read O
                         wait(&sh.p_ready[s], done & 1u);
                         tc_fence_after_sync();
                         const uint64_t vd = v_desc0 + uint64_t((vs * SH::UNIT) >> 4);
@@ -389,43 +401,41 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         for (int pp = 1; pp >= 0; --pp)
 #pragma unroll
                             for (int k = 0; k < kTcTile / 16; ++k)
-                                umma_bf16_ta(o_tm, s_tm + k * 16 + pp * 8,
-                                             vd + uint32_t((k * 16 * 128) >> 4), IDESC_O, 1u);
+                                umma_bf16_ta(o_tm, s_tm + k * 16 + pp * 8, vd + uint32_t((k * 16 * 128) >> 4), IDESC_O, 1u);
                         umma_commit(&sh.empty[vs]);
                         umma_commit(&sh.o_full[s]);
                     }
                 }
                 __syncwarp();
-                mine0 += uint32_t(RT == 1 ? (ntl + 1 - s) / 2 : ntl);
             }
             unit0 += 2 * ntl;
             tile0 += ntl;
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTcRegsMany));
-        constexpr int DH = D / 2;                                  // channels of a thread
+        constexpr int CW = D / 4;                                  // channels of a thread
         const int s = warp >> 3;                                   // slot
-        const int h = (warp >> 2) & 1;                             // which tokens and channels
-        const int row = 32 * (warp & 3) + lane;                    // row of the slot's tile
+        const int h = (warp >> 2) & 1;                             // which half of a tile's tokens
+        const int row = 32 * (warp & 3) + lane;                    // query row of the item
+        const int ch0 = (2 * s + h) * CW;                          // first channel
         const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
-        const uint32_t s_tm = tmem + S_COL + s * 128 + lanes, o_tm = tmem + O_COL + s * 128 + lanes;
-        const int pair_bar = 5 + 4 * s + (warp & 3);               // the two warps that share rows
+        const uint32_t s_tm = tmem + S_COL + s * 128 + 64 * h + lanes, o_tm = tmem + O_COL + ch0 + lanes;
+        const int pair_bar = 5 + 4 * s + (warp & 3);               // the two warps that share rows of a slot
         const float scale = a.scale_log2;
-        uint32_t tile0 = 0, done = 0, unit0 = 0;
+        uint32_t tile0 = 0, unit0 = 0, soft_n = 0, acc_n[2] = {0, 0};
         while (tc_next(a, part, lo, start, item, g)) {
             const int ntl = g.t1 - g.t0;
             const uint32_t* mask_b = a.mask != nullptr ? a.mask + (long long)g.b * a.Q * a.mask_words : nullptr;
             // ---- the item's queries, and the drafts that some query sees ----------------
             {
                 constexpr int CPR = D / 8;                         // 16-byte chunks of a row
-                for (int i = tid; i < RT * 128 * CPR; i += kTcSoft) {
+                for (int i = tid; i < 128 * CPR; i += kTcSoft) {
                     const int r = i / CPR, c = i - r * CPR;
                     uint4 v = make_uint4(0u, 0u, 0u, 0u);
                     if (g.row0 + r < a.R)
                         v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
                                                                  tree_out_row(a, g.b, g.kvh, g.row0 + r) * D) + c);
-                    *reinterpret_cast<uint4*>(smem + (r >> 7) * SH::Q_TILE + (c >> 3) * SH::HALF + (r & 127) * 128 +
-                                              (((c & 7) ^ (r & 7)) << 4)) = v;
+                    *reinterpret_cast<uint4*>(smem + (c >> 3) * SH::HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
                 }
                 const long long list = dense ? g.un.len : (long long)g.un.n_ctx << a.bs_shift;
                 if ((long long)g.t1 * kTcTile > list) {            // this part meets drafts
@@ -435,157 +445,194 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         for (int i = tid; i < a.Q * a.mask_words; i += kTcSoft) atomicOr(&sh.any[i % a.mask_words], mask_b[i]);
                     }
                 }
-                fence_proxy_async_smem();                          // before TMA and the tensor core use this memory
+                fence_proxy_async_smem();                          // before the tensor core uses this memory
             }
-            bar_sync(1, kTcThreads);
+            bar_sync(1, kTcSoft + 64);
 
-            const int r_unit = g.row0 + (RT == 2 ? s * 128 : 0) + row;
-            const bool live = g.row0 + (RT == 2 ? s * 128 : 0) + 32 * (warp & 3) < a.R;    // any of this warp's rows
+            const int r_unit = g.row0 + row;
+            const bool live = g.row0 + 32 * (warp & 3) < a.R;      // any of this warp's rows
             const int q_row = r_unit < a.R ? r_unit / a.G : 0;
-            F2 acc[DH / 2];
+            const uint32_t* words = mask_b != nullptr ? mask_b + (long long)q_row * a.mask_words : nullptr;
+            const int limit = r_unit < a.R ? (mask_b != nullptr ? a.Q : q_row + 1) : 0;
+            F2 acc[CW / 2];
 #pragma unroll
-            for (int d = 0; d < DH / 2; ++d) acc[d] = make_f2(0.f, 0.f);
-            float m_run = -INFINITY, l_run = 0.f;
+            for (int d = 0; d < CW / 2; ++d) acc[d] = make_f2(0.f, 0.f);
+            float m_soft = -INFINITY, l_run = 0.f;                 // this slot's reference and half-row sum
+            float m_other = -INFINITY;                             // the other slot's reference
+            float m_acc = -INFINITY;                               // what acc is relative to
 
-            for (int i = RT == 1 ? s : 0; i < ntl; i += SLOT_STEP, ++done) {
-                wait(&sh.s_full[s], done & 1u);
+            // Tokens 8 g8 .. + 7 of local tile i that a query with these mask words sees.
+            auto tokens8 = [&](int i, int g8, const uint32_t* w, int lim) -> uint32_t {
+                const int le = (g8 * 8) >> a.bs_shift;
+                const int first = sh.token[(tile0 + i) % SH::INFO][le];
+                if (first == kNoToken) return 0u;
+                const int tok = first + ((g8 * 8) & (a.bs - 1));
+                const bool ctx = dense || (((g.t0 + i) * kTcTile) >> a.bs_shift) + le < g.un.n_ctx;
+                uint32_t bits = 0u;
+                if (ctx) bits = (1u << min(8, max(0, g.un.len - tok))) - 1u;
+                if (dense || !ctx) bits |= mask_bits8(w, tok - g.un.len, lim);
+                return bits;
+            };
+            // Adds O of local tile i to this thread's channels.
+            auto add_up = [&](int i) {
+                const int sl = i & 1;
+                wait(&sh.o_full[sl], acc_n[sl] & 1u);
+                __syncwarp();
+                tc_fence_after_sync();
+                if (live) {
+                    uint32_t v[CW / 16][16];
+#pragma unroll
+                    for (int c = 0; c < CW / 16; ++c) tmem_ld16(o_tm + sl * 128 + 16 * c, v[c]);
+                    float m = m_soft;
+                    if (sl != s) {
+                        const uint32_t pr = acc_n[sl] & 1u;
+                        m_other = fmaxf(m_other, fmaxf(__uint_as_float(uint32_t(sh.top[sl][pr][0][row]) << 16),
+                                                       __uint_as_float(uint32_t(sh.top[sl][pr][1][row]) << 16)));
+                        m = m_other;
+                    }
+                    const float m_new = fmaxf(m_acc, m);
+                    const float w0 = m_acc == -INFINITY ? 0.f : fast_exp2(m_acc - m_new);
+                    const float w1 = m == -INFINITY ? 0.f : fast_exp2(m - m_new);
+                    m_acc = m_new;
+                    const F2 w02 = make_f2(w0, w0), w12 = make_f2(w1, w1);
+#pragma unroll
+                    for (int c = 0; c < CW / 16; ++c) {
+                        tmem_wait_ld16(v[c]);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            acc[8 * c + j] = fma2(make_f2(__uint_as_float(v[c][2 * j]), __uint_as_float(v[c][2 * j + 1])), w12,
+                                                  mul2(acc[8 * c + j], w02));
+                    }
+                    const uint32_t info = (tile0 + i) % SH::INFO;
+                    if (sh.masked[info] != 0 && (sh.odd[info][0] | sh.odd[info][1] | sh.odd[info][2] | sh.odd[info][3])) {
+                        // infinities and NaN were taken out of V: they come back where they are seen
+#pragma unroll 1
+                        for (int j = 0; j < kTcTile; ++j) {
+                            if (!((sh.odd[info][j >> 5] >> (j & 31)) & 1u)) continue;
+                            if (!((tokens8(i, j >> 3, words, limit) >> (j & 7)) & 1u)) continue;
+                            const int2 en = tree_entry(a, g.u, g.un, (((g.t0 + i) * kTcTile) + j) >> a.bs_shift);
+                            const uint16_t* vg = static_cast<const uint16_t*>(a.v_pages) +
+                                                 (size_t(en.x) * a.bs + (j & (a.bs - 1))) * D + ch0;
+#pragma unroll
+                            for (int x = 0; x < CW / 2; ++x) {
+                                const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(vg) + x);
+                                if ((w & 0x7f80u) == 0x7f80u) acc[x].f.x += bf16_lo(w);
+                                if ((w & 0x7f800000u) == 0x7f800000u) acc[x].f.y += bf16_hi(w);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                }
+                tc_fence_before_sync();
+                if (sl != s) mbar_arrive(&sh.o_read[sl]);
+                ++acc_n[sl];
+            };
+
+            int added = 0;                                         // tiles whose O is added up
+            for (int i = s; i < ntl; i += 2, ++soft_n) {
+                wait(&sh.s_full[s], soft_n & 1u);
                 __syncwarp();
                 tc_fence_after_sync();
                 const uint32_t info = (tile0 + i) % SH::INFO;
-                bool odd_drafts = false;
                 if (sh.masked[info] != 0) {
                     // Scores of tokens that the row does not see become -infinity.  V rows of tokens
-                    // that nobody sees are zeroed (their memory may hold anything), and so are drafts
-                    // with infinities or NaN, which are added below where they are seen.
-                    const int e0 = ((g.t0 + i) * kTcTile) >> a.bs_shift;
-                    auto tokens8 = [&](int g8, const uint32_t* words, int limit) -> uint32_t {
-                        const int le = (g8 * 8) >> a.bs_shift;
-                        const int first = sh.entry[info][le].y;
-                        if (first == kNoToken) return 0u;
-                        const int tok = first + ((g8 * 8) & (a.bs - 1));
-                        const bool ctx = dense || e0 + le < g.un.n_ctx;
-                        uint32_t bits = 0u;
-                        if (ctx) bits = (1u << min(8, max(0, g.un.len - tok))) - 1u;
-                        if (dense || !ctx) bits |= mask_bits8(words, tok - g.un.len, limit);
-                        return bits;
-                    };
+                    // that nobody sees are zeroed (their memory may hold anything), and so are
+                    // infinities and NaN of drafts, which are added back where they are seen.
                     if (live) {
-                        const uint32_t* words = mask_b != nullptr ? mask_b + (long long)q_row * a.mask_words : nullptr;
-                        const int limit = r_unit < a.R ? (mask_b != nullptr ? a.Q : q_row + 1) : 0;
 #pragma unroll 1
                         for (int c = 0; c < 4; ++c) {
-                            const uint32_t mk = tokens8(8 * h + 2 * c, words, limit) | tokens8(8 * h + 2 * c + 1, words, limit) << 8;
+                            const uint32_t mk = tokens8(i, 8 * h + 2 * c, words, limit) |
+                                                tokens8(i, 8 * h + 2 * c + 1, words, limit) << 8;
                             uint32_t v[16];
                             __syncwarp();
-                            tmem_ld16(s_tm + 64 * h + 16 * c, v);
-                            tmem_wait_ld();
+                            tmem_ld16(s_tm + 16 * c, v);
+                            tmem_wait_ld16(v);
 #pragma unroll
                             for (int j = 0; j < 16; ++j)
                                 if (!((mk >> j) & 1u)) v[j] = 0xff800000u;
-                            tmem_st16(s_tm + 64 * h + 16 * c, v);
+                            tmem_st16(s_tm + 16 * c, v);
                         }
                         tmem_wait_st();
                     }
                     const uint32_t vn = unit0 + 2 * i + 1, vs = vn % SH::UNITS;
                     wait(&sh.full[vs], (vn / SH::UNITS) & 1u);
-                    // this thread looks after token `row`, together with the others that have it
-                    constexpr int CHUNKS = SH::HALVES * 8 / (2 * RT);
-                    const int c0 = (RT == 1 ? h : 2 * s + h) * CHUNKS;
-                    uint32_t* s_bad = sh.bad[RT == 1 ? s : i & 1];
-                    const int bar_id = RT == 1 ? 3 + s : 2, bar_n = RT == 1 ? 256 : 512;
+                    // the slot's two threads of number `row` look after token `row`, half its channels each
+                    constexpr int CHUNKS = SH::HALVES * 4;
                     unsigned char* vrow = smem + SH::OFF_RING + vs * SH::UNIT + row * 128;
-                    if ((RT == 1 || s == 0) && h == 0 && row < 4) s_bad[row] = 0u;
-                    const bool seen = (tokens8(row >> 3, sh.any, a.Q) >> (row & 7)) & 1u;
-                    const int first = sh.entry[info][row >> a.bs_shift].y;
+                    const bool seen = (tokens8(i, row >> 3, sh.any, a.Q) >> (row & 7)) & 1u;
+                    const int first = sh.token[info][row >> a.bs_shift];
                     const bool draft = first != kNoToken && first + (row & (a.bs - 1)) >= g.un.len;
-                    tc_fence_before_sync();
-                    bar_sync(bar_id, bar_n);
-                    if (seen && draft) {
-                        bool odd = false;
-                        for (int c = c0; c < c0 + CHUNKS; ++c) {
-                            const uint4 v = *reinterpret_cast<const uint4*>(vrow + (c >> 3) * SH::HALF + (c & 7) * 16);
-                            const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
+                    if (h == 0 && row < 4) sh.odd[info][row] = 0u;
+                    bar_sync(3 + s, kTcSoft / 2);
+                    bool changed = false;
+                    for (int c = h * CHUNKS; c < (h + 1) * CHUNKS; ++c) {
+                        uint4* at = reinterpret_cast<uint4*>(vrow + (c >> 3) * SH::HALF + (c & 7) * 16);
+                        if (!seen) {
+                            *at = make_uint4(0u, 0u, 0u, 0u);
+                            changed = true;
+                        } else if (draft) {
+                            const uint4 v = *at;
+                            uint32_t w4[4] = {v.x, v.y, v.z, v.w};
+                            bool odd = false;
 #pragma unroll
-                            for (int x = 0; x < 4; ++x)
-                                odd |= (w4[x] & 0x7f800000u) == 0x7f800000u || (w4[x] & 0x7f80u) == 0x7f80u;
+                            for (int x = 0; x < 4; ++x) {
+                                if ((w4[x] & 0x7f800000u) == 0x7f800000u) {
+                                    w4[x] &= 0xffffu;
+                                    odd = true;
+                                }
+                                if ((w4[x] & 0x7f80u) == 0x7f80u) {
+                                    w4[x] &= 0xffff0000u;
+                                    odd = true;
+                                }
+                            }
+                            if (odd) {
+                                *at = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+                                atomicOr(&sh.odd[info][row >> 5], 1u << (row & 31));
+                                changed = true;
+                            }
                         }
-                        if (odd) atomicOr(&s_bad[row >> 5], 1u << (row & 31));
                     }
-                    bar_sync(bar_id, bar_n);
-                    odd_drafts = (s_bad[0] | s_bad[1] | s_bad[2] | s_bad[3]) != 0u;
-                    if (!seen || ((s_bad[row >> 5] >> (row & 31)) & 1u)) {
-                        for (int c = c0; c < c0 + CHUNKS; ++c)
-                            *reinterpret_cast<uint4*>(vrow + (c >> 3) * SH::HALF + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-                        fence_proxy_async_smem();
-                    }
-                    bar_sync(bar_id, bar_n);                       // s_bad is read, every V row is ready
-                    tc_fence_after_sync();
+                    if (changed) fence_proxy_async_smem();
                 }
-                float alpha = 1.f;
+                __syncwarp();
                 if (live) {
                     // ---- the maximum: of half a row, then of both halves ----------------------
+                    uint32_t va[2][16], vb[2][16];
+                    tmem_ld16(s_tm, va[0]);
+                    tmem_ld16(s_tm + 16, va[1]);
+                    tmem_wait_ld16(va[0]);
+                    tmem_wait_ld16(va[1]);
+                    tmem_ld16(s_tm + 32, vb[0]);
+                    tmem_ld16(s_tm + 48, vb[1]);
                     float x0 = -INFINITY, x1 = -INFINITY;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t v[16];
-                        tmem_ld16(s_tm + 64 * h + 16 * c, v);
-                        tmem_wait_ld();
+                    auto top_of = [&](const uint32_t (&v)[16]) {
 #pragma unroll
                         for (int j = 0; j < 16; j += 4) {
                             x0 = max3(x0, __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
                             x1 = max3(x1, __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
                         }
-                    }
-                    // Any reference near the maximum will do, as long as the row's two threads use
-                    // the same one: they exchange it as bf16, rounded up.
-                    const uint32_t top = round_up_bf16(fmaxf(x0, x1) * scale);
-                    sh.top[s][h][row] = uint16_t(top >> 16);
+                    };
+                    top_of(va[0]);
+                    top_of(va[1]);
+                    tmem_wait_ld16(vb[0]);
+                    tmem_wait_ld16(vb[1]);
+                    top_of(vb[0]);
+                    top_of(vb[1]);
+                    // Any reference near the maximum will do, as long as the row's threads use the
+                    // same one: they exchange it as bf16, rounded up.
+                    const uint32_t top = round_up_bf16(fmaxf(x0, x1) * scale), pr = soft_n & 1u;
+                    sh.top[s][pr][h][row] = uint16_t(top >> 16);
                     bar_sync(pair_bar, 64);
-                    const float other = __uint_as_float(uint32_t(sh.top[s][1 - h][row]) << 16);
-                    const float m_new = fmaxf(m_run, fmaxf(__uint_as_float(top), other));
-                    alpha = m_run == -INFINITY ? 0.f : fast_exp2(m_run - m_new);
-                    m_run = m_new;
+                    const float other = __uint_as_float(uint32_t(sh.top[s][pr][1 - h][row]) << 16);
+                    const float m_new = fmaxf(m_soft, fmaxf(__uint_as_float(top), other));
+                    l_run *= m_soft == -INFINITY ? 0.f : fast_exp2(m_soft - m_new);
+                    m_soft = m_new;
                     const float m_sub = m_new == -INFINITY ? 0.f : m_new;      // nothing seen yet: every weight is 0
-                    l_run *= alpha;
-                    if (odd_drafts) {
-                        const uint32_t* s_bad = sh.bad[RT == 1 ? s : i & 1];
-#pragma unroll
-                        for (int d = 0; d < DH / 2; ++d) acc[d] = make_f2(acc[d].f.x * alpha, acc[d].f.y * alpha);
-                        alpha = 1.f;
-#pragma unroll 1
-                        for (int j = 0; j < kTcTile; ++j) {
-                            if (!((s_bad[j >> 5] >> (j & 31)) & 1u)) continue;
-                            const float sj = __uint_as_float(tmem_ld1(s_tm + j));
-                            tmem_wait_ld();
-                            const float p = fast_exp2(fmaf(sj, scale, -m_sub));
-                            const uint4* vg = reinterpret_cast<const uint4*>(
-                                static_cast<const uint16_t*>(a.v_pages) +
-                                (size_t(sh.entry[info][j >> a.bs_shift].x) * a.bs + (j & (a.bs - 1))) * D + h * DH);
-                            if (p != 0.f) {
-#pragma unroll
-                                for (int c = 0; c < DH / 8; ++c) {
-                                    float f[8];
-                                    unpack16<true>(__ldg(vg + c), f);
-#pragma unroll
-                                    for (int x = 0; x < 4; ++x)
-                                        acc[4 * c + x] = fma2(make_f2(p, p), make_f2(f[2 * x], f[2 * x + 1]), acc[4 * c + x]);
-                                }
-                            }
-                            __syncwarp();
-                        }
-                        tc_fence_before_sync();
-                        bar_sync(pair_bar, 64);                    // both have read the row's scores
-                        tc_fence_after_sync();
-                    }
                     // ---- the weights, in three bf16 parts, over the scores' own columns -----------
                     unsigned char* p_row = smem + SH::OFF_P + s * SH::P_TILE + h * SH::HALF + row * 128;
                     const F2 scale2 = make_f2(scale, scale), m2 = make_f2(-m_sub, -m_sub);
                     F2 sum_a = make_f2(0.f, 0.f), sum_b = make_f2(0.f, 0.f);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t v[16];
-                        tmem_ld16(s_tm + 64 * h + 16 * c, v);
-                        tmem_wait_ld();
+                    auto weights = [&](int c, const uint32_t (&v)[16]) {
                         uint32_t hm[16], small[8];
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
@@ -597,12 +644,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             hm[8 + j] = cut_bf16x2(p);
                             small[j] = __byte_perm(__float_as_uint(p.f.x), __float_as_uint(p.f.y), 0x7632);
                         }
-                        tmem_st16(s_tm + 64 * h + 16 * c, hm);
+                        tmem_st16(s_tm + 16 * c, hm);
 #pragma unroll
                         for (int x = 0; x < 2; ++x)
                             *reinterpret_cast<uint4*>(p_row + (((2 * c + x) ^ (row & 7)) << 4)) =
                                 make_uint4(small[4 * x], small[4 * x + 1], small[4 * x + 2], small[4 * x + 3]);
-                    }
+                    };
+                    weights(2, vb[0]);
+                    tmem_ld16(s_tm, va[0]);
+                    weights(3, vb[1]);
+                    tmem_wait_ld16(va[0]);
+                    tmem_ld16(s_tm + 16, va[1]);
+                    weights(0, va[0]);
+                    tmem_wait_ld16(va[1]);
+                    weights(1, va[1]);
                     const F2 sum = add2(sum_a, sum_b);
                     l_run += sum.f.x + sum.f.y;
                     tmem_wait_st();
@@ -610,76 +665,36 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 tc_fence_before_sync();
                 mbar_arrive(&sh.p_ready[s]);
-                wait(&sh.o_full[s], done & 1u);
-                __syncwarp();
-                tc_fence_after_sync();
-                if (live) {
-                    const F2 alpha2 = make_f2(alpha, alpha);
-#pragma unroll
-                    for (int c = 0; c < DH / 16; ++c) {
-                        uint32_t v[16];
-                        tmem_ld16(o_tm + h * DH + 16 * c, v);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            acc[8 * c + j] = fma2(acc[8 * c + j], alpha2,
-                                                  make_f2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])));
-                    }
-                    tc_fence_before_sync();
-                }
+                for (; added <= i; ++added) add_up(added);         // the other slot's last tile, then this one
             }
+            for (; added < ntl; ++added) add_up(added);
 
             // ---- the part's (m, l, o): the output itself, or a partial -------------------------
-            // The halves' sums meet through the query tiles, the rows leave through the P tiles and the
-            // ring (all idle now): with one row tile the odd tiles' rows join the even tiles' on the
-            // way; then whole rows go out, a warp 512 bytes at a time.
+            // The four threads' sums meet through the query tile, the rows leave through the P tiles
+            // (both idle now), a warp 512 bytes at a time.
             const bool complete = g.t0 == 0 && g.t1 == g.tiles;
             constexpr int V4 = D / 4;
-            float2* x_ml = reinterpret_cast<float2*>(smem);                    // [slot][half][row]
+            float* x_l = reinterpret_cast<float*>(smem);                       // [slot][half][row]
             float4* x_rows = reinterpret_cast<float4*>(smem + SH::OFF_P);
-            const int x_row = RT == 2 ? s * 128 + row : row;
             auto cell = [&](int r, int c) -> float4& { return x_rows[r * V4 + ((c + r) & (V4 - 1))]; };
+            if (live) l_run = m_soft == -INFINITY ? 0.f : l_run * fast_exp2(m_soft - m_acc);
             tree_sync<kTcSoft>();
-            x_ml[(2 * s + h) * 128 + row] = make_float2(m_run, l_run);
-            if (RT == 1 && s == 1 && live) {
-#pragma unroll
-                for (int c = 0; c < DH / 4; ++c)
-                    cell(x_row, h * (DH / 4) + c) =
-                        make_float4(acc[2 * c].f.x, acc[2 * c].f.y, acc[2 * c + 1].f.x, acc[2 * c + 1].f.y);
-            }
+            x_l[(2 * s + h) * 128 + row] = l_run;
             tree_sync<kTcSoft>();
-            if ((RT == 2 || s == 0) && live) {
-                l_run += x_ml[(2 * s + 1 - h) * 128 + row].y;
-                float w0 = 1.f, w1 = 0.f;
-                if (RT == 1) {
-                    const float2 ml = x_ml[256 + row];
-                    const float m_new = fmaxf(m_run, ml.x);
-                    w0 = m_run == -INFINITY ? 0.f : fast_exp2(m_run - m_new);
-                    w1 = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - m_new);
-                    l_run = l_run * w0 + (ml.y + x_ml[384 + row].y) * w1;
-                    m_run = m_new;
-                }
+            if (live) {
+                l_run = (x_l[row] + x_l[128 + row]) + (x_l[256 + row] + x_l[384 + row]);
+                float inv = 1.f;
                 if (complete) {
-                    const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
-                    w0 *= inv;
-                    w1 *= inv;
-                } else if (h == 0 && r_unit < a.R) {
-                    const long long slot =
-                        (long long)tree_slot(blockIdx.x, part.per, g.start) * a.item_rows + r_unit - g.row0;
-                    a.part_m[slot] = m_run;
+                    inv = l_run == 0.f ? 0.f : 1.f / l_run;
+                } else if (s == 0 && h == 0 && r_unit < a.R) {
+                    const long long slot = (long long)tree_slot(blockIdx.x, part.per, g.start) * a.item_rows + row;
+                    a.part_m[slot] = m_acc;
                     a.part_l[slot] = l_run;
                 }
 #pragma unroll
-                for (int c = 0; c < DH / 4; ++c) {
-                    float4& x = cell(x_row, h * (DH / 4) + c);
-                    float4 o = make_float4(acc[2 * c].f.x * w0, acc[2 * c].f.y * w0, acc[2 * c + 1].f.x * w0,
-                                           acc[2 * c + 1].f.y * w0);
-                    if (RT == 1) {
-                        const float4 y = x;
-                        o = make_float4(fmaf(y.x, w1, o.x), fmaf(y.y, w1, o.y), fmaf(y.z, w1, o.z), fmaf(y.w, w1, o.w));
-                    }
-                    x = o;
-                }
+                for (int c = 0; c < CW / 4; ++c)
+                    cell(row, ch0 / 4 + c) = make_float4(acc[2 * c].f.x * inv, acc[2 * c].f.y * inv, acc[2 * c + 1].f.x * inv,
+                                                         acc[2 * c + 1].f.y * inv);
             }
             tree_sync<kTcSoft>();
             {
@@ -695,8 +710,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             if (!complete)
                 tree_arrive_and_merge<kTcSoft>(a, g.item, g.start, g.tiles, part.per, &sh.last,
-                                               reinterpret_cast<float*>(smem + SH::OFF_P),
-                                               (2 * SH::P_TILE + SH::UNITS * SH::UNIT) / 4);
+                                               reinterpret_cast<float*>(smem + SH::OFF_P), 2 * SH::P_TILE / 4);
             tree_sync<kTcSoft>();                                  // this memory is free for the next item
             unit0 += 2 * ntl;
             tile0 += ntl;
@@ -739,13 +753,13 @@ inline cudaError_t encode_tree_map(CUtensorMap* map, const void* pool, int D, in
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int D, int RT>
+template <int D>
 cudaError_t launch_tc_t(const TreeArgs& a, cudaStream_t s)
 {
     static std::atomic<unsigned long long> configured{0};   // devices set up
     const cudaError_t cfg = once_per_device(configured, [&]() -> cudaError_t {
-        return cudaFuncSetAttribute(tree_tc_kernel<D, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    int(tc_smem<D, RT>()));
+        return cudaFuncSetAttribute(tree_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    int(tc_smem<D>()));
     });
     if (cfg != cudaSuccess) return cfg;
     CUtensorMap kmap, vmap;
@@ -755,7 +769,7 @@ cudaError_t launch_tc_t(const TreeArgs& a, cudaStream_t s)
     e = encode_tree_map(&vmap, a.v_pages, D, a.bs, tiles);
     if (e != cudaSuccess) return e;
     const int ctas = num_sms() < kTreeMaxCtas ? num_sms() : kTreeMaxCtas;
-    return launch_after_previous(tree_tc_kernel<D, RT>, dim3(unsigned(ctas)), dim3(kTcThreads), tc_smem<D, RT>(), s, a,
+    return launch_after_previous(tree_tc_kernel<D>, dim3(unsigned(ctas)), dim3(kTcThreads), tc_smem<D>(), s, a,
                                  kmap, vmap);
 }
 
@@ -764,11 +778,11 @@ cudaError_t launch_tc_t(const TreeArgs& a, cudaStream_t s)
 cudaError_t launch_tree_tc(TreeArgs a, cudaStream_t s)
 {
     a.tile = kTcTile;
-    a.item_rows = a.R <= 16 ? 16 : (a.R <= 64 ? 64 : (a.R <= 128 ? 128 : 256));
+    a.item_rows = tree_item_rows(a.R);
     a.row_groups = (a.R + a.item_rows - 1) / a.item_rows;
     a.min_per = 2;
-    if (a.R <= 128) return a.D == 128 ? launch_tc_t<128, 1>(a, s) : launch_tc_t<64, 1>(a, s);
-    return a.D == 128 ? launch_tc_t<128, 2>(a, s) : launch_tc_t<64, 2>(a, s);
+    a.whole_slack = 7;
+    return a.D == 128 ? launch_tc_t<128>(a, s) : launch_tc_t<64>(a, s);
 }
 
 }  // namespace sa
