@@ -357,64 +357,100 @@ def sparse_attn_get_device_error(ws, stream=None) -> int:
 
 
 # ------------------------------- growing the cache, verifying drafted tokens --
+# These calls are a few microseconds on the device, so their host side is kept short: one
+# lookup for what the parameters say about shapes, one comparison per property of a tensor.
 
-def _device_ptr(t: Optional[torch.Tensor], device: torch.device, what: str, shape=None, dtype=None):
-    """Pointer of a contiguous tensor on `device`, of that shape and dtype where given; None
-    stays None."""
-    if t is None:
-        return None
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{what}: expected a CUDA tensor on {device}, got {t.device}")
+class _Shapes:
+    """What a problem's parameters say about its tensors."""
+
+    def __init__(self, p):
+        dtypes = {BF16: torch.bfloat16, F32: torch.float32}
+        nb_cap = meta_rows(p)[0]
+        n = max(1, p.num_queries)
+        self.q_dtype, self.kv_dtype = dtypes[p.q_dtype], dtypes[p.kv_dtype]
+        self.q_heads, self.kv_heads, self.dim, self.drafts = p.num_q_heads, p.num_kv_heads, p.head_dim, n
+        self.pool = (p.num_pages, p.num_kv_heads, p.block_size, p.head_dim)
+        self.table = (p.batch, nb_cap)
+        self.box = (p.batch, p.num_kv_heads, nb_cap, p.head_dim)
+        self.per_seq, self.ends, self.per_unit = (p.batch,), (p.batch + 1,), (p.batch, p.num_kv_heads)
+        self.out = (p.batch, n, p.num_q_heads, p.head_dim)
+        self.out_one = (p.batch, p.num_q_heads, p.head_dim) if n == 1 else self.out
+        self.mask = (p.batch, n, -(-n // 32))
+        one = sparse_attn_params.from_buffer_copy(p)
+        one.num_queries = 1                          # the stride does not depend on the number of queries
+        self.sel = (p.batch, p.num_kv_heads, int(lib().sparse_attn_sel_stride(C.byref(one))))
+
+
+_shapes_of = {}
+
+
+def _shapes(p) -> _Shapes:
+    key = bytes(p)
+    s = _shapes_of.get(key)
+    if s is None:
+        if len(_shapes_of) >= 256:                   # a growing context passes through many parameter sets
+            _shapes_of.clear()
+        s = _shapes_of[key] = _Shapes(p)
+    return s
+
+
+_I32 = torch.int32
+
+
+def _tensor_ptr(t: torch.Tensor, device: int, what: str, shape, dtype) -> int:
+    """Pointer of a contiguous tensor of that shape and dtype on CUDA device `device`."""
+    if t.get_device() != device:
+        raise ValueError(f"{what}: expected a CUDA tensor on cuda:{device}, got {t.device}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{what}: expected a contiguous tensor")
-    if dtype is not None and t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
-        raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     return t.data_ptr()
 
 
-def _rows_ptr(t: torch.Tensor, device: torch.device, what: str, heads: int, dim: int, dtype):
+def _rows_ptr(t: torch.Tensor, device: int, what: str, shape, dtype):
     """Pointer and row stride of [rows, heads, dim] whose rows may be strided."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{what}: expected [rows, {heads}, {dim}], got {tuple(t.shape)}")
-    if t.device != device or not t.is_cuda or t.dtype != dtype:
-        raise ValueError(f"{what}: expected a {dtype} CUDA tensor on {device}")
+    if t.shape != shape:
+        raise ValueError(f"{what}: expected [rows, heads, dim] = {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != device or t.dtype is not dtype:
+        raise ValueError(f"{what}: expected a {dtype} CUDA tensor on cuda:{device}, got {t.dtype} on {t.device}")
+    rows, heads, dim = shape
     s0, s1, s2 = t.stride()
-    if t.shape[0] > 0 and (s2 != 1 or (heads > 1 and s1 != dim)):
+    if rows > 0 and (s2 != 1 or (heads > 1 and s1 != dim)):
         raise ValueError(f"{what}: the heads of a row must be contiguous")
-    return t.data_ptr(), max(s0, heads * dim) if t.shape[0] <= 1 else s0
+    return t.data_ptr(), s0 if rows > 1 else heads * dim
 
 
-def _torch_dtypes(p):
-    of = {BF16: torch.bfloat16, F32: torch.float32}
-    return of[p.q_dtype], of[p.kv_dtype]
+def _device_of(t: torch.Tensor, what: str) -> int:
+    device = t.get_device()
+    if device < 0:
+        raise ValueError(f"{what}: expected a CUDA tensor (the library takes device pointers)")
+    return device
 
 
-def _cache_ptrs(p, device, k_pages, v_pages, block_table, kmin=None, kmax=None):
-    """Pointers of the page pools, the page table and the key box, their shapes checked."""
-    kvt = _torch_dtypes(p)[1]
-    pool = (p.num_pages, p.num_kv_heads, p.block_size, p.head_dim)
-    nb_cap = meta_rows(p)[0]
-    box = (p.batch, p.num_kv_heads, nb_cap, p.head_dim)
-    return (_device_ptr(k_pages, device, "k_pages", pool, kvt), _device_ptr(v_pages, device, "v_pages", pool, kvt),
-            _device_ptr(block_table, device, "block_table", (p.batch, nb_cap), torch.int32),
-            _device_ptr(kmin, device, "kmin", box, kvt), _device_ptr(kmax, device, "kmax", box, kvt))
+def _workspace(ws: torch.Tensor, device: int):
+    if ws.get_device() != device or not ws.is_contiguous():
+        raise ValueError(f"ws: expected a contiguous CUDA tensor on cuda:{device}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
-def _launch_on(device: torch.device, fn: str, stream, *args) -> None:
-    """Calls `fn` with the device of its tensors current, on `stream` or that device's
-    current stream."""
+def _launch_on(device: int, name: str, stream, *args) -> None:
+    """Calls the entry point with the device of its tensors current, on `stream` or that
+    device's current stream."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    s = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-    if torch.cuda.current_device() == device.index:
-        status = getattr(lib(), fn)(*args, s)
+        stream = torch._C._cuda_getCurrentRawStream(device)
+    elif isinstance(stream, torch.cuda.Stream):
+        stream = stream.cuda_stream
+    fn = getattr(_lib or lib(), name)
+    if torch._C._cuda_getDevice() == device:
+        status = fn(*args, int(stream))
     else:
         with torch.cuda.device(device):
-            status = getattr(lib(), fn)(*args, s)
+            status = fn(*args, int(stream))
     if status != OK:
-        raise SparseAttnError(fn, status)
+        raise SparseAttnError(name, status)
 
 
 def sparse_attn_append_kv(p, q_new, k_new, v_new, inv_freq, q_out, k_pages, v_pages, block_table, ws,
@@ -423,25 +459,26 @@ def sparse_attn_append_kv(p, q_new, k_new, v_new, inv_freq, q_out, k_pages, v_pa
     """Append rows of new tokens to the cache: q_new [rows, Hq, D] (or None), k_new and v_new
     [rows, Hkv, D], rows possibly strided (slices of one projection); inv_freq float64
     [rotary_dim / 2] or None for no rotation; q_out [rows, Hq, D]."""
-    dev, (qt, _) = k_new.device, _torch_dtypes(p)
-    rows, hkv, dim = k_new.shape[0], p.num_kv_heads, p.head_dim
-    k, ks = _rows_ptr(k_new, dev, "k_new", hkv, dim, qt)
-    v, vs = _rows_ptr(v_new, dev, "v_new", hkv, dim, qt)
-    q, qs = (None, 0) if q_new is None else _rows_ptr(q_new, dev, "q_new", p.num_q_heads, dim, qt)
-    if v_new.shape[0] != rows or (q_new is not None and q_new.shape[0] != rows):
-        raise ValueError("q_new, k_new and v_new must have the same number of rows")
-    kp, vp, bt, lo, hi = _cache_ptrs(p, dev, k_pages, v_pages, block_table, kmin, kmax)
-    i32 = torch.int32
-    if inv_freq is not None and inv_freq.dim() != 1:
-        raise ValueError("inv_freq: expected [rotary_dim / 2]")
+    g, dev, rows = _shapes(p), _device_of(k_new, "k_new"), k_new.shape[0]
+    kv_rows, q_rows, qt, kvt = (rows, g.kv_heads, g.dim), (rows, g.q_heads, g.dim), g.q_dtype, g.kv_dtype
+    k, ks = _rows_ptr(k_new, dev, "k_new", kv_rows, qt)
+    v, vs = _rows_ptr(v_new, dev, "v_new", kv_rows, qt)
+    q, qs = (None, 0) if q_new is None else _rows_ptr(q_new, dev, "q_new", q_rows, qt)
+    rotary, freq = 0, None
+    if inv_freq is not None:
+        rotary = 2 * inv_freq.numel()
+        freq = _tensor_ptr(inv_freq, dev, "inv_freq", (rotary // 2,), torch.float64)
+    w, n = _workspace(ws, dev)
     _launch_on(dev, "sparse_attn_append_kv", stream, C.byref(p), rows,
-               _device_ptr(cu_rows, dev, "cu_rows", (p.batch + 1,), i32),
-               _device_ptr(seq_lens, dev, "seq_lens", (p.batch,), i32),
-               _device_ptr(positions, dev, "positions", (rows,), i32),
-               0 if inv_freq is None else 2 * inv_freq.shape[0], int(pairing),
-               _device_ptr(inv_freq, dev, "inv_freq", None, torch.float64), q, qs, k, ks, v, vs,
-               _device_ptr(q_out, dev, "q_out", (rows, p.num_q_heads, dim), qt), kp, vp, bt, lo, hi,
-               _device_ptr(ws, dev, "ws"), ws.numel() * ws.element_size())
+               None if cu_rows is None else _tensor_ptr(cu_rows, dev, "cu_rows", g.ends, _I32),
+               None if seq_lens is None else _tensor_ptr(seq_lens, dev, "seq_lens", g.per_seq, _I32),
+               None if positions is None else _tensor_ptr(positions, dev, "positions", (rows,), _I32),
+               rotary, pairing, freq, q, qs, k, ks, v, vs,
+               None if q_out is None else _tensor_ptr(q_out, dev, "q_out", q_rows, qt),
+               _tensor_ptr(k_pages, dev, "k_pages", g.pool, kvt), _tensor_ptr(v_pages, dev, "v_pages", g.pool, kvt),
+               _tensor_ptr(block_table, dev, "block_table", g.table, _I32),
+               None if kmin is None else _tensor_ptr(kmin, dev, "kmin", g.box, kvt),
+               None if kmax is None else _tensor_ptr(kmax, dev, "kmax", g.box, kvt), w, n)
 
 
 def sparse_attn_tree_workspace_size(p: sparse_attn_params) -> int:
@@ -454,37 +491,36 @@ def sparse_attn_tree_decode(p, q, k_pages, v_pages, block_table, out, ws, seq_le
                             sel_count=None, tree_mask=None, stream=None) -> None:
     """Attention of Q = max(1, p.num_queries) drafts per sequence; q and out [B, Q, Hq, D] (or
     [B, Hq, D] for one), tree_mask 32-bit words [B, Q, ceil(Q / 32)]."""
-    dev, (qt, _) = q.device, _torch_dtypes(p)
-    n = max(1, p.num_queries)
-    shape = (p.batch, n, p.num_q_heads, p.head_dim)
-    if n == 1 and q.dim() == 3:
-        shape = (p.batch, p.num_q_heads, p.head_dim)
-    kp, vp, bt, _, _ = _cache_ptrs(p, dev, k_pages, v_pages, block_table)
-    i32 = torch.int32
-    sel = None
-    if sel_ids is not None:        # the stride does not depend on the number of queries
-        one = sparse_attn_params.from_buffer_copy(p)
-        one.num_queries = 1
-        sel = (p.batch, p.num_kv_heads, sparse_attn_sel_stride(one))
-    _launch_on(dev, "sparse_attn_tree_decode", stream, C.byref(p), _device_ptr(q, dev, "q", shape, qt), kp, vp, bt,
-               _device_ptr(seq_lens, dev, "seq_lens", (p.batch,), i32), _device_ptr(sel_ids, dev, "sel_ids", sel, i32),
-               _device_ptr(sel_count, dev, "sel_count", (p.batch, p.num_kv_heads), i32),
-               _device_ptr(tree_mask, dev, "tree_mask", (p.batch, n, -(-n // 32)), (torch.int32, torch.uint32)),
-               _device_ptr(out, dev, "out", shape, torch.float32), _device_ptr(ws, dev, "ws"),
-               ws.numel() * ws.element_size())
+    g, dev = _shapes(p), _device_of(q, "q")
+    shape = g.out if q.dim() == 4 else g.out_one
+    w, n = _workspace(ws, dev)
+    _launch_on(dev, "sparse_attn_tree_decode", stream, C.byref(p), _tensor_ptr(q, dev, "q", shape, g.q_dtype),
+               _tensor_ptr(k_pages, dev, "k_pages", g.pool, g.kv_dtype),
+               _tensor_ptr(v_pages, dev, "v_pages", g.pool, g.kv_dtype),
+               _tensor_ptr(block_table, dev, "block_table", g.table, _I32),
+               None if seq_lens is None else _tensor_ptr(seq_lens, dev, "seq_lens", g.per_seq, _I32),
+               None if sel_ids is None else _tensor_ptr(sel_ids, dev, "sel_ids", g.sel, _I32),
+               None if sel_count is None else _tensor_ptr(sel_count, dev, "sel_count", g.per_unit, _I32),
+               None if tree_mask is None else _tensor_ptr(
+                   tree_mask, dev, "tree_mask", g.mask, torch.uint32 if tree_mask.dtype is torch.uint32 else _I32),
+               _tensor_ptr(out, dev, "out", shape, torch.float32), w, n)
 
 
 def sparse_attn_commit_drafts(p, path, path_len, k_pages, v_pages, block_table, new_lens, ws, seq_lens=None,
                               kmin=None, kmax=None, stream=None) -> None:
     """Move the accepted drafts path [B, stride] (path_len [B] of them) to the end of the
     context; new_lens [B] gets the new lengths."""
-    dev, i32 = path.device, torch.int32
+    g, dev = _shapes(p), _device_of(path, "path")
     if path.dim() != 2:
         raise ValueError("path: expected [B, stride]")
-    kp, vp, bt, lo, hi = _cache_ptrs(p, dev, k_pages, v_pages, block_table, kmin, kmax)
+    stride, kvt = path.shape[1], g.kv_dtype
+    w, n = _workspace(ws, dev)
     _launch_on(dev, "sparse_attn_commit_drafts", stream, C.byref(p),
-               _device_ptr(seq_lens, dev, "seq_lens", (p.batch,), i32),
-               _device_ptr(path, dev, "path", (p.batch, path.shape[1]), i32), path.shape[1],
-               _device_ptr(path_len, dev, "path_len", (p.batch,), i32), kp, vp, bt, lo, hi,
-               _device_ptr(new_lens, dev, "new_lens", (p.batch,), i32), _device_ptr(ws, dev, "ws"),
-               ws.numel() * ws.element_size())
+               None if seq_lens is None else _tensor_ptr(seq_lens, dev, "seq_lens", g.per_seq, _I32),
+               _tensor_ptr(path, dev, "path", g.per_seq + (stride,), _I32), stride,
+               _tensor_ptr(path_len, dev, "path_len", g.per_seq, _I32),
+               _tensor_ptr(k_pages, dev, "k_pages", g.pool, kvt), _tensor_ptr(v_pages, dev, "v_pages", g.pool, kvt),
+               _tensor_ptr(block_table, dev, "block_table", g.table, _I32),
+               None if kmin is None else _tensor_ptr(kmin, dev, "kmin", g.box, kvt),
+               None if kmax is None else _tensor_ptr(kmax, dev, "kmax", g.box, kvt),
+               _tensor_ptr(new_lens, dev, "new_lens", g.per_seq, _I32), w, n)
