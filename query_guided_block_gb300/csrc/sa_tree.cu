@@ -23,7 +23,8 @@ namespace {
 
 constexpr int kTrThreads = 128;
 constexpr int kTrTile = 64;
-constexpr int kTrEntries = 1024;     // list entries resolved at a time
+constexpr int kTrEntries = 512;      // list entries resolved at a time
+constexpr int kTrInfo = 4;           // tiles looked up ahead of their copies, at least the stages + 1
 
 __device__ __forceinline__ void mma_tf32_1688(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
@@ -91,6 +92,9 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
 
     extern __shared__ __align__(128) unsigned char smem_raw[];
     __shared__ int2 s_ent[kTrEntries];
+    __shared__ long long s_src[kTrInfo][kTrTile];           // a tile's token rows in the pools, -1: none
+    __shared__ uint32_t s_part[kTrInfo][2];                 // a tile's halves: 1 not only context tokens, 2 drafts
+    __shared__ uint32_t s_see[ROWS][2];                     // tokens of the tile that a row sees
     __shared__ uint32_t s_any[kTreeMaxDrafts / 32];         // drafts that some query sees
     __shared__ long long s_scan[kTreeScan<kTrThreads>];
     __shared__ int s_last;
@@ -98,7 +102,7 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g4 = lane >> 2, t4 = lane & 3;
-    const int wr = RW == 1 ? 0 : warp, wt = RW == 1 ? warp : 0;    // the warp's rows / tokens
+    const int wr = warp % RW, wt = warp / RW;                      // the warp's rows / tokens
     unsigned char* smem = smem_raw + ((128u - (smem_u32(smem_raw) & 127u)) & 127u);
     const uint32_t base = smem_u32(smem);
     float* s_q = reinterpret_cast<float*>(smem + SH::STAGES * SH::STAGE);   // fp32 K/V: [ROWS][Q_ROW]
@@ -125,32 +129,33 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
         const uint32_t* mask_b = a.mask != nullptr ? a.mask + (long long)b * a.Q * a.mask_words : nullptr;
 
         __syncthreads();                                     // the previous item is done with shared memory
-        for (int w = tid; w < a.mask_words; w += kTrThreads) {
-            uint32_t m = 0u;
-            if (mask_b == nullptr) m = ~0u;
-            else
-                for (int i = 0; i < a.Q; ++i) m |= mask_b[(long long)i * a.mask_words + w];
-            s_any[w] = m;
+        const long long list = dense ? un.len : (long long)un.n_ctx << a.bs_shift;
+        if ((long long)t1 * kTrTile > list) {                // this part meets drafts
+            if (tid < a.mask_words) s_any[tid] = mask_b == nullptr ? ~0u : 0u;
+            __syncthreads();
+            if (mask_b != nullptr)
+                for (int i = tid; i < a.Q * a.mask_words; i += kTrThreads) atomicOr(&s_any[i % a.mask_words], mask_b[i]);
         }
 
         // ---- the queries: A fragments in registers, or fp32 rows in shared memory -------
         const int r_lo = row0 + wr * 16 + g4, r_hi = r_lo + 8;
         uint32_t qa[KB ? NQ : 1][KB ? D / 16 : 1][4];
         if constexpr (KB) {
+            const size_t at_lo = r_lo < a.R ? size_t(tree_out_row(a, b, kvh, r_lo)) * D + 2 * t4 : 0;
+            const size_t at_hi = r_hi < a.R ? size_t(tree_out_row(a, b, kvh, r_hi)) * D + 2 * t4 : 0;
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
                 for (int hc = 0; hc < 4; ++hc) {             // a0, a1: k 0-7 of rows lo, hi; a2, a3: k 8-15
-                    const int r = (hc & 1) ? r_hi : r_lo;
-                    float f0 = 0.f, f1 = 0.f;
-                    if (r < a.R) {
-                        const size_t at = size_t(tree_out_row(a, b, kvh, r)) * D + ks * 16 + (hc >> 1) * 8 + 2 * t4;
-                        f0 = load_q(a.q, at, a.q_bf16 != 0);
-                        f1 = load_q(a.q, at + 1, a.q_bf16 != 0);
-                    }
+                    const bool have = ((hc & 1) ? r_hi : r_lo) < a.R;
+                    const size_t at = ((hc & 1) ? at_hi : at_lo) + ks * 16 + (hc >> 1) * 8;
+                    if constexpr (NQ == 1) {
+                        qa[0][ks][hc] = have ? __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) + at)) : 0u;
+                    } else {
+                        float2 f = have ? __ldg(reinterpret_cast<const float2*>(static_cast<const float*>(a.q) + at))
+                                        : make_float2(0.f, 0.f);
 #pragma unroll
-                    for (int part_q = 0; part_q < NQ; ++part_q) {
-                        qa[part_q][ks][hc] = cut_bf16x2(f0, f1);
+                        for (int part_q = 0; part_q < NQ; ++part_q) qa[part_q][ks][hc] = cut_bf16x2(f.x, f.y);
                     }
                 }
         } else {
@@ -175,42 +180,36 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
             for (int e = e0 + tid; e < e1; e += kTrThreads) s_ent[e - e0] = tree_entry(a, u, un, e);
             __syncthreads();
 
-            // 1: context token, 2: draft that some query sees, 0: neither
-            auto token_kind = [&](int gi, int& draft) -> int {
-                const int e = gi >> a.bs_shift;
-                if (e >= e1) return 0;
-                const int2 en = s_ent[e - e0];
-                const int tok = en.y + (gi & (a.bs - 1));
-                draft = tok - un.len;
-                if (en.x < 0) return 0;
-                if (draft < 0) return (dense || e < un.n_ctx) ? 1 : 0;
-                if (draft >= a.Q || !(dense || e >= un.n_ctx)) return 0;
-                return ((s_any[draft >> 5] >> (draft & 31)) & 1u) ? 2 : 0;
+            // Where the rows of a tile's tokens are, by two warps a tile: tokens that nobody sees get
+            // no row (their memory may hold anything).
+            auto look_up = [&](int tile, int tr) {
+                const int p = tile * kTrTile + tr, e = p >> a.bs_shift;
+                const int2 en = e < e1 ? s_ent[e - e0] : make_int2(-1, 0);
+                const int tok = en.y + (p & (a.bs - 1)), draft = tok - un.len;
+                const bool in_ctx = en.x >= 0 && draft < 0 && (dense || e < un.n_ctx);
+                const bool is_draft = en.x >= 0 && draft >= 0 && draft < a.Q && (dense || e >= un.n_ctx);
+                const bool row = in_ctx || (is_draft && ((s_any[draft >> 5] >> (draft & 31)) & 1u));
+                s_src[tile % kTrInfo][tr] = row ? (long long)en.x * a.bs + (p & (a.bs - 1)) : -1;
+                const uint32_t part_of = __any_sync(kFullMask, !in_ctx) | (__any_sync(kFullMask, is_draft) << 1);
+                if ((tr & 31) == 0) s_part[tile % kTrInfo][tr >> 5] = part_of;
             };
-            auto sees = [&](int r, int draft) -> bool {      // unit row r, a draft in [0, Q)
-                if (r >= a.R) return false;
-                const int t = r / a.G;
-                if (mask_b == nullptr) return draft <= t;
-                return (__ldg(mask_b + (long long)t * a.mask_words + (draft >> 5)) >> (draft & 31)) & 1u;
-            };
-            const char* kp = static_cast<const char*>(a.k_pages);
-            const char* vp = static_cast<const char*>(a.v_pages);
             const int cp_c = tid % SH::CPR, cp_r = tid / SH::CPR;
+            const char* kp = static_cast<const char*>(a.k_pages) + cp_c * 16;
+            const char* vp = static_cast<const char*>(a.v_pages) + cp_c * 16;
             auto issue_tile = [&](int tile, int st) {
                 const uint32_t kd = base + uint32_t(st) * SH::STAGE, vd = kd + SH::TENSOR;
 #pragma unroll
                 for (int i = 0; i < CPT; ++i) {
                     const int tr = cp_r + i * (kTrThreads / SH::CPR);
-                    const int gi = tile * kTrTile + tr;
-                    int draft;
-                    const bool ok = token_kind(gi, draft) != 0;
-                    const size_t off =
-                        ok ? (size_t(s_ent[(gi >> a.bs_shift) - e0].x) * a.bs + (gi & (a.bs - 1))) * SH::ROW + cp_c * 16 : 0;
-                    cp_async_16_zfill(kd + SH::at(tr, cp_c), kp + off, ok ? 16u : 0u);
-                    cp_async_16_zfill(vd + SH::at(tr, cp_c), vp + off, ok ? 16u : 0u);
+                    const long long src = s_src[tile % kTrInfo][tr];
+                    const size_t off = src < 0 ? 0 : size_t(src) * SH::ROW;
+                    cp_async_16_zfill(kd + SH::at(tr, cp_c), kp + off, src < 0 ? 0u : 16u);
+                    cp_async_16_zfill(vd + SH::at(tr, cp_c), vp + off, src < 0 ? 0u : 16u);
                 }
             };
-#pragma unroll
+            for (int kk = tid >> 6; kk < SH::STAGES; kk += 2) look_up(ca + kk, tid & 63);
+            __syncthreads();
+#pragma unroll 1
             for (int kk = 0; kk < SH::STAGES - 1; ++kk) {
                 if (ca + kk < cb) issue_tile(ca + kk, kk);
                 cp_async_commit();
@@ -222,22 +221,29 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
                 __syncthreads();          // tile k is staged; stage k - 1 is free
                 if (tile + SH::STAGES - 1 < cb) issue_tile(tile + SH::STAGES - 1, (k + SH::STAGES - 1) % SH::STAGES);
                 cp_async_commit();
+                if (tid < kTrTile) look_up(tile + SH::STAGES, tid);
                 unsigned char* stage = smem + (k % SH::STAGES) * SH::STAGE;
                 const uint32_t kst = base + uint32_t(k % SH::STAGES) * SH::STAGE, vst = kst + SH::TENSOR;
-
-                // does the tile hold anything but context tokens, and drafts?
-                bool whole = true, drafts = false;
-                for (int p = tile * kTrTile; p < (tile + 1) * kTrTile; p += min(a.bs, kTrTile)) {
-                    const int e = p >> a.bs_shift;
-                    if (e >= e1) {
-                        whole = false;
-                        break;
+                const uint32_t parts = s_part[tile % kTrInfo][0] | s_part[tile % kTrInfo][1];
+                const bool whole = (parts & 1u) == 0u, drafts = (parts & 2u) != 0u;
+                if (!whole) {
+                    for (int i = tid; i < ROWS * 2; i += kTrThreads) {
+                        const int r = row0 + (i >> 1), t = r / a.G;
+                        uint32_t bits = 0u;
+#pragma unroll 1
+                        for (int x = 0; x < 4; ++x) {
+                            const int p = tile * kTrTile + 32 * (i & 1) + 8 * x, e = p >> a.bs_shift;
+                            const int2 en = e < e1 ? s_ent[e - e0] : make_int2(-1, 0);
+                            bits |= tree_tokens8(a, un, p, e, en.x < 0 ? kNoToken : en.y,
+                                                 mask_b != nullptr && r < a.R ? mask_b + (long long)t * a.mask_words : nullptr,
+                                                 r >= a.R ? 0 : (mask_b != nullptr ? a.Q : t + 1))
+                                    << (8 * x);
+                        }
+                        s_see[i >> 1][i & 1] = bits;
                     }
-                    const int2 en = s_ent[e - e0];
-                    const int end = en.y + a.bs;
-                    if (en.x < 0 || end > un.len || !(dense || e < un.n_ctx)) whole = false;
-                    if (en.x >= 0 && end > un.len && (dense || e >= un.n_ctx)) drafts = true;
+                    __syncthreads();
                 }
+
                 // A draft's V may hold infinities or NaN that other queries must not meet as
                 // 0 * inf: such rows are taken out of the product and added where they are seen.
                 uint32_t bad0 = 0u, bad1 = 0u;
@@ -323,17 +329,22 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
                 }
                 // ---- scale, mask, running maximum and sum ---------------------------------
                 float mx[2] = {-INFINITY, -INFINITY};
+                uint32_t see[2][(NT + 3) / 4];               // this warp's tokens, rows lo and hi
+#pragma unroll
+                for (int w = 0; w < (NT + 3) / 4; ++w) see[0][w] = see[1][w] = ~0u;
+                if (!whole) {
+#pragma unroll
+                    for (int w = 0; w < (NT + 3) / 4; ++w) {
+                        see[0][w] = s_see[wr * 16 + g4][(tok0 >> 5) + w] >> (tok0 & 31);
+                        see[1][w] = s_see[wr * 16 + g4 + 8][(tok0 >> 5) + w] >> (tok0 & 31);
+                    }
+                }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        bool ok0 = true, ok1 = true;
-                        if (!whole) {
-                            int draft;
-                            const int kind = token_kind(tile * kTrTile + tok0 + nt * 8 + 2 * t4 + e, draft);
-                            ok0 = kind == 1 || (kind == 2 && sees(r_lo, draft));
-                            ok1 = kind == 1 || (kind == 2 && sees(r_hi, draft));
-                        }
+                        const bool ok0 = (see[0][nt / 4] >> ((nt & 3) * 8 + 2 * t4 + e)) & 1u;
+                        const bool ok1 = (see[1][nt / 4] >> ((nt & 3) * 8 + 2 * t4 + e)) & 1u;
                         c[nt][e] = ok0 ? c[nt][e] : -INFINITY;
                         c[nt][e + 2] = ok1 ? c[nt][e + 2] : -INFINITY;
                         mx[0] = fmaxf(mx[0], c[nt][e]);
@@ -426,14 +437,13 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
                 if (bad0 | bad1) {                           // rows taken out above
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
+#pragma unroll 1
                         for (int x = 0; x < 8; ++x) {
                             const int tr = tok0 + nt * 8 + x;
                             if (!(((tr < 32 ? bad0 : bad1) >> (tr & 31)) & 1u)) continue;
-                            const float p0 = __shfl_sync(kFullMask, c[nt][x & 1], (lane & ~3) | (x >> 1));
-                            const float p1 = __shfl_sync(kFullMask, c[nt][2 + (x & 1)], (lane & ~3) | (x >> 1));
-                            const int gi = tile * kTrTile + tr;
-                            const size_t at = (size_t(s_ent[(gi >> a.bs_shift) - e0].x) * a.bs + (gi & (a.bs - 1))) * D;
+                            const float p0 = __shfl_sync(kFullMask, (x & 1) ? c[nt][1] : c[nt][0], (lane & ~3) | (x >> 1));
+                            const float p1 = __shfl_sync(kFullMask, (x & 1) ? c[nt][3] : c[nt][2], (lane & ~3) | (x >> 1));
+                            const size_t at = size_t(s_src[tile % kTrInfo][tr]) * D;
 #pragma unroll
                             for (int j = 0; j < DT; ++j)
 #pragma unroll
@@ -472,38 +482,38 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
                 }
             }
         } else {
-            // the four warps' token shares of the same 16 rows, through the freed stages
-            float* x_o = reinterpret_cast<float*>(smem);                 // [TW][16][D + 4]
-            float* x_m = x_o + TW * 16 * (D + 4);                        // [TW][16]
-            float* x_l = x_m + TW * 16;
+            // the warps' token shares of the same rows, through the freed stages
+            float* x_o = reinterpret_cast<float*>(smem);                 // [TW][ROWS][D + 4]
+            float* x_m = x_o + TW * ROWS * (D + 4);                      // [TW][ROWS]
+            float* x_l = x_m + TW * ROWS;
             __syncthreads();
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int rr = g4 + 8 * h;
-                float* dst = x_o + (wt * 16 + rr) * (D + 4) + 2 * t4;
+                const int rr = wt * ROWS + wr * 16 + g4 + 8 * h;
+                float* dst = x_o + rr * (D + 4) + 2 * t4;
 #pragma unroll
                 for (int j = 0; j < DT; ++j) *reinterpret_cast<float2*>(dst + j * 8) = make_float2(acc[j][2 * h], acc[j][2 * h + 1]);
                 if (t4 == 0) {
-                    x_m[wt * 16 + rr] = m_run[h];
-                    x_l[wt * 16 + rr] = l_run[h];
+                    x_m[rr] = m_run[h];
+                    x_l[rr] = l_run[h];
                 }
             }
             __syncthreads();
-            for (int i = tid; i < 16 * (D / 4); i += kTrThreads) {
+            for (int i = tid; i < ROWS * (D / 4); i += kTrThreads) {
                 const int rr = i / (D / 4), d = (i - rr * (D / 4)) * 4;
                 if (row0 + rr >= a.R) continue;
                 float M = -INFINITY;
 #pragma unroll
-                for (int w = 0; w < TW; ++w) M = fmaxf(M, x_m[w * 16 + rr]);
+                for (int w = 0; w < TW; ++w) M = fmaxf(M, x_m[w * ROWS + rr]);
                 float den = 0.f;
                 float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int w = 0; w < TW; ++w) {
-                    const float mw = x_m[w * 16 + rr];
+                    const float mw = x_m[w * ROWS + rr];
                     if (mw == -INFINITY) continue;
                     const float wgt = fast_exp2(mw - M);
-                    den = fmaf(x_l[w * 16 + rr], wgt, den);
-                    const float4 o = *reinterpret_cast<const float4*>(x_o + (w * 16 + rr) * (D + 4) + d);
+                    den = fmaf(x_l[w * ROWS + rr], wgt, den);
+                    const float4 o = *reinterpret_cast<const float4*>(x_o + (w * ROWS + rr) * (D + 4) + d);
                     num.x = fmaf(o.x, wgt, num.x);
                     num.y = fmaf(o.y, wgt, num.y);
                     num.z = fmaf(o.z, wgt, num.z);
@@ -542,8 +552,8 @@ cudaError_t launch_tree_t(TreeArgs a, cudaStream_t s)
     a.tile = kTrTile;
     a.item_rows = 16 * RW;
     a.row_groups = (a.R + a.item_rows - 1) / a.item_rows;
-    a.min_per = 4;
-    a.whole_slack = 8;
+    a.min_per = 2;
+    a.slack = 8;
     int ctas = num_sms() * (2 * (smem + 10 * 1024) <= size_t(kSmemPerSm) ? 2 : 1);
     if (ctas > kTreeMaxCtas) ctas = kTreeMaxCtas;
     return launch_after_previous(tree_kernel<D, KB, NQ, RW>, dim3(unsigned(ctas)), dim3(kTrThreads), smem, s, a);
@@ -609,11 +619,11 @@ cudaError_t launch_tree(const Geometry& g, const TreeCall& c, char* ws, cudaStre
     a.part_o = reinterpret_cast<float*>(ws + L.part_o);
     a.counters = reinterpret_cast<uint32_t*>(ws + L.counters);
     a.err = reinterpret_cast<uint32_t*>(ws);
-    if (g.kv_bf16) {
-        if (g.q_bf16 && a.R > 16) return launch_tree_tc(a, s);
-        if (g.q_bf16) return g.D == 128 ? launch_tree_rows<128, true, 1>(a, s) : launch_tree_rows<64, true, 1>(a, s);
-        return g.D == 128 ? launch_tree_rows<128, true, 3>(a, s) : launch_tree_rows<64, true, 3>(a, s);
+    if (g.kv_bf16 && g.q_bf16) {
+        if (a.R > 16) return launch_tree_tc(a, s);
+        return g.D == 128 ? launch_tree_t<128, true, 1, 1>(a, s) : launch_tree_t<64, true, 1, 1>(a, s);
     }
+    if (g.kv_bf16) return g.D == 128 ? launch_tree_rows<128, true, 3>(a, s) : launch_tree_rows<64, true, 3>(a, s);
     return g.D == 128 ? launch_tree_rows<128, false, 1>(a, s) : launch_tree_rows<64, false, 1>(a, s);
 }
 

@@ -6,11 +6,12 @@
 // 0 .. of the sequence and a block may hold context and drafts.  Entry e covers list
 // positions e * bs .. e * bs + bs - 1; tiles of T positions are cut from the list.
 //
-// Work split: the tiles of all items (unit, row group) form one line, cut into equal parts of
-// `per` tiles, one per CTA, whatever the contexts' lengths are (they are only known on the
-// device).  An item that lies in one part is finished there; one that several parts share
-// leaves (m, l, o) per part in the workspace, and the CTA that arrives last adds them up in
-// the parts' order, so the result does not depend on timing.
+// Work split: the items (unit, row group) lie on one line of tiles that is cut into equal parts
+// of `per` tiles, one per CTA, whatever the contexts' lengths are (they are only known on the
+// device).  Items begin anywhere, or, when that costs few tiles, at the beginning of a part:
+// then no CTA works on two items, and an item that fits one part has nothing to merge.  An
+// item that several parts share leaves (m, l, o) per part in the workspace, and the CTA that
+// arrives last adds them up in the parts' order, so the result does not depend on timing.
 #pragma once
 
 #include "sa_common.cuh"
@@ -26,7 +27,7 @@ inline int tree_item_rows(int R) { return R <= 16 ? 16 : (R <= 64 ? 64 : kTreeMa
 
 // Words of shared memory that tree_part needs.
 template <int NT>
-constexpr int kTreeScan = 3 * (NT / 32) + 2;
+constexpr int kTreeScan = NT / 32 + 3;
 
 struct TreeArgs {
     const void* q;
@@ -40,7 +41,7 @@ struct TreeArgs {
     int item_rows;             // query rows of an item at most
     int tile;                  // list positions per tile
     int min_per;               // tiles of a part at least
-    int whole_slack;           // tiles that a part may grow by so that it holds whole items
+    int slack;                 // tiles that a part may grow by so that items begin with a part
     float scale_log2;
     float *part_m, *part_l, *part_o;   // [2 * CTA + which][item_rows] ([D])
     uint32_t *counters, *err;
@@ -114,6 +115,41 @@ __device__ __forceinline__ int2 tree_entry(const TreeArgs& a, int u, const TreeU
     return make_int2(page * a.Hkv + kvh, j << a.bs_shift);
 }
 
+constexpr int kNoToken = INT32_MIN;  // first token of an entry without a page
+
+// Bits d0 .. d0 + 7 of a draft mask (bit j of word j / 32), those in [0, limit).
+__device__ __forceinline__ uint32_t mask_bits8(const uint32_t* words, int d0, int limit)
+{
+    if (d0 <= -8 || d0 >= limit) return 0u;
+    uint32_t v;
+    if (words == nullptr) {
+        v = 0xffu;
+        if (d0 < 0) v = (v << -d0) & 0xffu;
+    } else if (d0 < 0) {
+        v = words[0] << -d0;
+    } else {
+        const int w = d0 >> 5, s = d0 & 31;
+        v = words[w] >> s;
+        if (s > 24 && (w + 1) * 32 < limit) v |= words[w + 1] << (32 - s);
+    }
+    if (d0 + 8 > limit) v &= (1u << (limit - d0)) - 1u;
+    return v & 0xffu;
+}
+
+// Which of the 8 list positions from p (a multiple of 8) a query with these mask words sees; e
+// is their entry, `first` the entry's first token.
+__device__ __forceinline__ uint32_t tree_tokens8(const TreeArgs& a, const TreeUnit& un, int p, int e, int first,
+                                                 const uint32_t* words, int limit)
+{
+    if (first == kNoToken) return 0u;
+    const int tok = first + (p & (a.bs - 1));
+    const bool ctx = a.sel_ids == nullptr || e < un.n_ctx;
+    uint32_t bits = 0u;
+    if (ctx) bits = (1u << min(8, max(0, un.len - tok))) - 1u;
+    if (a.sel_ids == nullptr || !ctx) bits |= mask_bits8(words, tok - un.len, limit);
+    return bits;
+}
+
 // This CTA's part [lo, hi) of the line of tiles and the item that holds tile lo, found by all
 // threads (NT of them, a multiple of 32).
 struct TreePart {
@@ -123,76 +159,88 @@ struct TreePart {
     int per;              // tiles of a part
 };
 
+// Sums of v over the CTA's threads before this one (first) and over all of them.
 template <int NT>
-__device__ TreePart tree_part(const TreeArgs& a, long long* s_scan /* [kTreeScan<NT>] shared */)
+__device__ __forceinline__ void tree_scan(long long v, long long* s_scan, long long& before, long long& total)
 {
-    constexpr int W = NT / 32;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int units = a.B * a.Hkv;
-    // thread t owns units [t * ch, (t + 1) * ch)
-    const int ch = (units + NT - 1) / NT;
-    const int u0 = min(units, tid * ch), u1 = min(units, u0 + ch);
-    long long mine = 0;
-    int most = 0, least = INT32_MAX;                         // tiles of an active item
-    for (int u = u0; u < u1; ++u) {
-        const int t = tree_tiles(a, tree_unit(a, u));
-        mine += t;
-        most = max(most, t);
-        if (t > 0) least = min(least, t);
-    }
-    mine *= a.row_groups;
-    long long incl = mine;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long incl = v;
 #pragma unroll
     for (int off = 1; off < kWarp; off <<= 1) {
         const long long t = __shfl_up_sync(kFullMask, incl, off);
         if (lane >= off) incl += t;
     }
-    most = __reduce_max_sync(kFullMask, most);
-    least = __reduce_min_sync(kFullMask, least);
-    if (lane == 31) {
-        s_scan[warp] = incl;
-        s_scan[W + warp] = most;
-        s_scan[2 * W + warp] = least;
-    }
+    if (lane == 31) s_scan[warp] = incl;
     __syncthreads();
-    long long before = 0, total = 0;
+    before = incl - v;
+    total = 0;
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
+    for (int w = 0; w < NT / 32; ++w) {
         if (w < warp) before += s_scan[w];
         total += s_scan[w];
-        most = max(most, int(s_scan[W + w]));
-        least = min(least, int(s_scan[2 * W + w]));
     }
-    before += incl - mine;
-    TreePart p;
-    const long long share = (total + gridDim.x - 1) / gridDim.x;
-    p.per = int(share < a.min_per ? a.min_per : share);
-    if (most == least && most > 0) {
-        // equal items: parts of whole items leave nothing to merge, if they are not much longer
-        const int whole = (p.per + most - 1) / most * most;
-        if (whole - p.per <= a.whole_slack) p.per = whole;
+    __syncthreads();
+}
+
+template <int NT>
+__device__ TreePart tree_part(const TreeArgs& a, long long* s_scan /* [kTreeScan<NT>] shared */)
+{
+    const int units = a.B * a.Hkv, ctas = gridDim.x;
+    // thread t owns units [t * ch, (t + 1) * ch)
+    const int ch = (units + NT - 1) / NT;
+    const int u0 = min(units, int(threadIdx.x) * ch), u1 = min(units, u0 + ch);
+    const int t_first = u0 < u1 ? tree_tiles(a, tree_unit(a, u0)) : 0;
+    auto tiles_of = [&](int u) { return u == u0 ? t_first : tree_tiles(a, tree_unit(a, u)); };
+    long long mine = 0, before, total;
+    for (int u = u0; u < u1; ++u) mine += tiles_of(u);
+    mine *= a.row_groups;
+    tree_scan<NT>(mine, s_scan, before, total);
+    const long long share = (total + ctas - 1) / ctas;
+    int per = int(share < a.min_per ? a.min_per : share);
+    // items that begin with a part: at no cost, with half of the slack, then with all of it
+    bool aligned = false;
+    for (int more = 0; !aligned && more <= a.slack; more += max(1, a.slack / 2)) {
+        const int p = per + more;
+        long long parts = 0, parts_before, all_parts;
+        for (int u = u0; u < u1; ++u) parts += (tiles_of(u) + p - 1) / p;
+        parts *= a.row_groups;
+        tree_scan<NT>(parts, s_scan, parts_before, all_parts);
+        if (all_parts <= ctas) {
+            aligned = true;
+            per = p;
+            mine = parts * p;
+            before = parts_before * p;
+            total = all_parts * p;
+        }
     }
-    p.lo = min(total, (long long)blockIdx.x * p.per);
-    p.hi = min(total, p.lo + p.per);
-    if (p.lo < p.hi && mine > 0 && p.lo >= before && p.lo < before + mine) {
+    TreePart r;
+    r.per = per;
+    r.lo = min(total, (long long)blockIdx.x * per);
+    r.hi = min(total, r.lo + per);
+    if (r.lo < r.hi && mine > 0 && r.lo >= before && r.lo < before + mine) {
         long long at = before;
         for (int u = u0; u < u1; ++u) {
-            const int t = tree_tiles(a, tree_unit(a, u));
-            const long long all = (long long)t * a.row_groups;
-            if (p.lo < at + all) {
-                const int rg = int((p.lo - at) / t);
-                s_scan[3 * W] = (long long)u * a.row_groups + rg;
-                s_scan[3 * W + 1] = at + (long long)rg * t;
+            const int t = tiles_of(u);
+            const int len = aligned ? (t + per - 1) / per * per : t;      // the item's stretch of the line
+            const long long all = (long long)len * a.row_groups;
+            if (r.lo < at + all) {
+                const int rg = int((r.lo - at) / len);
+                s_scan[NT / 32] = (long long)u * a.row_groups + rg;
+                s_scan[NT / 32 + 1] = at + (long long)rg * len;
+                s_scan[NT / 32 + 2] = aligned ? at + (long long)rg * len + t : r.hi;
                 break;
             }
             at += all;
         }
     }
     __syncthreads();
-    p.item = int(s_scan[3 * W]);
-    p.start = s_scan[3 * W + 1];
+    if (r.lo < r.hi) {
+        r.item = int(s_scan[NT / 32]);
+        r.start = s_scan[NT / 32 + 1];
+        r.hi = min(r.hi, s_scan[NT / 32 + 2]);
+    }
     __syncthreads();                                         // s_scan may be used for something else
-    return p;
+    return r;
 }
 
 // The output row of an item's query row r (query r / G, head r % G of the KV head's group).
@@ -241,22 +289,28 @@ __device__ void tree_arrive_and_merge(const TreeArgs& a, int item, long long sta
     const int u = item / a.row_groups, row0 = (item - u * a.row_groups) * a.item_rows;
     const int b = u / a.Hkv, kvh = u - b * a.Hkv;
     const int rows = min(a.item_rows, a.R - row0);
-    const int vec = a.D / 4, batch = min(rows, n_w / np);
+    const int vec = a.D / 4, batch = min(rows, n_w / (2 * np));
+    float* s_l = s_w + batch * np;
     for (int r0 = 0; r0 < rows; r0 += batch) {
         const int n = min(batch, rows - r0);
+        for (int i = tid; i < n * np; i += NT) {
+            const int c = i / n, r = i - c * n;
+            const long long at = (long long)tree_slot(c0 + c, per, start) * a.item_rows + r0 + r;
+            s_w[r * np + c] = __ldcg(a.part_m + at);
+            s_l[r * np + c] = __ldcg(a.part_l + at);
+        }
+        tree_sync<NT>();
         for (int r = tid >> 5; r < n; r += NT / 32) {
             float M = -INFINITY;
-            for (int c = lane; c < np; c += 32)
-                M = fmaxf(M, __ldcg(a.part_m + (long long)tree_slot(c0 + c, per, start) * a.item_rows + r0 + r));
+            for (int c = lane; c < np; c += 32) M = fmaxf(M, s_w[r * np + c]);
 #pragma unroll
             for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, x));
             float den = 0.f;
             for (int c = lane; c < np; c += 32) {
-                const long long at = (long long)tree_slot(c0 + c, per, start) * a.item_rows + r0 + r;
-                const float m = __ldcg(a.part_m + at);
+                const float m = s_w[r * np + c];
                 const float w = m == -INFINITY ? 0.f : fast_exp2(m - M);   // a part that saw nothing has no weight
                 s_w[r * np + c] = w;
-                den = fmaf(w, __ldcg(a.part_l + at), den);
+                den = fmaf(w, s_l[r * np + c], den);
             }
 #pragma unroll
             for (int x = 16; x > 0; x >>= 1) den += __shfl_xor_sync(kFullMask, den, x);
@@ -268,11 +322,11 @@ __device__ void tree_arrive_and_merge(const TreeArgs& a, int item, long long sta
         for (int i = tid; i < n * vec; i += NT) {
             const int r = i / vec, d = (i - r * vec) * 4;
             float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int c = 0; c < np; c += 4) {
-                float4 o[4];
-                float w[4];
+            for (int c = 0; c < np; c += 8) {               // eight loads in flight
+                float4 o[8];
+                float w[8];
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
+                for (int x = 0; x < 8; ++x) {
                     w[x] = c + x < np ? s_w[r * np + c + x] : 0.f;
                     o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
                     if (w[x] != 0.f)
@@ -280,7 +334,7 @@ __device__ void tree_arrive_and_merge(const TreeArgs& a, int item, long long sta
                             a.part_o + ((long long)tree_slot(c0 + c + x, per, start) * a.item_rows + r0 + r) * a.D + d));
                 }
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
+                for (int x = 0; x < 8; ++x) {
                     num.x = fmaf(o[x].x, w[x], num.x);
                     num.y = fmaf(o[x].y, w[x], num.y);
                     num.z = fmaf(o[x].z, w[x], num.z);

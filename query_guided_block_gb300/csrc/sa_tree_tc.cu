@@ -38,7 +38,6 @@ namespace {
 constexpr int kTcSoft = 512;           // softmax threads, 256 a slot
 constexpr int kTcThreads = kTcSoft + 128;
 constexpr int kTcTile = 128;
-constexpr int kNoToken = INT32_MIN;
 
 template <int D>
 struct TcShape {
@@ -172,25 +171,6 @@ __device__ __forceinline__ uint32_t round_up_bf16(float x)
     const uint32_t u = __float_as_uint(x);
     // toward zero is up for negative values; positive ones go up unless they are exact
     return (u & 0x80000000u) ? u & 0xffff0000u : (u + (x < INFINITY ? 0xffffu : 0u)) & 0xffff0000u;
-}
-
-// Bits d0 .. d0 + 7 of a draft mask (bit j of word j / 32), those in [0, limit).
-__device__ __forceinline__ uint32_t mask_bits8(const uint32_t* words, int d0, int limit)
-{
-    if (d0 <= -8 || d0 >= limit) return 0u;
-    uint32_t v;
-    if (words == nullptr) {
-        v = 0xffu;
-        if (d0 < 0) v = (v << -d0) & 0xffu;
-    } else if (d0 < 0) {
-        v = words[0] << -d0;
-    } else {
-        const int w = d0 >> 5, s = d0 & 31;
-        v = words[w] >> s;
-        if (s > 24 && (w + 1) * 32 < limit) v |= words[w + 1] << (32 - s);
-    }
-    if (d0 + 8 > limit) v &= (1u << (limit - d0)) - 1u;
-    return v & 0xffu;
 }
 
 // Register shares: the CTA starts with 20 warps x 96; the softmax threads hold a quarter of an
@@ -464,14 +444,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // Tokens 8 g8 .. + 7 of local tile i that a query with these mask words sees.
             auto tokens8 = [&](int i, int g8, const uint32_t* w, int lim) -> uint32_t {
                 const int le = (g8 * 8) >> a.bs_shift;
-                const int first = sh.token[(tile0 + i) % SH::INFO][le];
-                if (first == kNoToken) return 0u;
-                const int tok = first + ((g8 * 8) & (a.bs - 1));
-                const bool ctx = dense || (((g.t0 + i) * kTcTile) >> a.bs_shift) + le < g.un.n_ctx;
-                uint32_t bits = 0u;
-                if (ctx) bits = (1u << min(8, max(0, g.un.len - tok))) - 1u;
-                if (dense || !ctx) bits |= mask_bits8(w, tok - g.un.len, lim);
-                return bits;
+                return tree_tokens8(a, g.un, g8 * 8, (((g.t0 + i) * kTcTile) >> a.bs_shift) + le,
+                                    sh.token[(tile0 + i) % SH::INFO][le], w, lim);
             };
             // Adds O of local tile i to this thread's channels.
             auto add_up = [&](int i) {
@@ -781,7 +755,7 @@ cudaError_t launch_tree_tc(TreeArgs a, cudaStream_t s)
     a.item_rows = tree_item_rows(a.R);
     a.row_groups = (a.R + a.item_rows - 1) / a.item_rows;
     a.min_per = 2;
-    a.whole_slack = 7;
+    a.slack = 7;
     return a.D == 128 ? launch_tc_t<128>(a, s) : launch_tc_t<64>(a, s);
 }
 
