@@ -583,6 +583,18 @@ static int draft_geometry(const sparse_attn_params* p, Geometry* g)
     return SPARSE_ATTN_OK;
 }
 
+// draft_geometry for the tree attention.
+static int tree_geometry(const sparse_attn_params* p, Geometry* g)
+{
+    const int st = draft_geometry(p, g);
+    if (st) return st;
+    if (g->Q > kTreeMaxDrafts) return SPARSE_ATTN_UNSUPPORTED;
+    // the tiles of all units are numbered in 32 bits
+    const long long tiles = ((long long)g->nb_cap + g->sel_stride + 2) * g->bs / kTreeLeastTile + 1;
+    if (tiles * g->units() * ((g->Q * g->G + 15) / 16) > INT32_MAX / 2) return SPARSE_ATTN_UNSUPPORTED;
+    return SPARSE_ATTN_OK;
+}
+
 static long long capacity_of(const sparse_attn_params* p)
 {
     return p->capacity_tokens > 0 ? p->capacity_tokens : p->n_tokens;
@@ -650,9 +662,8 @@ int sparse_attn_tree_workspace_size(const sparse_attn_params* p, size_t* bytes)
 {
     if (!bytes) return SPARSE_ATTN_INVALID_ARG;
     Geometry g;
-    const int st = draft_geometry(p, &g);
+    const int st = tree_geometry(p, &g);
     if (st) return st;
-    if (g.Q > kTreeMaxDrafts) return SPARSE_ATTN_UNSUPPORTED;
     *bytes = tree_layout(g).total;
     return SPARSE_ATTN_OK;
 }
@@ -663,9 +674,8 @@ int sparse_attn_tree_decode(const sparse_attn_params* p, const void* q, const vo
                             float* out, void* ws, size_t ws_bytes, sparse_attn_stream stream)
 {
     Geometry g;
-    const int st = draft_geometry(p, &g);
+    const int st = tree_geometry(p, &g);
     if (st) return st;
-    if (g.Q > kTreeMaxDrafts) return SPARSE_ATTN_UNSUPPORTED;
     if (!ws || !aligned(ws, 256) || ws_bytes < tree_layout(g).total) return SPARSE_ATTN_INVALID_ARG;
     if ((sel_ids == nullptr) != (sel_count == nullptr)) return SPARSE_ATTN_INVALID_ARG;
     if (capacity_of(p) < (long long)g.N + g.Q) return SPARSE_ATTN_INVALID_ARG;   // the drafts' pages

@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
     __shared__ uint32_t s_part[kTrInfo][2];                 // a tile's halves: 1 not only context tokens, 2 drafts
     __shared__ uint32_t s_see[ROWS][2];                     // tokens of the tile that a row sees
     __shared__ uint32_t s_any[kTreeMaxDrafts / 32];         // drafts that some query sees
-    __shared__ long long s_scan[kTreeScan<kTrThreads>];
+    __shared__ int s_scan[kTreeScan<kTrThreads>];
     __shared__ int s_last;
     __shared__ uint32_t s_bad[2];
 
@@ -112,8 +112,7 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
 
     const TreePart part = tree_part<kTrThreads>(a, s_scan);
     const bool dense = a.sel_ids == nullptr;
-    long long lo = part.lo, start = part.start;
-    int item = part.item;
+    int lo = part.lo, start = part.start, item = part.item;
 
     while (lo < part.hi) {
         const int u = item / a.row_groups, rg = item - u * a.row_groups;
@@ -124,7 +123,7 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
             ++item;
             continue;
         }
-        const int t0 = int(lo - start), t1 = int(min((long long)tiles, part.hi - start));
+        const int t0 = lo - start, t1 = min(tiles, part.hi - start);
         const int row0 = rg * ROWS;                          // first unit row of the item
         const uint32_t* mask_b = a.mask != nullptr ? a.mask + (long long)b * a.Q * a.mask_words : nullptr;
 
@@ -229,15 +228,15 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
                 if (!whole) {
                     for (int i = tid; i < ROWS * 2; i += kTrThreads) {
                         const int r = row0 + (i >> 1), t = r / a.G;
+                        const DraftView view = draft_view(
+                            mask_b != nullptr && r < a.R ? mask_b + (long long)t * a.mask_words : nullptr, a.mask_words,
+                            r >= a.R ? 0 : (mask_b != nullptr ? a.Q : t + 1));
                         uint32_t bits = 0u;
 #pragma unroll 1
                         for (int x = 0; x < 4; ++x) {
                             const int p = tile * kTrTile + 32 * (i & 1) + 8 * x, e = p >> a.bs_shift;
                             const int2 en = e < e1 ? s_ent[e - e0] : make_int2(-1, 0);
-                            bits |= tree_tokens8(a, un, p, e, en.x < 0 ? kNoToken : en.y,
-                                                 mask_b != nullptr && r < a.R ? mask_b + (long long)t * a.mask_words : nullptr,
-                                                 r >= a.R ? 0 : (mask_b != nullptr ? a.Q : t + 1))
-                                    << (8 * x);
+                            bits |= tree_tokens8(a, un, p, e, en.x < 0 ? kNoToken : en.y, view) << (8 * x);
                         }
                         s_see[i >> 1][i & 1] = bits;
                     }
@@ -528,9 +527,12 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
                 }
             }
         }
-        if (!complete)
+        if (a.combine) {
+            if (tid == 0 && t0 == 0) tree_note_parts(a, item, start, tiles, part.per);
+        } else if (!complete) {
             tree_arrive_and_merge<kTrThreads>(a, item, start, tiles, part.per, &s_last, reinterpret_cast<float*>(smem),
                                               SH::STAGES * SH::STAGE / 4);
+        }
         lo = start + t1;
         if (t1 == tiles) {
             start += tiles;
@@ -553,10 +555,12 @@ cudaError_t launch_tree_t(TreeArgs a, cudaStream_t s)
     a.item_rows = 16 * RW;
     a.row_groups = (a.R + a.item_rows - 1) / a.item_rows;
     a.min_per = 2;
-    a.slack = 8;
+    a.half_slack = 4;
     int ctas = num_sms() * (2 * (smem + 10 * 1024) <= size_t(kSmemPerSm) ? 2 : 1);
     if (ctas > kTreeMaxCtas) ctas = kTreeMaxCtas;
-    return launch_after_previous(tree_kernel<D, KB, NQ, RW>, dim3(unsigned(ctas)), dim3(kTrThreads), smem, s, a);
+    tree_choose_combine(a, ctas);
+    const cudaError_t e = launch_after_previous(tree_kernel<D, KB, NQ, RW>, dim3(unsigned(ctas)), dim3(kTrThreads), smem, s, a);
+    return e == cudaSuccess && a.combine ? launch_tree_combine(a, s) : e;
 }
 
 template <int D, bool KB, int NQ>
@@ -565,9 +569,85 @@ cudaError_t launch_tree_rows(const TreeArgs& a, cudaStream_t s)
     return a.R <= 16 ? launch_tree_t<D, KB, NQ, 1>(a, s) : launch_tree_t<D, KB, NQ, 4>(a, s);
 }
 
+// Adds up the parts of shared items: a warp per query row, a quarter of a float4 row per lane.
+template <int D>
+__global__ void __launch_bounds__(128) tree_combine_kernel(TreeArgs a)
+{
+    allow_dependents_early();
+    grid_dependency_wait();   // the parts come from the previous kernel
+    const int lane = threadIdx.x & 31;
+    const int row = blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (row >= a.B * a.Hkv * a.R) return;
+    const int u = row / a.R, r = row - u * a.R, rg = r / a.item_rows, rr = r - rg * a.item_rows;
+    const int b = u / a.Hkv, kvh = u - b * a.Hkv;
+    const int len = a.seq_lens != nullptr ? a.seq_lens[b] : a.N;
+    if (len < 0 || len > a.N) return;                         // inactive: no output
+    const int2 at = a.item_parts[u * a.row_groups + rg];
+    if (at.y <= 1) return;                                    // written whole
+    // the first part of an item is the second slot of its CTA, the others are first slots
+    auto slot = [&](int c) { return (long long)(2 * (at.x + c) + (c == 0 ? 1 : 0)) * a.item_rows + rr; };
+    float M = -INFINITY;
+    for (int c = lane; c < at.y; c += 32) M = fmaxf(M, __ldcg(a.part_m + slot(c)));
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, x));
+    float den = 0.f;
+    float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c0 = 0; c0 < at.y; c0 += 32) {
+        float w = 0.f;
+        if (c0 + lane < at.y) {
+            const float m = __ldcg(a.part_m + slot(c0 + lane));
+            w = m == -INFINITY ? 0.f : fast_exp2(m - M);
+            den = fmaf(w, __ldcg(a.part_l + slot(c0 + lane)), den);
+        }
+        const int n = min(32, at.y - c0);
+        for (int c = 0; c < n; c += 8) {
+            float4 o[8];
+            float wc[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                wc[x] = __shfl_sync(kFullMask, w, (c + x) & 31);
+                o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (c + x < n && wc[x] != 0.f && lane < D / 4)
+                    o[x] = __ldcg(reinterpret_cast<const float4*>(a.part_o + slot(c0 + c + x) * D) + lane);
+            }
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const float wx = c + x < n ? wc[x] : 0.f;
+                num.x = fmaf(o[x].x, wx, num.x);
+                num.y = fmaf(o[x].y, wx, num.y);
+                num.z = fmaf(o[x].z, wx, num.z);
+                num.w = fmaf(o[x].w, wx, num.w);
+            }
+        }
+    }
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) den += __shfl_xor_sync(kFullMask, den, x);
+    const float inv = den == 0.f ? 0.f : 1.f / den;
+    if (lane < D / 4)
+        reinterpret_cast<float4*>(a.out + tree_out_row(a, b, kvh, r) * D)[lane] =
+            make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
+}
+
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 }  // namespace
+
+void tree_choose_combine(TreeArgs& a, int ctas)
+{
+    const long long items = (long long)a.B * a.Hkv * a.row_groups;
+    const long long list = a.sel_ids == nullptr ? (long long)a.N + a.Q : (long long)a.sel_stride * a.bs + a.Q + 2 * a.bs;
+    long long parts = (list + a.tile - 1) / a.tile / a.min_per;      // of an item at most
+    if (parts > ctas / items) parts = ctas / items;
+    const int rows = a.R < a.item_rows ? a.R : a.item_rows;
+    a.combine = parts * rows * a.D * 4 >= kTreeCombineBytes;
+}
+
+cudaError_t launch_tree_combine(const TreeArgs& a, cudaStream_t s)
+{
+    const unsigned grid = unsigned(((long long)a.B * a.Hkv * a.R + 3) / 4);
+    return a.D == 128 ? launch_after_previous(tree_combine_kernel<128>, dim3(grid), dim3(128), 0, s, a)
+                      : launch_after_previous(tree_combine_kernel<64>, dim3(grid), dim3(128), 0, s, a);
+}
 
 TreeLayout tree_layout(const Geometry& g)
 {
@@ -576,7 +656,9 @@ TreeLayout tree_layout(const Geometry& g)
     const size_t rows = size_t(tree_item_rows(R));
     const size_t slots = 2 * size_t(kTreeMaxCtas);
     L.counters = 256;
-    L.part_m = align256(L.counters + size_t(g.units()) * ((R + 15) / 16) * sizeof(uint32_t));
+    const size_t items = size_t(g.units()) * ((R + 15) / 16);
+    L.item_parts = align256(L.counters + items * sizeof(uint32_t));
+    L.part_m = align256(L.item_parts + items * sizeof(int2));
     L.part_l = align256(L.part_m + slots * rows * sizeof(float));
     L.part_o = align256(L.part_l + slots * rows * sizeof(float));
     L.total = align256(L.part_o + slots * rows * g.D * sizeof(float));
@@ -618,6 +700,7 @@ cudaError_t launch_tree(const Geometry& g, const TreeCall& c, char* ws, cudaStre
     a.part_l = reinterpret_cast<float*>(ws + L.part_l);
     a.part_o = reinterpret_cast<float*>(ws + L.part_o);
     a.counters = reinterpret_cast<uint32_t*>(ws + L.counters);
+    a.item_parts = reinterpret_cast<int2*>(ws + L.item_parts);
     a.err = reinterpret_cast<uint32_t*>(ws);
     if (g.kv_bf16 && g.q_bf16) {
         if (a.R > 16) return launch_tree_tc(a, s);

@@ -27,7 +27,7 @@ inline int tree_item_rows(int R) { return R <= 16 ? 16 : (R <= 64 ? 64 : kTreeMa
 
 // Words of shared memory that tree_part needs.
 template <int NT>
-constexpr int kTreeScan = NT / 32 + 3;
+constexpr int kTreeScan = 5 * (NT / 32) + 3;
 
 struct TreeArgs {
     const void* q;
@@ -41,9 +41,11 @@ struct TreeArgs {
     int item_rows;             // query rows of an item at most
     int tile;                  // list positions per tile
     int min_per;               // tiles of a part at least
-    int slack;                 // tiles that a part may grow by so that items begin with a part
+    int half_slack;            // a part may grow by twice as many tiles so that items begin with a part
     float scale_log2;
+    int combine;               // shared items are added up by a launch of their own
     float *part_m, *part_l, *part_o;   // [2 * CTA + which][item_rows] ([D])
+    int2* item_parts;          // combine: an item's first part and how many it has
     uint32_t *counters, *err;
 };
 
@@ -117,129 +119,165 @@ __device__ __forceinline__ int2 tree_entry(const TreeArgs& a, int u, const TreeU
 
 constexpr int kNoToken = INT32_MIN;  // first token of an entry without a page
 
-// Bits d0 .. d0 + 7 of a draft mask (bit j of word j / 32), those in [0, limit).
-__device__ __forceinline__ uint32_t mask_bits8(const uint32_t* words, int d0, int limit)
+// A row's view of the drafts: their bits, the first 64 at hand.
+struct DraftView {
+    const uint32_t* words;    // bit j of word j / 32; null: all of them
+    uint64_t first;           // bits 0 .. 63
+    int limit;                // drafts from here on are not seen
+};
+
+__device__ __forceinline__ DraftView draft_view(const uint32_t* words, int n_words, int limit)
 {
-    if (d0 <= -8 || d0 >= limit) return 0u;
-    uint32_t v;
-    if (words == nullptr) {
-        v = 0xffu;
-        if (d0 < 0) v = (v << -d0) & 0xffu;
-    } else if (d0 < 0) {
-        v = words[0] << -d0;
-    } else {
-        const int w = d0 >> 5, s = d0 & 31;
-        v = words[w] >> s;
-        if (s > 24 && (w + 1) * 32 < limit) v |= words[w + 1] << (32 - s);
+    DraftView v{words, ~0ull, limit};
+    if (words != nullptr) {
+        v.first = words[0];
+        if (n_words > 1) v.first |= uint64_t(words[1]) << 32;
     }
-    if (d0 + 8 > limit) v &= (1u << (limit - d0)) - 1u;
+    return v;
+}
+
+// Bits d0 .. d0 + 7 of the view.
+__device__ __forceinline__ uint32_t draft_bits8(const DraftView& w, int d0)
+{
+    if (d0 <= -8 || d0 >= w.limit) return 0u;
+    uint32_t v;
+    if (d0 < 0) {
+        v = uint32_t(w.first) << -d0;
+    } else if (d0 <= 56 || w.words == nullptr) {
+        v = uint32_t(w.first >> min(d0, 32));                // no words: every bit is set
+        if (d0 > 32 && w.words != nullptr) v = uint32_t(w.first >> d0);
+    } else {
+        const int x = d0 >> 5, s = d0 & 31;
+        v = w.words[x] >> s;
+        if (s > 24 && (x + 1) * 32 < w.limit) v |= w.words[x + 1] << (32 - s);
+    }
+    if (d0 + 8 > w.limit) v &= (1u << (w.limit - d0)) - 1u;
     return v & 0xffu;
 }
 
-// Which of the 8 list positions from p (a multiple of 8) a query with these mask words sees; e
-// is their entry, `first` the entry's first token.
+// Which of the 8 list positions from p (a multiple of 8) a query with this view sees; e is
+// their entry, `first` the entry's first token.
 __device__ __forceinline__ uint32_t tree_tokens8(const TreeArgs& a, const TreeUnit& un, int p, int e, int first,
-                                                 const uint32_t* words, int limit)
+                                                 const DraftView& view)
 {
     if (first == kNoToken) return 0u;
     const int tok = first + (p & (a.bs - 1));
     const bool ctx = a.sel_ids == nullptr || e < un.n_ctx;
     uint32_t bits = 0u;
     if (ctx) bits = (1u << min(8, max(0, un.len - tok))) - 1u;
-    if (a.sel_ids == nullptr || !ctx) bits |= mask_bits8(words, tok - un.len, limit);
+    if (a.sel_ids == nullptr || !ctx) bits |= draft_bits8(view, tok - un.len);
     return bits;
 }
 
-// This CTA's part [lo, hi) of the line of tiles and the item that holds tile lo, found by all
-// threads (NT of them, a multiple of 32).
+// This CTA's part [lo, hi) of the line of tiles and the item that holds tile lo.  The line is
+// shorter than 2^31 tiles.
 struct TreePart {
-    long long lo, hi;     // tiles of the line
-    long long start;      // first tile of `item`
+    int lo, hi;       // tiles of the line
+    int start;        // first tile of `item`
     int item;
-    int per;              // tiles of a part
+    int per;          // tiles of a part
 };
 
-// Sums of v over the CTA's threads before this one (first) and over all of them.
+// Found by all threads (NT of them): as many warps as the units need count tiles, the others
+// only keep step.  `s`: kTreeScan<NT> words of shared memory.
 template <int NT>
-__device__ __forceinline__ void tree_scan(long long v, long long* s_scan, long long& before, long long& total)
+__device__ TreePart tree_part(const TreeArgs& a, int* s)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long long incl = v;
-#pragma unroll
-    for (int off = 1; off < kWarp; off <<= 1) {
-        const long long t = __shfl_up_sync(kFullMask, incl, off);
-        if (lane >= off) incl += t;
-    }
-    if (lane == 31) s_scan[warp] = incl;
-    __syncthreads();
-    before = incl - v;
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < NT / 32; ++w) {
-        if (w < warp) before += s_scan[w];
-        total += s_scan[w];
-    }
-    __syncthreads();
-}
-
-template <int NT>
-__device__ TreePart tree_part(const TreeArgs& a, long long* s_scan /* [kTreeScan<NT>] shared */)
-{
+    constexpr int W = NT / 32;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int units = a.B * a.Hkv, ctas = gridDim.x;
-    // thread t owns units [t * ch, (t + 1) * ch)
-    const int ch = (units + NT - 1) / NT;
-    const int u0 = min(units, int(threadIdx.x) * ch), u1 = min(units, u0 + ch);
+    const int warps = min(W, (units + 31) / 32);
+    const int ch = (units + warps * 32 - 1) / (warps * 32);    // units per counting thread, consecutive
+    const int u0 = warp < warps ? min(units, tid * ch) : units, u1 = min(units, u0 + ch);
     const int t_first = u0 < u1 ? tree_tiles(a, tree_unit(a, u0)) : 0;
     auto tiles_of = [&](int u) { return u == u0 ? t_first : tree_tiles(a, tree_unit(a, u)); };
-    long long mine = 0, before, total;
-    for (int u = u0; u < u1; ++u) mine += tiles_of(u);
-    mine *= a.row_groups;
-    tree_scan<NT>(mine, s_scan, before, total);
-    const long long share = (total + ctas - 1) / ctas;
-    int per = int(share < a.min_per ? a.min_per : share);
-    // items that begin with a part: at no cost, with half of the slack, then with all of it
-    bool aligned = false;
-    for (int more = 0; !aligned && more <= a.slack; more += max(1, a.slack / 2)) {
-        const int p = per + more;
-        long long parts = 0, parts_before, all_parts;
-        for (int u = u0; u < u1; ++u) parts += (tiles_of(u) + p - 1) / p;
-        parts *= a.row_groups;
-        tree_scan<NT>(parts, s_scan, parts_before, all_parts);
-        if (all_parts <= ctas) {
-            aligned = true;
-            per = p;
-            mine = parts * p;
-            before = parts_before * p;
-            total = all_parts * p;
+    int* s_sum = s;                   // [W] tiles
+    int* s_parts = s + W;             // [3][W] parts at three lengths
+    int* s_line = s + 4 * W;          // [W] stretches of the line
+    int* s_found = s + 5 * W;         // item, start, end
+
+    int tiles = 0;
+    for (int u = u0; u < u1; ++u) tiles += tiles_of(u);
+    tiles *= a.row_groups;
+    if (warp < warps) {
+        const int sum = __reduce_add_sync(kFullMask, tiles);
+        if (lane == 0) s_sum[warp] = sum;
+    }
+    __syncthreads();
+    int total = 0;
+    for (int w = 0; w < warps; ++w) total += s_sum[w];
+    int per = max(a.min_per, (total + ctas - 1) / ctas);
+    // Items may begin with a part if the parts then suffice: at no cost, with half of the slack
+    // added to a part, or with all of it.
+    int parts[3] = {0, 0, 0};
+    for (int u = u0; u < u1; ++u) {
+        const int t = tiles_of(u);
+#pragma unroll
+        for (int x = 0; x < 3; ++x) parts[x] += (t + per + x * a.half_slack - 1) / (per + x * a.half_slack);
+    }
+    if (warp < warps) {
+#pragma unroll
+        for (int x = 0; x < 3; ++x) {
+            parts[x] *= a.row_groups;
+            const int sum = __reduce_add_sync(kFullMask, parts[x]);
+            if (lane == 0) s_parts[x * W + warp] = sum;
         }
     }
+    __syncthreads();
+    int all[3] = {0, 0, 0};
+    for (int w = 0; w < warps; ++w) {
+#pragma unroll
+        for (int x = 0; x < 3; ++x) all[x] += s_parts[x * W + w];
+    }
+    int mine = tiles;
+    bool aligned = false;
+#pragma unroll
+    for (int x = 2; x >= 0; --x) {
+        if (all[x] > ctas) continue;
+        aligned = true;
+        mine = parts[x];
+        total = all[x];
+    }
+    if (aligned) {
+        per += (all[0] <= ctas ? 0 : (all[1] <= ctas ? 1 : 2)) * a.half_slack;
+        mine *= per;
+        total *= per;
+    }
+    int incl = mine;
+    if (warp < warps) {
+        incl = warp_inclusive_scan(mine, lane);
+        if (lane == 31) s_line[warp] = incl;
+    }
+    __syncthreads();
     TreePart r;
     r.per = per;
-    r.lo = min(total, (long long)blockIdx.x * per);
-    r.hi = min(total, r.lo + per);
-    if (r.lo < r.hi && mine > 0 && r.lo >= before && r.lo < before + mine) {
-        long long at = before;
-        for (int u = u0; u < u1; ++u) {
-            const int t = tiles_of(u);
-            const int len = aligned ? (t + per - 1) / per * per : t;      // the item's stretch of the line
-            const long long all = (long long)len * a.row_groups;
-            if (r.lo < at + all) {
-                const int rg = int((r.lo - at) / len);
-                s_scan[NT / 32] = (long long)u * a.row_groups + rg;
-                s_scan[NT / 32 + 1] = at + (long long)rg * len;
-                s_scan[NT / 32 + 2] = aligned ? at + (long long)rg * len + t : r.hi;
-                break;
+    r.lo = int(min((long long)total, (long long)blockIdx.x * per));
+    r.hi = int(min((long long)total, (long long)r.lo + per));
+    if (r.lo < r.hi && mine > 0) {
+        int at = incl - mine;
+        for (int w = 0; w < warp; ++w) at += s_line[w];
+        if (r.lo >= at && r.lo < at + mine) {
+            for (int u = u0; u < u1; ++u) {
+                const int t = tiles_of(u);
+                const int len = aligned ? (t + per - 1) / per * per : t;      // the item's stretch of the line
+                if (r.lo < at + len * a.row_groups) {
+                    const int rg = (r.lo - at) / len;
+                    s_found[0] = u * a.row_groups + rg;
+                    s_found[1] = at + rg * len;
+                    s_found[2] = aligned ? at + rg * len + t : r.hi;
+                    break;
+                }
+                at += len * a.row_groups;
             }
-            at += all;
         }
     }
     __syncthreads();
     if (r.lo < r.hi) {
-        r.item = int(s_scan[NT / 32]);
-        r.start = s_scan[NT / 32 + 1];
-        r.hi = min(r.hi, s_scan[NT / 32 + 2]);
+        r.item = s_found[0];
+        r.start = s_found[1];
+        r.hi = min(r.hi, s_found[2]);
     }
-    __syncthreads();                                         // s_scan may be used for something else
+    __syncthreads();                                         // s may be used for something else
     return r;
 }
 
@@ -252,9 +290,9 @@ __device__ __forceinline__ long long tree_out_row(const TreeArgs& a, int b, int 
 
 // Partial slot of CTA `cta` for an item that starts at tile `start`: 0 when the item began in
 // an earlier part, 1 when it begins in this one (and goes on in the next).
-__device__ __forceinline__ int tree_slot(int cta, int per, long long start)
+__device__ __forceinline__ int tree_slot(int cta, int per, int start)
 {
-    return 2 * cta + (start < (long long)cta * per ? 0 : 1);
+    return 2 * cta + (start < cta * per ? 0 : 1);
 }
 
 // Barrier of the first NT threads of the CTA (barrier 2 is theirs).
@@ -265,6 +303,13 @@ __device__ __forceinline__ void tree_sync()
     asm volatile("bar.sync 2, %0;" ::"n"(NT) : "memory");
 }
 
+// What the combining launch has to know of an item, by the CTA that begins it (one thread).
+__device__ __forceinline__ void tree_note_parts(const TreeArgs& a, int item, int start, int tiles, int per)
+{
+    const int c0 = start / per;
+    a.item_parts[item] = make_int2(c0, (start + tiles - 1) / per - c0 + 1);
+}
+
 // Called by the CTA's first NT threads once its (m, l, o) of a shared item is written: counts the
 // arrival; the last one merges the parts c0 .. c1 and writes the output rows.  `s_w`: floats of
 // shared memory free for use (at least as many as CTAs in the grid).
@@ -272,11 +317,11 @@ __device__ __forceinline__ void tree_sync()
 // maxima and sums (lane = part) and leaves the parts' weights in shared memory, then a thread
 // per four channels adds up its parts.
 template <int NT>
-__device__ void tree_arrive_and_merge(const TreeArgs& a, int item, long long start, int tiles, int per, int* s_last,
+__device__ void tree_arrive_and_merge(const TreeArgs& a, int item, int start, int tiles, int per, int* s_last,
                                       float* s_w, int n_w)
 {
     const int tid = threadIdx.x, lane = tid & 31;
-    const int c0 = int(start / per), np = int((start + tiles - 1) / per) - c0 + 1;
+    const int c0 = start / per, np = (start + tiles - 1) / per - c0 + 1;
     tree_sync<NT>();
     if (tid == 0) {
         const uint32_t before = atomic_add_acq_rel_u32(&a.counters[item], 1u);
@@ -346,6 +391,13 @@ __device__ void tree_arrive_and_merge(const TreeArgs& a, int item, long long sta
         tree_sync<NT>();
     }
 }
+
+// Items whose parts hold this much are added up by a launch of their own (a warp per row, over
+// the whole GPU) instead of by the CTA that arrives last, whose SM reads about 100 KB a
+// microsecond; the second launch costs the host 2.5 us and the device about as much.
+constexpr long long kTreeCombineBytes = 192 * 1024;
+void tree_choose_combine(TreeArgs& a, int ctas);
+cudaError_t launch_tree_combine(const TreeArgs& a, cudaStream_t s);
 
 // The tensor-core kernel (sa_tree_tc.cu): bf16 queries and K/V.
 cudaError_t launch_tree_tc(TreeArgs a, cudaStream_t s);

@@ -6,6 +6,11 @@
 // output tile in tensor memory (all 512 columns) and a softmax warpgroup pair of its own, so
 // that one slot's products run while the other's softmax does.
 //
+// Few rows: with at most 64 (32) query rows the 128 rows of the tiles hold each of them 2 (4)
+// times.  A copy takes its share of the tile's tokens, 16-token steps of P are zero in the
+// others, and the copies are joined at the item's end like parts.  The products cost the same,
+// the softmax, which they wait for, half (a quarter).
+//
 // Roles (20 warps):
 //   warps 0-7, 8-15  the slots' softmax: two threads of a slot own a query row, each half of the
 //               tile's tokens.  They read S, take the maximum, write P.  All four threads of a
@@ -183,7 +188,7 @@ struct TcShared {
     using SH = TcShape<D>;
     uint64_t full[SH::UNITS], empty[SH::UNITS], s_full[2], o_full[2], p_ready[2], o_read[2];
     union {
-        long long scan[kTreeScan<kTcThreads>];
+        int scan[kTreeScan<kTcThreads>];
         uint16_t top[2][2][2][128];             // half rows' maxima (slot, tile parity, half, row), bf16 rounded up
     };
     int token[SH::INFO][16];                    // first token of each entry of a tile
@@ -203,13 +208,12 @@ constexpr size_t tc_smem()
 
 // One item's share of this CTA's part: tiles [t0, t1) of the item's list.
 struct TcSegment {
-    int u, b, kvh, item, row0, t0, t1, tiles;
-    long long start;
+    int u, b, kvh, item, row0, t0, t1, tiles, start;
     TreeUnit un;
 };
 
-__device__ __forceinline__ bool tc_next(const TreeArgs& a, const TreePart& part, long long& lo, long long& start,
-                                        int& item, TcSegment& g)
+__device__ __forceinline__ bool tc_next(const TreeArgs& a, const TreePart& part, int& lo, int& start, int& item,
+                                        TcSegment& g)
 {
     while (lo < part.hi) {
         g.u = item / a.row_groups;
@@ -224,8 +228,8 @@ __device__ __forceinline__ bool tc_next(const TreeArgs& a, const TreePart& part,
         g.item = item;
         g.row0 = (item - g.u * a.row_groups) * a.item_rows;
         g.start = start;
-        g.t0 = int(lo - start);
-        g.t1 = int(min((long long)g.tiles, part.hi - start));
+        g.t0 = lo - start;
+        g.t1 = min(g.tiles, part.hi - start);
         lo = start + g.t1;
         if (g.t1 == g.tiles) {
             start += g.tiles;
@@ -236,7 +240,7 @@ __device__ __forceinline__ bool tc_next(const TreeArgs& a, const TreePart& part,
     return false;
 }
 
-template <int D>
+template <int D, int REP>
 __global__ void __launch_bounds__(kTcThreads, 1)
     tree_tc_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap)
 {
@@ -279,8 +283,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc_fence_after_sync();
     const uint32_t tmem = sh.tmem;
     const bool dense = a.sel_ids == nullptr;
-    long long lo = part.lo, start = part.start;
-    int item = part.item;
+    int lo = part.lo, start = part.start, item = part.item;
     TcSegment g;
 
     auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -394,6 +397,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTcRegsMany));
         constexpr int CW = D / 4;                                  // channels of a thread
+        constexpr int COPY = 128 / REP;                            // rows of a copy
+        constexpr int OWN = 4 / REP;                               // 16-token steps a thread has of its half
         const int s = warp >> 3;                                   // slot
         const int h = (warp >> 2) & 1;                             // which half of a tile's tokens
         const int row = 32 * (warp & 3) + lane;                    // query row of the item
@@ -401,6 +406,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
         const uint32_t s_tm = tmem + S_COL + s * 128 + 64 * h + lanes, o_tm = tmem + O_COL + ch0 + lanes;
         const int pair_bar = 5 + 4 * s + (warp & 3);               // the two warps that share rows of a slot
+        const int own0 = row / COPY * OWN;                         // the first of them
+        unsigned char* p_row = smem + SH::OFF_P + s * SH::P_TILE + h * SH::HALF + row * 128;
         const float scale = a.scale_log2;
         uint32_t tile0 = 0, unit0 = 0, soft_n = 0, acc_n[2] = {0, 0};
         while (tc_next(a, part, lo, start, item, g)) {
@@ -411,11 +418,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 constexpr int CPR = D / 8;                         // 16-byte chunks of a row
                 for (int i = tid; i < 128 * CPR; i += kTcSoft) {
                     const int r = i / CPR, c = i - r * CPR;
+                    const int ru = g.row0 + r % COPY;
                     uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (g.row0 + r < a.R)
+                    if (ru < a.R)
                         v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
-                                                                 tree_out_row(a, g.b, g.kvh, g.row0 + r) * D) + c);
+                                                                 tree_out_row(a, g.b, g.kvh, ru) * D) + c);
                     *reinterpret_cast<uint4*>(smem + (c >> 3) * SH::HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+                }
+                if (REP > 1) {                                     // the third part's tokens of other copies
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        *reinterpret_cast<uint4*>(p_row + 16 * x) = make_uint4(0u, 0u, 0u, 0u);
                 }
                 const long long list = dense ? g.un.len : (long long)g.un.n_ctx << a.bs_shift;
                 if ((long long)g.t1 * kTcTile > list) {            // this part meets drafts
@@ -429,11 +442,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             bar_sync(1, kTcSoft + 64);
 
-            const int r_unit = g.row0 + row;
-            const bool live = g.row0 + 32 * (warp & 3) < a.R;      // any of this warp's rows
+            const int r_unit = g.row0 + row % COPY;
+            const bool live = g.row0 + 32 * (warp & 3) % COPY < a.R;           // any of this warp's rows
             const int q_row = r_unit < a.R ? r_unit / a.G : 0;
+            // what the row sees of the drafts, and what any query sees
             const uint32_t* words = mask_b != nullptr ? mask_b + (long long)q_row * a.mask_words : nullptr;
-            const int limit = r_unit < a.R ? (mask_b != nullptr ? a.Q : q_row + 1) : 0;
+            const DraftView view = draft_view(words, a.mask_words, r_unit < a.R ? (mask_b != nullptr ? a.Q : q_row + 1) : 0);
             F2 acc[CW / 2];
 #pragma unroll
             for (int d = 0; d < CW / 2; ++d) acc[d] = make_f2(0.f, 0.f);
@@ -441,11 +455,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             float m_other = -INFINITY;                             // the other slot's reference
             float m_acc = -INFINITY;                               // what acc is relative to
 
-            // Tokens 8 g8 .. + 7 of local tile i that a query with these mask words sees.
-            auto tokens8 = [&](int i, int g8, const uint32_t* w, int lim) -> uint32_t {
+            // Tokens 8 g8 .. + 7 of local tile i that a query with this view sees.
+            auto tokens8 = [&](int i, int g8, const DraftView& v) -> uint32_t {
                 const int le = (g8 * 8) >> a.bs_shift;
                 return tree_tokens8(a, g.un, g8 * 8, (((g.t0 + i) * kTcTile) >> a.bs_shift) + le,
-                                    sh.token[(tile0 + i) % SH::INFO][le], w, lim);
+                                    sh.token[(tile0 + i) % SH::INFO][le], v);
             };
             // Adds O of local tile i to this thread's channels.
             auto add_up = [&](int i) {
@@ -469,13 +483,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     const float w1 = m == -INFINITY ? 0.f : fast_exp2(m - m_new);
                     m_acc = m_new;
                     const F2 w02 = make_f2(w0, w0), w12 = make_f2(w1, w1);
+                    const bool move = __any_sync(kFullMask, w0 != 1.f);          // rarely after the first tiles
 #pragma unroll
                     for (int c = 0; c < CW / 16; ++c) {
                         tmem_wait_ld16(v[c]);
+                        if (move) {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) acc[8 * c + j] = mul2(acc[8 * c + j], w02);
+                        }
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
                             acc[8 * c + j] = fma2(make_f2(__uint_as_float(v[c][2 * j]), __uint_as_float(v[c][2 * j + 1])), w12,
-                                                  mul2(acc[8 * c + j], w02));
+                                                  acc[8 * c + j]);
                     }
                     const uint32_t info = (tile0 + i) % SH::INFO;
                     if (sh.masked[info] != 0 && (sh.odd[info][0] | sh.odd[info][1] | sh.odd[info][2] | sh.odd[info][3])) {
@@ -483,7 +502,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll 1
                         for (int j = 0; j < kTcTile; ++j) {
                             if (!((sh.odd[info][j >> 5] >> (j & 31)) & 1u)) continue;
-                            if (!((tokens8(i, j >> 3, words, limit) >> (j & 7)) & 1u)) continue;
+                            if (unsigned(((j >> 4) & 3) - own0) >= unsigned(OWN) || !((tokens8(i, j >> 3, view) >> (j & 7)) & 1u)) continue;
                             const int2 en = tree_entry(a, g.u, g.un, (((g.t0 + i) * kTcTile) + j) >> a.bs_shift);
                             const uint16_t* vg = static_cast<const uint16_t*>(a.v_pages) +
                                                  (size_t(en.x) * a.bs + (j & (a.bs - 1))) * D + ch0;
@@ -514,9 +533,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     // infinities and NaN of drafts, which are added back where they are seen.
                     if (live) {
 #pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            const uint32_t mk = tokens8(i, 8 * h + 2 * c, words, limit) |
-                                                tokens8(i, 8 * h + 2 * c + 1, words, limit) << 8;
+                        for (int c = own0; c < own0 + OWN; ++c) {
+                            const uint32_t mk = tokens8(i, 8 * h + 2 * c, view) |
+                                                tokens8(i, 8 * h + 2 * c + 1, view) << 8;
                             uint32_t v[16];
                             __syncwarp();
                             tmem_ld16(s_tm + 16 * c, v);
@@ -533,7 +552,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     // the slot's two threads of number `row` look after token `row`, half its channels each
                     constexpr int CHUNKS = SH::HALVES * 4;
                     unsigned char* vrow = smem + SH::OFF_RING + vs * SH::UNIT + row * 128;
-                    const bool seen = (tokens8(i, row >> 3, sh.any, a.Q) >> (row & 7)) & 1u;
+                    const bool seen = (tokens8(i, row >> 3, draft_view(sh.any, a.mask_words, a.Q)) >> (row & 7)) & 1u;
                     const int first = sh.token[info][row >> a.bs_shift];
                     const bool draft = first != kNoToken && first + (row & (a.bs - 1)) >= g.un.len;
                     if (h == 0 && row < 4) sh.odd[info][row] = 0u;
@@ -571,13 +590,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 __syncwarp();
                 if (live) {
                     // ---- the maximum: of half a row, then of both halves ----------------------
-                    uint32_t va[2][16], vb[2][16];
-                    tmem_ld16(s_tm, va[0]);
-                    tmem_ld16(s_tm + 16, va[1]);
-                    tmem_wait_ld16(va[0]);
-                    tmem_wait_ld16(va[1]);
-                    tmem_ld16(s_tm + 32, vb[0]);
-                    tmem_ld16(s_tm + 48, vb[1]);
+                    // The first steps stay in registers; with four, two are read again below.
+                    constexpr int KEEP = OWN == 1 ? 1 : 2;
+                    uint32_t va[2][16], vb[KEEP][16];
                     float x0 = -INFINITY, x1 = -INFINITY;
                     auto top_of = [&](const uint32_t (&v)[16]) {
 #pragma unroll
@@ -586,12 +601,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             x1 = max3(x1, __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
                         }
                     };
-                    top_of(va[0]);
-                    top_of(va[1]);
-                    tmem_wait_ld16(vb[0]);
-                    tmem_wait_ld16(vb[1]);
-                    top_of(vb[0]);
-                    top_of(vb[1]);
+                    const uint32_t own_tm = s_tm + 16 * own0;
+                    if (OWN == 4) {
+                        tmem_ld16(own_tm + 32, va[0]);
+                        tmem_ld16(own_tm + 48, va[1]);
+                        tmem_wait_ld16(va[0]);
+                        tmem_wait_ld16(va[1]);
+                    }
+#pragma unroll
+                    for (int c = 0; c < KEEP; ++c) tmem_ld16(own_tm + 16 * c, vb[c]);
+                    if (OWN == 4) {
+                        top_of(va[0]);
+                        top_of(va[1]);
+                    }
+#pragma unroll
+                    for (int c = 0; c < KEEP; ++c) {
+                        tmem_wait_ld16(vb[c]);
+                        top_of(vb[c]);
+                    }
                     // Any reference near the maximum will do, as long as the row's threads use the
                     // same one: they exchange it as bf16, rounded up.
                     const uint32_t top = round_up_bf16(fmaxf(x0, x1) * scale), pr = soft_n & 1u;
@@ -603,7 +630,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     m_soft = m_new;
                     const float m_sub = m_new == -INFINITY ? 0.f : m_new;      // nothing seen yet: every weight is 0
                     // ---- the weights, in three bf16 parts, over the scores' own columns -----------
-                    unsigned char* p_row = smem + SH::OFF_P + s * SH::P_TILE + h * SH::HALF + row * 128;
                     const F2 scale2 = make_f2(scale, scale), m2 = make_f2(-m_sub, -m_sub);
                     F2 sum_a = make_f2(0.f, 0.f), sum_b = make_f2(0.f, 0.f);
                     auto weights = [&](int c, const uint32_t (&v)[16]) {
@@ -618,20 +644,29 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             hm[8 + j] = cut_bf16x2(p);
                             small[j] = __byte_perm(__float_as_uint(p.f.x), __float_as_uint(p.f.y), 0x7632);
                         }
-                        tmem_st16(s_tm + 16 * c, hm);
+                        tmem_st16(own_tm + 16 * c, hm);
 #pragma unroll
                         for (int x = 0; x < 2; ++x)
-                            *reinterpret_cast<uint4*>(p_row + (((2 * c + x) ^ (row & 7)) << 4)) =
+                            *reinterpret_cast<uint4*>(p_row + (((2 * (own0 + c) + x) ^ (row & 7)) << 4)) =
                                 make_uint4(small[4 * x], small[4 * x + 1], small[4 * x + 2], small[4 * x + 3]);
                     };
-                    weights(2, vb[0]);
-                    tmem_ld16(s_tm, va[0]);
-                    weights(3, vb[1]);
-                    tmem_wait_ld16(va[0]);
-                    tmem_ld16(s_tm + 16, va[1]);
-                    weights(0, va[0]);
-                    tmem_wait_ld16(va[1]);
-                    weights(1, va[1]);
+                    if (REP > 1) {
+                        uint32_t none[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) none[j] = 0u;
+#pragma unroll
+                        for (int c = OWN; c < 4; ++c) tmem_st16(s_tm + 16 * ((own0 + c) & 3), none);
+                    }
+                    weights(0, vb[0]);
+                    if (OWN == 4) tmem_ld16(own_tm + 32, va[0]);
+                    if (OWN > 1) weights(1, vb[KEEP - 1]);
+                    if (OWN == 4) {
+                        tmem_wait_ld16(va[0]);
+                        tmem_ld16(own_tm + 48, va[1]);
+                        weights(2, va[0]);
+                        tmem_wait_ld16(va[1]);
+                        weights(3, va[1]);
+                    }
                     const F2 sum = add2(sum_a, sum_b);
                     l_run += sum.f.x + sum.f.y;
                     tmem_wait_st();
@@ -644,31 +679,43 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (; added < ntl; ++added) add_up(added);
 
             // ---- the part's (m, l, o): the output itself, or a partial -------------------------
-            // The four threads' sums meet through the query tile, the rows leave through the P tiles
-            // (both idle now), a warp 512 bytes at a time.
+            // The four threads' sums (and the copies') meet through the query tile, the rows leave through
+            // the P tiles (both idle now), a warp 512 bytes at a time.
             const bool complete = g.t0 == 0 && g.t1 == g.tiles;
             constexpr int V4 = D / 4;
             float* x_l = reinterpret_cast<float*>(smem);                       // [slot][half][row]
+            float* x_m = x_l + 512;                                            // [row]
             float4* x_rows = reinterpret_cast<float4*>(smem + SH::OFF_P);
             auto cell = [&](int r, int c) -> float4& { return x_rows[r * V4 + ((c + r) & (V4 - 1))]; };
             if (live) l_run = m_soft == -INFINITY ? 0.f : l_run * fast_exp2(m_soft - m_acc);
             tree_sync<kTcSoft>();
             x_l[(2 * s + h) * 128 + row] = l_run;
+            if (s == 0 && h == 0) x_m[row] = m_acc;
             tree_sync<kTcSoft>();
             if (live) {
-                l_run = (x_l[row] + x_l[128 + row]) + (x_l[256 + row] + x_l[384 + row]);
-                float inv = 1.f;
+                float M = m_acc;
+#pragma unroll
+                for (int y = 1; y < REP; ++y) M = fmaxf(M, x_m[(row + y * COPY) & 127]);
+                float w = 1.f;
+                l_run = 0.f;
+#pragma unroll
+                for (int y = 0; y < REP; ++y) {                                // in the copies' order
+                    const int r = row % COPY + y * COPY;
+                    const float my = x_m[r], wy = REP == 1 ? 1.f : (my == -INFINITY ? 0.f : fast_exp2(my - M));
+                    l_run = fmaf(wy, (x_l[r] + x_l[128 + r]) + (x_l[256 + r] + x_l[384 + r]), l_run);
+                    if (REP > 1 && r == row) w = wy;
+                }
                 if (complete) {
-                    inv = l_run == 0.f ? 0.f : 1.f / l_run;
-                } else if (s == 0 && h == 0 && r_unit < a.R) {
+                    w = l_run == 0.f ? 0.f : w / l_run;
+                } else if (s == 0 && h == 0 && row < COPY && r_unit < a.R) {
                     const long long slot = (long long)tree_slot(blockIdx.x, part.per, g.start) * a.item_rows + row;
-                    a.part_m[slot] = m_acc;
+                    a.part_m[slot] = M;
                     a.part_l[slot] = l_run;
                 }
 #pragma unroll
                 for (int c = 0; c < CW / 4; ++c)
-                    cell(row, ch0 / 4 + c) = make_float4(acc[2 * c].f.x * inv, acc[2 * c].f.y * inv, acc[2 * c + 1].f.x * inv,
-                                                         acc[2 * c + 1].f.y * inv);
+                    cell(row, ch0 / 4 + c) = make_float4(acc[2 * c].f.x * w, acc[2 * c].f.y * w, acc[2 * c + 1].f.x * w,
+                                                         acc[2 * c + 1].f.y * w);
             }
             tree_sync<kTcSoft>();
             {
@@ -679,12 +726,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     const int r = i / V4, c = i % V4;
                     float4* dst = complete ? reinterpret_cast<float4*>(a.out) + tree_out_row(a, g.b, g.kvh, g.row0 + r) * V4
                                            : part_rows + (long long)r * V4;
-                    dst[c] = cell(r, c);
+                    float4 o = cell(r, c);
+#pragma unroll
+                    for (int y = 1; y < REP; ++y) {
+                        const float4 z = cell(r + y * COPY, c);
+                        o = make_float4(o.x + z.x, o.y + z.y, o.z + z.z, o.w + z.w);
+                    }
+                    dst[c] = o;
                 }
             }
-            if (!complete)
+            if (a.combine) {
+                if (tid == 0 && g.t0 == 0) tree_note_parts(a, g.item, g.start, g.tiles, part.per);
+            } else if (!complete) {
                 tree_arrive_and_merge<kTcSoft>(a, g.item, g.start, g.tiles, part.per, &sh.last,
                                                reinterpret_cast<float*>(smem + SH::OFF_P), 2 * SH::P_TILE / 4);
+            }
             tree_sync<kTcSoft>();                                  // this memory is free for the next item
             unit0 += 2 * ntl;
             tile0 += ntl;
@@ -727,12 +783,12 @@ inline cudaError_t encode_tree_map(CUtensorMap* map, const void* pool, int D, in
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int D>
-cudaError_t launch_tc_t(const TreeArgs& a, cudaStream_t s)
+template <int D, int REP>
+cudaError_t launch_tc_t(TreeArgs a, cudaStream_t s)
 {
     static std::atomic<unsigned long long> configured{0};   // devices set up
     const cudaError_t cfg = once_per_device(configured, [&]() -> cudaError_t {
-        return cudaFuncSetAttribute(tree_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(tree_tc_kernel<D, REP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     int(tc_smem<D>()));
     });
     if (cfg != cudaSuccess) return cfg;
@@ -743,8 +799,9 @@ cudaError_t launch_tc_t(const TreeArgs& a, cudaStream_t s)
     e = encode_tree_map(&vmap, a.v_pages, D, a.bs, tiles);
     if (e != cudaSuccess) return e;
     const int ctas = num_sms() < kTreeMaxCtas ? num_sms() : kTreeMaxCtas;
-    return launch_after_previous(tree_tc_kernel<D>, dim3(unsigned(ctas)), dim3(kTcThreads), tc_smem<D>(), s, a,
-                                 kmap, vmap);
+    tree_choose_combine(a, ctas);
+    e = launch_after_previous(tree_tc_kernel<D, REP>, dim3(unsigned(ctas)), dim3(kTcThreads), tc_smem<D>(), s, a, kmap, vmap);
+    return e == cudaSuccess && a.combine ? launch_tree_combine(a, s) : e;
 }
 
 }  // namespace
@@ -755,8 +812,10 @@ cudaError_t launch_tree_tc(TreeArgs a, cudaStream_t s)
     a.item_rows = tree_item_rows(a.R);
     a.row_groups = (a.R + a.item_rows - 1) / a.item_rows;
     a.min_per = 2;
-    a.slack = 7;
-    return a.D == 128 ? launch_tc_t<128>(a, s) : launch_tc_t<64>(a, s);
+    a.half_slack = 3;
+    if (a.R <= 32) return a.D == 128 ? launch_tc_t<128, 4>(a, s) : launch_tc_t<64, 4>(a, s);
+    if (a.R <= 64) return a.D == 128 ? launch_tc_t<128, 2>(a, s) : launch_tc_t<64, 2>(a, s);
+    return a.D == 128 ? launch_tc_t<128, 1>(a, s) : launch_tc_t<64, 1>(a, s);
 }
 
 }  // namespace sa
