@@ -15,6 +15,12 @@
 // rows over its lane groups, so a block's minimum and maximum need shuffles only; the block
 // belongs to one CTA, so the box is updated without atomics.  HBM traffic: every new row
 // once in and once out, the box rows of the touched blocks.
+//
+// Bound by memory on long inputs, by latency on short ones.  What bounds the long ones is the bytes
+// in flight: each thread copies its next three items ahead into shared memory.  48K rows of 32
+// query and 8 KV heads of 128 channels (1.2 GB moved): 198 us, 6.0 TB/s; with two plain loads in
+// flight a thread 248 us, with five items ahead 198 us, with 256 threads and 3 CTAs an SM 216 us.
+// One token: 4.5 us, the chain of lengths, pages, rows and box.
 #include "sa_common.cuh"
 #include "sa_internal.h"
 
@@ -24,6 +30,7 @@ namespace {
 constexpr int kAppThreads = 384;
 constexpr int kAppWarps = kAppThreads / 32;
 constexpr int kAppRun = 64;          // tokens of a run when blocks are smaller
+constexpr int kAppSlots = 4;         // items of a thread on their way from memory
 constexpr int kAppMaxBlocks = 8;     // blocks of a run
 
 struct AppendArgs {
@@ -37,6 +44,7 @@ struct AppendArgs {
     int num_rows, uniform_rows, uniform_len;
     int run;                 // tokens per run, a multiple of bs
     int runs_uniform;        // cu_rows null: runs a sequence may touch
+    int cs_words;            // 16-byte words of the cosines and sines
     int rotary, pairs;       // pairs: neighbouring channels turn together
 };
 
@@ -71,6 +79,40 @@ __device__ __forceinline__ Raw16<BF16> load16(const void* row, int a, int b)
     return r;
 }
 
+// A thread's own ring of kAppSlots items in shared memory, filled by asynchronous copies: nobody
+// else reads it, so waiting for the thread's own copies is all the order it needs.
+template <bool BF16>
+struct Ring16 {
+    static constexpr int WORDS = BF16 ? 2 : 4;
+    uint4* at;                                                // this thread's first word
+
+    __device__ __forceinline__ void fetch(int slot, const void* row, int a, int b) const
+    {
+        const uint4* pa = reinterpret_cast<const uint4*>(at_elem<BF16>(row, a));
+        const uint4* pb = reinterpret_cast<const uint4*>(at_elem<BF16>(row, b));
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                             smem_u32(at + (slot * WORDS + i) * kAppThreads)),
+                         "l"(i < WORDS / 2 ? pa + i : pb + (i - WORDS / 2))
+                         : "memory");
+    }
+    // Every step ends a group of copies, an empty one too, so that "all but the newest
+    // kAppSlots - 1" always means the item of this step.
+    __device__ __forceinline__ static void close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+    __device__ __forceinline__ static void wait()
+    {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAppSlots - 1) : "memory");
+    }
+    __device__ __forceinline__ Raw16<BF16> item(int slot) const
+    {
+        Raw16<BF16> r;
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) r.v[i] = at[(slot * WORDS + i) * kAppThreads];
+        return r;
+    }
+};
+
 template <bool BF16>
 __device__ __forceinline__ void widen16(const Raw16<BF16>& r, float (&f)[16])
 {
@@ -85,37 +127,52 @@ __device__ __forceinline__ void widen16(const Raw16<BF16>& r, float (&f)[16])
 
 // fp32 -> stored type (round to nearest even): 8 words of bf16 pairs, or 16 floats.
 template <bool BF16>
-__device__ __forceinline__ void store16(void* row, int a, int b, const float (&f)[16])
+__device__ __forceinline__ void narrow16(const float (&f)[16], uint32_t (&w)[BF16 ? 8 : 16])
 {
-    uint4* pa = reinterpret_cast<uint4*>(const_cast<char*>(at_elem<BF16>(row, a)));
-    uint4* pb = reinterpret_cast<uint4*>(const_cast<char*>(at_elem<BF16>(row, b)));
-    if constexpr (BF16) {
-        *pa = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                         pack_bf16x2(f[6], f[7]));
-        *pb = make_uint4(pack_bf16x2(f[8], f[9]), pack_bf16x2(f[10], f[11]), pack_bf16x2(f[12], f[13]),
-                         pack_bf16x2(f[14], f[15]));
-    } else {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            pa[i] = make_uint4(__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]), __float_as_uint(f[4 * i + 2]),
-                               __float_as_uint(f[4 * i + 3]));
-            pb[i] = make_uint4(__float_as_uint(f[8 + 4 * i]), __float_as_uint(f[9 + 4 * i]),
-                               __float_as_uint(f[10 + 4 * i]), __float_as_uint(f[11 + 4 * i]));
-        }
+    for (int i = 0; i < (BF16 ? 8 : 16); ++i) {
+        if constexpr (BF16) w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+        else w[i] = __float_as_uint(f[i]);
     }
 }
 
-// Rounds to the stored type's values (what a later reader of the page sees).
+template <bool BF16, int N>
+__device__ __forceinline__ void store16(void* row, int a, int b, const uint32_t (&w)[N])
+{
+    static_assert(N == (BF16 ? 8 : 16), "16 channels");
+    uint4* pa = reinterpret_cast<uint4*>(const_cast<char*>(at_elem<BF16>(row, a)));
+    uint4* pb = reinterpret_cast<uint4*>(const_cast<char*>(at_elem<BF16>(row, b)));
+#pragma unroll
+    for (int i = 0; i < N / 8; ++i) {
+        pa[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        pb[i] = make_uint4(w[N / 2 + 4 * i], w[N / 2 + 4 * i + 1], w[N / 2 + 4 * i + 2], w[N / 2 + 4 * i + 3]);
+    }
+}
+
 template <bool BF16>
-__device__ __forceinline__ void round16(float (&f)[16])
+__device__ __forceinline__ void store16(void* row, int a, int b, const float (&f)[16])
+{
+    uint32_t w[BF16 ? 8 : 16];
+    narrow16<BF16>(f, w);
+    store16<BF16>(row, a, b, w);
+}
+
+// The minimum and maximum of 16 channels over rows, in the stored type: its values are what a later
+// reader of the pages sees, and pairs of bf16 take half the registers.  A NaN counts as no value.
+template <bool BF16>
+struct Box16 {
+    uint32_t lo[BF16 ? 8 : 16], hi[BF16 ? 8 : 16];
+};
+
+template <bool BF16>
+__device__ __forceinline__ void box_join(uint32_t& lo, uint32_t& hi, uint32_t x, uint32_t y)
 {
     if constexpr (BF16) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t w = pack_bf16x2(f[2 * i], f[2 * i + 1]);
-            f[2 * i] = bf16_lo(w);
-            f[2 * i + 1] = bf16_hi(w);
-        }
+        asm("min.bf16x2 %0, %0, %1;" : "+r"(lo) : "r"(x));
+        asm("max.bf16x2 %0, %0, %1;" : "+r"(hi) : "r"(y));
+    } else {
+        lo = __float_as_uint(fminf(__uint_as_float(lo), __uint_as_float(x)));
+        hi = __float_as_uint(fmaxf(__uint_as_float(hi), __uint_as_float(y)));
     }
 }
 
@@ -248,6 +305,7 @@ __global__ void __launch_bounds__(kAppThreads, 2) append_kernel(AppendArgs a)
         float2* dst = reinterpret_cast<float2*>(s_cs + size_t(r) * (a.rotary / 4));
         dst[(((i & 7) >> 1) * rchunks + (i >> 3)) * 2 + (i & 1)] = make_float2(cn, sn);
     }
+    const Ring16<QB> ring{reinterpret_cast<uint4*>(s_cs) + a.cs_words + tid};
     __syncthreads();
 
     const int CH = a.D / 16, ch_shift = __ffs(CH) - 1;        // 16-channel items of a row
@@ -276,58 +334,57 @@ __global__ void __launch_bounds__(kAppThreads, 2) append_kernel(AppendArgs a)
                 const int ra = max(t0, tb) - t0, rb = min(t1, tb + a.bs) - t0;
                 char* tile = const_cast<char*>(
                     at_elem<KB>(a.k_pages, ((long long)page * a.Hkv + kvh) * a.bs * a.D));
-                float lo[16], hi[16];
+                constexpr int W = KB ? 8 : 16;
+                Box16<KB> box;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    lo[e] = INFINITY;
-                    hi[e] = -INFINITY;
+                for (int e = 0; e < W; ++e) {
+                    box.lo[e] = KB ? 0x7f807f80u : 0x7f800000u;
+                    box.hi[e] = KB ? 0xff80ff80u : 0xff800000u;
                 }
-                constexpr int U = 2;
-                for (int r = ra + rlane; live && r < rb; r += U * rl) {
-                    Raw16<QB> raw[U];
+                const int first_row = live ? ra + rlane : rb;
+                auto fetch = [&](int r, int slot) {
+                    if (r < rb) ring.fetch(slot, at_elem<QB>(a.k_new, (r0 + r) * a.k_stride + kvh * a.D), ea, eb);
+                    ring.close();
+                };
 #pragma unroll
-                    for (int u = 0; u < U; ++u)
-                        if (r + u * rl < rb)
-                            raw[u] = load16<QB>(at_elem<QB>(a.k_new, (r0 + r + u * rl) * a.k_stride + kvh * a.D), ea, eb);
+                for (int s = 0; s < kAppSlots - 1; ++s) fetch(first_row + s * rl, s);
+                int slot = 0;
+                for (int r = first_row; r < rb; r += rl) {
+                    fetch(r + (kAppSlots - 1) * rl, (slot + kAppSlots - 1) % kAppSlots);
+                    ring.wait();
+                    float f[16];
+                    widen16<QB>(ring.item(slot), f);
+                    if (c < rchunks) rotate16(f, s_cs + size_t(r) * (a.rotary / 4), c, rchunks, a.pairs);
+                    uint32_t w[W];
+                    narrow16<KB>(f, w);
+                    store16<KB>(const_cast<char*>(at_elem<KB>(tile, (long long)(t0 + r - tb) * a.D)), ea, eb, w);
 #pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        const int ru = r + u * rl;
-                        if (ru >= rb) break;
-                        float f[16];
-                        widen16<QB>(raw[u], f);
-                        if (c < rchunks) rotate16(f, s_cs + size_t(ru) * (a.rotary / 4), c, rchunks, a.pairs);
-                        round16<KB>(f);
-                        store16<KB>(const_cast<char*>(at_elem<KB>(tile, (long long)(t0 + ru - tb) * a.D)), ea, eb, f);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            lo[e] = fminf(lo[e], f[e]);
-                            hi[e] = fmaxf(hi[e], f[e]);
-                        }
-                    }
+                    for (int e = 0; e < W; ++e) box_join<KB>(box.lo[e], box.hi[e], w[e], w[e]);
+                    slot = (slot + 1) % kAppSlots;
                 }
                 if (a.kmin == nullptr) continue;
                 for (int m = CH; m < CH * rl; m <<= 1) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        lo[e] = fminf(lo[e], __shfl_xor_sync(kFullMask, lo[e], m));
-                        hi[e] = fmaxf(hi[e], __shfl_xor_sync(kFullMask, hi[e], m));
-                    }
+                    for (int e = 0; e < W; ++e)
+                        box_join<KB>(box.lo[e], box.hi[e], __shfl_xor_sync(kFullMask, box.lo[e], m),
+                                     __shfl_xor_sync(kFullMask, box.hi[e], m));
                 }
                 if (live && rlane == 0) {
                     const long long row = (((long long)b * a.Hkv + kvh) * a.nb_cap + blk0 + j) * a.D;
                     char* pmin = const_cast<char*>(at_elem<KB>(a.kmin, row));
                     char* pmax = const_cast<char*>(at_elem<KB>(a.kmax, row));
                     if (tb < t0) {                            // the block held tokens before
-                        float g[16];
-                        widen16<KB>(load16<KB>(pmin, ea, eb), g);
+                        const Raw16<KB> lo = load16<KB>(pmin, ea, eb), hi = load16<KB>(pmax, ea, eb);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) lo[e] = fminf(lo[e], g[e]);
-                        widen16<KB>(load16<KB>(pmax, ea, eb), g);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) hi[e] = fmaxf(hi[e], g[e]);
+                        for (int x = 0; x < W / 4; ++x) {
+                            box_join<KB>(box.lo[4 * x], box.hi[4 * x], lo.v[x].x, hi.v[x].x);
+                            box_join<KB>(box.lo[4 * x + 1], box.hi[4 * x + 1], lo.v[x].y, hi.v[x].y);
+                            box_join<KB>(box.lo[4 * x + 2], box.hi[4 * x + 2], lo.v[x].z, hi.v[x].z);
+                            box_join<KB>(box.lo[4 * x + 3], box.hi[4 * x + 3], lo.v[x].w, hi.v[x].w);
+                        }
                     }
-                    store16<KB>(pmin, ea, eb, lo);
-                    store16<KB>(pmax, ea, eb, hi);
+                    store16<KB>(pmin, ea, eb, box.lo);
+                    store16<KB>(pmax, ea, eb, box.hi);
                 }
             }
         }
@@ -335,65 +392,78 @@ __global__ void __launch_bounds__(kAppThreads, 2) append_kernel(AppendArgs a)
     // ---- queries and values: chunk fastest, then head, then row ----------------------
     {
         const int per_row = (qn + kvn) * CH;
-        const int items = n * per_row;
-        constexpr int U = 2;
-        for (int i0 = tid; i0 < items; i0 += U * kAppThreads) {
-            Raw16<QB> raw[U];
-            int row[U], head[U], ch[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int it = i0 + u * kAppThreads;
-                row[u] = it / per_row;
-                const int rest = it - row[u] * per_row;
-                ch[u] = rest & (CH - 1);
-                head[u] = rest >> ch_shift;
-                if (it >= items) continue;
-                if (head[u] < qn)
-                    raw[u] = load16<QB>(at_elem<QB>(a.q_new, (r0 + row[u]) * a.q_stride + (q0 + head[u]) * a.D),
-                                        elem_a(ch[u]), elem_b(ch[u]));
-                else
-                    raw[u] = load16<QB>(at_elem<QB>(a.v_new, (r0 + row[u]) * a.v_stride + (kv0 + head[u] - qn) * a.D),
-                                        16 * ch[u], 16 * ch[u] + 8);
+        if (per_row == 0) return;                             // without queries, more shares than heads
+        struct Cursor {
+            int row, rest;                                    // rest: channel chunk fastest, then head
+        };
+        const int rows_step = kAppThreads / per_row, rest_step = kAppThreads - rows_step * per_row;
+        auto step = [&](Cursor& x) {
+            x.row += rows_step;
+            x.rest += rest_step;
+            if (x.rest >= per_row) {
+                x.rest -= per_row;
+                ++x.row;
             }
+        };
+        auto fetch = [&](const Cursor& x, int slot) {
+            const int c = x.rest & (CH - 1), head = x.rest >> ch_shift;
+            if (x.row < n) {
+                if (head < qn)
+                    ring.fetch(slot, at_elem<QB>(a.q_new, (r0 + x.row) * a.q_stride + (q0 + head) * a.D), elem_a(c), elem_b(c));
+                else
+                    ring.fetch(slot, at_elem<QB>(a.v_new, (r0 + x.row) * a.v_stride + (kv0 + head - qn) * a.D), 16 * c,
+                               16 * c + 8);
+            }
+            ring.close();
+        };
+        Cursor at{tid / per_row, tid % per_row}, ahead = at;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (i0 + u * kAppThreads >= items) break;
-                const int c = ch[u];
-                if (head[u] < qn) {
-                    float f[16];
-                    widen16<QB>(raw[u], f);
-                    if (c < rchunks) rotate16(f, s_cs + size_t(row[u]) * (a.rotary / 4), c, rchunks, a.pairs);
-                    store16<QB>(const_cast<char*>(at_elem<QB>(a.q_out, ((long long)(r0 + row[u]) * a.Hq + q0 + head[u]) * a.D)),
-                                elem_a(c), elem_b(c), f);
-                    continue;
-                }
-                const int t = t0 + row[u], page = s_page[t / a.bs - blk0];
-                if (page < 0) continue;
-                void* dst = const_cast<char*>(at_elem<KB>(
-                    a.v_pages, (((long long)page * a.Hkv + kv0 + head[u] - qn) * a.bs + t % a.bs) * a.D));
-                if constexpr (QB == KB) {                     // same type: the bits as they are
-                    uint4* p = reinterpret_cast<uint4*>(const_cast<char*>(at_elem<KB>(dst, 16 * c)));
+        for (int s = 0; s < kAppSlots - 1; ++s) {
+            fetch(ahead, s);
+            step(ahead);
+        }
+        for (int slot = 0; at.row < n; step(at), slot = (slot + 1) % kAppSlots) {
+            fetch(ahead, (slot + kAppSlots - 1) % kAppSlots);
+            step(ahead);
+            ring.wait();
+            const Raw16<QB> raw = ring.item(slot);
+            const int c = at.rest & (CH - 1), head = at.rest >> ch_shift;
+            if (head < qn) {
+                float f[16];
+                widen16<QB>(raw, f);
+                if (c < rchunks) rotate16(f, s_cs + size_t(at.row) * (a.rotary / 4), c, rchunks, a.pairs);
+                store16<QB>(const_cast<char*>(at_elem<QB>(a.q_out, ((long long)(r0 + at.row) * a.Hq + q0 + head) * a.D)),
+                            elem_a(c), elem_b(c), f);
+                continue;
+            }
+            const int t = t0 + at.row, page = s_page[t / a.bs - blk0];
+            if (page < 0) continue;
+            void* dst = const_cast<char*>(at_elem<KB>(
+                a.v_pages, (((long long)page * a.Hkv + kv0 + head - qn) * a.bs + t % a.bs) * a.D));
+            if constexpr (QB == KB) {                         // same type: the bits as they are
+                uint4* p = reinterpret_cast<uint4*>(const_cast<char*>(at_elem<KB>(dst, 16 * c)));
 #pragma unroll
-                    for (int i = 0; i < (KB ? 2 : 4); ++i) p[i] = raw[u].v[i];
-                } else {
-                    float f[16];
-                    widen16<QB>(raw[u], f);
-                    store16<KB>(dst, 16 * c, 16 * c + 8, f);
-                }
+                for (int i = 0; i < (KB ? 2 : 4); ++i) p[i] = raw.v[i];
+            } else {
+                float f[16];
+                widen16<QB>(raw, f);
+                store16<KB>(dst, 16 * c, 16 * c + 8, f);
             }
         }
     }
 }
 
 template <bool QB, bool KB>
-cudaError_t launch_append_t(const AppendArgs& a, dim3 grid, size_t smem, cudaStream_t s)
+cudaError_t launch_append_t(const AppendArgs& a, dim3 grid, cudaStream_t s)
 {
     static std::atomic<unsigned long long> configured{0};   // devices set up
     const cudaError_t cfg = once_per_device(configured, [&]() -> cudaError_t {
-        return cudaFuncSetAttribute(append_kernel<QB, KB>, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 64 * 8);
+        return cudaFuncSetAttribute(append_kernel<QB, KB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    128 * 64 * 8 + kAppThreads * kAppSlots * (QB ? 32 : 64));
     });
     if (cfg != cudaSuccess) return cfg;
-    return launch_after_previous(append_kernel<QB, KB>, grid, dim3(kAppThreads), smem, s, a);
+    return launch_after_previous(append_kernel<QB, KB>, grid, dim3(kAppThreads),
+                                 16 * size_t(a.cs_words) + kAppThreads * kAppSlots * (QB ? 32 : 64), s, a);
 }
 
 // ------------------------------------------------------------------ commit ---
@@ -569,10 +639,10 @@ cudaError_t launch_append(const Geometry& g, const AppendCall& c, uint32_t* err,
     const long long items = (long long)rows * (g.Hq + 2 * g.Hkv) * (g.D / 16);
     unsigned Y = 1;
     while (Y < 8 && runs * Y < num_sms() && items / Y > 2 * kAppThreads) Y *= 2;
-    const size_t smem = size_t(rows < a.run && !c.cu_rows ? rows : a.run) * (c.rotary_dim / 2) * 8;
+    a.cs_words = (rows < a.run && !c.cu_rows ? rows : a.run) * (c.rotary_dim / 4);
     const dim3 grid{unsigned(runs), Y, 1};
-    if (g.q_bf16) return g.kv_bf16 ? launch_append_t<true, true>(a, grid, smem, s) : launch_append_t<true, false>(a, grid, smem, s);
-    return g.kv_bf16 ? launch_append_t<false, true>(a, grid, smem, s) : launch_append_t<false, false>(a, grid, smem, s);
+    if (g.q_bf16) return g.kv_bf16 ? launch_append_t<true, true>(a, grid, s) : launch_append_t<true, false>(a, grid, s);
+    return g.kv_bf16 ? launch_append_t<false, true>(a, grid, s) : launch_append_t<false, false>(a, grid, s);
 }
 
 cudaError_t launch_commit(const Geometry& g, const int32_t* seq_lens, const int32_t* path, int path_stride,
