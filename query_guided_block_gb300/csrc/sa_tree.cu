@@ -23,6 +23,7 @@ namespace {
 
 constexpr int kTrThreads = 128;
 constexpr int kTrTile = 64;
+constexpr int kTreeSmallWork = 4;
 constexpr int kTrEntries = 512;      // list entries resolved at a time
 constexpr int kTrInfo = 4;           // tiles looked up ahead of their copies, at least the stages + 1
 
@@ -632,14 +633,19 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 }  // namespace
 
+// Tokens that a sequence's queries meet at most, rounded up to whole selected blocks.
+static long long tree_list(const TreeArgs& a)
+{
+    return a.sel_ids == nullptr ? (long long)a.N + a.Q : (long long)a.sel_stride * a.bs + a.Q + 2 * a.bs;
+}
+
 void tree_choose_combine(TreeArgs& a, int ctas)
 {
     const long long items = (long long)a.B * a.Hkv * a.row_groups;
-    const long long list = a.sel_ids == nullptr ? (long long)a.N + a.Q : (long long)a.sel_stride * a.bs + a.Q + 2 * a.bs;
-    long long parts = (list + a.tile - 1) / a.tile / a.min_per;      // of an item at most
+    long long parts = (tree_list(a) + a.tile - 1) / a.tile / a.min_per;      // of an item at most
     if (parts > ctas / items) parts = ctas / items;
     const int rows = a.R < a.item_rows ? a.R : a.item_rows;
-    a.combine = parts * rows * a.D * 4 >= kTreeCombineBytes;
+    a.combine = rows >= kTreeCombineRows && parts * rows * a.D * 4 >= kTreeCombineBytes;
 }
 
 cudaError_t launch_tree_combine(const TreeArgs& a, cudaStream_t s)
@@ -703,7 +709,8 @@ cudaError_t launch_tree(const Geometry& g, const TreeCall& c, char* ws, cudaStre
     a.item_parts = reinterpret_cast<int2*>(ws + L.item_parts);
     a.err = reinterpret_cast<uint32_t*>(ws);
     if (g.kv_bf16 && g.q_bf16) {
-        if (a.R > 16) return launch_tree_tc(a, s);
+        const long long work = (long long)g.units() * ((a.R + 15) / 16) * ((tree_list(a) + kTrTile - 1) / kTrTile);
+        if (a.R > 16 && work > (long long)kTreeSmallWork * num_sms()) return launch_tree_tc(a, s);
         return g.D == 128 ? launch_tree_t<128, true, 1, 1>(a, s) : launch_tree_t<64, true, 1, 1>(a, s);
     }
     if (g.kv_bf16) return g.D == 128 ? launch_tree_rows<128, true, 3>(a, s) : launch_tree_rows<64, true, 3>(a, s);

@@ -395,7 +395,8 @@ __device__ void tree_arrive_and_merge(const TreeArgs& a, int item, int start, in
 // Items whose parts hold this much are added up by a launch of their own (a warp per row, over
 // the whole GPU) instead of by the CTA that arrives last, whose SM reads about 100 KB a
 // microsecond; the second launch costs the host 2.5 us and the device about as much.
-constexpr long long kTreeCombineBytes = 192 * 1024;
+constexpr long long kTreeCombineBytes = 16 * 1024;
+constexpr int kTreeCombineRows = 8;
 void tree_choose_combine(TreeArgs& a, int ctas);
 cudaError_t launch_tree_combine(const TreeArgs& a, cudaStream_t s);
 
