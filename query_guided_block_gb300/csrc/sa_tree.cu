@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
             ++item;
             continue;
         }
-        const int t0 = lo - start, t1 = min(tiles, part.hi - start);
+        const int t0 = lo - start, t1 = part.whole ? tiles : min(tiles, part.hi - start);
         const int row0 = rg * ROWS;                          // first unit row of the item
         const uint32_t* mask_b = a.mask != nullptr ? a.mask + (long long)b * a.Q * a.mask_words : nullptr;
 

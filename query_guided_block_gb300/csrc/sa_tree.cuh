@@ -27,7 +27,7 @@ inline int tree_item_rows(int R) { return R <= 16 ? 16 : (R <= 64 ? 64 : kTreeMa
 
 // Words of shared memory that tree_part needs.
 template <int NT>
-constexpr int kTreeScan = 5 * (NT / 32) + 3;
+constexpr int kTreeScan = 6 * (NT / 32) + 3;
 
 struct TreeArgs {
     const void* q;
@@ -176,6 +176,7 @@ struct TreePart {
     int start;        // first tile of `item`
     int item;
     int per;          // tiles of a part
+    bool whole;       // the items that begin in the part belong to it to their ends
 };
 
 // Found by all threads (NT of them): as many warps as the units need count tiles, the others
@@ -194,7 +195,8 @@ __device__ TreePart tree_part(const TreeArgs& a, int* s)
     int* s_sum = s;                   // [W] tiles
     int* s_parts = s + W;             // [3][W] parts at three lengths
     int* s_line = s + 4 * W;          // [W] stretches of the line
-    int* s_found = s + 5 * W;         // item, start, end
+    int* s_longest = s + 5 * W;       // [W] tiles of the longest item
+    int* s_found = s + 6 * W;         // item, start, end
 
     int tiles = 0;
     for (int u = u0; u < u1; ++u) tiles += tiles_of(u);
@@ -208,10 +210,12 @@ __device__ TreePart tree_part(const TreeArgs& a, int* s)
     for (int w = 0; w < warps; ++w) total += s_sum[w];
     int per = max(a.min_per, (total + ctas - 1) / ctas);
     // Items may begin with a part if the parts then suffice: at no cost, with half of the slack
-    // added to a part, or with all of it.
-    int parts[3] = {0, 0, 0};
+    // added to a part, or with all of it.  Where items are too many for that and none is longer
+    // than the slack, the parts take whole items, those that begin in them.
+    int parts[3] = {0, 0, 0}, longest = 0;
     for (int u = u0; u < u1; ++u) {
         const int t = tiles_of(u);
+        longest = max(longest, t);
 #pragma unroll
         for (int x = 0; x < 3; ++x) parts[x] += (t + per + x * a.half_slack - 1) / (per + x * a.half_slack);
     }
@@ -222,10 +226,13 @@ __device__ TreePart tree_part(const TreeArgs& a, int* s)
             const int sum = __reduce_add_sync(kFullMask, parts[x]);
             if (lane == 0) s_parts[x * W + warp] = sum;
         }
+        longest = __reduce_max_sync(kFullMask, longest);
+        if (lane == 0) s_longest[warp] = longest;
     }
     __syncthreads();
     int all[3] = {0, 0, 0};
     for (int w = 0; w < warps; ++w) {
+        longest = max(longest, s_longest[w]);
 #pragma unroll
         for (int x = 0; x < 3; ++x) all[x] += s_parts[x * W + w];
     }
@@ -251,6 +258,7 @@ __device__ TreePart tree_part(const TreeArgs& a, int* s)
     __syncthreads();
     TreePart r;
     r.per = per;
+    r.whole = !aligned && longest <= 2 * a.half_slack;
     r.lo = int(min((long long)total, (long long)blockIdx.x * per));
     r.hi = int(min((long long)total, (long long)r.lo + per));
     if (r.lo < r.hi && mine > 0) {
@@ -262,8 +270,9 @@ __device__ TreePart tree_part(const TreeArgs& a, int* s)
                 const int len = aligned ? (t + per - 1) / per * per : t;      // the item's stretch of the line
                 if (r.lo < at + len * a.row_groups) {
                     const int rg = (r.lo - at) / len;
-                    s_found[0] = u * a.row_groups + rg;
-                    s_found[1] = at + rg * len;
+                    const int next = r.whole && at + rg * len < r.lo;         // it began in an earlier part
+                    s_found[0] = u * a.row_groups + rg + next;
+                    s_found[1] = at + (rg + next) * len;
                     s_found[2] = aligned ? at + rg * len + t : r.hi;
                     break;
                 }
@@ -276,7 +285,9 @@ __device__ TreePart tree_part(const TreeArgs& a, int* s)
         r.item = s_found[0];
         r.start = s_found[1];
         r.hi = min(r.hi, s_found[2]);
+        if (r.whole) r.lo = r.start;
     }
+    if (r.whole) r.per = max(total, 1);                      // every item is one part
     __syncthreads();                                         // s may be used for something else
     return r;
 }
@@ -292,7 +303,7 @@ __device__ __forceinline__ long long tree_out_row(const TreeArgs& a, int b, int 
 // an earlier part, 1 when it begins in this one (and goes on in the next).
 __device__ __forceinline__ int tree_slot(int cta, int per, int start)
 {
-    return 2 * cta + (start < cta * per ? 0 : 1);
+    return 2 * cta + (start < (long long)cta * per ? 0 : 1);
 }
 
 // Barrier of the first NT threads of the CTA (barrier 2 is theirs).

@@ -263,7 +263,7 @@ __device__ __forceinline__ bool tc_next(const TreeArgs& a, const TreePart& part,
         g.row0 = (item - g.u * a.row_groups) * a.item_rows;
         g.start = start;
         g.t0 = lo - start;
-        g.t1 = min(g.tiles, part.hi - start);
+        g.t1 = part.whole ? g.tiles : min(g.tiles, part.hi - start);
         lo = start + g.t1;
         if (g.t1 == g.tiles) {
             start += g.tiles;
