@@ -642,10 +642,15 @@ static long long tree_list(const TreeArgs& a)
 void tree_choose_combine(TreeArgs& a, int ctas)
 {
     const long long items = (long long)a.B * a.Hkv * a.row_groups;
-    long long parts = (tree_list(a) + a.tile - 1) / a.tile / a.min_per;      // of an item at most
+    const long long tiles = (tree_list(a) + a.tile - 1) / a.tile;    // of an item at most
+    long long parts = tiles / a.min_per;
     if (parts > ctas / items) parts = ctas / items;
+    // With more than half as many items as CTAs, those of equal length need no join unless they are
+    // longer than a part and the slack that keeps them whole.
+    const long long part = items <= ctas ? (items * tiles + ctas - 1) / ctas : 0;
+    const bool joins = parts > 1 || tiles > part + 2 * a.half_slack;
     const int rows = a.R < a.item_rows ? a.R : a.item_rows;
-    a.combine = rows >= kTreeCombineRows && parts * rows * a.D * 4 >= kTreeCombineBytes;
+    a.combine = joins && rows >= kTreeCombineRows && (parts > 2 ? parts : 2) * rows * a.D * 4 >= kTreeCombineBytes;
 }
 
 cudaError_t launch_tree_combine(const TreeArgs& a, cudaStream_t s)

@@ -70,7 +70,7 @@ struct TcShape {
     // tile, where the copies are added up in turn.
     static constexpr int OFF_ROWS = P_TILES ? OFF_P : 0;
     static constexpr int ROWS_BYTES = P_TILES ? P_TILES * P_TILE : Q_TILE;
-    static_assert(ROWS_BYTES >= 128 / REP * D * 4, "the rows of an item");
+    static_assert(ROWS_BYTES >= (REP == 4 ? 2 : 1) * (128 / REP) * D * 4, "an item's rows, of two copies with four");
 };
 
 // Where the weights of tokens 16 k .. + 15 lie in the 64 columns of their half tile's scores: two
@@ -409,6 +409,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         const uint32_t info = (tile0 + i) % SH::INFO;
                         if (mine) sh.token[info][lane] = ok ? en.y : kNoToken;
                         if (lane == 0) sh.masked[info] = any_partly;
+                        if (lane < 4) sh.odd[info][lane] = 0u;
                         __syncwarp();
                         load(unit0 + k_unit(i), &kmap, en.x, n_ok);
                     }
@@ -558,17 +559,32 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             constexpr int V4 = D / 4;
             float4* x_row = reinterpret_cast<float4*>(smem + SH::OFF_ROWS) + row % COPY * V4;
-#pragma unroll 1
-            for (int y = 0; y < (REP == 4 ? 3 : REP); ++y) {       // one copy after another
-                if (REP > 1) bar_sync(14, kTcWork - kTcSoft);
-                if (live && row / COPY == y) {
+            auto scaled = [&](int c) {
+                return make_float4(acc[2 * c].f.x * w, acc[2 * c].f.y * w, acc[2 * c + 1].f.x * w, acc[2 * c + 1].f.y * w);
+            };
+            if (REP > 1) {                                         // the first copy adds up the others
+                bar_sync(14, kTcWork - kTcSoft);                   // the sums there have been read
+                if (live && row >= COPY) {
 #pragma unroll
-                    for (int c = 0; c < V4; ++c) {
-                        float4& x = x_row[(c + row) & (V4 - 1)];
-                        float4 o = make_float4(acc[2 * c].f.x * w, acc[2 * c].f.y * w, acc[2 * c + 1].f.x * w,
-                                               acc[2 * c + 1].f.y * w);
-                        if (REP > 1 && y > 0) o = make_float4(o.x + x.x, o.y + x.y, o.z + x.z, o.w + x.w);
-                        x = o;
+                    for (int c = 0; c < V4; ++c) x_row[(row / COPY - 1) * COPY * V4 + ((c + row) & (V4 - 1))] = scaled(c);
+                }
+                bar_sync(14, kTcWork - kTcSoft);
+            }
+            if (live && row < COPY) {
+#pragma unroll
+                for (int c0 = 0; c0 < V4; c0 += 4) {
+                    float4 x[REP == 4 ? 2 : 1][4];
+#pragma unroll
+                    for (int y = 0; y < (REP == 4 ? 2 : REP - 1); ++y)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) x[y][c] = x_row[y * COPY * V4 + ((c0 + c + row) & (V4 - 1))];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        float4 o = scaled(c0 + c);
+#pragma unroll
+                        for (int y = 0; y < (REP == 4 ? 2 : REP - 1); ++y)
+                            o = make_float4(o.x + x[y][c].x, o.y + x[y][c].y, o.z + x[y][c].z, o.w + x[y][c].w);
+                        x_row[(c0 + c + row) & (V4 - 1)] = o;
                     }
                 }
             }
@@ -592,6 +608,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             {
                 constexpr int CPR = D / 8;                         // 16-byte chunks of a row
                 constexpr int N = COPY * CPR / kTcSoft;            // chunks of this thread
+                const long long list = dense ? g.un.len : (long long)g.un.n_ctx << a.bs_shift;
+                const bool drafts = (long long)g.t1 * kTcTile > list;               // this part meets drafts
+                const int bits = mask_b != nullptr && drafts ? a.Q * a.mask_words : 0;
+                const uint32_t first_bits = tid < bits ? __ldg(mask_b + tid) : 0u;  // on its way with the queries
                 uint4 v[N];
 #pragma unroll
                 for (int x = 0; x < N; ++x) {
@@ -609,12 +629,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         *reinterpret_cast<uint4*>(smem + (c >> 3) * SH::HALF + (r + y * COPY) * 128 +
                                                   (((c & 7) ^ (r & 7)) << 4)) = v[x];
                 }
-                const long long list = dense ? g.un.len : (long long)g.un.n_ctx << a.bs_shift;
-                if ((long long)g.t1 * kTcTile > list) {            // this part meets drafts
+                if (drafts) {
                     if (tid < a.mask_words) sh.any[tid] = mask_b == nullptr ? ~0u : 0u;
                     if (mask_b != nullptr) {
                         bar_sync(15, kTcSoft);
-                        for (int i = tid; i < a.Q * a.mask_words; i += kTcSoft) atomicOr(&sh.any[i % a.mask_words], mask_b[i]);
+                        if (tid < bits) atomicOr(&sh.any[tid % a.mask_words], first_bits);
+                        for (int i = tid + kTcSoft; i < bits; i += kTcSoft) atomicOr(&sh.any[i % a.mask_words], mask_b[i]);
                     }
                 }
                 fence_proxy_async_smem();                          // before the tensor core uses this memory
@@ -671,10 +691,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     const bool seen = (tokens8(i, row >> 3, draft_view(sh.any, a.mask_words, a.Q)) >> (row & 7)) & 1u;
                     const int first = sh.token[info][row >> a.bs_shift];
                     const bool draft = first != kNoToken && first + (row & (a.bs - 1)) >= g.un.len;
-                    if (h == 0 && row < 4) sh.odd[info][row] = 0u;
-                    bar_sync(3, kTcSoft);
                     bool changed = false;
-                    for (int c = h * CHUNKS; c < (h + 1) * CHUNKS; ++c) {
+                    for (int c = h * CHUNKS; c < (h + 1) * CHUNKS && (!seen || draft); ++c) {
                         uint4* at = reinterpret_cast<uint4*>(vrow + (c >> 3) * SH::HALF + (c & 7) * 16);
                         if (!seen) {
                             *at = make_uint4(0u, 0u, 0u, 0u);
