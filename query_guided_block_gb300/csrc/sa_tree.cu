@@ -23,6 +23,11 @@ namespace {
 
 constexpr int kTrThreads = 128;
 constexpr int kTrTile = 64;
+// bf16 calls with more than 16 rows and at most so many tiles (of 64 tokens x 16 rows) an SM run here
+// too, 16 rows to an item: a tensor-memory item takes longer to begin and end.  24 rows over 777 tokens
+// (1.4 tiles an SM) 13.4 us against 19.0, 64 rows over 777 (2.7) 14.4 against 18.7, over 4 x 300 (4.2)
+// 18.1 against 18.7, 32 rows over 4 x 777 (5.5) 21.2 against 20.0, 128 rows over 777 (5.5) 21.5
+// against 19.1, 64 rows over 16 x 100 (6.7) 22.2 against 15.6.
 constexpr int kTreeSmallWork = 4;
 constexpr int kTrEntries = 512;      // list entries resolved at a time
 constexpr int kTrInfo = 4;           // tiles looked up ahead of their copies, at least the stages + 1
