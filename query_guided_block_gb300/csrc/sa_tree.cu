@@ -114,7 +114,8 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
     float* s_q = reinterpret_cast<float*>(smem + SH::STAGES * SH::STAGE);   // fp32 K/V: [ROWS][Q_ROW]
 
     allow_dependents_early();
-    grid_dependency_wait();   // queries, pages and lengths may come from the previous kernel
+    grid_dependency_wait();   // queries, pages and lengths may come from the previous kernel,
+                              // so nothing of them is read through the read-only cache
 
     const TreePart part = tree_part<kTrThreads>(a, s_scan);
     const bool dense = a.sel_ids == nullptr;
@@ -155,9 +156,9 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
                     const bool have = ((hc & 1) ? r_hi : r_lo) < a.R;
                     const size_t at = ((hc & 1) ? at_hi : at_lo) + ks * 16 + (hc >> 1) * 8;
                     if constexpr (NQ == 1) {
-                        qa[0][ks][hc] = have ? __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) + at)) : 0u;
+                        qa[0][ks][hc] = have ? *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) + at) : 0u;
                     } else {
-                        float2 f = have ? __ldg(reinterpret_cast<const float2*>(static_cast<const float*>(a.q) + at))
+                        float2 f = have ? *reinterpret_cast<const float2*>(static_cast<const float*>(a.q) + at)
                                         : make_float2(0.f, 0.f);
 #pragma unroll
                         for (int part_q = 0; part_q < NQ; ++part_q) qa[part_q][ks][hc] = cut_bf16x2(f.x, f.y);

@@ -542,7 +542,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                 (size_t(tree_entry(a, g.u, g.un, e).x) * a.bs + (j & (a.bs - 1))) * D);
 #pragma unroll
                             for (int x = 0; x < D / 2; ++x) {
-                                const uint32_t w = __ldg(vg + x);
+                                const uint32_t w = vg[x];
                                 if ((w & 0x7f80u) == 0x7f80u) acc[x].f.x += bf16_lo(w);
                                 if ((w & 0x7f800000u) == 0x7f800000u) acc[x].f.y += bf16_hi(w);
                             }
@@ -617,14 +617,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const long long list = dense ? g.un.len : (long long)g.un.n_ctx << a.bs_shift;
                 const bool drafts = (long long)g.t1 * kTcTile > list;               // this part meets drafts
                 const int bits = mask_b != nullptr && drafts ? a.Q * a.mask_words : 0;
-                const uint32_t first_bits = tid < bits ? __ldg(mask_b + tid) : 0u;  // on its way with the queries
+                const uint32_t first_bits = tid < bits ? mask_b[tid] : 0u;  // on its way with the queries
                 uint4 v[N];
 #pragma unroll
                 for (int x = 0; x < N; ++x) {
                     const int r = (tid + x * kTcSoft) / CPR, c = (tid + x * kTcSoft) % CPR;
                     v[x] = make_uint4(0u, 0u, 0u, 0u);
                     if (g.row0 + r < a.R)
-                        v[x] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
+                        v[x] = *(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
                                                                     tree_out_row(a, g.b, g.kvh, g.row0 + r) * D) + c);
                 }
 #pragma unroll
