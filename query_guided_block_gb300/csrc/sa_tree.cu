@@ -165,10 +165,24 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
                     }
                 }
         } else {
-            for (int i = tid; i < ROWS * D; i += kTrThreads) {
-                const int rr = i / D, d = i - rr * D;
-                s_q[rr * SH::Q_ROW + d] =
-                    row0 + rr < a.R ? load_q(a.q, size_t(tree_out_row(a, b, kvh, row0 + rr)) * D + d, a.q_bf16 != 0) : 0.f;
+#pragma unroll
+            for (int i = tid; i < ROWS * (D / 4); i += kTrThreads) {
+                const int rr = i / (D / 4), d = (i - rr * (D / 4)) * 4;
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (row0 + rr < a.R) {
+                    const size_t at = size_t(tree_out_row(a, b, kvh, row0 + rr)) * D + d;
+                    if (a.q_bf16) {
+                        const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q) + at);
+                        x = make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+                    } else {
+                        x = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at);
+                    }
+                }
+                float* dst = s_q + rr * SH::Q_ROW + d;
+                dst[0] = x.x;
+                dst[1] = x.y;
+                dst[2] = x.z;
+                dst[3] = x.w;
             }
         }
 
