@@ -127,6 +127,10 @@ CASES = {
     "bf16_rows_fp32_cache": (Case(batch=2, block=128, lens=(100, 300), drafts=300, kv=F32), [300, 129], {}),
     "many_heads": (Case(batch=2, hq=64, hkv=64, block=128, lens=(129, 0), drafts=130), [130, 128], {}),
     "one_kv_head": (Case(batch=3, hq=8, hkv=1, dim=64, block=8, lens=(8, 16, 300), drafts=9), [9, 8, 7], {}),
+    "rows_longer_than_a_step": (Case(batch=80, hq=64, hkv=8, context=40, lens=tuple(7 * i % 41 for i in range(80)), drafts=5),
+                                [i % 6 for i in range(80)], {}),
+    "keys_only_one_head": (Case(batch=2, hq=8, hkv=1, lens=(33, 5), drafts=130), [130, 64], dict(with_q=False)),
+    "long_prompt": (Case(batch=1, hq=4, hkv=2, dim=64, block=16, context=1000, lens=(77,), drafts=900), [900], {}),
     "more_sequences_than_threads": (Case(batch=401, hq=2, hkv=1, dim=64, block=8, context=9,
                                          lens=tuple(i % 10 for i in range(401)), drafts=3), [i % 4 for i in range(401)], {}),
 }

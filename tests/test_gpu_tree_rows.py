@@ -222,3 +222,38 @@ def test_bad_lengths_and_pages_are_reported_and_skipped():
         assert ((out[1].cpu().double() - ref[1]).abs() <= bnd[1]).all()
         for b in (0, 2):
             assert ((out[b].cpu().double() - exact[b]).abs() <= bound[b]).all()
+
+
+def test_two_streams_at_once():
+    """Two problems, each with its own workspace, on two streams without any order between them."""
+    probs = [Case(batch=2, drafts=16, context=LONG, lens=(3000, 100)), Case(batch=1, drafts=7, context=LONG, seed=1, lens=(5000,)),
+             Case(batch=2, drafts=3, seed=2)]
+    data, expect = [], []
+    for x in probs:
+        table = x.block_table()
+        q, pools = x.normal("q", x.batch, x.drafts, x.hq, x.dim).cuda(), [t.cuda() for t in x.fill(x.pools(), table)]
+        lens, p = torch.tensor(x.all_lens, dtype=torch.int32, device="cuda"), x.params()
+        data.append((p, q, pools[0], pools[1], table.cuda(), lens, workspace(p)))
+        expect.append(call(x, q, pools, table)[0])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in probs]
+    outs = [[torch.zeros_like(e) for _ in range(30)] for e in expect]
+    torch.cuda.synchronize()
+    for k in range(30):
+        for (p, q, kp, vp, table, lens, ws), o, s in zip(data, outs, streams):
+            B.sparse_attn_tree_decode(p, q, kp, vp, table, o[k], ws, seq_lens=lens, stream=s)
+    torch.cuda.synchronize()
+    for (*_, ws), o, e in zip(data, outs, expect):
+        assert B.sparse_attn_get_device_error(ws) == 0
+        assert all(torch.equal(x, e) for x in o)
+
+
+def test_growing_context_under_one_parameter_set():
+    """The problem's length only bounds the sequences': right with little room above them and with much
+    (the two kernels)."""
+    for room in (300, LONG):
+        c = Case(batch=2, drafts=9, context=room, lens=(299, 64))
+        table, pools, q = prepared(c)
+        out, ws = call(c, q, pools, table)
+        check(c, out, *tree_exact(c, q, pools, table))
+        assert B.sparse_attn_get_device_error(ws) == 0
