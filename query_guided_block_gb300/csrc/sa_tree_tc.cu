@@ -208,13 +208,14 @@ __device__ __forceinline__ F2 less(F2 p, uint32_t mask)
     return sub2(p, make_f2(__uint_as_float(__float_as_uint(p.f.x) & mask), __uint_as_float(__float_as_uint(p.f.y) & mask)));
 }
 
-// The smallest bf16 not below x, as an fp32's bits (NaN may become anything).
-__device__ __forceinline__ uint32_t round_up_bf16(float x)
-{
-    const uint32_t u = __float_as_uint(x);
-    // toward zero is up for negative values; positive ones go up unless they are exact
-    return (u & 0x80000000u) ? u & 0xffff0000u : (u + (x < INFINITY ? 0xffffu : 0u)) & 0xffff0000u;
-}
+// fp32 values as whole numbers of the same order (its own inverse), so that an integer maximum finds
+// the largest.
+__device__ __forceinline__ int ordered_bits(int x) { return x ^ ((x >> 31) & 0x7fffffff); }
+constexpr int kOrderedLeast = int(0x807fffffu);                     // -infinity
+
+// A row's reference for a tile: the maximum, rounded up to a whole number so that it changes rarely.
+// It lies at most 1 above the maximum whatever its size: weights below 2^-126 of it come out as 0.
+__device__ __forceinline__ float tc_reference(float m, int top) { return fmaxf(m, ceilf(__int_as_float(ordered_bits(top)))); }
 
 // Register shares: the CTA starts with 16 warps x 128.  With 152 for both the output threads have two
 // loads fewer in flight: 96 rows over 128K tokens 123 us instead of 119.
@@ -230,7 +231,7 @@ struct TcShared {
     uint64_t full[SH::UNITS], empty[SH::UNITS], s_full[2], o_full[2], p_ready[2], o_read[2];
     union {
         int scan[kTreeScan<kTcThreads>];
-        uint16_t top[4][2][128];                // half rows' maxima (tile mod 4, half, row), bf16 rounded up
+        int top[4][128];                        // a row's maximum (tile mod 4, row) as ordered_bits
     };
     int token[SH::INFO][16];                    // first token of each entry of a tile
     int masked[SH::INFO];
@@ -504,8 +505,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 tc_fence_after_sync();
                 if (live) {
                     // the softmax's reference of this tile
-                    const float m_new = fmaxf(m_acc, fmaxf(__uint_as_float(uint32_t(sh.top[gt & 3u][0][row]) << 16),
-                                                           __uint_as_float(uint32_t(sh.top[gt & 3u][1][row]) << 16)));
+                    const float m_new = tc_reference(m_acc, sh.top[gt & 3u][row]);
+                    sh.top[gt & 3u][row] = kOrderedLeast;                      // for the tile four on, whose scores wait for this one's output
                     const float w0 = m_acc == -INFINITY ? 0.f : fast_exp2(m_acc - m_new);
                     m_acc = m_new;
                     if (__any_sync(kFullMask, w0 != 1.f)) {                    // rarely after the first tiles
@@ -608,6 +609,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int copy = 32 * (warp & 3) / COPY;                   // which copy of the row: one for a whole warp
         const float scale = a.scale_log2;
         uint32_t tile0 = 0, unit0 = 0;
+        sh.top[2 * h][row] = sh.top[2 * h + 1][row] = kOrderedLeast;           // before the first item's barriers
         while (tc_next(a, part, lo, start, item, g)) {
             const int ntl = g.t1 - g.t0;
             const uint32_t* mask_b = a.mask != nullptr ? a.mask + (long long)g.b * a.Q * a.mask_words : nullptr;
@@ -744,13 +746,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             x1 = max3(x1, __uint_as_float(v[c][j + 2]), __uint_as_float(v[c][j + 3]));
                         }
                     }
-                    // Any reference near the maximum will do, as long as the row's threads use the
-                    // same one: they exchange it as bf16, rounded up.
-                    const uint32_t top = round_up_bf16(fmaxf(x0, x1) * scale);
-                    sh.top[gt & 3u][h][row] = uint16_t(top >> 16);
+                    const float mine = fmaxf(x0, x1) * scale;
+                    int* top = &sh.top[gt & 3u][row];
+                    atomicMax(top, ordered_bits(__float_as_int(mine)));
                     bar_sync(pair_bar, 64);
-                    const float other = __uint_as_float(uint32_t(sh.top[gt & 3u][1 - h][row]) << 16);
-                    const float m_new = fmaxf(m_soft, fmaxf(__uint_as_float(top), other));
+                    const float m_new = tc_reference(m_soft, *reinterpret_cast<volatile int*>(top));
                     l_run *= m_soft == -INFINITY ? 0.f : fast_exp2(m_soft - m_new);
                     m_soft = m_new;
                     const float m_sub = m_new == -INFINITY ? 0.f : m_new;      // nothing seen yet: every weight is 0
