@@ -432,7 +432,8 @@ int sparse_attn_tree_workspace_size(const sparse_attn_params* p, size_t* bytes);
  * the context; both or neither) those of its KV head's selected blocks; and draft j iff bit
  * j % 32 of word j / 32 of tree_mask[b][i] is set (device 32-bit words
  * [B, Q, ceil(Q / 32)]; bits past Q are ignored).  tree_mask == NULL: drafts 0 .. i, a chain.
- * A query that sees nothing gets a zero row.
+ * A query that sees nothing gets a zero row.  Scores may have any size and sign that fp32 holds
+ * (q . k and its product with softmax_scale * log2(e); beyond, a row becomes NaN).
  * Context tokens must be finite; a draft's K and V may hold anything (infinities and NaN
  * too) as long as the queries that see it are meant to: they reach no other query's row.
  * Memory behind the drafts is never read into a result.

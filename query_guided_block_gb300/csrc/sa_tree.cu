@@ -375,18 +375,23 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
                 for (int h = 0; h < 2; ++h) {
                     mx[h] = fmaxf(mx[h], __shfl_xor_sync(kFullMask, mx[h], 1));
                     mx[h] = fmaxf(mx[h], __shfl_xor_sync(kFullMask, mx[h], 2));
-                    const float m_new = fmaxf(m_run[h], mx[h] * a.scale_log2);
-                    alpha[h] = (m_run[h] == -INFINITY) ? 0.f : fast_exp2(m_run[h] - m_new);
+                    const float m_new = fmaxf(m_run[h], mx[h]);
+                    alpha[h] = (m_run[h] == -INFINITY) ? 0.f : fast_exp2((m_run[h] - m_new) * a.scale_log2);
                     m_run[h] = m_new;
                 }
+                // (score - maximum) * scale, in that order: a rounded product would be off by its own size.
                 float psum[2] = {0.f, 0.f};
+                const F2 scale2 = make_f2(a.scale_log2, a.scale_log2);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int h = e >> 1;
-                        c[nt][e] = (c[nt][e] == -INFINITY) ? 0.f : fast_exp2(fmaf(c[nt][e], a.scale_log2, -m_run[h]));
-                        psum[h] += c[nt][e];
+                    for (int h = 0; h < 2; ++h) {
+                        float &x = c[nt][2 * h], &y = c[nt][2 * h + 1];
+                        const F2 d = mul2(add2(make_f2(x, y), make_f2(-m_run[h], -m_run[h])), scale2);
+                        x = x == -INFINITY ? 0.f : fast_exp2(d.f.x);
+                        y = y == -INFINITY ? 0.f : fast_exp2(d.f.y);
+                        psum[h] += x;
+                        psum[h] += y;
                     }
                 l_run[0] = fmaf(l_run[0], alpha[0], psum[0]);
                 l_run[1] = fmaf(l_run[1], alpha[1], psum[1]);
@@ -531,7 +536,7 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
                 for (int w = 0; w < TW; ++w) {
                     const float mw = x_m[w * ROWS + rr];
                     if (mw == -INFINITY) continue;
-                    const float wgt = fast_exp2(mw - M);
+                    const float wgt = fast_exp2((mw - M) * a.scale_log2);
                     den = fmaf(x_l[w * ROWS + rr], wgt, den);
                     const float4 o = *reinterpret_cast<const float4*>(x_o + (w * ROWS + rr) * (D + 4) + d);
                     num.x = fmaf(o.x, wgt, num.x);
@@ -617,7 +622,7 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(TreeArgs a)
         float w = 0.f;
         if (c0 + lane < at.y) {
             const float m = __ldcg(a.part_m + slot(c0 + lane));
-            w = m == -INFINITY ? 0.f : fast_exp2(m - M);
+            w = m == -INFINITY ? 0.f : fast_exp2((m - M) * a.merge_scale);
             den = fmaf(w, __ldcg(a.part_l + slot(c0 + lane)), den);
         }
         const int n = min(32, at.y - c0);
@@ -727,6 +732,7 @@ cudaError_t launch_tree(const Geometry& g, const TreeCall& c, char* ws, cudaStre
     a.sel_stride = g.sel_stride;
     a.mask_words = (g.Q + 31) / 32;
     a.scale_log2 = g.scale_log2;
+    a.merge_scale = g.scale_log2;
     a.part_m = reinterpret_cast<float*>(ws + L.part_m);
     a.part_l = reinterpret_cast<float*>(ws + L.part_l);
     a.part_o = reinterpret_cast<float*>(ws + L.part_o);

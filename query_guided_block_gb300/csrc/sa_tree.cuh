@@ -43,6 +43,7 @@ struct TreeArgs {
     int min_per;               // tiles of a part at least
     int half_slack;            // a part may grow by twice as many tiles so that items begin with a part
     float scale_log2;
+    float merge_scale;         // base-2 logits in a step of the kernel's maxima (part_m)
     int combine;               // shared items are added up by a launch of their own
     float *part_m, *part_l, *part_o;   // [2 * CTA + which][item_rows] ([D])
     int2* item_parts;          // combine: an item's first part and how many it has
@@ -292,6 +293,42 @@ __device__ TreePart tree_part(const TreeArgs& a, int* s)
     return r;
 }
 
+// Two fp32 operations in one instruction (each rounded as usual).
+union F2 {
+    unsigned long long u;
+    float2 f;
+};
+__device__ __forceinline__ F2 make_f2(float x, float y)
+{
+    F2 r;
+    r.f = make_float2(x, y);
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
+{
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.u) : "l"(a.u), "l"(b.u), "l"(c.u));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b)
+{
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(a.u), "l"(b.u));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b)
+{
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(a.u), "l"(b.u));
+    return r;
+}
+__device__ __forceinline__ F2 sub2(F2 a, F2 b)
+{
+    F2 r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(a.u), "l"(b.u));
+    return r;
+}
+
 // The output row of an item's query row r (query r / G, head r % G of the KV head's group).
 __device__ __forceinline__ long long tree_out_row(const TreeArgs& a, int b, int kvh, int r)
 {
@@ -364,7 +401,7 @@ __device__ void tree_arrive_and_merge(const TreeArgs& a, int item, int start, in
             float den = 0.f;
             for (int c = lane; c < np; c += 32) {
                 const float m = s_w[r * np + c];
-                const float w = m == -INFINITY ? 0.f : fast_exp2(m - M);   // a part that saw nothing has no weight
+                const float w = m == -INFINITY ? 0.f : fast_exp2((m - M) * a.merge_scale);   // a part that saw nothing has no weight
                 s_w[r * np + c] = w;
                 den = fmaf(w, s_l[r * np + c], den);
             }

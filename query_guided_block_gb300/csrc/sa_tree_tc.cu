@@ -149,42 +149,6 @@ __device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16])
                  : "memory");
 }
 
-// Two fp32 operations in one instruction (each rounded as usual).
-union F2 {
-    unsigned long long u;
-    float2 f;
-};
-__device__ __forceinline__ F2 make_f2(float x, float y)
-{
-    F2 r;
-    r.f = make_float2(x, y);
-    return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
-{
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.u) : "l"(a.u), "l"(b.u), "l"(c.u));
-    return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b)
-{
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(a.u), "l"(b.u));
-    return r;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b)
-{
-    F2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(a.u), "l"(b.u));
-    return r;
-}
-__device__ __forceinline__ F2 sub2(F2 a, F2 b)
-{
-    F2 r;
-    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(a.u), "l"(b.u));
-    return r;
-}
-
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float r;
@@ -213,9 +177,26 @@ __device__ __forceinline__ F2 less(F2 p, uint32_t mask)
 __device__ __forceinline__ int ordered_bits(int x) { return x ^ ((x >> 31) & 0x7fffffff); }
 constexpr int kOrderedLeast = int(0x807fffffu);                     // -infinity
 
-// A row's reference for a tile: the maximum, rounded up to a whole number so that it changes rarely.
-// It lies at most 1 above the maximum whatever its size: weights below 2^-126 of it come out as 0.
-__device__ __forceinline__ float tc_reference(float m, int top) { return fmaxf(m, ceilf(__int_as_float(ordered_bits(top)))); }
+// A row's reference for a tile: the largest score so far, unscaled and whatever its size, or an earlier
+// one at most 6 below it in base-2 logits, so that it changes rarely (a weight is 2^6 at most then).  Its
+// product with the scale is rounded by itself wherever it is used (__fmul_rn): what the weights are
+// relative to is the rounded one.
+__device__ __forceinline__ float tc_reference(float m, int top, float scale)
+{
+    const float t = __int_as_float(ordered_bits(top));
+    return __fmul_rn(t, scale) > __fmul_rn(m, scale) + 6.f ? t : m;   // beyond 2^28 any larger one
+}
+
+// A weight is exp2(score * scale - m) by one fused multiply-add, m = reference * scale rounded: all weights
+// are off by the same factor, which the total takes out again.  From |m| = 2^29 on (2^16 in that
+// factor) two scores are equal or at least 2^5 apart, so that only equal ones of the largest count:
+// there the scale gives way to a power of two that takes the reference to 2^30 .. 2^31, exactly.
+__device__ __forceinline__ bool tc_large(float m) { return fabsf(m) >= 536870912.f; }
+__device__ __forceinline__ float tc_power(float reference)
+{
+    const int e = 284 - ((__float_as_int(reference) >> 23) & 255);  // 127 + 30 - (its exponent)
+    return __int_as_float(min(e, 254) << 23);
+}
 
 // Register shares: the CTA starts with 16 warps x 128.  With 152 for both the output threads have two
 // loads fewer in flight: 96 rows over 128K tokens 123 us instead of 119.
@@ -505,10 +486,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 tc_fence_after_sync();
                 if (live) {
                     // the softmax's reference of this tile
-                    const float m_new = tc_reference(m_acc, sh.top[gt & 3u][row]);
+                    const float m_old = __fmul_rn(m_acc, a.scale_log2);
+                    m_acc = tc_reference(m_acc, sh.top[gt & 3u][row], a.scale_log2);
                     sh.top[gt & 3u][row] = kOrderedLeast;                      // for the tile four on, whose scores wait for this one's output
-                    const float w0 = m_acc == -INFINITY ? 0.f : fast_exp2(m_acc - m_new);
-                    m_acc = m_new;
+                    const float w0 = m_old == -INFINITY ? 0.f : fast_exp2(m_old - __fmul_rn(m_acc, a.scale_log2));
                     if (__any_sync(kFullMask, w0 != 1.f)) {                    // rarely after the first tiles
                         const F2 w02 = make_f2(w0, w0);
 #pragma unroll
@@ -562,7 +543,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const float w = !complete ? 1.f : (l == 0.f ? 0.f : 1.f / l);
             if (!complete && row < COPY && r_unit < a.R) {
                 const long long slot = (long long)tree_slot(blockIdx.x, part.per, g.start) * a.item_rows + row;
-                a.part_m[slot] = m_acc;
+                a.part_m[slot] = m_acc * a.scale_log2;
                 a.part_l[slot] = l;
             }
             constexpr int V4 = D / 4;
@@ -656,7 +637,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // what the row sees of the drafts, and what any query sees
             const uint32_t* words = mask_b != nullptr ? mask_b + (long long)q_row * a.mask_words : nullptr;
             const DraftView view = draft_view(words, a.mask_words, r_unit < a.R ? (mask_b != nullptr ? a.Q : q_row + 1) : 0);
-            float m_soft = -INFINITY, l_run = 0.f;                 // the row's reference, the half-row's sum
+            float reference = -INFINITY, l_run = 0.f;              // the row's, the half-row's sum
 
             // Tokens 8 g8 .. + 7 of local tile i that a query with this view sees.
             auto tokens8 = [&](int i, int g8, const DraftView& v) -> uint32_t {
@@ -746,16 +727,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             x1 = max3(x1, __uint_as_float(v[c][j + 2]), __uint_as_float(v[c][j + 3]));
                         }
                     }
-                    const float mine = fmaxf(x0, x1) * scale;
                     int* top = &sh.top[gt & 3u][row];
-                    atomicMax(top, ordered_bits(__float_as_int(mine)));
+                    atomicMax(top, ordered_bits(__float_as_int(fmaxf(x0, x1))));
                     bar_sync(pair_bar, 64);
-                    const float m_new = tc_reference(m_soft, *reinterpret_cast<volatile int*>(top));
-                    l_run *= m_soft == -INFINITY ? 0.f : fast_exp2(m_soft - m_new);
-                    m_soft = m_new;
-                    const float m_sub = m_new == -INFINITY ? 0.f : m_new;      // nothing seen yet: every weight is 0
+                    const float m_old = __fmul_rn(reference, scale);
+                    reference = tc_reference(reference, *reinterpret_cast<volatile int*>(top), scale);
+                    const float m_new = __fmul_rn(reference, scale);
+                    l_run *= m_old == -INFINITY ? 0.f : fast_exp2(m_old - m_new);
                     // ---- the weights, in three bf16 parts, over the scores' own columns -----------
-                    const F2 scale2 = make_f2(scale, scale), m2 = make_f2(-m_sub, -m_sub);
+                    const float factor = tc_large(m_new) ? tc_power(reference) : scale;
+                    const float m_sub = m_new == -INFINITY ? 0.f : __fmul_rn(reference, factor);   // -infinity: every weight is 0
+                    const F2 scale2 = make_f2(factor, factor), m2 = make_f2(-m_sub, -m_sub);
                     F2 sum_a = make_f2(0.f, 0.f), sum_b = make_f2(0.f, 0.f);
                     auto weight = [&](uint32_t (&x)[16], int j) {
                         const F2 p = fma2(make_f2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), scale2, m2);
@@ -904,6 +886,7 @@ cudaError_t launch_tc_t(TreeArgs a, cudaStream_t s)
 cudaError_t launch_tree_tc(TreeArgs a, cudaStream_t s)
 {
     a.tile = kTcTile;
+    a.merge_scale = 1.f;           // maxima are scaled
     a.item_rows = tree_item_rows(a.R);
     a.row_groups = (a.R + a.item_rows - 1) / a.item_rows;
     // 128 rows over 777 tokens 18.9 us, with parts of at least 1 tile 19.8, of 4 32.8; an item's start and

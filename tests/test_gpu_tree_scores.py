@@ -1,5 +1,5 @@
-"""Draft-tree attention where scores are large: of either sign, on both
-kernels.  Scores are whole numbers that every partial sum holds exactly, so the weights are known
+"""Draft-tree attention where scores are large: of either sign, from 2e4 to beyond 2^31 in base 2, on
+both kernels.  Scores are whole numbers that every partial sum holds exactly, so the weights are known
 well whatever their size, and a row's tokens lie close enough together for several to count."""
 import math
 
@@ -8,7 +8,7 @@ import torch
 
 from query_guided_block_gb300 import binding as B
 from query_guided_block_gb300.build import build
-from tests.draft_reference import U, Case, chain_mask, place, random_tree
+from tests.draft_reference import U, Case, chain_mask, place, random_tree, tree_exact
 from tests.test_gpu_tree import call
 
 pytestmark = pytest.mark.gpu
@@ -57,8 +57,8 @@ def expected(c, q, pools, table, see, scale):
 
     Scores are exact.  What the exponent of a weight is off by, relative to the row's largest: the
     scale in base 2 is rounded twice (2 U of the distance), the distance from the reference once (U of
-    it; the reference lies at most one above the largest), exp2 gives 2^-22.  Beyond 2^24 scaled scores
-    are rounded, but there the next score is 2^7 steps away: equal ones stay equal, others have no weight.
+    it; the reference lies at most 6 below the largest: U (far + 6)), exp2 gives 2^-22.  At 1e11 and
+    beyond the next score is 2^19 away: only equal ones of the largest count.
     The weighted sum: at most 24 matrix steps a tile of two units 2^-23 and 8 tiles and shares of half
     a unit, the total likewise; fp32 K/V keep 22 bits of weights and values (2^-22 each, and as much
     for the product left out).  A last division and product."""
@@ -76,14 +76,14 @@ def expected(c, q, pools, table, see, scale):
             far = (s.amax(-1, keepdim=True) - s).masked_fill(~ok, 0.0)
             p = torch.softmax(s, -1)
             out[b, :, h] = p @ v
-            err = 3 * U * (far + 1) + 2 ** -22
+            err = U * (3 * far + 6) + 2 ** -22
             mag = p @ v.abs()
             steps = (24 + 8) * 2 ** -22 + (3 * 2 ** -22 if c.kv == F32 else 0)
             bound[b, :, h] = (p * err) @ v.abs() + (p * err).sum(-1, keepdim=True) * mag + (2 * steps + 4 * U) * mag
     return out, bound
 
 
-@pytest.mark.parametrize("logit", [2e4, 1e5, 3e6])
+@pytest.mark.parametrize("logit", [2e4, 1e5, 3e6, 1e11, 1e30])
 @pytest.mark.parametrize("sign", [1, -1])
 @pytest.mark.parametrize("kind", KINDS)
 def test_large_scores_of_either_sign(kind, sign, logit):
@@ -110,3 +110,47 @@ def test_large_scores_split_between_parts():
         assert B.sparse_attn_get_device_error(ws) == 0
         exact, bound = expected(c, q, pools, table, see, scale)
         assert ((out.cpu().double() - exact).abs() <= bound + 64 * U * exact.abs().amax(-1, keepdim=True)).all(), kind
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_rows_that_see_huge_keys(kind):
+    """Two drafts with keys of 1e30: a query that sees them attends to them alone (equal scores share),
+    or, where its score is as low as that, not at all."""
+    c = Case(batch=3, lens=(37, 300, 121), block=16, **KINDS[kind])
+    table = c.block_table()
+    pools = c.fill(c.pools(), table)
+    q = c.normal("q", c.batch, c.drafts, c.hq, c.dim)
+    see = random_tree(c)
+    odd = [c.drafts // 2, c.drafts - 1]
+    without = see.clone()
+    without[:, :, odd] = False
+    exact, bound = tree_exact(c, q, pools, table, without)
+    for b, n in enumerate(c.all_lens):
+        for j in odd:
+            page, off = place(c, table, b, torch.tensor([n + j]))
+            pools[0][page, :, off] = 1e30
+    out, ws = call(c, q, pools, table, see)
+    assert B.sparse_attn_get_device_error(ws) == 0
+    met = up = 0
+    for b, n in enumerate(c.all_lens):
+        page, off = place(c, table, b, torch.arange(n, n + c.drafts))
+        v = pools[1][page, :, off].double()                        # [Q, Hkv, D]
+        for i in range(c.drafts):
+            mine = [j for j in odd if see[b, i, j]]
+            if not mine:
+                continue
+            met += 1
+            for h in range(c.hq):
+                total = float(q[b, i, h].double().sum())
+                got = out[b, i, h].cpu().double()
+                assert torch.isfinite(got).all()
+                if abs(total) < 1e-2:             # its sign is within the rounding of the sum
+                    continue
+                if total < 0:
+                    assert ((got - exact[b, i, h]).abs() <= bound[b, i, h]).all()
+                else:
+                    up += 1
+                    want = v[mine, h // (c.hq // c.hkv)].mean(0)
+                    # equal weights: a product and a sum of two, the total, the division
+                    assert ((got - want).abs() <= 8 * 2 ** -22 * v[mine, h // (c.hq // c.hkv)].abs().mean(0) + 1e-30).all()
+    assert met > 0 and up > 0
