@@ -421,7 +421,10 @@ int sparse_attn_append_kv(const sparse_attn_params* p, int32_t num_rows, const i
 
 /* Workspace of sparse_attn_tree_decode for this problem (it also serves
  * sparse_attn_append_kv and sparse_attn_commit_drafts, which use its first 256 bytes);
- * independent of n_tokens, so one workspace serves a growing context. */
+ * independent of n_tokens, so one workspace serves a growing context.  A workspace large
+ * enough for each may serve these three calls for problems of different shapes in turn (one
+ * stream's order).  The other calls keep other counters: between them and
+ * sparse_attn_tree_decode a workspace needs sparse_attn_workspace_init. */
 int sparse_attn_tree_workspace_size(const sparse_attn_params* p, size_t* bytes);
 
 /* Attention of Q drafted tokens per sequence over the cached context and each other:

@@ -169,8 +169,9 @@ cudaError_t launch_commit(const Geometry& g, const int32_t* seq_lens, const int3
                           const int32_t* path_len, void* k_pages, void* v_pages, const int32_t* block_table,
                           void* kmin, void* kmax, int32_t* new_lens, uint32_t* err, cudaStream_t s);
 
-// Draft-tree attention (sa_tree.cu).  Workspace: header, one arrival counter and one note per
-// (unit, row group), then the partial results of units that several CTAs share.
+// Draft-tree attention (sa_tree.cu).  Workspace: header, an arrival counter per CTA (zero between
+// calls, in one place for all problems), then what a call writes before it reads: a note per (unit,
+// row group) and the partial results of units that several CTAs share.
 struct TreeLayout {
     size_t counters, item_parts, part_m, part_l, part_o, total;
 };

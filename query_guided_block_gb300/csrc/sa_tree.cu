@@ -693,7 +693,8 @@ TreeLayout tree_layout(const Geometry& g)
     const size_t slots = 2 * size_t(kTreeMaxCtas);
     L.counters = 256;
     const size_t items = size_t(g.units()) * ((R + 15) / 16);
-    L.item_parts = align256(L.counters + items * sizeof(uint32_t));
+    // the counters are what calls leave to each other: the same words whatever the problem
+    L.item_parts = align256(L.counters + kTreeMaxCtas * sizeof(uint32_t));
     L.part_m = align256(L.item_parts + items * sizeof(int2));
     L.part_l = align256(L.part_m + slots * rows * sizeof(float));
     L.part_o = align256(L.part_l + slots * rows * sizeof(float));

@@ -47,7 +47,8 @@ struct TreeArgs {
     int combine;               // shared items are added up by a launch of their own
     float *part_m, *part_l, *part_o;   // [2 * CTA + which][item_rows] ([D])
     int2* item_parts;          // combine: an item's first part and how many it has
-    uint32_t *counters, *err;
+    uint32_t* counters;        // [CTA] arrivals of the item that goes on behind this CTA's part; zero between calls
+    uint32_t* err;
 };
 
 // The list of a unit.
@@ -359,7 +360,8 @@ __device__ __forceinline__ void tree_note_parts(const TreeArgs& a, int item, int
 }
 
 // Called by the CTA's first NT threads once its (m, l, o) of a shared item is written: counts the
-// arrival; the last one merges the parts c0 .. c1 and writes the output rows.  `s_w`: floats of
+// arrival at the counter of the item's first part (one item at most begins in a part and goes on
+// behind it); the last one merges the parts c0 .. c1 and writes the output rows.  `s_w`: floats of
 // shared memory free for use (at least as many as CTAs in the grid).
 //   Two steps, so that no load waits for another one's result: a warp per row takes the parts'
 // maxima and sums (lane = part) and leaves the parts' weights in shared memory, then a thread
@@ -372,9 +374,9 @@ __device__ void tree_arrive_and_merge(const TreeArgs& a, int item, int start, in
     const int c0 = start / per, np = (start + tiles - 1) / per - c0 + 1;
     tree_sync<NT>();
     if (tid == 0) {
-        const uint32_t before = atomic_add_acq_rel_u32(&a.counters[item], 1u);
+        const uint32_t before = atomic_add_acq_rel_u32(&a.counters[c0], 1u);
         *s_last = before + 1u == uint32_t(np);
-        if (*s_last) a.counters[item] = 0u;
+        if (*s_last) a.counters[c0] = 0u;
     }
     tree_sync<NT>();
     const bool last = *s_last != 0;
