@@ -451,9 +451,9 @@ int sparse_attn_tree_decode(const sparse_attn_params* p, const void* q, const vo
  * all were read before any is written; new_lens[b] = seq_lens[b] + path_len[b].
  * path: device int32 [B, path_stride], strictly ascending draft numbers in [0, Q) (a path of a
  * tree whose parents come before their children); path_len: device int32 [B] in
- * [0, path_stride].  A path that breaks this sets SPARSE_ATTN_ERR_LENGTH; nothing of that
- * sequence moves and new_lens[b] = seq_lens[b].  new_lens [B] must not overlap seq_lens; an
- * inactive sequence keeps -1.
+ * [0, path_stride].  path may be NULL when path_stride is 0 (nothing is accepted).  A path that
+ * breaks this sets SPARSE_ATTN_ERR_LENGTH; nothing of that sequence moves and new_lens[b] =
+ * seq_lens[b].  new_lens [B] must not overlap seq_lens; an inactive sequence keeps -1.
  * kmin / kmax: both or neither; the touched blocks' rows become the box of their tokens
  * below new_lens[b], as in sparse_attn_append_kv.
  * On return the drafts that were not accepted are undefined. */

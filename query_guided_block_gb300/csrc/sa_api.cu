@@ -704,7 +704,7 @@ int sparse_attn_commit_drafts(const sparse_attn_params* p, const int32_t* seq_le
     if (g.B == 0) return SPARSE_ATTN_OK;
     if (!path_len || !new_lens || !aligned(path_len, 4) || !aligned(new_lens, 4) || !aligned(seq_lens, 4))
         return SPARSE_ATTN_INVALID_ARG;
-    if (g.num_pages < 1 || !path || !k_pages || !v_pages || !block_table) return SPARSE_ATTN_INVALID_ARG;
+    if (g.num_pages < 1 || (!path && path_stride > 0) || !k_pages || !v_pages || !block_table) return SPARSE_ATTN_INVALID_ARG;
     if (!aligned(path, 4) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(block_table, 4) ||
         !aligned(kmin, 16) || !aligned(kmax, 16))
         return SPARSE_ATTN_INVALID_ARG;
