@@ -148,7 +148,8 @@ int32_t sparse_attn_num_blocks(const sparse_attn_params* p);
 
 /* int32 entries per unit row of sel_ids (and of every diff list): the largest
  * selection possible, min(topk, candidates) + min(num_reserve, candidates) + window
- * blocks; -1 on bad params. */
+ * blocks; -1 on bad params.  Known for every problem that sparse_attn_tree_decode takes,
+ * also where sparse_attn_select and sparse_attn_decode are UNSUPPORTED. */
 int32_t sparse_attn_sel_stride(const sparse_attn_params* p);
 
 /* k for a context of n_tokens in pages of block_size tokens, by the SparDA page's §3.2

@@ -376,9 +376,7 @@ class _Shapes:
         self.out = (p.batch, n, p.num_q_heads, p.head_dim)
         self.out_one = (p.batch, p.num_q_heads, p.head_dim) if n == 1 else self.out
         self.mask = (p.batch, n, -(-n // 32))
-        one = sparse_attn_params.from_buffer_copy(p)
-        one.num_queries = 1                          # the stride does not depend on the number of queries
-        self.sel = (p.batch, p.num_kv_heads, int(lib().sparse_attn_sel_stride(C.byref(one))))
+        self.sel = (p.batch, p.num_kv_heads, int(lib().sparse_attn_sel_stride(C.byref(p))))
 
 
 _shapes_of = {}

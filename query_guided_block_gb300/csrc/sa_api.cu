@@ -181,8 +181,8 @@ int32_t sparse_attn_num_blocks(const sparse_attn_params* p)
 
 int32_t sparse_attn_sel_stride(const sparse_attn_params* p)
 {
-    Geometry g;
-    return make_geometry(p, &g) == SPARSE_ATTN_OK ? g.sel_stride : -1;
+    Geometry g;   // draft trees take selections where the single-query kernels do not fit: their limits
+    return make_geometry(p, &g, true) == SPARSE_ATTN_OK ? g.sel_stride : -1;
 }
 
 int sparse_attn_workspace_size(const sparse_attn_params* p, size_t* bytes)

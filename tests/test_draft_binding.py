@@ -1,0 +1,47 @@
+"""The binding and the classes of the draft calls, without a GPU: what they ask of the library and on
+which device."""
+import ctypes as C
+
+import pytest
+import torch
+
+from query_guided_block_gb300 import binding as B
+from query_guided_block_gb300.build import build
+
+F32, BF = torch.float32, torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build()
+    B.lib()
+
+
+def params(**over):
+    kw = dict(batch=2, num_q_heads=8, num_kv_heads=2, head_dim=128, n_tokens=1000, block_size=32, num_pages=100,
+              window_tokens=40, topk=4, num_queries=5, capacity_tokens=1005)
+    kw.update(over)
+    return B.make_params(**kw)
+
+
+@pytest.mark.parametrize("kv", [BF, F32])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("block", [8, 16, 32, 64, 128])
+@pytest.mark.parametrize("queries", [1, 5])
+@pytest.mark.parametrize("two_level", [False, True])
+def test_selection_width_is_known_wherever_the_tree_call_takes_a_selection(kv, dim, block, queries, two_level):
+    p = params(kv_dtype=kv, head_dim=dim, block_size=block, num_queries=queries, two_level=two_level, coarse_block=256,
+               topk_coarse=2)
+    size = C.c_size_t()
+    assert B.lib().sparse_attn_tree_workspace_size(C.byref(p), C.byref(size)) == B.OK
+    nb = -(-1000 // block)
+    first = 960 // block
+    width = min(4, first) + nb - first
+    assert B.sparse_attn_sel_stride(p) == width
+    assert B._shapes(p).sel == (2, 2, width)
+
+
+def test_selection_width_of_bad_parameters_is_refused():
+    for over in (dict(head_dim=96), dict(num_q_heads=6), dict(block_size=48), dict(topk=-1), dict(n_tokens=32 * 16384 + 1, capacity_tokens=0)):
+        with pytest.raises(B.SparseAttnError):
+            B.sparse_attn_sel_stride(params(**over))
