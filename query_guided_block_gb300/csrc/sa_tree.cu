@@ -535,8 +535,7 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
 #pragma unroll
                 for (int w = 0; w < TW; ++w) {
                     const float mw = x_m[w * ROWS + rr];
-                    if (mw == -INFINITY) continue;
-                    const float wgt = fast_exp2((mw - M) * a.scale_log2);
+                    const float wgt = tree_share(mw, M, x_l[w * ROWS + rr], a.scale_log2);
                     den = fmaf(x_l[w * ROWS + rr], wgt, den);
                     const float4 o = *reinterpret_cast<const float4*>(x_o + (w * ROWS + rr) * (D + 4) + d);
                     num.x = fmaf(o.x, wgt, num.x);
@@ -622,8 +621,9 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(TreeArgs a)
         float w = 0.f;
         if (c0 + lane < at.y) {
             const float m = __ldcg(a.part_m + slot(c0 + lane));
-            w = m == -INFINITY ? 0.f : fast_exp2((m - M) * a.merge_scale);
-            den = fmaf(w, __ldcg(a.part_l + slot(c0 + lane)), den);
+            const float l = __ldcg(a.part_l + slot(c0 + lane));
+            w = tree_share(m, M, l, a.merge_scale);
+            den = fmaf(w, l, den);
         }
         const int n = min(32, at.y - c0);
         for (int c = 0; c < n; c += 8) {

@@ -359,6 +359,13 @@ __device__ __forceinline__ void tree_note_parts(const TreeArgs& a, int item, int
     a.item_parts[item] = make_int2(c0, (start + tiles - 1) / per - c0 + 1);
 }
 
+// The weight of a share with maximum m and total l among shares whose largest maximum is M.  One that saw
+// nothing has none; one whose scores are all NaN has a NaN total and no maximum either, and is kept.
+__device__ __forceinline__ float tree_share(float m, float M, float l, float scale)
+{
+    return m == -INFINITY && l == 0.f ? 0.f : fast_exp2((m - M) * scale);
+}
+
 // Called by the CTA's first NT threads once its (m, l, o) of a shared item is written: counts the
 // arrival at the counter of the item's first part (one item at most begins in a part and goes on
 // behind it); the last one merges the parts c0 .. c1 and writes the output rows.  `s_w`: floats of
@@ -403,7 +410,7 @@ __device__ void tree_arrive_and_merge(const TreeArgs& a, int item, int start, in
             float den = 0.f;
             for (int c = lane; c < np; c += 32) {
                 const float m = s_w[r * np + c];
-                const float w = m == -INFINITY ? 0.f : fast_exp2((m - M) * a.merge_scale);   // a part that saw nothing has no weight
+                const float w = tree_share(m, M, s_l[r * np + c], a.merge_scale);
                 s_w[r * np + c] = w;
                 den = fmaf(w, s_l[r * np + c], den);
             }

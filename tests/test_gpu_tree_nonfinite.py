@@ -1,0 +1,56 @@
+"""Drafts that hold infinities and NaN reach every query that sees them, wherever the work is cut: a
+share of the tokens whose scores are all NaN."""
+import pytest
+import torch
+
+from query_guided_block_gb300 import binding as B
+from query_guided_block_gb300.build import build
+from tests.draft_reference import Case, place, tree_exact
+from tests.test_gpu_tree import call
+
+pytestmark = pytest.mark.gpu
+F32 = torch.float32
+NAN = float("nan")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    build()
+    B.lib()
+
+
+# Context lengths that put the drafts into a share of their own: 16 tokens (a warp's share of a tile
+# with few rows), 2048 and 4096 (the only tile of the last part: 33 tiles in parts of two)
+NAN_KEYS = {
+    "warp_share": Case(batch=1, drafts=1, context=16, lens=(16,)),
+    "warp_share_48": Case(batch=1, drafts=2, context=48, lens=(48,)),
+    "warp_share_fp32": Case(batch=1, drafts=1, context=16, lens=(16,), dtype=F32, kv=F32),
+    "last_part": Case(batch=1, drafts=1, hq=4, hkv=1, context=2048, lens=(2048,)),
+    "last_part_fp32": Case(batch=1, drafts=2, hq=4, hkv=1, dim=64, context=2048, lens=(2048,), dtype=F32, kv=F32),
+    "last_part_joined_apart": Case(batch=1, drafts=4, hq=4, hkv=1, context=2048, lens=(2048,)),
+    "last_part_r28": Case(batch=1, drafts=7, hq=16, hkv=4, context=8000, lens=(4096,)),
+    "last_part_r64": Case(batch=1, drafts=16, hq=16, hkv=4, context=8000, lens=(4096,)),
+    "last_part_r100": Case(batch=1, drafts=25, hq=16, hkv=4, context=8000, lens=(4096,)),
+    "last_part_r100_d64": Case(batch=1, drafts=25, hq=16, hkv=4, dim=64, context=8000, lens=(4096,)),
+}
+
+
+@pytest.mark.parametrize("name", NAN_KEYS)
+def test_nan_keys_alone_in_a_share(name):
+    """Every query sees one draft, its own, whose key is NaN for the odd drafts (the first one where
+    there is only one): those rows are NaN, the others are as without."""
+    c = NAN_KEYS[name]
+    table = c.block_table()
+    pools = c.fill(c.pools(), table)
+    q = c.normal("q", c.batch, c.drafts, c.hq, c.dim)
+    see = torch.eye(c.drafts, dtype=torch.bool).expand(c.batch, -1, -1).clone()
+    exact, bound = tree_exact(c, q, pools, table, see)
+    bad = torch.arange(c.drafts) % 2 == (1 if c.drafts > 1 else 0)
+    page, off = place(c, table, 0, c.all_lens[0] + torch.arange(c.drafts)[bad])
+    pools[0][page, :, off] = NAN
+    out, ws = call(c, q, pools, table, see)
+    assert B.sparse_attn_get_device_error(ws) == 0
+    out = out.cpu()
+    assert torch.isnan(out[0, bad]).all(), f"{int((~torch.isnan(out[0, bad])).any(-1).sum())} rows lost their NaN"
+    assert ((out.double() - exact).abs()[0, ~bad] <= bound[0, ~bad]).all()
