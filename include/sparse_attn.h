@@ -439,7 +439,9 @@ int sparse_attn_tree_workspace_size(const sparse_attn_params* p, size_t* bytes);
  * A query that sees nothing gets a zero row.  Scores may have any size and sign that fp32 holds
  * (q . k and its product with softmax_scale * log2(e); beyond, a row becomes NaN).
  * Context tokens must be finite; a draft's K and V may hold anything (infinities and NaN
- * too) as long as the queries that see it are meant to: they reach no other query's row.
+ * too) as long as the queries that see it are meant to: they reach no other query's row.  In
+ * the rows that see it a NaN score makes all channels NaN, and an infinity or NaN in V that
+ * channel infinite or NaN, however small its weight.
  * Memory behind the drafts is never read into a result.
  * Q <= 1024, else UNSUPPORTED.  The result does not depend on the launch's timing. */
 int sparse_attn_tree_decode(const sparse_attn_params* p, const void* q, const void* k_pages,

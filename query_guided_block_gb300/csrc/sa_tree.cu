@@ -459,7 +459,12 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
                         join(acc[j], x);
                     }
                 }
-                if (bad0 | bad1) {                           // rows taken out above
+                if (bad0 | bad1) {                           // rows taken out above, where they are seen (weight or none)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (!((see[e >> 1][nt / 4] >> ((nt & 3) * 8 + 2 * t4 + (e & 1))) & 1u)) c[nt][e] = -1.f;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll 1
@@ -474,8 +479,8 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
 #pragma unroll
                                 for (int e = 0; e < 2; ++e) {
                                     const float v = load_q(a.v_pages, at + j * 8 + 2 * t4 + e, KB);
-                                    if (p0 != 0.f) acc[j][e] = fmaf(p0, v, acc[j][e]);
-                                    if (p1 != 0.f) acc[j][2 + e] = fmaf(p1, v, acc[j][2 + e]);
+                                    if (p0 >= 0.f) acc[j][e] = fmaf(p0, v, acc[j][e]);
+                                    if (p1 >= 0.f) acc[j][2 + e] = fmaf(p1, v, acc[j][2 + e]);
                                 }
                         }
                 }
@@ -633,7 +638,7 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(TreeArgs a)
             for (int x = 0; x < 8; ++x) {
                 wc[x] = __shfl_sync(kFullMask, w, (c + x) & 31);
                 o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (c + x < n && wc[x] != 0.f && lane < D / 4)
+                if (c + x < n && lane < D / 4)
                     o[x] = __ldcg(reinterpret_cast<const float4*>(a.part_o + slot(c0 + c + x) * D) + lane);
             }
 #pragma unroll

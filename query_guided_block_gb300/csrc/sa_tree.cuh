@@ -431,7 +431,7 @@ __device__ void tree_arrive_and_merge(const TreeArgs& a, int item, int start, in
                 for (int x = 0; x < 8; ++x) {
                     w[x] = c + x < np ? s_w[r * np + c + x] : 0.f;
                     o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (w[x] != 0.f)
+                    if (c + x < np)                         // without a weight too: it may hold infinities
                         o[x] = __ldcg(reinterpret_cast<const float4*>(
                             a.part_o + ((long long)tree_slot(c0 + c + x, per, start) * a.item_rows + r0 + r) * a.D + d));
                 }

@@ -1,16 +1,16 @@
 """Drafts that hold infinities and NaN reach every query that sees them, wherever the work is cut: a
-share of the tokens whose scores are all NaN."""
+share of the tokens whose scores are all NaN, a value whose weight is too small for fp32."""
 import pytest
 import torch
 
 from query_guided_block_gb300 import binding as B
 from query_guided_block_gb300.build import build
-from tests.draft_reference import Case, place, tree_exact
+from tests.draft_reference import Case, chain_mask, place, tree_exact
 from tests.test_gpu_tree import call
 
 pytestmark = pytest.mark.gpu
 F32 = torch.float32
-NAN = float("nan")
+NAN, INF = float("nan"), float("inf")
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -54,3 +54,59 @@ def test_nan_keys_alone_in_a_share(name):
     out = out.cpu()
     assert torch.isnan(out[0, bad]).all(), f"{int((~torch.isnan(out[0, bad])).any(-1).sum())} rows lost their NaN"
     assert ((out.double() - exact).abs()[0, ~bad] <= bound[0, ~bad]).all()
+
+
+VALUES = {
+    "few": Case(batch=2, drafts=3, lens=(37, 300)),
+    "few_parts": Case(batch=1, drafts=2, hq=4, hkv=1, context=2048, lens=(2048,)),
+    "small_rows": Case(batch=1, drafts=9, lens=(37,)),
+    "fp32": Case(batch=2, drafts=7, lens=(37, 300), dtype=F32, kv=F32, dim=64),
+    "fp32_parts": Case(batch=1, drafts=2, hq=4, hkv=1, dim=64, context=2048, lens=(2048,), dtype=F32, kv=F32),
+    "fp32_q": Case(batch=2, drafts=7, lens=(37, 300), dtype=F32),
+    "r28": Case(batch=2, drafts=7, context=8000, lens=(37, 300)),
+    "r28_parts": Case(batch=1, drafts=7, hq=16, hkv=4, context=8000, lens=(4096,)),
+    "r64": Case(batch=2, drafts=16, context=8000, lens=(37, 300)),
+    "r100": Case(batch=2, drafts=25, context=8000, lens=(37, 300)),
+    "few_alone": Case(batch=1, drafts=2, hq=4, hkv=1, context=2048, lens=(2048,)),
+    "joined_apart_alone": Case(batch=1, drafts=4, hq=4, hkv=1, context=2048, lens=(2048,)),
+    "r28_alone": Case(batch=1, drafts=7, hq=16, hkv=4, context=8000, lens=(4096,)),
+    "r64_alone": Case(batch=1, drafts=16, hq=16, hkv=4, context=8000, lens=(4096,)),
+    "r100_alone": Case(batch=1, drafts=25, hq=16, hkv=4, context=8000, lens=(4096,)),
+    "r100_parts": Case(batch=1, drafts=25, hq=16, hkv=4, dim=64, context=8000, lens=(4096,)),
+}
+
+
+@pytest.mark.parametrize("value", [INF, -INF, NAN])
+@pytest.mark.parametrize("name", VALUES)
+def test_values_whose_weight_is_too_small(name, value):
+    """Draft 1 holds `value` in one channel and a key whose weight is far below 2^-149: that channel is
+    not finite in the rows that see it, all others are as without the draft.  In the cases `alone` no
+    query sees another draft, so that the last part of the row has no weight at all."""
+    c = VALUES[name]
+    table = c.block_table()
+    pools = c.fill(c.pools(), table)
+    q = c.normal("q", c.batch, c.drafts, c.hq, c.dim)
+    q[..., 5] = 4.0
+    see = chain_mask(c.drafts).expand(c.batch, -1, -1).clone()
+    if name.endswith("alone"):
+        see[:] = False
+        see[:, 1:, 1] = True
+    for b, n in enumerate(c.all_lens):
+        page, off = place(c, table, b, torch.tensor([n + 1]))
+        key = torch.zeros(1, c.hkv, c.dim, dtype=c.kv)
+        key[..., 5] = -2000.0                     # the score: -8000 / sqrt(D), below -700
+        pools[0][page, :, off] = key
+    exact, bound = tree_exact(c, q, pools, table, see)             # the draft's weight is 0 there
+    for b, n in enumerate(c.all_lens):
+        page, off = place(c, table, b, torch.tensor([n + 1]))
+        row = pools[1][page, :, off]
+        row[..., 3] = value
+        pools[1][page, :, off] = row
+    out, ws = call(c, q, pools, table, see)
+    assert B.sparse_attn_get_device_error(ws) == 0
+    out = out.cpu()
+    rest = torch.arange(c.dim) != 3
+    assert ((out.double() - exact).abs()[..., rest] <= bound[..., rest]).all()
+    assert ((out.double() - exact).abs()[:, 0] <= bound[:, 0]).all()
+    hit = ~torch.isfinite(out[:, 1:, :, 3])
+    assert hit.all(), f"{int((~hit).sum())} of {hit.numel()} rows that see the draft are finite there"
