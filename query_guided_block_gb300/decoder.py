@@ -234,4 +234,5 @@ class DraftDecoder:
             self.seq_lens.copy_(self.new_lens)
 
     def device_error(self, stream=None) -> int:
-        return B.sparse_attn_get_device_error(self.ws, stream)
+        with torch.cuda.device(self.device):         # whose current stream is the default
+            return B.sparse_attn_get_device_error(self.ws, stream)

@@ -1,11 +1,13 @@
 """The binding and the classes of the draft calls, without a GPU: what they ask of the library and on
 which device."""
+import contextlib
 import ctypes as C
 
 import pytest
 import torch
 
 from query_guided_block_gb300 import binding as B
+from query_guided_block_gb300 import decoder
 from query_guided_block_gb300.build import build
 
 F32, BF = torch.float32, torch.bfloat16
@@ -45,3 +47,37 @@ def test_selection_width_of_bad_parameters_is_refused():
     for over in (dict(head_dim=96), dict(num_q_heads=6), dict(block_size=48), dict(topk=-1), dict(n_tokens=32 * 16384 + 1, capacity_tokens=0)):
         with pytest.raises(B.SparseAttnError):
             B.sparse_attn_sel_stride(params(**over))
+
+
+def test_the_error_word_is_read_on_the_decoders_device(monkeypatch):
+    """With another device current, the read must wait for the stream of the decoder's device."""
+    asked = []
+
+    class Stream:
+        cuda_stream = 1234
+
+    def current_stream(device=None):
+        asked.append(("stream", None if device is None else torch.device(device)))
+        return Stream()
+
+    @contextlib.contextmanager
+    def on(device):
+        asked.append(("device", torch.device(device)))
+        yield
+
+    def read(ws, stream=None):
+        asked.append(("read", stream))
+        return 0
+
+    monkeypatch.setattr(torch.cuda, "current_stream", current_stream)
+    monkeypatch.setattr(torch.cuda, "device", on)
+    monkeypatch.setattr(decoder.B, "sparse_attn_get_device_error", read)
+    dec = decoder.DraftDecoder.__new__(decoder.DraftDecoder)
+    dec.device, dec.ws = torch.device("cuda", 3), None
+    assert dec.device_error() == 0
+    (first, device), *_, (last, stream) = asked
+    assert (first, device) == ("device", torch.device("cuda", 3)) and last == "read"
+    # the default of the read is the current stream of the current device, which is 3 by then
+    assert stream is None or ("stream", torch.device("cuda", 3)) in asked
+    asked.clear()
+    assert dec.device_error(77) == 0 and asked[-1] == ("read", 77)
