@@ -195,7 +195,14 @@ class DraftDecoder:
     context, attends a tree of them over the context and each other, and moves the accepted
     path to the context's end.  Owns the context lengths, the output and the workspace; the
     page pools, the page table (and its key box) belong to the caller.  No call waits for
-    the device, so a step can be captured into a CUDA graph."""
+    the device, so a step can be captured into a CUDA graph.
+
+    ``p.n_tokens`` is the longest context that ``decode`` and ``commit`` take.  A commit may
+    carry a context past it (the pages reach as far as ``p.capacity_tokens``); from then on that
+    sequence is treated as inactive, its rows of ``out`` stay as they were, and
+    ``device_error`` reports ``ERR_LENGTH``, until ``p`` is replaced by parameters with a larger
+    ``n_tokens``.  That may be done between any two calls, also to follow the contexts
+    closely: the workspace does not depend on ``n_tokens``, and the kernels are chosen by it."""
 
     def __init__(self, params: B.sparse_attn_params, seq_lens: torch.Tensor):
         p = params
