@@ -456,7 +456,8 @@ int sparse_attn_tree_decode(const sparse_attn_params* p, const void* q, const vo
  * tree whose parents come before their children); path_len: device int32 [B] in
  * [0, path_stride].  path may be NULL when path_stride is 0 (nothing is accepted).  A path that
  * breaks this sets SPARSE_ATTN_ERR_LENGTH; nothing of that sequence moves and new_lens[b] =
- * seq_lens[b].  new_lens [B] must not overlap seq_lens; an inactive sequence keeps -1.
+ * seq_lens[b].  new_lens [B] must not overlap seq_lens, path or path_len; an inactive
+ * sequence keeps -1.
  * kmin / kmax: both or neither; the touched blocks' rows become the box of their tokens
  * below new_lens[b], as in sparse_attn_append_kv.
  * On return the drafts that were not accepted are undefined. */

@@ -708,7 +708,10 @@ int sparse_attn_commit_drafts(const sparse_attn_params* p, const int32_t* seq_le
     if (!aligned(path, 4) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(block_table, 4) ||
         !aligned(kmin, 16) || !aligned(kmax, 16))
         return SPARSE_ATTN_INVALID_ARG;
-    if (seq_lens && new_lens < seq_lens + g.B && seq_lens < new_lens + g.B) return SPARSE_ATTN_INVALID_ARG;
+    // what every KV head's CTA reads must not be what the first one writes
+    auto over_new = [&](const int32_t* in, size_t n) { return in && new_lens < in + n && in < new_lens + g.B; };
+    if (over_new(seq_lens, g.B) || over_new(path_len, g.B) || over_new(path, size_t(g.B) * path_stride))
+        return SPARSE_ATTN_INVALID_ARG;
     return status_of(launch_commit(g, seq_lens, path, path_stride, path_len, k_pages, v_pages, block_table, kmin, kmax,
                                    new_lens, static_cast<uint32_t*>(ws), reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -81,3 +81,19 @@ def test_the_error_word_is_read_on_the_decoders_device(monkeypatch):
     assert stream is None or ("stream", torch.device("cuda", 3)) in asked
     asked.clear()
     assert dec.device_error(77) == 0 and asked[-1] == ("read", 77)
+
+
+def test_commit_refuses_new_lengths_over_its_other_inputs():
+    """Every KV head's CTA reads the path and its length while the first one writes the new length.
+    (Refused on the host: nothing is launched.)"""
+    p = params()
+    at = 1 << 20
+    lens, path, count, pools, new = at, at + 256, at + 512, at + 4096, at + 1024
+
+    def commit(lens=lens, path=path, stride=4, count=count, new=new):
+        return B.lib().sparse_attn_commit_drafts(C.byref(p), lens, path, stride, count, pools, pools, at, None, None, new,
+                                                 at, 256, None)
+
+    for over in (dict(new=lens), dict(new=lens + 4), dict(new=lens - 4), dict(new=path), dict(new=path + 28),
+                 dict(new=path - 4), dict(new=count), dict(new=count + 4), dict(new=count - 4)):
+        assert commit(**over) == B.INVALID_ARG, over
