@@ -441,7 +441,8 @@ int sparse_attn_tree_workspace_size(const sparse_attn_params* p, size_t* bytes);
  * Context tokens must be finite; a draft's K and V may hold anything (infinities and NaN
  * too) as long as the queries that see it are meant to: they reach no other query's row.  In
  * the rows that see it a NaN score makes all channels NaN, and an infinity or NaN in V that
- * channel infinite or NaN, however small its weight.
+ * channel infinite or NaN, however small its weight.  A score of -infinity is a weight of 0 (with
+ * fp32 queries or K/V an infinite key gives NaN).
  * Memory behind the drafts is never read into a result.
  * Q <= 1024, else UNSUPPORTED.  The result does not depend on the launch's timing. */
 int sparse_attn_tree_decode(const sparse_attn_params* p, const void* q, const void* k_pages,

@@ -29,6 +29,7 @@ constexpr int kTrTile = 64;
 // 18.1 against 18.7, 32 rows over 4 x 777 (5.5) 21.2 against 20.0, 128 rows over 777 (5.5) 21.5
 // against 19.1, 64 rows over 16 x 100 (6.7) 22.2 against 15.6.
 constexpr int kTreeSmallWork = 4;
+constexpr uint32_t kNotSeen = 0xffffffffu;   // score of a token that the row does not see: a NaN that no product gives
 constexpr int kTrEntries = 512;      // list entries resolved at a time
 constexpr int kTrInfo = 4;           // tiles looked up ahead of their copies, at least the stages + 1
 
@@ -365,8 +366,8 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
                     for (int e = 0; e < 2; ++e) {
                         const bool ok0 = (see[0][nt / 4] >> ((nt & 3) * 8 + 2 * t4 + e)) & 1u;
                         const bool ok1 = (see[1][nt / 4] >> ((nt & 3) * 8 + 2 * t4 + e)) & 1u;
-                        c[nt][e] = ok0 ? c[nt][e] : -INFINITY;
-                        c[nt][e + 2] = ok1 ? c[nt][e + 2] : -INFINITY;
+                        c[nt][e] = ok0 ? c[nt][e] : __uint_as_float(kNotSeen);
+                        c[nt][e + 2] = ok1 ? c[nt][e + 2] : __uint_as_float(kNotSeen);
                         mx[0] = fmaxf(mx[0], c[nt][e]);
                         mx[1] = fmaxf(mx[1], c[nt][e + 2]);
                     }
@@ -382,14 +383,15 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
                 // (score - maximum) * scale, in that order: a rounded product would be off by its own size.
                 float psum[2] = {0.f, 0.f};
                 const F2 scale2 = make_f2(a.scale_log2, a.scale_log2);
+                const float sub[2] = {m_run[0] == -INFINITY ? 0.f : -m_run[0], m_run[1] == -INFINITY ? 0.f : -m_run[1]};
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         float &x = c[nt][2 * h], &y = c[nt][2 * h + 1];
-                        const F2 d = mul2(add2(make_f2(x, y), make_f2(-m_run[h], -m_run[h])), scale2);
-                        x = x == -INFINITY ? 0.f : fast_exp2(d.f.x);
-                        y = y == -INFINITY ? 0.f : fast_exp2(d.f.y);
+                        const F2 d = mul2(add2(make_f2(x, y), make_f2(sub[h], sub[h])), scale2);
+                        x = __float_as_uint(x) == kNotSeen ? -0.f : fast_exp2(d.f.x);
+                        y = __float_as_uint(y) == kNotSeen ? -0.f : fast_exp2(d.f.y);
                         psum[h] += x;
                         psum[h] += y;
                     }
@@ -459,12 +461,8 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
                         join(acc[j], x);
                     }
                 }
-                if (bad0 | bad1) {                           // rows taken out above, where they are seen (weight or none)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (!((see[e >> 1][nt / 4] >> ((nt & 3) * 8 + 2 * t4 + (e & 1))) & 1u)) c[nt][e] = -1.f;
+                if (bad0 | bad1) {                           // rows taken out above, where they are seen (their
+                                                             // weight may be 0; those not seen have -0)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll 1
@@ -479,8 +477,8 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
 #pragma unroll
                                 for (int e = 0; e < 2; ++e) {
                                     const float v = load_q(a.v_pages, at + j * 8 + 2 * t4 + e, KB);
-                                    if (p0 >= 0.f) acc[j][e] = fmaf(p0, v, acc[j][e]);
-                                    if (p1 >= 0.f) acc[j][2 + e] = fmaf(p1, v, acc[j][2 + e]);
+                                    if (!signbit(p0)) acc[j][e] = fmaf(p0, v, acc[j][e]);
+                                    if (!signbit(p1)) acc[j][2 + e] = fmaf(p1, v, acc[j][2 + e]);
                                 }
                         }
                 }

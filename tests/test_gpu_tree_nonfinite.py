@@ -110,3 +110,35 @@ def test_values_whose_weight_is_too_small(name, value):
     assert ((out.double() - exact).abs()[:, 0] <= bound[:, 0]).all()
     hit = ~torch.isfinite(out[:, 1:, :, 3])
     assert hit.all(), f"{int((~hit).sum())} of {hit.numel()} rows that see the draft are finite there"
+
+
+@pytest.mark.parametrize("value", [0.5, INF])
+@pytest.mark.parametrize("name", ["few", "few_parts", "small_rows", "r28", "r28_parts", "r64", "r100", "r100_parts"])
+def test_scores_of_minus_infinity(name, value):
+    """Draft 1 has a key that is infinite in one channel, and scores of -infinity: its weight is 0, also
+    in rows that see nothing else; an infinite value of it shows in its channel all the same."""
+    c = VALUES[name]
+    if name == "few":
+        c = Case(**{**c.__dict__, "lens": (0, 300)})               # the first sequence has no context
+    table = c.block_table()
+    pools = c.fill(c.pools(), table)
+    q = c.normal("q", c.batch, c.drafts, c.hq, c.dim)
+    q[..., 5] = 4.0
+    see = chain_mask(c.drafts).expand(c.batch, -1, -1).clone()
+    if name == "few":
+        see[0, 2] = torch.tensor([False, True, False])
+    without = see.clone()
+    without[:, :, 1] = False
+    exact, bound = tree_exact(c, q, pools, table, without)
+    for b, n in enumerate(c.all_lens):
+        page, off = place(c, table, b, torch.tensor([n + 1]))
+        key, row = pools[0][page, :, off], pools[1][page, :, off]
+        key[..., 5], row[..., 3] = -INF, value
+        pools[0][page, :, off], pools[1][page, :, off] = key, row
+    out, ws = call(c, q, pools, table, see)
+    assert B.sparse_attn_get_device_error(ws) == 0
+    out = out.cpu()
+    rest = torch.arange(c.dim) != 3 if value == INF else torch.ones(c.dim, dtype=torch.bool)
+    assert ((out.double() - exact).abs()[..., rest] <= bound[..., rest]).all()
+    if value == INF:
+        assert not torch.isfinite(out[..., 3][see[:, :, 1]]).any()
