@@ -5,8 +5,9 @@
 // (x_a cos(p w_i) - x_b sin(p w_i), x_b cos(p w_i) + x_a sin(p w_i)).  p w_i is needed to
 // far below a turn although p may be in the millions: the frequency is held in turns per
 // position as a 64-bit fraction f = frac(w_i / 2 pi) 2^64, so p f mod 2^64 is the exact
-// fraction of a turn of the rounded frequency (the integer product wraps at a turn) and its
-// upper half, as a signed number of half turns, goes to sincospi.
+// fraction of a turn of the rounded frequency (the integer product wraps at a turn).  What the
+// nearest quarter turn leaves of it, at most an eighth, goes to sincospi in fp32: off by 2.4e-8
+// at most, where the whole fraction in fp32 would be off by 9.4e-8, more than a step of a sine.
 //
 // Mapping: CTA = a run of tokens of one sequence (a block, or as many blocks as make 64
 // tokens) and a share of the heads.  The run's cosines and sines are computed once into
@@ -300,8 +301,19 @@ __global__ void __launch_bounds__(kAppThreads, 2) append_kernel(AppendArgs a)
         const int r = e / half, i = e - r * half;
         const long long pos = a.positions != nullptr ? a.positions[r0 + r] : t0 + r;
         const unsigned long long phase = (unsigned long long)pos * s_freq[i];
+        const unsigned quarter = (unsigned(phase >> 32) + 0x20000000u) >> 30;           // the nearest one
+        const long long rest = (long long)(phase - ((unsigned long long)quarter << 62));
         float sn, cn;
-        sincospif(float(int(phase >> 32)) * 4.656612873077392578125e-10f, &sn, &cn);   // 2^-31
+        sincospif(float(int(rest >> 30)) * 1.16415321826934814453125e-10f, &sn, &cn);  // 2^-33: in half turns
+        if (quarter & 1u) {
+            const float c = cn;
+            cn = -sn;
+            sn = c;
+        }
+        if (quarter & 2u) {
+            cn = -cn;
+            sn = -sn;
+        }
         float2* dst = reinterpret_cast<float2*>(s_cs + size_t(r) * (a.rotary / 4));
         dst[(((i & 7) >> 1) * rchunks + (i >> 3)) * 2 + (i & 1)] = make_float2(cn, sn);
     }
