@@ -9,11 +9,14 @@
 //     bits, which add up to it exactly (two would leave 2^-18 in every weight, more than an
 //     fp32 softmax's own error), an fp32 query likewise.
 //   fp32 K/V: mma.m16n8k8 on tf32 parts, x = hi + lo rounded to nearest (22 bits), the three
-//     products that matter.  The channel (token) order inside a k-step is permuted alike on
+//     products that matter: each operand is off by at most 2^-22 of itself and lo lo, as much, is
+//     left out.  Three parts would take six products for these three, which bound such calls.
+//     (Measured error against 64 bits 3.5e-7, a plain fp32 computation's 4.1e-7.)  The channel (token) order inside a k-step is permuted alike on
 //     both sides, so that a thread's two elements are neighbours in memory.
 // The matrix unit rounds its running sum toward zero at every step, so a long chain drifts
 // (measured: 1e-5 of the output after 8K tokens).  A tile's product is therefore summed from
 // zero and joins the running O by one fused multiply-add, which carries the rescaling too.
+// Weights are ex2.approx: 2^-22 of themselves, 0 below 2^-126 of the largest.
 // Four warps: 4 x 16 rows over the same tokens, or with at most 16 rows 4 x 16 tokens over the
 // same rows, their (m, l, o) joined at the item's end.
 #include "sa_tree.cuh"
@@ -25,9 +28,9 @@ constexpr int kTrThreads = 128;
 constexpr int kTrTile = 64;
 // bf16 calls with more than 16 rows and at most so many tiles (of 64 tokens x 16 rows) an SM run here
 // too, 16 rows to an item: a tensor-memory item takes longer to begin and end.  24 rows over 777 tokens
-// (1.4 tiles an SM) 13.4 us against 19.0, 64 rows over 777 (2.7) 14.4 against 18.7, over 4 x 300 (4.2)
-// 18.1 against 18.7, 32 rows over 4 x 777 (5.5) 21.2 against 20.0, 128 rows over 777 (5.5) 21.5
-// against 19.1, 64 rows over 16 x 100 (6.7) 22.2 against 15.6.
+// (1.4 tiles an SM) 13.2 us against 16.8, 64 rows over 777 (2.7) 14.8 against 18.3, over 4 x 300 (4.2)
+// 15.8 against 25.0 (18.6 where the parts are joined by a launch), 32 rows over 4 x 777 (5.5) 21.2
+// against 18.2, 128 rows over 777 (5.5) 21.3 against 19.6, 64 rows over 16 x 100 (6.7) 21.9 against 15.6.
 constexpr int kTreeSmallWork = 4;
 constexpr uint32_t kNotSeen = 0xffffffffu;   // score of a token that the row does not see: a NaN that no product gives
 constexpr int kTrEntries = 512;      // list entries resolved at a time

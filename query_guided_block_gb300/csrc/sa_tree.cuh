@@ -451,10 +451,10 @@ __device__ void tree_arrive_and_merge(const TreeArgs& a, int item, int start, in
 
 // Items whose parts hold this much are added up by a launch of their own (a warp per row, over
 // the whole GPU) instead of by the CTA that arrives last, whose SM reads about 100 KB a
-// microsecond; the second launch costs the host 2.5 us.  16 rows over 777 tokens (48 KB) 12.2 us
-// against 16.0, over 300 (24 KB) 12.3 against 15.5, 64 rows over 8 x 777 (64 KB) 23.3 against 29.2.
+// microsecond; the second launch costs the host 2.5 us.  16 rows over 777 tokens (48 KB) 12.0 us
+// against 16.8, over 300 (24 KB) 12.3 against 16.0, 64 rows over 8 x 777 (64 KB) 23.8 against 30.2.
 // With few rows the launch has few warps, each with all the parts: 4 rows over 8K tokens (36 KB)
-// 21.9 us against 18.9, 8 rows over 777 (24 KB) 11.4 against 12.9.
+// 19.8 us against 18.2, 8 rows over 777 (24 KB) 11.4 against 13.4.
 constexpr long long kTreeCombineBytes = 16 * 1024;
 constexpr int kTreeCombineRows = 8;
 void tree_choose_combine(TreeArgs& a, int ctas);

@@ -12,12 +12,12 @@
 // the first two (all three) parts at once, and the copies of O are added up at the item's end.  V
 // is read from shared memory twice (once) instead of three times, and all parts fit into tensor
 // memory, which leaves room for two more ring units.  Against copies that share the tokens out
-// (three passes over V, the third part through shared memory): 32 rows over 16 x 32K tokens 332 us
-// for 402, 64 rows over 16 ragged contexts of up to 32K 277 for 320, 80 selected blocks 46.6 for 53.
+// (three passes over V, the third part through shared memory): 32 rows over 16 x 32K tokens 328 us
+// for 402, 64 rows over 16 ragged contexts of up to 32K 277 for 320, 80 selected blocks 48 for 53.
 //
 // Roles (16 warps):
 //   warps 0-7   the softmax: two threads own a query row, each half of the tile's tokens.  They
-//               read S, take the maximum, write P.
+//               read S, join their maxima in a word of shared memory, write P.
 //   warps 8-11  add every finished O tile to the running O: a thread per row, the whole row in
 //               registers.
 //   warp 12     resolves the list's entries 32 at a time and brings K and V by TMA, one box
@@ -35,8 +35,8 @@
 // Per 128 tokens the tensor core does 4 x 128 x 128 x D multiply-adds (one part for S, three
 // for P V), about 2050 cycles at D = 128; the 64 KB of K and V arrive in about 2800 cycles
 // at the SM's share of the HBM bandwidth.  Up to 64 rows memory bounds it (32 rows: 95% of the
-// measured copy bandwidth); at 96 rows over 128K tokens (116 us, 79 us of memory) and 256 rows
-// over 8 x 16K (250 us, 81 us of memory, 162 us of the four products) it is the chain S, softmax, P V
+// measured copy bandwidth); at 96 rows over 128K tokens (114 us, 79 us of memory) and 256 rows
+// over 8 x 16K (233 us, 81 us of memory, 162 us of the four products) it is the chain S, softmax, P V
 // of a tile and the passes over V, whose shared-memory reads (3 x 32 KB, with Q, K and the third
 // part 190 KB a tile) take about as long as the products.
 #include "sa_tcgen05.cuh"
@@ -889,7 +889,7 @@ cudaError_t launch_tree_tc(TreeArgs a, cudaStream_t s)
     a.merge_scale = 1.f;           // maxima are scaled
     a.item_rows = tree_item_rows(a.R);
     a.row_groups = (a.R + a.item_rows - 1) / a.item_rows;
-    // 128 rows over 777 tokens 18.9 us, with parts of at least 1 tile 19.8, of 4 32.8; an item's start and
+    // 128 rows over 777 tokens 19.6 us, with parts of at least 1 tile 20.4, of 4 35.4; an item's start and
     // end take about as long as six tiles.
     a.min_per = 2;
     a.half_slack = 3;
