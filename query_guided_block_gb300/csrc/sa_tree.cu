@@ -6,13 +6,14 @@
 // rows: S = Q K^T, the softmax with a running maximum and sum on the accumulator fragments,
 // O += P V with the score fragments as the A operand.
 //   bf16 K/V: mma.m16n8k16, fp32 accumulation.  P goes in as three bf16 parts cut off its 24
-//     bits, which add up to it exactly (two would leave 2^-18 in every weight, more than an
-//     fp32 softmax's own error), an fp32 query likewise.
+//     bits, which add up to it exactly (two would leave up to 2^-15 of every weight, more than
+//     an fp32 softmax's own error), an fp32 query likewise.
 //   fp32 K/V: mma.m16n8k8 on tf32 parts, x = hi + lo rounded to nearest (22 bits), the three
 //     products that matter: each operand is off by at most 2^-22 of itself and lo lo, as much, is
 //     left out.  Three parts would take six products for these three, which bound such calls.
-//     (Measured error against 64 bits 3.5e-7 to 8e-7, a plain fp32 computation's 4.1e-7 to 5e-7.)  The channel (token) order inside a k-step is permuted alike on
-//     both sides, so that a thread's two elements are neighbours in memory.
+//     (Measured error against 64 bits 3.5e-7 to 8e-7, a plain fp32 computation's 4.1e-7 to 5e-7.)
+//     The channel (token) order inside a k-step is permuted alike on both sides, so that a thread's
+//     two elements are neighbours in memory.
 // The matrix unit rounds its running sum toward zero at every step, so a long chain drifts
 // (measured: 1e-5 of the output after 8K tokens).  A tile's product is therefore summed from
 // zero and joins the running O by one fused multiply-add, which carries the rescaling too.

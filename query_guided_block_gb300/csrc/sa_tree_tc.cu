@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     // the softmax's reference of this tile
                     const float m_old = __fmul_rn(m_acc, a.scale_log2);
                     m_acc = tc_reference(m_acc, sh.top[gt & 3u][row], a.scale_log2);
-                    sh.top[gt & 3u][row] = kOrderedLeast;                      // for the tile four on, whose scores wait for this one's output
+                    sh.top[gt & 3u][row] = kOrderedLeast;          // for the tile four on (its scores wait for o_read of this one)
                     const float w0 = m_old == -INFINITY ? 0.f : fast_exp2(m_old - __fmul_rn(m_acc, a.scale_log2));
                     if (__any_sync(kFullMask, w0 != 1.f)) {                    // rarely after the first tiles
                         const F2 w02 = make_f2(w0, w0);
