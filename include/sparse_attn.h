@@ -420,6 +420,27 @@ int sparse_attn_append_kv(const sparse_attn_params* p, int32_t num_rows, const i
                           void* q_out, void* k_pages, void* v_pages, const int32_t* block_table,
                           void* kmin, void* kmax, void* ws, size_t ws_bytes, sparse_attn_stream stream);
 
+/* sparse_attn_append_kv with a norm of the queries and keys of each head before the rotation, and
+ * with positions of several axes (time, height, width of images and video), in the same launch.
+ *   Norm: x[d] / sqrt(mean over the head's D channels of x^2 + eps) * weight[d], of queries when
+ *   q_weight is given and of keys when k_weight is; values are not normed.  Weights are device
+ *   floats, 16-byte aligned: [D] for all heads (stride 0) or [heads, D] (stride D).  eps > 0 when
+ *   there is a weight.  Norm and rotation are fp32; each result is rounded once.
+ *   Axes: with num_axes = A > 1 (at most 8), positions is device int32 [A, num_rows] and
+ *   axis_of device int32 [rotary_dim / 2] says which axis turns pair i:
+ *   angle_i = positions[axis_of[i]][row] * inv_freq[i].  An axis outside [0, A) sets
+ *   SPARSE_ATTN_ERR_LENGTH and counts as axis 0.  With A = 1 axis_of is not read and positions may be
+ *   NULL, as in sparse_attn_append_kv.
+ * Everything else, and the result where nothing of this is asked for, as sparse_attn_append_kv. */
+int sparse_attn_append_kv_norm(const sparse_attn_params* p, int32_t num_rows, const int32_t* cu_rows,
+                               const int32_t* seq_lens, const int32_t* positions, int32_t num_axes,
+                               const int32_t* axis_of, int32_t rotary_dim, int32_t pairing, const double* inv_freq,
+                               const float* q_weight, int64_t q_weight_stride, const float* k_weight,
+                               int64_t k_weight_stride, float eps, const void* q_new, int64_t q_stride,
+                               const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,
+                               void* q_out, void* k_pages, void* v_pages, const int32_t* block_table,
+                               void* kmin, void* kmax, void* ws, size_t ws_bytes, sparse_attn_stream stream);
+
 /* Workspace of sparse_attn_tree_decode for this problem (it also serves
  * sparse_attn_append_kv and sparse_attn_commit_drafts, which use its first 256 bytes);
  * independent of n_tokens, so one workspace serves a growing context.  A workspace large
@@ -466,6 +487,69 @@ int sparse_attn_commit_drafts(const sparse_attn_params* p, const int32_t* seq_le
                               int32_t path_stride, const int32_t* path_len, void* k_pages, void* v_pages,
                               const int32_t* block_table, void* kmin, void* kmax, int32_t* new_lens,
                               void* ws, size_t ws_bytes, sparse_attn_stream stream);
+
+/* ---- Long contexts: shared prefixes, attention weights, eviction ---------------------
+ * No counterpart in the pages.  Conventions as for the draft calls above (seq_lens, inactive
+ * sequences, capacity, CUDA graphs); a workspace large enough for each may serve these calls and the
+ * draft calls in turn. */
+
+/* Workspace of sparse_attn_shared_decode with this many groups; independent of n_tokens. */
+int sparse_attn_shared_workspace_size(const sparse_attn_params* p, int32_t num_groups, size_t* bytes);
+
+/* sparse_attn_tree_decode (no selection) for a batch whose sequences share prefixes: the keys and values
+ * of a prefix are read once for all the sequences of its group.  The result is that of
+ * sparse_attn_tree_decode up to the order of its fp32 sums.
+ *   cu_seqs, device int32 [num_groups + 1], ascending: group g is sequences cu_seqs[g] ..
+ *   cu_seqs[g + 1] - 1, which hold the same first prefix_lens[g] tokens (device int32 [num_groups],
+ *   0 .. n_tokens, any number): the same pages, or for the block that the prefix ends in a copy
+ *   that each sequence fills further.  They are read through the page table of the first sequence
+ *   of the group that holds that many tokens.  Empty groups, groups of one sequence and sequences in
+ *   no group (which share nothing) are allowed.
+ *   A sequence with fewer tokens than its group's prefix, cu_seqs that are not ascending numbers in
+ *   0 .. B and prefix_lens out of range set SPARSE_ATTN_ERR_LENGTH; the sequences concerned are then
+ *   treated as inactive or, with cu_seqs out of order, their rows are unspecified.
+ * num_groups >= 1.  q, out, tree_mask and what may be NULL or infinite as in sparse_attn_tree_decode. */
+int sparse_attn_shared_decode(const sparse_attn_params* p, const void* q, const void* k_pages, const void* v_pages,
+                              const int32_t* block_table, const int32_t* seq_lens, int32_t num_groups,
+                              const int32_t* cu_seqs, const int32_t* prefix_lens, const uint32_t* tree_mask, float* out,
+                              void* ws, size_t ws_bytes, sparse_attn_stream stream);
+
+/* Workspace of sparse_attn_weigh_decode for contexts up to the capacity. */
+int sparse_attn_weigh_workspace_size(const sparse_attn_params* p, size_t* bytes);
+
+/* sparse_attn_tree_decode of a chain (no selection, tree_mask NULL) that also adds up the attention weight
+ * of every token: weights, device float [B, Hkv, nb_cap * block_size], 16-byte aligned,
+ *   weights[b][kvh][t] += sum over the Q x G query rows of the KV head of softmax_t  for t < seq_lens[b];
+ * the Q new tokens' entries are set to that sum (whatever they held), entries behind them are left
+ * alone.  With Q = 1 a decode step; with the last Q tokens of a prompt as queries the weights by which
+ * its first eviction may go.  All tokens must be finite.  The sums do not depend on timing. */
+int sparse_attn_weigh_decode(const sparse_attn_params* p, const void* q, const void* k_pages, const void* v_pages,
+                             const int32_t* block_table, const int32_t* seq_lens, float* weights, float* out, void* ws,
+                             size_t ws_bytes, sparse_attn_stream stream);
+
+/* Workspace of sparse_attn_evict_tokens. */
+int sparse_attn_evict_workspace_size(const sparse_attn_params* p, int32_t keep_tokens, size_t* bytes);
+
+/* Keep the tokens with the largest weights and drop the others, for each KV head by itself.
+ *   Sequence b keeps k = keep_lens[b] tokens (device int32 [B], sink_tokens + recent_tokens ..
+ *   keep_tokens, or -1: leave the sequence alone; NULL: keep_tokens for all), all of them when it has no
+ *   more: its first sink_tokens, its last recent_tokens, and of the others those with the largest
+ *   weights[b][kvh][t] (layout of sparse_attn_weigh_decode; not NaN), the lower index first
+ *   among equals.
+ *   Kept tokens stay in their order: the i-th one's K and V go to page new_table[b][i / block_size]
+ *   (device int32 [B, ceil(keep_tokens / block_size)]) at i % block_size, its weight to
+ *   weights[b][kvh][i], its index to kept_ids[b][kvh][i] (device int32 [B, Hkv, keep_tokens]; entries
+ *   behind the kept ones are left alone).  new_lens[b] = the number kept (an inactive sequence keeps
+ *   -1, one left alone its length); new_lens must not overlap seq_lens or keep_lens.
+ *   The new pages must not be pages that any sequence of the call reads, and belong to one sequence.
+ *   kmin / kmax: both or neither; the rows of the new blocks become the box of their tokens.
+ * Afterwards new_table's row is the sequence's page table.  A token's index no longer tells its position:
+ * later tokens are appended with `positions`.  keep_tokens >= 1. */
+int sparse_attn_evict_tokens(const sparse_attn_params* p, const int32_t* seq_lens, int32_t keep_tokens,
+                             const int32_t* keep_lens, int32_t sink_tokens, int32_t recent_tokens, float* weights,
+                             void* k_pages, void* v_pages, const int32_t* block_table, const int32_t* new_table,
+                             void* kmin, void* kmax, int32_t* kept_ids, int32_t* new_lens, void* ws, size_t ws_bytes,
+                             sparse_attn_stream stream);
 
 /* Synchronise `stream`, copy the device error word to *flags (SPARSE_ATTN_ERR_* bits)
  * and clear it.  Returns SPARSE_ATTN_DEVICE_BOUNDS when any bit was set. */

@@ -113,9 +113,17 @@ def lib():
                                              vp], C.c_int),
             "sparse_attn_append_kv": ([P, i32, vp, vp, vp, i32, i32, vp, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp,
                                        vp, vp, vp, sz, vp], C.c_int),
+            "sparse_attn_append_kv_norm": ([P, i32, vp, vp, vp, i32, vp, i32, i32, vp, vp, i64, vp, i64, C.c_float, vp, i64,
+                                            vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, sz, vp], C.c_int),
             "sparse_attn_tree_workspace_size": ([P, C.POINTER(C.c_size_t)], C.c_int),
             "sparse_attn_tree_decode": ([P, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp], C.c_int),
             "sparse_attn_commit_drafts": ([P, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp], C.c_int),
+            "sparse_attn_shared_workspace_size": ([P, i32, C.POINTER(C.c_size_t)], C.c_int),
+            "sparse_attn_shared_decode": ([P, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, sz, vp], C.c_int),
+            "sparse_attn_weigh_workspace_size": ([P, C.POINTER(C.c_size_t)], C.c_int),
+            "sparse_attn_weigh_decode": ([P, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp], C.c_int),
+            "sparse_attn_evict_workspace_size": ([P, i32, C.POINTER(C.c_size_t)], C.c_int),
+            "sparse_attn_evict_tokens": ([P, vp, i32, vp, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp], C.c_int),
         }
         for name, (args, res) in sigs.items():
             fn = getattr(L, name)
@@ -135,7 +143,10 @@ def exported_symbols():
             "sparse_attn_append_meta", "sparse_attn_step", "sparse_attn_step_launches",
             "sparse_attn_select_noalloc_device_error", "sparse_attn_workspace_set_wait_limit",
             "sparse_attn_decode_slots_io", "sparse_attn_diff_slots", "sparse_attn_append_kv",
-            "sparse_attn_tree_workspace_size", "sparse_attn_tree_decode", "sparse_attn_commit_drafts"]
+            "sparse_attn_tree_workspace_size", "sparse_attn_tree_decode", "sparse_attn_commit_drafts",
+            "sparse_attn_append_kv_norm", "sparse_attn_shared_workspace_size", "sparse_attn_shared_decode",
+            "sparse_attn_weigh_workspace_size", "sparse_attn_weigh_decode", "sparse_attn_evict_workspace_size",
+            "sparse_attn_evict_tokens"]
 
 
 def _status_string(status: int) -> str:
@@ -376,6 +387,7 @@ class _Shapes:
         self.out = (p.batch, n, p.num_q_heads, p.head_dim)
         self.out_one = (p.batch, p.num_q_heads, p.head_dim) if n == 1 else self.out
         self.mask = (p.batch, n, -(-n // 32))
+        self.weights = (p.batch, p.num_kv_heads, nb_cap * p.block_size)
         self.sel = (p.batch, p.num_kv_heads, int(lib().sparse_attn_sel_stride(C.byref(p))))
 
 
@@ -479,6 +491,50 @@ def sparse_attn_append_kv(p, q_new, k_new, v_new, inv_freq, q_out, k_pages, v_pa
                None if kmax is None else _tensor_ptr(kmax, dev, "kmax", g.box, kvt), w, n)
 
 
+def _norm_weight(t, device: int, what: str, heads: int, dim: int):
+    """Pointer and head stride of a norm's weights, [dim] or [heads, dim]."""
+    if t is None:
+        return None, 0
+    per_head = t.dim() == 2
+    return _tensor_ptr(t, device, what, (heads, dim) if per_head else (dim,), torch.float32), dim if per_head else 0
+
+
+def sparse_attn_append_kv_norm(p, q_new, k_new, v_new, q_weight, k_weight, eps, inv_freq, q_out, k_pages, v_pages,
+                               block_table, ws, cu_rows=None, seq_lens=None, positions=None, axis_of=None,
+                               pairing=ROTATE_HALVES, kmin=None, kmax=None, stream=None) -> None:
+    """sparse_attn_append_kv with a norm of each head's queries and keys (q_weight, k_weight: float32
+    [D] or [heads, D], or None for no norm) and positions of several axes: positions int32
+    [axes, rows] with axis_of int32 [rotary_dim / 2], or [rows] (or None) without it."""
+    g, dev, rows = _shapes(p), _device_of(k_new, "k_new"), k_new.shape[0]
+    kv_rows, q_rows, qt, kvt = (rows, g.kv_heads, g.dim), (rows, g.q_heads, g.dim), g.q_dtype, g.kv_dtype
+    k, ks = _rows_ptr(k_new, dev, "k_new", kv_rows, qt)
+    v, vs = _rows_ptr(v_new, dev, "v_new", kv_rows, qt)
+    q, qs = (None, 0) if q_new is None else _rows_ptr(q_new, dev, "q_new", q_rows, qt)
+    qw, qws = _norm_weight(q_weight, dev, "q_weight", g.q_heads, g.dim)
+    kw, kws = _norm_weight(k_weight, dev, "k_weight", g.kv_heads, g.dim)
+    rotary, freq, axes, axis, pos = 0, None, 1, None, None
+    if inv_freq is not None:
+        rotary = 2 * inv_freq.numel()
+        freq = _tensor_ptr(inv_freq, dev, "inv_freq", (rotary // 2,), torch.float64)
+    if axis_of is not None:
+        if positions is None or positions.dim() != 2:
+            raise ValueError("positions: expected [axes, rows] with axis_of")
+        axes = positions.shape[0]
+        axis = _tensor_ptr(axis_of, dev, "axis_of", (rotary // 2,), _I32)
+    if positions is not None:
+        pos = _tensor_ptr(positions, dev, "positions", (rows,) if axis_of is None else (axes, rows), _I32)
+    w, n = _workspace(ws, dev)
+    _launch_on(dev, "sparse_attn_append_kv_norm", stream, C.byref(p), rows,
+               None if cu_rows is None else _tensor_ptr(cu_rows, dev, "cu_rows", g.ends, _I32),
+               None if seq_lens is None else _tensor_ptr(seq_lens, dev, "seq_lens", g.per_seq, _I32),
+               pos, axes, axis, rotary, pairing, freq, qw, qws, kw, kws, eps, q, qs, k, ks, v, vs,
+               None if q_out is None else _tensor_ptr(q_out, dev, "q_out", q_rows, qt),
+               _tensor_ptr(k_pages, dev, "k_pages", g.pool, kvt), _tensor_ptr(v_pages, dev, "v_pages", g.pool, kvt),
+               _tensor_ptr(block_table, dev, "block_table", g.table, _I32),
+               None if kmin is None else _tensor_ptr(kmin, dev, "kmin", g.box, kvt),
+               None if kmax is None else _tensor_ptr(kmax, dev, "kmax", g.box, kvt), w, n)
+
+
 def sparse_attn_tree_workspace_size(p: sparse_attn_params) -> int:
     n = C.c_size_t(0)
     _check("sparse_attn_tree_workspace_size", lib().sparse_attn_tree_workspace_size(C.byref(p), C.byref(n)))
@@ -521,4 +577,90 @@ def sparse_attn_commit_drafts(p, path, path_len, k_pages, v_pages, block_table, 
                _tensor_ptr(block_table, dev, "block_table", g.table, _I32),
                None if kmin is None else _tensor_ptr(kmin, dev, "kmin", g.box, kvt),
                None if kmax is None else _tensor_ptr(kmax, dev, "kmax", g.box, kvt),
+               _tensor_ptr(new_lens, dev, "new_lens", g.per_seq, _I32), w, n)
+
+
+# -------------------- long contexts: shared prefixes, attention weights, eviction --
+
+def _mask_ptr(tree_mask, device: int, shape):
+    if tree_mask is None:
+        return None
+    return _tensor_ptr(tree_mask, device, "tree_mask", shape, torch.uint32 if tree_mask.dtype is torch.uint32 else _I32)
+
+
+def sparse_attn_shared_workspace_size(p: sparse_attn_params, num_groups: int) -> int:
+    n = C.c_size_t(0)
+    _check("sparse_attn_shared_workspace_size",
+           lib().sparse_attn_shared_workspace_size(C.byref(p), int(num_groups), C.byref(n)))
+    return int(n.value)
+
+
+def sparse_attn_shared_decode(p, q, k_pages, v_pages, block_table, cu_seqs, prefix_lens, out, ws, seq_lens=None,
+                              tree_mask=None, stream=None) -> None:
+    """Attention of Q drafts per sequence as sparse_attn_tree_decode, with the sequences cu_seqs[g] ..
+    cu_seqs[g + 1] - 1 sharing their first prefix_lens[g] tokens, which are read once; q and out
+    [B, Q, Hq, D] (or [B, Hq, D] for one)."""
+    g, dev = _shapes(p), _device_of(q, "q")
+    shape = g.out if q.dim() == 4 else g.out_one
+    groups = prefix_lens.numel()
+    w, n = _workspace(ws, dev)
+    _launch_on(dev, "sparse_attn_shared_decode", stream, C.byref(p), _tensor_ptr(q, dev, "q", shape, g.q_dtype),
+               _tensor_ptr(k_pages, dev, "k_pages", g.pool, g.kv_dtype),
+               _tensor_ptr(v_pages, dev, "v_pages", g.pool, g.kv_dtype),
+               _tensor_ptr(block_table, dev, "block_table", g.table, _I32),
+               None if seq_lens is None else _tensor_ptr(seq_lens, dev, "seq_lens", g.per_seq, _I32), groups,
+               _tensor_ptr(cu_seqs, dev, "cu_seqs", (groups + 1,), _I32),
+               _tensor_ptr(prefix_lens, dev, "prefix_lens", (groups,), _I32), _mask_ptr(tree_mask, dev, g.mask),
+               _tensor_ptr(out, dev, "out", shape, torch.float32), w, n)
+
+
+def sparse_attn_weigh_workspace_size(p: sparse_attn_params) -> int:
+    n = C.c_size_t(0)
+    _check("sparse_attn_weigh_workspace_size", lib().sparse_attn_weigh_workspace_size(C.byref(p), C.byref(n)))
+    return int(n.value)
+
+
+def sparse_attn_weigh_decode(p, q, k_pages, v_pages, block_table, weights, out, ws, seq_lens=None, stream=None) -> None:
+    """Attention of a chain of Q tokens per sequence that adds the attention weight of every token to
+    weights [B, Hkv, blocks of the capacity * block_size] (and sets the new tokens'); q and out
+    [B, Q, Hq, D] (or [B, Hq, D] for one)."""
+    g, dev = _shapes(p), _device_of(q, "q")
+    shape = g.out if q.dim() == 4 else g.out_one
+    w, n = _workspace(ws, dev)
+    _launch_on(dev, "sparse_attn_weigh_decode", stream, C.byref(p), _tensor_ptr(q, dev, "q", shape, g.q_dtype),
+               _tensor_ptr(k_pages, dev, "k_pages", g.pool, g.kv_dtype),
+               _tensor_ptr(v_pages, dev, "v_pages", g.pool, g.kv_dtype),
+               _tensor_ptr(block_table, dev, "block_table", g.table, _I32),
+               None if seq_lens is None else _tensor_ptr(seq_lens, dev, "seq_lens", g.per_seq, _I32),
+               _tensor_ptr(weights, dev, "weights", g.weights, torch.float32),
+               _tensor_ptr(out, dev, "out", shape, torch.float32), w, n)
+
+
+def sparse_attn_evict_workspace_size(p: sparse_attn_params, keep_tokens: int) -> int:
+    n = C.c_size_t(0)
+    _check("sparse_attn_evict_workspace_size",
+           lib().sparse_attn_evict_workspace_size(C.byref(p), int(keep_tokens), C.byref(n)))
+    return int(n.value)
+
+
+def sparse_attn_evict_tokens(p, keep_tokens, sink_tokens, recent_tokens, weights, k_pages, v_pages, block_table,
+                             new_table, kept_ids, new_lens, ws, seq_lens=None, keep_lens=None, kmin=None, kmax=None,
+                             stream=None) -> None:
+    """Keep keep_tokens tokens (or keep_lens [B]) of every sequence and KV head, those with the largest
+    weights besides the first sink_tokens and the last recent_tokens, in the pages of new_table
+    [B, ceil(keep_tokens / block_size)]; kept_ids [B, Hkv, keep_tokens] says which."""
+    g, dev = _shapes(p), _device_of(weights, "weights")
+    keep, kvt = int(keep_tokens), g.kv_dtype
+    blocks = -(-keep // p.block_size)
+    w, n = _workspace(ws, dev)
+    _launch_on(dev, "sparse_attn_evict_tokens", stream, C.byref(p),
+               None if seq_lens is None else _tensor_ptr(seq_lens, dev, "seq_lens", g.per_seq, _I32), keep,
+               None if keep_lens is None else _tensor_ptr(keep_lens, dev, "keep_lens", g.per_seq, _I32),
+               int(sink_tokens), int(recent_tokens), _tensor_ptr(weights, dev, "weights", g.weights, torch.float32),
+               _tensor_ptr(k_pages, dev, "k_pages", g.pool, kvt), _tensor_ptr(v_pages, dev, "v_pages", g.pool, kvt),
+               _tensor_ptr(block_table, dev, "block_table", g.table, _I32),
+               _tensor_ptr(new_table, dev, "new_table", g.per_seq + (blocks,), _I32),
+               None if kmin is None else _tensor_ptr(kmin, dev, "kmin", g.box, kvt),
+               None if kmax is None else _tensor_ptr(kmax, dev, "kmax", g.box, kvt),
+               _tensor_ptr(kept_ids, dev, "kept_ids", g.per_unit + (keep,), _I32),
                _tensor_ptr(new_lens, dev, "new_lens", g.per_seq, _I32), w, n)

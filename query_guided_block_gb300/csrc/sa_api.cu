@@ -600,12 +600,24 @@ static long long capacity_of(const sparse_attn_params* p)
     return p->capacity_tokens > 0 ? p->capacity_tokens : p->n_tokens;
 }
 
-int sparse_attn_append_kv(const sparse_attn_params* p, int32_t num_rows, const int32_t* cu_rows,
-                          const int32_t* seq_lens, const int32_t* positions, int32_t rotary_dim,
-                          int32_t pairing, const double* inv_freq, const void* q_new, int64_t q_stride,
-                          const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,
-                          void* q_out, void* k_pages, void* v_pages, const int32_t* block_table,
-                          void* kmin, void* kmax, void* ws, size_t ws_bytes, sparse_attn_stream stream)
+// What sparse_attn_append_kv_norm has beyond sparse_attn_append_kv.
+struct AppendNorm {
+    int32_t num_axes;
+    const int32_t* axis_of;
+    const float* q_weight;
+    int64_t q_wstride;
+    const float* k_weight;
+    int64_t k_wstride;
+    float eps;
+};
+
+static int append_common(const sparse_attn_params* p, int32_t num_rows, const int32_t* cu_rows,
+                         const int32_t* seq_lens, const int32_t* positions, int32_t rotary_dim,
+                         int32_t pairing, const double* inv_freq, const void* q_new, int64_t q_stride,
+                         const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,
+                         void* q_out, void* k_pages, void* v_pages, const int32_t* block_table,
+                         void* kmin, void* kmax, void* ws, size_t ws_bytes, sparse_attn_stream stream,
+                         const AppendNorm& x)
 {
     Geometry g;
     int st = draft_geometry(p, &g);
@@ -618,6 +630,12 @@ int sparse_attn_append_kv(const sparse_attn_params* p, int32_t num_rows, const i
     if (cu_rows && !seq_lens) return SPARSE_ATTN_INVALID_ARG;
     if (!aligned(cu_rows, 4) || !aligned(seq_lens, 4) || !aligned(positions, 4)) return SPARSE_ATTN_INVALID_ARG;
     if ((q_new == nullptr) != (q_out == nullptr) || (kmin == nullptr) != (kmax == nullptr)) return SPARSE_ATTN_INVALID_ARG;
+    if (x.num_axes < 1 || x.num_axes > 8 || (x.num_axes > 1 && (!x.axis_of || !positions || rotary_dim == 0)))
+        return SPARSE_ATTN_INVALID_ARG;
+    if ((x.q_weight || x.k_weight) && !(x.eps > 0.f && !isinf(x.eps))) return SPARSE_ATTN_INVALID_ARG;
+    if (x.q_weight && !q_new) return SPARSE_ATTN_INVALID_ARG;
+    if ((x.q_wstride != 0 && x.q_wstride != g.D) || (x.k_wstride != 0 && x.k_wstride != g.D)) return SPARSE_ATTN_INVALID_ARG;
+    if (!aligned(x.axis_of, 4) || !aligned(x.q_weight, 16) || !aligned(x.k_weight, 16)) return SPARSE_ATTN_INVALID_ARG;
     if (g.B == 0 || num_rows == 0) return SPARSE_ATTN_OK;
     const int per_seq = num_rows / g.B;
     if (!cu_rows && num_rows % g.B != 0) return SPARSE_ATTN_INVALID_ARG;
@@ -655,7 +673,40 @@ int sparse_attn_append_kv(const sparse_attn_params* p, int32_t num_rows, const i
     c.kmin = kmin;
     c.kmax = kmax;
     c.capacity = int(capacity_of(p));
+    c.q_weight = x.q_weight;
+    c.k_weight = x.k_weight;
+    c.q_wstride = int(x.q_wstride);
+    c.k_wstride = int(x.k_wstride);
+    c.eps = x.eps;
+    c.num_axes = x.num_axes;
+    c.axis_of = x.num_axes > 1 ? x.axis_of : nullptr;   // with one axis there is nothing to look up
     return status_of(launch_append(g, c, static_cast<uint32_t*>(ws), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int sparse_attn_append_kv(const sparse_attn_params* p, int32_t num_rows, const int32_t* cu_rows,
+                          const int32_t* seq_lens, const int32_t* positions, int32_t rotary_dim,
+                          int32_t pairing, const double* inv_freq, const void* q_new, int64_t q_stride,
+                          const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,
+                          void* q_out, void* k_pages, void* v_pages, const int32_t* block_table,
+                          void* kmin, void* kmax, void* ws, size_t ws_bytes, sparse_attn_stream stream)
+{
+    return append_common(p, num_rows, cu_rows, seq_lens, positions, rotary_dim, pairing, inv_freq, q_new, q_stride, k_new,
+                         k_stride, v_new, v_stride, q_out, k_pages, v_pages, block_table, kmin, kmax, ws, ws_bytes, stream,
+                         AppendNorm{1, nullptr, nullptr, 0, nullptr, 0, 0.f});
+}
+
+int sparse_attn_append_kv_norm(const sparse_attn_params* p, int32_t num_rows, const int32_t* cu_rows,
+                               const int32_t* seq_lens, const int32_t* positions, int32_t num_axes,
+                               const int32_t* axis_of, int32_t rotary_dim, int32_t pairing, const double* inv_freq,
+                               const float* q_weight, int64_t q_weight_stride, const float* k_weight,
+                               int64_t k_weight_stride, float eps, const void* q_new, int64_t q_stride,
+                               const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,
+                               void* q_out, void* k_pages, void* v_pages, const int32_t* block_table,
+                               void* kmin, void* kmax, void* ws, size_t ws_bytes, sparse_attn_stream stream)
+{
+    return append_common(p, num_rows, cu_rows, seq_lens, positions, rotary_dim, pairing, inv_freq, q_new, q_stride, k_new,
+                         k_stride, v_new, v_stride, q_out, k_pages, v_pages, block_table, kmin, kmax, ws, ws_bytes, stream,
+                         AppendNorm{num_axes, axis_of, q_weight, q_weight_stride, k_weight, k_weight_stride, eps});
 }
 
 int sparse_attn_tree_workspace_size(const sparse_attn_params* p, size_t* bytes)
@@ -714,6 +765,136 @@ int sparse_attn_commit_drafts(const sparse_attn_params* p, const int32_t* seq_le
         return SPARSE_ATTN_INVALID_ARG;
     return status_of(launch_commit(g, seq_lens, path, path_stride, path_len, k_pages, v_pages, block_table, kmin, kmax,
                                    new_lens, static_cast<uint32_t*>(ws), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// ---- shared prefixes, weighed attention, eviction --------------------------------
+// Common to the two attentions: the pages of context and drafts, and what may not be null.
+static int attention_args(const sparse_attn_params* p, const Geometry& g, const void* q, const void* k_pages,
+                          const void* v_pages, const int32_t* block_table, const int32_t* seq_lens, const float* out)
+{
+    if (capacity_of(p) < (long long)g.N + g.Q) return SPARSE_ATTN_INVALID_ARG;   // the drafts' pages
+    if (g.B == 0) return SPARSE_ATTN_OK;
+    if (g.num_pages < 1 || !q || !out || !k_pages || !v_pages || !block_table) return SPARSE_ATTN_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(block_table, 4) ||
+        !aligned(seq_lens, 4))
+        return SPARSE_ATTN_INVALID_ARG;
+    return SPARSE_ATTN_OK;
+}
+
+// tree_geometry for a batch in groups: rows of all members are numbered in 32 bits, and so are the tiles of
+// their items.
+static int shared_geometry(const sparse_attn_params* p, int32_t num_groups, Geometry* g)
+{
+    const int st = tree_geometry(p, g);
+    if (st) return st;
+    if (num_groups < 1) return SPARSE_ATTN_INVALID_ARG;
+    const long long rows = (long long)g->B * g->Q * g->Hq;
+    const long long groups = ((long long)g->B * g->Q * g->G + 15) / 16 + num_groups;      // row groups of a KV head at most
+    const long long tiles = (long long)g->nb_cap * g->bs / kTreeLeastTile + 1;
+    if (rows > INT32_MAX / 2 || tiles * groups * g->Hkv > INT32_MAX / 2 ||
+        (long long)num_groups * g->Hkv * (((long long)g->B * g->Q * g->G + 15) / 16) > INT32_MAX / 2)
+        return SPARSE_ATTN_UNSUPPORTED;
+    return SPARSE_ATTN_OK;
+}
+
+int sparse_attn_shared_workspace_size(const sparse_attn_params* p, int32_t num_groups, size_t* bytes)
+{
+    if (!bytes) return SPARSE_ATTN_INVALID_ARG;
+    Geometry g;
+    const int st = shared_geometry(p, num_groups, &g);
+    if (st) return st;
+    *bytes = shared_workspace(g, num_groups);
+    return SPARSE_ATTN_OK;
+}
+
+int sparse_attn_shared_decode(const sparse_attn_params* p, const void* q, const void* k_pages, const void* v_pages,
+                              const int32_t* block_table, const int32_t* seq_lens, int32_t num_groups,
+                              const int32_t* cu_seqs, const int32_t* prefix_lens, const uint32_t* tree_mask, float* out,
+                              void* ws, size_t ws_bytes, sparse_attn_stream stream)
+{
+    Geometry g;
+    int st = shared_geometry(p, num_groups, &g);
+    if (st) return st;
+    if (!ws || !aligned(ws, 256) || ws_bytes < shared_workspace(g, num_groups)) return SPARSE_ATTN_INVALID_ARG;
+    st = attention_args(p, g, q, k_pages, v_pages, block_table, seq_lens, out);
+    if (st || g.B == 0) return st;
+    if (!cu_seqs || !prefix_lens || !aligned(cu_seqs, 4) || !aligned(prefix_lens, 4) || !aligned(tree_mask, 4))
+        return SPARSE_ATTN_INVALID_ARG;
+    const TreeCall c{q, k_pages, v_pages, block_table, seq_lens, nullptr, nullptr, tree_mask, out};
+    return status_of(launch_shared(g, c, num_groups, cu_seqs, prefix_lens, static_cast<char*>(ws),
+                                   reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int sparse_attn_weigh_workspace_size(const sparse_attn_params* p, size_t* bytes)
+{
+    if (!bytes) return SPARSE_ATTN_INVALID_ARG;
+    Geometry g;
+    const int st = tree_geometry(p, &g);
+    if (st) return st;
+    const long long most = (long long)g.N + g.Q, cap = capacity_of(p);
+    *bytes = weigh_workspace(g, cap > most ? cap : most);
+    return SPARSE_ATTN_OK;
+}
+
+int sparse_attn_weigh_decode(const sparse_attn_params* p, const void* q, const void* k_pages, const void* v_pages,
+                             const int32_t* block_table, const int32_t* seq_lens, float* weights, float* out, void* ws,
+                             size_t ws_bytes, sparse_attn_stream stream)
+{
+    Geometry g;
+    int st = tree_geometry(p, &g);
+    if (st) return st;
+    if (!ws || !aligned(ws, 256) || ws_bytes < weigh_workspace(g, (long long)g.N + g.Q)) return SPARSE_ATTN_INVALID_ARG;
+    st = attention_args(p, g, q, k_pages, v_pages, block_table, seq_lens, out);
+    if (st || g.B == 0) return st;
+    if (!weights || !aligned(weights, 16)) return SPARSE_ATTN_INVALID_ARG;
+    const TreeCall c{q, k_pages, v_pages, block_table, seq_lens, nullptr, nullptr, nullptr, out};
+    return status_of(launch_weigh(g, c, weights, static_cast<char*>(ws), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+static int evict_geometry(const sparse_attn_params* p, int32_t keep_tokens, Geometry* g)
+{
+    const int st = draft_geometry(p, g);
+    if (st) return st;
+    if (keep_tokens < 1) return SPARSE_ATTN_INVALID_ARG;
+    if ((long long)g->units() * ((keep_tokens + 63) / 64) > INT32_MAX / 8) return SPARSE_ATTN_UNSUPPORTED;
+    return SPARSE_ATTN_OK;
+}
+
+int sparse_attn_evict_workspace_size(const sparse_attn_params* p, int32_t keep_tokens, size_t* bytes)
+{
+    if (!bytes) return SPARSE_ATTN_INVALID_ARG;
+    Geometry g;
+    const int st = evict_geometry(p, keep_tokens, &g);
+    if (st) return st;
+    *bytes = evict_workspace(g, keep_tokens);
+    return SPARSE_ATTN_OK;
+}
+
+int sparse_attn_evict_tokens(const sparse_attn_params* p, const int32_t* seq_lens, int32_t keep_tokens,
+                             const int32_t* keep_lens, int32_t sink_tokens, int32_t recent_tokens, float* weights,
+                             void* k_pages, void* v_pages, const int32_t* block_table, const int32_t* new_table,
+                             void* kmin, void* kmax, int32_t* kept_ids, int32_t* new_lens, void* ws, size_t ws_bytes,
+                             sparse_attn_stream stream)
+{
+    Geometry g;
+    const int st = evict_geometry(p, keep_tokens, &g);
+    if (st) return st;
+    if (!ws || !aligned(ws, 256) || ws_bytes < evict_workspace(g, keep_tokens)) return SPARSE_ATTN_INVALID_ARG;
+    if (sink_tokens < 0 || recent_tokens < 0 || (long long)sink_tokens + recent_tokens > keep_tokens) return SPARSE_ATTN_INVALID_ARG;
+    if ((kmin == nullptr) != (kmax == nullptr)) return SPARSE_ATTN_INVALID_ARG;
+    if (g.B == 0) return SPARSE_ATTN_OK;
+    if (g.num_pages < 1 || !weights || !k_pages || !v_pages || !block_table || !new_table || !kept_ids || !new_lens)
+        return SPARSE_ATTN_INVALID_ARG;
+    if (!aligned(weights, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(kmin, 16) || !aligned(kmax, 16) ||
+        !aligned(block_table, 4) || !aligned(new_table, 4) || !aligned(kept_ids, 4) || !aligned(new_lens, 4) ||
+        !aligned(seq_lens, 4) || !aligned(keep_lens, 4))
+        return SPARSE_ATTN_INVALID_ARG;
+    // what every CTA reads must not be what one of them writes
+    auto over_new = [&](const int32_t* in, size_t n) { return in && new_lens < in + n && in < new_lens + g.B; };
+    if (over_new(seq_lens, g.B) || over_new(keep_lens, g.B)) return SPARSE_ATTN_INVALID_ARG;
+    const EvictCall c{seq_lens, keep_lens, keep_tokens, sink_tokens, recent_tokens, weights, k_pages, v_pages, block_table,
+                      new_table, kmin, kmax, kept_ids, new_lens};
+    return status_of(launch_evict(g, c, static_cast<char*>(ws), reinterpret_cast<cudaStream_t>(stream)));
 }
 
 // ---- selection for callers that cannot allocate device memory ---------------

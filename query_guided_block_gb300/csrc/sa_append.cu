@@ -9,6 +9,11 @@
 // nearest quarter turn leaves of it, at most an eighth, goes to sincospi in fp32: off by 2.4e-8
 // at most, where the whole fraction in fp32 would be off by 9.4e-8, more than a step of a sine.
 //
+// Norm.  x / sqrt(mean(x^2) + eps) * w over the channels of a head, before the rotation: the lanes
+// that hold a head row's channels are neighbours, so its sum of squares is two or three shuffles.
+// Squares, mean, root and the rotation stay in fp32; the one rounding to the stored type is at the
+// end.  Positions of several axes cost a look-up per frequency where the cosines are made.
+//
 // Mapping: CTA = a run of tokens of one sequence (a block, or as many blocks as make 64
 // tokens) and a share of the heads.  The run's cosines and sines are computed once into
 // shared memory for all heads.  A thread's item is 16 channels of one head row: the 8 pairs
@@ -47,6 +52,12 @@ struct AppendArgs {
     int runs_uniform;        // cu_rows null: runs a sequence may touch
     int cs_words;            // 16-byte words of the cosines and sines
     int rotary, pairs;       // pairs: neighbouring channels turn together
+    // head norms and position axes (the kernel's EXT form)
+    const float *q_weight, *k_weight;    // [D] or [heads, D]; null: no norm
+    int q_wstride, k_wstride;            // floats from a head's weights to the next one's
+    float eps;
+    const int32_t* axis_of;              // [rotary / 2], null: one axis
+    int num_axes;
 };
 
 // 16 channels of a row as fp32: 8 at `a`, 8 at `b` (16-byte aligned both).
@@ -201,6 +212,42 @@ __device__ __forceinline__ void rotate16(float (&f)[16], const float4* cs_row, i
     }
 }
 
+// The norm of a head row, 16 channels at `f` of each of the CH (4 or 8) neighbouring lanes that hold it,
+// which come here together.  A sum of squares past fp32 (values from 2^60 on) is taken of smaller
+// values; eps is nothing beside it.
+__device__ __forceinline__ void norm16(float (&f)[16], const float* weight, int ea, int eb, int CH, int lane, float eps)
+{
+    const unsigned seg = ((1u << CH) - 1u) << (lane & ~(CH - 1));
+    auto sum_squares = [&](float by) {
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+            s0 = fmaf(f[i] * by, f[i] * by, s0);
+            s1 = fmaf(f[i + 1] * by, f[i + 1] * by, s1);
+        }
+        s0 += s1;
+        for (int m = 1; m < CH; m <<= 1) s0 += __shfl_xor_sync(seg, s0, m);
+        return s0;
+    };
+    const float inv_n = CH == 8 ? 1.f / 128.f : 1.f / 64.f;
+    float by = 1.f, ss = sum_squares(1.f);
+    if (ss == INFINITY) {
+        by = 8.470329472543003e-22f;                          // 2^-70
+        ss = sum_squares(by);
+        eps = 0.f;
+    }
+    const float r = 1.f / sqrtf(fmaf(ss, inv_n, eps));
+    const float4 w[4] = {*reinterpret_cast<const float4*>(weight + ea), *reinterpret_cast<const float4*>(weight + ea + 4),
+                         *reinterpret_cast<const float4*>(weight + eb), *reinterpret_cast<const float4*>(weight + eb + 4)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[4 * i] = f[4 * i] * by * r * w[i].x;
+        f[4 * i + 1] = f[4 * i + 1] * by * r * w[i].y;
+        f[4 * i + 2] = f[4 * i + 2] * by * r * w[i].z;
+        f[4 * i + 3] = f[4 * i + 3] * by * r * w[i].w;
+    }
+}
+
 // The rows and the context length of sequence b; 0 rows when it is inactive or its numbers
 // are out of range.
 __device__ __forceinline__ int sequence_rows(const AppendArgs& a, int b, int& row0, int& len)
@@ -224,12 +271,13 @@ __device__ __forceinline__ int sequence_rows(const AppendArgs& a, int b, int& ro
 
 __device__ __forceinline__ int runs_of(int n, int len, int run) { return n > 0 ? (len + n - 1) / run - len / run + 1 : 0; }
 
-template <bool QB, bool KB>
+template <bool QB, bool KB, bool EXT>
 __global__ void __launch_bounds__(kAppThreads, 2) append_kernel(AppendArgs a)
 {
     extern __shared__ __align__(16) float4 s_cs[];            // [rows of the run][rotary / 4]
     __shared__ unsigned long long s_freq[64];
     __shared__ int s_warp[kAppWarps], s_find[2], s_page[kAppMaxBlocks];
+    __shared__ int s_axis[EXT ? 64 : 1];
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     allow_dependents_early();
@@ -239,6 +287,14 @@ __global__ void __launch_bounds__(kAppThreads, 2) append_kernel(AppendArgs a)
         double f = a.inv_freq[tid] * 0.15915494309189533577;   // turns per position
         f -= floor(f);
         s_freq[tid] = __double2ull_rn(f * 18446744073709551616.0);
+        if constexpr (EXT) {
+            int axis = a.axis_of != nullptr ? a.axis_of[tid] : 0;
+            if (axis < 0 || axis >= a.num_axes) {
+                raise_error(a.err, SPARSE_ATTN_ERR_LENGTH);
+                axis = 0;
+            }
+            s_axis[tid] = axis;
+        }
     }
     // ---- which run of which sequence ------------------------------------------
     int b, k;                                                 // run k of sequence b
@@ -299,7 +355,8 @@ __global__ void __launch_bounds__(kAppThreads, 2) append_kernel(AppendArgs a)
     const int half = a.rotary / 2, rchunks = a.rotary / 16;
     for (int e = tid; e < n * half; e += kAppThreads) {
         const int r = e / half, i = e - r * half;
-        const long long pos = a.positions != nullptr ? a.positions[r0 + r] : t0 + r;
+        const long long first = EXT ? (long long)s_axis[EXT ? i : 0] * a.num_rows : 0;
+        const long long pos = a.positions != nullptr ? a.positions[first + r0 + r] : t0 + r;
         const unsigned long long phase = (unsigned long long)pos * s_freq[i];
         const unsigned quarter = (unsigned(phase >> 32) + 0x20000000u) >> 30;           // the nearest one
         const long long rest = (long long)(phase - ((unsigned long long)quarter << 62));
@@ -366,6 +423,9 @@ __global__ void __launch_bounds__(kAppThreads, 2) append_kernel(AppendArgs a)
                     ring.wait();
                     float f[16];
                     widen16<QB>(ring.item(slot), f);
+                    if constexpr (EXT) {
+                        if (a.k_weight != nullptr) norm16(f, a.k_weight + kvh * a.k_wstride, ea, eb, CH, lane, a.eps);
+                    }
                     if (c < rchunks) rotate16(f, s_cs + size_t(r) * (a.rotary / 4), c, rchunks, a.pairs);
                     uint32_t w[W];
                     narrow16<KB>(f, w);
@@ -443,6 +503,10 @@ __global__ void __launch_bounds__(kAppThreads, 2) append_kernel(AppendArgs a)
             if (head < qn) {
                 float f[16];
                 widen16<QB>(raw, f);
+                if constexpr (EXT) {
+                    if (a.q_weight != nullptr)
+                        norm16(f, a.q_weight + (q0 + head) * a.q_wstride, elem_a(c), elem_b(c), CH, lane, a.eps);
+                }
                 if (c < rchunks) rotate16(f, s_cs + size_t(at.row) * (a.rotary / 4), c, rchunks, a.pairs);
                 store16<QB>(const_cast<char*>(at_elem<QB>(a.q_out, ((long long)(r0 + at.row) * a.Hq + q0 + head) * a.D)),
                             elem_a(c), elem_b(c), f);
@@ -465,16 +529,16 @@ __global__ void __launch_bounds__(kAppThreads, 2) append_kernel(AppendArgs a)
     }
 }
 
-template <bool QB, bool KB>
+template <bool QB, bool KB, bool EXT>
 cudaError_t launch_append_t(const AppendArgs& a, dim3 grid, cudaStream_t s)
 {
     static std::atomic<unsigned long long> configured{0};   // devices set up
     const cudaError_t cfg = once_per_device(configured, [&]() -> cudaError_t {
-        return cudaFuncSetAttribute(append_kernel<QB, KB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(append_kernel<QB, KB, EXT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     128 * 64 * 8 + kAppThreads * kAppSlots * (QB ? 32 : 64));
     });
     if (cfg != cudaSuccess) return cfg;
-    return launch_after_previous(append_kernel<QB, KB>, grid, dim3(kAppThreads),
+    return launch_after_previous(append_kernel<QB, KB, EXT>, grid, dim3(kAppThreads),
                                  16 * size_t(a.cs_words) + kAppThreads * kAppSlots * (QB ? 32 : 64), s, a);
 }
 
@@ -641,6 +705,13 @@ cudaError_t launch_append(const Geometry& g, const AppendCall& c, uint32_t* err,
     a.uniform_rows = c.num_rows / g.B;
     a.uniform_len = c.uniform_len;
     a.run = g.bs > kAppRun ? g.bs : kAppRun;
+    a.q_weight = c.q_weight;
+    a.k_weight = c.k_weight;
+    a.q_wstride = c.q_wstride;
+    a.k_wstride = c.k_wstride;
+    a.eps = c.eps;
+    a.axis_of = c.axis_of;
+    a.num_axes = c.num_axes;
     a.rotary = c.rotary_dim;
     a.pairs = c.pairing == SPARSE_ATTN_ROTATE_PAIRS;
     // n > 0 tokens touch at most (n - 2 + run) / run + 1 aligned runs
@@ -653,8 +724,14 @@ cudaError_t launch_append(const Geometry& g, const AppendCall& c, uint32_t* err,
     while (Y < 8 && runs * Y < num_sms() && items / Y > 2 * kAppThreads) Y *= 2;
     a.cs_words = (rows < a.run && !c.cu_rows ? rows : a.run) * (c.rotary_dim / 4);
     const dim3 grid{unsigned(runs), Y, 1};
-    if (g.q_bf16) return g.kv_bf16 ? launch_append_t<true, true>(a, grid, s) : launch_append_t<true, false>(a, grid, s);
-    return g.kv_bf16 ? launch_append_t<false, true>(a, grid, s) : launch_append_t<false, false>(a, grid, s);
+    if (c.q_weight == nullptr && c.k_weight == nullptr && c.axis_of == nullptr) {
+        if (g.q_bf16)
+            return g.kv_bf16 ? launch_append_t<true, true, false>(a, grid, s) : launch_append_t<true, false, false>(a, grid, s);
+        return g.kv_bf16 ? launch_append_t<false, true, false>(a, grid, s) : launch_append_t<false, false, false>(a, grid, s);
+    }
+    if (g.q_bf16)
+        return g.kv_bf16 ? launch_append_t<true, true, true>(a, grid, s) : launch_append_t<true, false, true>(a, grid, s);
+    return g.kv_bf16 ? launch_append_t<false, true, true>(a, grid, s) : launch_append_t<false, false, true>(a, grid, s);
 }
 
 cudaError_t launch_commit(const Geometry& g, const int32_t* seq_lens, const int32_t* path, int path_stride,

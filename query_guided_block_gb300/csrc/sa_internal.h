@@ -163,6 +163,12 @@ struct AppendCall {
     const int32_t* block_table;
     void *kmin, *kmax;
     int capacity;                // tokens a sequence has pages for
+    // sparse_attn_append_kv_norm; sparse_attn_append_kv leaves them empty
+    const float *q_weight, *k_weight;
+    int q_wstride, k_wstride;    // 0 or head_dim
+    float eps;
+    int num_axes;
+    const int32_t* axis_of;
 };
 cudaError_t launch_append(const Geometry& g, const AppendCall& c, uint32_t* err, cudaStream_t s);
 cudaError_t launch_commit(const Geometry& g, const int32_t* seq_lens, const int32_t* path, int path_stride,
@@ -176,6 +182,9 @@ struct TreeLayout {
     size_t counters, item_parts, part_m, part_l, part_o, total;
 };
 TreeLayout tree_layout(const Geometry& g);
+constexpr int kTreeMaxCtas = 304;    // partial slots: two per CTA (the item a part begins in, the one it ends in)
+// Behind the header and the arrival counters: what a call writes before it reads, any call's.
+constexpr size_t kTreeWsFree = (256 + kTreeMaxCtas * 4 + 255) / 256 * 256;
 constexpr int kTreeMaxDrafts = 1024;
 constexpr int kTreeLeastTile = 64;   // tokens of the kernels' tiles at least
 struct TreeCall {
@@ -186,6 +195,26 @@ struct TreeCall {
     float* out;
 };
 cudaError_t launch_tree(const Geometry& g, const TreeCall& c, char* ws, cudaStream_t s);
+
+// Shared prefixes (sa_shared.cu) and weighed attention (sa_weigh.cu, scores of up to `tokens` tokens).
+size_t shared_workspace(const Geometry& g, int groups);
+cudaError_t launch_shared(const Geometry& g, const TreeCall& c, int groups, const int32_t* cu_seqs, const int32_t* prefix_lens,
+                          char* ws, cudaStream_t s);
+size_t weigh_workspace(const Geometry& g, long long tokens);
+cudaError_t launch_weigh(const Geometry& g, const TreeCall& c, float* weights, char* ws, cudaStream_t s);
+
+// Eviction by accumulated weight (sa_evict.cu).
+struct EvictCall {
+    const int32_t *seq_lens, *keep_lens;
+    int keep, sinks, recent;
+    float* weights;
+    void *k_pages, *v_pages;
+    const int32_t *block_table, *new_table;
+    void *kmin, *kmax;
+    int32_t *kept_ids, *new_lens;
+};
+size_t evict_workspace(const Geometry& g, int keep);
+cudaError_t launch_evict(const Geometry& g, const EvictCall& c, char* ws, cudaStream_t s);
 
 cudaError_t launch_diff(const Geometry& g, int step, const int32_t* sel_ids,
                         const int32_t* sel_count, const int32_t* prev_ids,

@@ -1,0 +1,226 @@
+// Attention of a batch whose groups of sequences share a long prefix, the prefix's keys and values read
+// once a group:
+//   out = sum_t w_t v_t / sum_t w_t,  w_t = exp(scale q.k_t),
+// over the prefix, the sequence's own context and the drafts it sees.  Sums over parts of the tokens
+// add up once they are relative to one maximum, so the prefix is one launch, in which all the
+// members' query rows are rows of one item, the own tokens are another, and a third joins the shares (m, l, o).
+//
+// The launches are the EXT form of the draft-tree kernels (sa_tree_kernel.cuh).
+#include "sa_tree.cuh"
+
+namespace sa {
+namespace {
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// One row's shares of a launch.
+struct Shares {
+    const float *m, *l, *o;        // of the first one
+    long long step;                // rows from the second slot of a CTA to the first one of the next
+    int n;
+};
+
+__device__ __forceinline__ Shares shares_of(const TreeArgs& a, int2 parts, int rr, long long out_row)
+{
+    if (parts.y <= 1) return Shares{a.row_m + out_row, a.row_l + out_row, a.out + out_row * a.D, 0, 1};
+    // the first part of an item is the second slot of its CTA, the others are first slots
+    const long long at = (2LL * parts.x + 1) * a.item_rows + rr;
+    return Shares{a.part_m + at, a.part_l + at, a.part_o + at * a.D, a.item_rows, parts.y};
+}
+__device__ __forceinline__ long long share_row(const Shares& x, int c) { return c == 0 ? 0 : (2LL * c - 1) * x.step; }
+
+// A warp per output row.  The chain of dependent loads (the sequence's group, notes, maxima, shares) is
+// what a small call waits for.
+template <int D>
+__global__ void __launch_bounds__(128) tree_join_kernel(TreeArgs own, TreeArgs pre, int with_prefix, float2* stats)
+{
+    allow_dependents_early();
+    grid_dependency_wait();   // the shares come from the previous kernels
+    const int lane = threadIdx.x & 31;
+    const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (row >= (long long)own.seqs * own.Q * own.Hq) return;
+    const int h = int(row % own.Hq), bt = int(row / own.Hq), b = bt / own.Q, t = bt - b * own.Q;
+    const int kvh = h / own.G, r = t * own.G + h - kvh * own.G;
+    int from = 0, group = 0;
+    if (with_prefix) {
+        from = own.seq_prefix[b];
+        group = own.seq_group[b];
+        if (from < 0) return;                                 // inactive: no output
+    } else {
+        const int len = own.seq_lens != nullptr ? own.seq_lens[b] : own.N;
+        if (len < 0 || len > own.N) return;
+    }
+    Shares x[2];
+    const int rg = r / own.item_rows;
+    x[0] = shares_of(own, own.item_parts[kvh * tree_notes_per_head(own, own.item_rows) + (long long)b * own.row_groups + rg],
+                     r - rg * own.item_rows, row);
+    x[1].n = 0;
+    if (from > 0) {
+        const int b0 = pre.cu_seqs[group];
+        const int rp = (b - b0) * pre.R + r, rgp = rp / pre.item_rows;
+        const long long note = kvh * tree_notes_per_head(pre, pre.item_rows) + (long long)b0 * pre.R / pre.item_rows + group + rgp;
+        x[1] = shares_of(pre, pre.item_parts[note], rp - rgp * pre.item_rows, row);
+    }
+    const float scale = own.scale_log2;
+    float M = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        for (int c = lane; c < x[k].n; c += 32) M = fmaxf(M, __ldcg(x[k].m + share_row(x[k], c)));
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, i));
+    float den = 0.f;
+    float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        for (int c0 = 0; c0 < x[k].n; c0 += 32) {
+            float w = 0.f;
+            if (c0 + lane < x[k].n) {
+                const float m = __ldcg(x[k].m + share_row(x[k], c0 + lane));
+                const float l = __ldcg(x[k].l + share_row(x[k], c0 + lane));
+                w = tree_share(m, M, l, scale);
+                den = fmaf(w, l, den);
+            }
+            const int n = min(32, x[k].n - c0);
+            for (int c = 0; c < n; c += 8) {
+                float4 o[8];
+                float wc[8];
+#pragma unroll
+                for (int y = 0; y < 8; ++y) {
+                    wc[y] = __shfl_sync(kFullMask, w, (c + y) & 31);
+                    o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (c + y < n && lane < D / 4)
+                        o[y] = __ldcg(reinterpret_cast<const float4*>(x[k].o + share_row(x[k], c0 + c + y) * D) + lane);
+                }
+#pragma unroll
+                for (int y = 0; y < 8; ++y) {
+                    const float wx = c + y < n ? wc[y] : 0.f;
+                    num.x = fmaf(o[y].x, wx, num.x);
+                    num.y = fmaf(o[y].y, wx, num.y);
+                    num.z = fmaf(o[y].z, wx, num.z);
+                    num.w = fmaf(o[y].w, wx, num.w);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) den += __shfl_xor_sync(kFullMask, den, i);
+    const float inv = den == 0.f ? 0.f : 1.f / den;
+    if (lane < D / 4)
+        reinterpret_cast<float4*>(own.out + row * D)[lane] = make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
+    if (stats != nullptr && lane == 0) stats[row] = make_float2(M, inv);
+}
+
+}  // namespace
+
+cudaError_t launch_tree_join(const TreeArgs& own, const TreeArgs* prefix, float2* stats, cudaStream_t s)
+{
+    const unsigned grid = unsigned(((long long)own.seqs * own.Q * own.Hq + 3) / 4);
+    const TreeArgs& pre = prefix != nullptr ? *prefix : own;
+    return own.D == 128
+               ? launch_after_previous(tree_join_kernel<128>, dim3(grid), dim3(128), 0, s, own, pre, int(prefix != nullptr), stats)
+               : launch_after_previous(tree_join_kernel<64>, dim3(grid), dim3(128), 0, s, own, pre, int(prefix != nullptr), stats);
+}
+
+TreeExtLayout tree_ext_layout(const Geometry& g, size_t at, int groups)
+{
+    TreeExtLayout L{};
+    TreeArgs a{};
+    a.pass = groups > 0 ? kTreePrefix : kTreeOwn;
+    a.seqs = g.B;
+    a.B = groups > 0 ? groups : g.B;
+    a.R = g.Q * g.G;
+    const size_t notes = size_t(g.Hkv) * size_t(tree_notes_per_head(a, 16));
+    const size_t slots = 2 * size_t(kTreeMaxCtas) * kTreeMaxRows, rows = size_t(g.B) * g.Q * g.Hq;
+    L.item_parts = at;
+    L.part_m = align256(L.item_parts + notes * sizeof(int2));
+    L.part_l = align256(L.part_m + slots * sizeof(float));
+    L.part_o = align256(L.part_l + slots * sizeof(float));
+    L.row_m = align256(L.part_o + slots * g.D * sizeof(float));
+    L.row_l = align256(L.row_m + rows * sizeof(float));
+    L.end = align256(L.row_l + rows * sizeof(float));
+    return L;
+}
+
+TreeArgs tree_ext_args(const Geometry& g, const TreeCall& c, char* ws, const TreeExtLayout& L)
+{
+    TreeArgs a{};
+    a.q = c.q;
+    a.q_bf16 = g.q_bf16;
+    a.k_pages = c.k_pages;
+    a.v_pages = c.v_pages;
+    a.block_table = c.block_table;
+    a.seq_lens = c.seq_lens;
+    a.mask = c.mask;
+    a.out = c.out;
+    a.B = a.seqs = g.B;
+    a.Hq = g.Hq;
+    a.Hkv = g.Hkv;
+    a.G = g.G;
+    a.Q = g.Q;
+    a.R = g.Q * g.G;
+    a.D = g.D;
+    a.N = g.N;
+    a.bs = g.bs;
+    while ((1 << a.bs_shift) < g.bs) ++a.bs_shift;
+    a.nb = g.nb;
+    a.nb_cap = g.nb_cap;
+    a.num_pages = g.num_pages;
+    a.mask_words = (g.Q + 31) / 32;
+    a.scale_log2 = g.scale_log2;
+    a.merge_scale = g.scale_log2;
+    a.combine = 1;
+    a.item_parts = reinterpret_cast<int2*>(ws + L.item_parts);
+    a.part_m = reinterpret_cast<float*>(ws + L.part_m);
+    a.part_l = reinterpret_cast<float*>(ws + L.part_l);
+    a.part_o = reinterpret_cast<float*>(ws + L.part_o);
+    a.row_m = reinterpret_cast<float*>(ws + L.row_m);
+    a.row_l = reinterpret_cast<float*>(ws + L.row_l);
+    a.err = reinterpret_cast<uint32_t*>(ws);
+    return a;
+}
+
+namespace {
+
+struct SharedLayout {
+    size_t seq_prefix, seq_group, prior;
+    TreeExtLayout prefix, own;
+};
+
+SharedLayout shared_layout(const Geometry& g, int groups)
+{
+    SharedLayout L{};
+    L.seq_prefix = kTreeWsFree;
+    L.seq_group = align256(L.seq_prefix + size_t(g.B) * sizeof(int32_t));
+    L.prior = align256(L.seq_group + size_t(g.B) * sizeof(int32_t));
+    L.prefix = tree_ext_layout(g, align256(L.prior + size_t(g.B) * g.Q * g.Hq * g.D * sizeof(float)), groups);
+    L.own = tree_ext_layout(g, L.prefix.end, 0);
+    return L;
+}
+
+}  // namespace
+
+size_t shared_workspace(const Geometry& g, int groups) { return shared_layout(g, groups).own.end; }
+
+cudaError_t launch_shared(const Geometry& g, const TreeCall& c, int groups, const int32_t* cu_seqs, const int32_t* prefix_lens,
+                          char* ws, cudaStream_t s)
+{
+    const SharedLayout L = shared_layout(g, groups);
+    TreeArgs pre = tree_ext_args(g, c, ws, L.prefix);
+    pre.pass = kTreePrefix;
+    pre.B = groups;
+    pre.cu_seqs = cu_seqs;
+    pre.prefix_lens = prefix_lens;
+    pre.seq_prefix = reinterpret_cast<int32_t*>(ws + L.seq_prefix);
+    pre.seq_group = reinterpret_cast<int32_t*>(ws + L.seq_group);
+    pre.out = reinterpret_cast<float*>(ws + L.prior);
+    TreeArgs own = tree_ext_args(g, c, ws, L.own);
+    own.pass = kTreeOwn;
+    own.seq_prefix = pre.seq_prefix;
+    own.seq_group = pre.seq_group;
+    const long long members = g.B / groups > 1 ? g.B / groups : 1;
+    cudaError_t e = launch_tree_ext(pre, g.kv_bf16, int(members * pre.R < 1024 ? members * pre.R : 1024), s);
+    if (e == cudaSuccess) e = launch_tree_ext(own, g.kv_bf16, own.R, s);
+    return e == cudaSuccess ? launch_tree_join(own, &pre, nullptr, s) : e;
+}
+
+}  // namespace sa

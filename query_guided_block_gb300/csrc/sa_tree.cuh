@@ -19,7 +19,6 @@
 
 namespace sa {
 
-constexpr int kTreeMaxCtas = 304;    // partial slots: two per CTA (the item a part begins in, the one it ends in)
 constexpr int kTreeMaxRows = 128;    // query rows of an item at most
 
 // Query rows of an item, in any kernel at most.
@@ -49,6 +48,23 @@ struct TreeArgs {
     int2* item_parts;          // combine: an item's first part and how many it has
     uint32_t* counters;        // [CTA] arrivals of the item that goes on behind this CTA's part; zero between calls
     uint32_t* err;
+
+    // The kernels' EXT form (sa_shared.cu, sa_weigh.cu): a launch of its own always joins the shares, so
+    // (m, l, o) are left as they are, those of items in one part in row_m, row_l and `out`.
+    int pass;                  // kTreeAll, kTreePrefix or kTreeOwn
+    int seqs;                  // sequences of the batch (B: units / Hkv, groups in the prefix pass)
+    const int32_t *cu_seqs, *prefix_lens;
+    int32_t *seq_prefix, *seq_group;     // [seqs]: shared tokens (-1: inactive) and group, by the prefix pass
+    float *row_m, *row_l;      // [seqs * Q * Hq]: unscaled maximum and sum
+    float* scores;             // [unit][R][score_stride] unscaled scores, null: not kept
+    long long score_stride;
+};
+
+// What the units of an EXT launch are.
+enum {
+    kTreeAll = 0,              // (sequence, KV head): its whole context and its drafts
+    kTreePrefix = 1,           // (group, KV head): the group's shared tokens, all its members' rows
+    kTreeOwn = 2               // (sequence, KV head): the context behind the shared tokens, and the drafts
 };
 
 // The list of a unit.
@@ -57,10 +73,65 @@ struct TreeUnit {
     int n_ctx;        // entries of the context (selection), or of everything without a selection
     int n_entries;
     int draft_blk;    // with a selection: the block of entry n_ctx
+    // EXT only
+    int b0;           // sequence of the unit's first query row
+    int rows;         // query rows
+    int table_row;    // sequence whose page table is read
+    int from;         // tokens below it are not the unit's
+    int first_blk;    // block of entry 0
+    int drafts;       // drafts behind the context
 };
 
+// The unit of a launch that EXT gives other units, from the arrays that say so.
+__device__ __forceinline__ TreeUnit tree_unit_ext(const TreeArgs& a, int u)
+{
+    TreeUnit t;
+    const int x = u / a.Hkv;
+    t.len = -1;
+    t.n_ctx = t.n_entries = t.draft_blk = 0;
+    t.b0 = t.table_row = x;
+    t.rows = a.R;
+    t.from = t.first_blk = 0;
+    t.drafts = a.Q;
+    if (a.pass == kTreePrefix) {
+        const int b0 = a.cu_seqs[x], b1 = a.cu_seqs[x + 1], n = a.prefix_lens[x];
+        if (b0 < 0 || b1 < b0 || b1 > a.seqs || n < 0 || n > a.N) {
+            raise_error(a.err, SPARSE_ATTN_ERR_LENGTH);
+            return t;
+        }
+        if (n == 0) return t;
+        // the pages are those of the first member that holds the prefix
+        int b = b0;
+        if (a.seq_lens != nullptr)
+            while (b < b1 && (a.seq_lens[b] < n || a.seq_lens[b] > a.N)) ++b;
+        if (b == b1) return t;
+        t.b0 = b0;
+        t.table_row = b;
+        t.rows = (b1 - b0) * a.R;
+        t.drafts = 0;
+        t.len = n;
+        t.n_ctx = t.n_entries = (n + a.bs - 1) >> a.bs_shift;
+        return t;
+    }
+    const int len = a.seq_lens != nullptr ? a.seq_lens[x] : a.N;
+    if (a.pass == kTreeOwn) {
+        const int p = a.seq_prefix[x];
+        if (p < 0) return t;                                 // the prefix pass has said why
+        t.from = p;
+        t.first_blk = p >> a.bs_shift;
+    } else if (len < 0 || len > a.N) {
+        if (len != -1) raise_error(a.err, SPARSE_ATTN_ERR_LENGTH);
+        return t;
+    }
+    t.len = len;
+    t.n_ctx = t.n_entries = ((len + a.Q - 1) >> a.bs_shift) + 1 - t.first_blk;
+    return t;
+}
+
+template <bool EXT = false>
 __device__ __forceinline__ TreeUnit tree_unit(const TreeArgs& a, int u)
 {
+    if constexpr (EXT) return tree_unit_ext(a, u);
     TreeUnit t;
     const int b = u / a.Hkv;
     t.len = a.seq_lens != nullptr ? a.seq_lens[b] : a.N;
@@ -86,20 +157,41 @@ __device__ __forceinline__ TreeUnit tree_unit(const TreeArgs& a, int u)
     return t;
 }
 
+template <bool EXT = false>
 __device__ __forceinline__ int tree_tiles(const TreeArgs& a, const TreeUnit& t)
 {
     if (t.len < 0) return 0;
+    if constexpr (EXT) return (t.len + t.drafts - (t.first_blk << a.bs_shift) + a.tile - 1) / a.tile;
     const long long n = a.sel_ids == nullptr ? t.len + a.Q : (long long)t.n_entries << a.bs_shift;
     return int((n + a.tile - 1) / a.tile);
 }
 
+// Row groups of a unit.
+template <bool EXT>
+__device__ __forceinline__ int tree_row_groups(const TreeArgs& a, const TreeUnit& t)
+{
+    return EXT ? (t.rows + a.item_rows - 1) / a.item_rows : a.row_groups;
+}
+
+// The item behind `item`, of the unit t.
+template <bool EXT>
+__device__ __forceinline__ int tree_next_item(const TreeArgs& a, const TreeUnit& t, int item)
+{
+    if constexpr (EXT) {
+        const int u = item / a.row_groups;
+        if (t.len < 0 || item + 1 - u * a.row_groups >= tree_row_groups<true>(a, t)) return (u + 1) * a.row_groups;
+    }
+    return item + 1;
+}
+
 // Entry e of the list: the page's tile index (page * Hkv + KV head; -1 when there is none)
 // and its first token.
+template <bool EXT = false>
 __device__ __forceinline__ int2 tree_entry(const TreeArgs& a, int u, const TreeUnit& t, int e)
 {
-    const int b = u / a.Hkv, kvh = u - b * a.Hkv;
-    int j = e;
-    if (a.sel_ids != nullptr) {
+    const int x = u / a.Hkv, kvh = u - x * a.Hkv, b = EXT ? t.table_row : x;
+    int j = EXT ? t.first_blk + e : e;
+    if (!EXT && a.sel_ids != nullptr) {
         if (e < t.n_ctx) {
             j = a.sel_ids[(long long)u * a.sel_stride + e];
             if (j < 0 || j >= a.nb) {
@@ -159,11 +251,17 @@ __device__ __forceinline__ uint32_t draft_bits8(const DraftView& w, int d0)
 
 // Which of the 8 list positions from p (a multiple of 8) a query with this view sees; e is
 // their entry, `first` the entry's first token.
+template <bool EXT = false>
 __device__ __forceinline__ uint32_t tree_tokens8(const TreeArgs& a, const TreeUnit& un, int p, int e, int first,
                                                  const DraftView& view)
 {
     if (first == kNoToken) return 0u;
     const int tok = first + (p & (a.bs - 1));
+    if constexpr (EXT) {
+        uint32_t bits = (1u << min(8, max(0, un.len - tok))) - 1u;
+        bits &= ~((1u << min(8, max(0, un.from - tok))) - 1u);
+        return bits | draft_bits8(view, tok - un.len);
+    }
     const bool ctx = a.sel_ids == nullptr || e < un.n_ctx;
     uint32_t bits = 0u;
     if (ctx) bits = (1u << min(8, max(0, un.len - tok))) - 1u;
@@ -183,7 +281,7 @@ struct TreePart {
 
 // Found by all threads (NT of them): as many warps as the units need count tiles, the others
 // only keep step.  `s`: kTreeScan<NT> words of shared memory.
-template <int NT>
+template <int NT, bool EXT = false>
 __device__ TreePart tree_part(const TreeArgs& a, int* s)
 {
     constexpr int W = NT / 32;
@@ -192,8 +290,15 @@ __device__ TreePart tree_part(const TreeArgs& a, int* s)
     const int warps = min(W, (units + 31) / 32);
     const int ch = (units + warps * 32 - 1) / (warps * 32);    // units per counting thread, consecutive
     const int u0 = warp < warps ? min(units, tid * ch) : units, u1 = min(units, u0 + ch);
-    const int t_first = u0 < u1 ? tree_tiles(a, tree_unit(a, u0)) : 0;
-    auto tiles_of = [&](int u) { return u == u0 ? t_first : tree_tiles(a, tree_unit(a, u)); };
+    struct Count {
+        int tiles, groups;            // of an item, row groups
+    };
+    auto count = [&](int u) {
+        const TreeUnit un = tree_unit<EXT>(a, u);
+        return Count{tree_tiles<EXT>(a, un), tree_row_groups<EXT>(a, un)};
+    };
+    const Count t_first = u0 < u1 ? count(u0) : Count{0, a.row_groups};
+    auto tiles_of = [&](int u) { return u == u0 ? t_first : count(u); };
     int* s_sum = s;                   // [W] tiles
     int* s_parts = s + W;             // [3][W] parts at three lengths
     int* s_line = s + 4 * W;          // [W] stretches of the line
@@ -201,8 +306,11 @@ __device__ TreePart tree_part(const TreeArgs& a, int* s)
     int* s_found = s + 6 * W;         // item, start, end
 
     int tiles = 0;
-    for (int u = u0; u < u1; ++u) tiles += tiles_of(u);
-    tiles *= a.row_groups;
+    for (int u = u0; u < u1; ++u) {
+        const Count n = tiles_of(u);
+        tiles += EXT ? n.tiles * n.groups : n.tiles;
+    }
+    if (!EXT) tiles *= a.row_groups;
     if (warp < warps) {
         const int sum = __reduce_add_sync(kFullMask, tiles);
         if (lane == 0) s_sum[warp] = sum;
@@ -216,15 +324,17 @@ __device__ TreePart tree_part(const TreeArgs& a, int* s)
     // than the slack, the parts take whole items, those that begin in them.
     int parts[3] = {0, 0, 0}, longest = 0;
     for (int u = u0; u < u1; ++u) {
-        const int t = tiles_of(u);
+        const Count n = tiles_of(u);
+        const int t = n.tiles;
         longest = max(longest, t);
 #pragma unroll
-        for (int x = 0; x < 3; ++x) parts[x] += (t + per + x * a.half_slack - 1) / (per + x * a.half_slack);
+        for (int x = 0; x < 3; ++x)
+            parts[x] += (t + per + x * a.half_slack - 1) / (per + x * a.half_slack) * (EXT ? n.groups : 1);
     }
     if (warp < warps) {
 #pragma unroll
         for (int x = 0; x < 3; ++x) {
-            parts[x] *= a.row_groups;
+            if (!EXT) parts[x] *= a.row_groups;
             const int sum = __reduce_add_sync(kFullMask, parts[x]);
             if (lane == 0) s_parts[x * W + warp] = sum;
         }
@@ -268,17 +378,19 @@ __device__ TreePart tree_part(const TreeArgs& a, int* s)
         for (int w = 0; w < warp; ++w) at += s_line[w];
         if (r.lo >= at && r.lo < at + mine) {
             for (int u = u0; u < u1; ++u) {
-                const int t = tiles_of(u);
+                const Count n = tiles_of(u);
+                const int t = n.tiles, groups = EXT ? n.groups : a.row_groups;
                 const int len = aligned ? (t + per - 1) / per * per : t;      // the item's stretch of the line
-                if (r.lo < at + len * a.row_groups) {
+                if (r.lo < at + len * groups) {
                     const int rg = (r.lo - at) / len;
                     const int next = r.whole && at + rg * len < r.lo;         // it began in an earlier part
-                    s_found[0] = u * a.row_groups + rg + next;
+                    s_found[0] = u * a.row_groups + rg;
+                    if (next) s_found[0] = EXT && rg + 1 >= groups ? (u + 1) * a.row_groups : s_found[0] + 1;
                     s_found[1] = at + (rg + next) * len;
                     s_found[2] = aligned ? at + rg * len + t : r.hi;
                     break;
                 }
-                at += len * a.row_groups;
+                at += len * groups;
             }
         }
     }
@@ -359,11 +471,56 @@ __device__ __forceinline__ void tree_note_parts(const TreeArgs& a, int item, int
     a.item_parts[item] = make_int2(c0, (start + tiles - 1) / per - c0 + 1);
 }
 
+// The first part of an item and how many it has.
+__device__ __forceinline__ int2 tree_parts(int start, int tiles, int per)
+{
+    const int c0 = start / per;
+    return make_int2(c0, (start + tiles - 1) / per - c0 + 1);
+}
+
+// Where the parts of row group rg of an EXT unit are noted: row groups of one KV head in the order of
+// their rows, a group of sequences beginning with one of its own.
+__host__ __device__ __forceinline__ long long tree_notes_per_head(const TreeArgs& a, int item_rows)
+{
+    return a.pass == kTreePrefix ? (long long)a.seqs * a.R / item_rows + a.B + 1
+                                 : (long long)a.seqs * ((a.R + item_rows - 1) / item_rows);
+}
+__device__ __forceinline__ long long tree_note_at(const TreeArgs& a, int u, const TreeUnit& un, int rg)
+{
+    const int x = u / a.Hkv, kvh = u - x * a.Hkv;
+    const long long first = a.pass == kTreePrefix ? (long long)un.b0 * a.R / a.item_rows + x
+                                                  : (long long)x * a.row_groups;
+    return kvh * tree_notes_per_head(a, a.item_rows) + first + rg;
+}
+
 // The weight of a share with maximum m and total l among shares whose largest maximum is M.  One that saw
 // nothing has none; one whose scores are all NaN has a NaN total and no maximum either, and is kept.
 __device__ __forceinline__ float tree_share(float m, float M, float l, float scale)
 {
     return m == -INFINITY && l == 0.f ? 0.f : fast_exp2((m - M) * scale);
+}
+
+// The prefix pass: which group and how many shared tokens every sequence has, for the launches behind it;
+// -1 where it is inactive.  By the last CTAs, which have the least to do when work is short.
+__device__ __forceinline__ void tree_note_sequences(const TreeArgs& a, int threads)
+{
+    if (a.pass != kTreePrefix) return;
+    for (int b = (gridDim.x - 1 - blockIdx.x) * threads + threadIdx.x; b < a.seqs; b += gridDim.x * threads) {
+        int lo = 0, hi = a.B;                                // the last group that begins at b or before
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (a.cu_seqs[mid] <= b) lo = mid;
+            else hi = mid;
+        }
+        const int b0 = a.cu_seqs[lo], b1 = a.cu_seqs[lo + 1];
+        const int len = a.seq_lens != nullptr ? a.seq_lens[b] : a.N;
+        int n = b >= b0 && b < b1 ? a.prefix_lens[lo] : 0;
+        bool bad = len < -1 || len > a.N;
+        if (b >= b0 && b < b1) bad = bad || b0 < 0 || b1 > a.seqs || n < 0 || (len >= 0 && n > len);
+        if (bad) raise_error(a.err, SPARSE_ATTN_ERR_LENGTH);
+        a.seq_prefix[b] = bad || len < 0 ? -1 : n;
+        a.seq_group[b] = lo;
+    }
 }
 
 // Called by the CTA's first NT threads once its (m, l, o) of a shared item is written: counts the
@@ -462,5 +619,26 @@ cudaError_t launch_tree_combine(const TreeArgs& a, cudaStream_t s);
 
 // The tensor-core kernel (sa_tree_tc.cu): bf16 queries and K/V.
 cudaError_t launch_tree_tc(TreeArgs a, cudaStream_t s);
+
+// The EXT form (sa_tree_ext64.cu, sa_tree_ext128.cu) for units of about `rows` query rows.
+cudaError_t launch_tree_ext64(TreeArgs& a, bool kv_bf16, int rows, cudaStream_t s);
+cudaError_t launch_tree_ext128(TreeArgs& a, bool kv_bf16, int rows, cudaStream_t s);
+inline cudaError_t launch_tree_ext(TreeArgs& a, bool kv_bf16, int rows, cudaStream_t s)
+{
+    return a.D == 128 ? launch_tree_ext128(a, kv_bf16, rows, s) : launch_tree_ext64(a, kv_bf16, rows, s);
+}
+
+// Joins the shares that EXT launches left and writes the output rows; `prefix` (null: none) has the group's
+// tokens.  `stats`: [seqs * Q * Hq] (maximum, 1 / total), null: not wanted.
+cudaError_t launch_tree_join(const TreeArgs& own, const TreeArgs* prefix, float2* stats, cudaStream_t s);
+
+// Workspace of one EXT launch, which a call carves out of its own: notes, shares of items in several parts,
+// and the maxima and sums of those in one.
+struct TreeExtLayout {
+    size_t item_parts, part_m, part_l, part_o, row_m, row_l, end;
+};
+TreeExtLayout tree_ext_layout(const Geometry& g, size_t at, int groups);
+// The fields that every EXT launch of this problem has in common.
+TreeArgs tree_ext_args(const Geometry& g, const TreeCall& c, char* ws, const TreeExtLayout& L);
 
 }  // namespace sa

@@ -1,0 +1,109 @@
+// Attention that also adds up, for every cached token, the weight that the query rows of its KV head gave
+// it:  weights[t] += sum_r exp(scale q_r.k_t) / sum_t' exp(scale q_r.k_t').
+//
+// A weight is known once its row's total is, after all keys.  The attention launch therefore leaves its
+// scores (4 bytes a row and token, beside 2 D bytes of keys and as many of values), the joining launch
+// every row's maximum and total, and a third launch turns the scores into weights: a thread has four
+// tokens and adds up the rows in their order, so the sums do not depend on timing.
+#include "sa_tree.cuh"
+
+namespace sa {
+namespace {
+
+constexpr int kWgThreads = 128;
+constexpr int kWgTokens = 4 * kWgThreads;
+constexpr int kWgRows = 256;                                 // rows whose maxima and totals are at hand
+constexpr uint32_t kNotSeenScore = 0xffffffffu;              // as the attention launch marks it
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// CTA = (unit, every `chunks`th run of 512 tokens).
+__global__ void __launch_bounds__(kWgThreads) weigh_kernel(TreeArgs a, const float2* stats, float* weights, long long w_stride,
+                                                          int chunks)
+{
+    __shared__ float2 s_row[kWgRows];
+    allow_dependents_early();
+    grid_dependency_wait();   // scores, totals and weights come from previous kernels
+    const int u = int(blockIdx.x) / chunks, b = u / a.Hkv, kvh = u - b * a.Hkv;
+    const int len = a.seq_lens != nullptr ? a.seq_lens[b] : a.N;
+    if (len < 0 || len > a.N) return;
+    const int end = len + a.Q;
+    for (int base = (int(blockIdx.x) - u * chunks) * kWgTokens; base < end; base += chunks * kWgTokens) {
+        const int t = base + 4 * threadIdx.x;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int r0 = 0; r0 < a.R; r0 += kWgRows) {
+            const int n = min(kWgRows, a.R - r0);
+            __syncthreads();
+            for (int i = threadIdx.x; i < n; i += kWgThreads) s_row[i] = stats[tree_out_row(a, b, kvh, r0 + i)];
+            __syncthreads();
+            if (t >= end) continue;
+            const float* at = a.scores + ((long long)u * a.R + r0) * a.score_stride + t;
+            for (int r = 0; r < n; r += 4) {
+                float4 x[4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                    if (r + y < n) x[y] = __ldcs(reinterpret_cast<const float4*>(at + (r + y) * a.score_stride));
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    if (r + y >= n) break;
+                    const float2 st = s_row[r + y];
+                    if (st.y == 0.f) continue;               // a row without a total
+                    const float s[4] = {x[y].x, x[y].y, x[y].z, x[y].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (__float_as_uint(s[e]) != kNotSeenScore) sum[e] = fmaf(fast_exp2((s[e] - st.x) * a.scale_log2), st.y, sum[e]);
+                }
+            }
+        }
+        float* w = weights + u * w_stride + t;
+        if (t + 4 <= len) {
+            const float4 old = *reinterpret_cast<const float4*>(w);
+            *reinterpret_cast<float4*>(w) = make_float4(old.x + sum[0], old.y + sum[1], old.z + sum[2], old.w + sum[3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (t + e < end) w[e] = t + e < len ? w[e] + sum[e] : sum[e];
+        }
+    }
+}
+
+struct WeighLayout {
+    TreeExtLayout own;
+    size_t stats, scores, end;
+    long long stride;
+};
+
+WeighLayout weigh_layout(const Geometry& g, long long tokens)
+{
+    WeighLayout L{};
+    L.own = tree_ext_layout(g, kTreeWsFree, 0);
+    L.stride = (tokens + kTreeLeastTile - 1) / kTreeLeastTile * kTreeLeastTile;   // whole tiles are written
+    L.stats = L.own.end;
+    L.scores = align256(L.stats + size_t(g.B) * g.Q * g.Hq * sizeof(float2));
+    L.end = align256(L.scores + size_t(g.units()) * g.Q * g.G * size_t(L.stride) * sizeof(float));
+    return L;
+}
+
+}  // namespace
+
+size_t weigh_workspace(const Geometry& g, long long tokens) { return weigh_layout(g, tokens).end; }
+
+cudaError_t launch_weigh(const Geometry& g, const TreeCall& c, float* weights, char* ws, cudaStream_t s)
+{
+    const WeighLayout L = weigh_layout(g, (long long)g.N + g.Q);
+    TreeArgs a = tree_ext_args(g, c, ws, L.own);
+    a.pass = kTreeAll;
+    a.scores = reinterpret_cast<float*>(ws + L.scores);
+    a.score_stride = L.stride;
+    float2* stats = reinterpret_cast<float2*>(ws + L.stats);
+    cudaError_t e = launch_tree_ext(a, g.kv_bf16, a.R, s);
+    if (e == cudaSuccess) e = launch_tree_join(a, nullptr, stats, s);
+    if (e != cudaSuccess) return e;
+    long long chunks = ((long long)g.N + g.Q + kWgTokens - 1) / kWgTokens;
+    const long long most = (8LL * num_sms() + g.units() - 1) / g.units() * 4;   // more would only start and end
+    if (chunks > most) chunks = most;
+    return launch_after_previous(weigh_kernel, dim3(unsigned(chunks * g.units())), dim3(kWgThreads), 0, s, a,
+                                 (const float2*)stats, weights, (long long)g.nb_cap * g.bs, int(chunks));
+}
+
+}  // namespace sa
