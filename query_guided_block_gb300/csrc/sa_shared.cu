@@ -27,6 +27,17 @@ __device__ __forceinline__ Shares shares_of(const TreeArgs& a, int2 parts, int r
     const long long at = (2LL * parts.x + 1) * a.item_rows + rr;
     return Shares{a.part_m + at, a.part_l + at, a.part_o + at * a.D, a.item_rows, parts.y};
 }
+// The weight of a share with maximum m and total l beside one whose maximum is M, unscaled both, and to which
+// M itself is the reference.  Shares of the warp-level kernel are relative to m * scale exactly, those of
+// the tensor-core one to the rounded product, which the difference takes into account; past 2^29 (in base-2
+// logits) they are relative to m itself again, and so are the weights here.
+__device__ __forceinline__ float share_weight(const TreeArgs& a, float m, float M, float l, float scale)
+{
+    if (m == -INFINITY && l == 0.f) return 0.f;
+    const float rounded = __fmul_rn(m, scale);
+    if (a.tensor && fabsf(rounded) < 536870912.f) return fast_exp2(-fmaf(M, scale, -rounded));
+    return fast_exp2((m - M) * scale);
+}
 __device__ __forceinline__ long long share_row(const Shares& x, int c) { return c == 0 ? 0 : (2LL * c - 1) * x.step; }
 
 // A warp per output row.  The chain of dependent loads (the sequence's group, notes, maxima, shares) is
@@ -77,7 +88,7 @@ __global__ void __launch_bounds__(128) tree_join_kernel(TreeArgs own, TreeArgs p
             if (c0 + lane < x[k].n) {
                 const float m = __ldcg(x[k].m + share_row(x[k], c0 + lane));
                 const float l = __ldcg(x[k].l + share_row(x[k], c0 + lane));
-                w = tree_share(m, M, l, scale);
+                w = share_weight(k == 0 ? own : pre, m, M, l, scale);
                 den = fmaf(w, l, den);
             }
             const int n = min(32, x[k].n - c0);
@@ -217,9 +228,12 @@ cudaError_t launch_shared(const Geometry& g, const TreeCall& c, int groups, cons
     own.pass = kTreeOwn;
     own.seq_prefix = pre.seq_prefix;
     own.seq_group = pre.seq_group;
-    const long long members = g.B / groups > 1 ? g.B / groups : 1;
-    cudaError_t e = launch_tree_ext(pre, g.kv_bf16, int(members * pre.R < 1024 ? members * pre.R : 1024), s);
-    if (e == cudaSuccess) e = launch_tree_ext(own, g.kv_bf16, own.R, s);
+    // What the launches go by: groups of even sizes; the prefixes and the rest are not known here, so each
+    // launch is taken for the larger part of the contexts.
+    const long long rows = (long long)(g.B > groups ? g.B : groups) * pre.R / groups;
+    const long long tiles = (g.N + kTreeLeastTile - 1) / kTreeLeastTile;
+    cudaError_t e = launch_tree_ext(pre, g.kv_bf16, int(rows < 1024 ? rows : 1024), tiles * groups * g.Hkv * ((rows + 15) / 16), s);
+    if (e == cudaSuccess) e = launch_tree_ext(own, g.kv_bf16, own.R, tiles * g.units() * ((own.R + 15) / 16), s);
     return e == cudaSuccess ? launch_tree_join(own, &pre, nullptr, s) : e;
 }
 

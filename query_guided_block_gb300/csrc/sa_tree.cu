@@ -25,13 +25,6 @@
 namespace sa {
 namespace {
 
-// bf16 calls with more than 16 rows and at most so many tiles (of 64 tokens x 16 rows) an SM run here
-// too, 16 rows to an item: a tensor-memory item takes longer to begin and end.  24 rows over 777 tokens
-// (1.4 tiles an SM) 13.2 us against 16.8, 64 rows over 777 (2.7) 14.8 against 18.3, over 4 x 300 (4.2)
-// 15.8 against 25.0 (18.6 where the parts are joined by a launch), 32 rows over 4 x 777 (5.5) 21.2
-// against 18.2, 128 rows over 777 (5.5) 21.3 against 19.6, 64 rows over 16 x 100 (6.7) 21.9 against 15.6.
-constexpr int kTreeSmallWork = 4;
-
 template <int D, bool KB, int NQ, int RW>
 cudaError_t launch_tree_t(TreeArgs a, cudaStream_t s)
 {

@@ -21,6 +21,13 @@ namespace sa {
 
 constexpr int kTreeMaxRows = 128;    // query rows of an item at most
 
+// bf16 calls with more than 16 rows and at most so many tiles (of 64 tokens x 16 rows) an SM run on the warp-level
+// kernel too, 16 rows to an item: a tensor-memory item takes longer to begin and end.  24 rows over 777 tokens
+// (1.4 tiles an SM) 13.2 us against 16.8, 64 rows over 777 (2.7) 14.8 against 18.3, over 4 x 300 (4.2)
+// 15.8 against 25.0 (18.6 where the parts are joined by a launch), 32 rows over 4 x 777 (5.5) 21.2
+// against 18.2, 128 rows over 777 (5.5) 21.3 against 19.6, 64 rows over 16 x 100 (6.7) 21.9 against 15.6.
+constexpr int kTreeSmallWork = 4;
+
 // Query rows of an item, in any kernel at most.
 inline int tree_item_rows(int R) { return R <= 16 ? 16 : (R <= 64 ? 64 : kTreeMaxRows); }
 
@@ -52,6 +59,7 @@ struct TreeArgs {
     // The kernels' EXT form (sa_shared.cu, sa_weigh.cu): a launch of its own always joins the shares, so
     // (m, l, o) are left as they are, those of items in one part in row_m, row_l and `out`.
     int pass;                  // kTreeAll, kTreePrefix or kTreeOwn
+    int tensor;                // the tensor-core kernel's shares: relative to the rounded product of maximum and scale
     int seqs;                  // sequences of the batch (B: units / Hkv, groups in the prefix pass)
     const int32_t *cu_seqs, *prefix_lens;
     int32_t *seq_prefix, *seq_group;     // [seqs]: shared tokens (-1: inactive) and group, by the prefix pass
@@ -620,11 +628,14 @@ cudaError_t launch_tree_combine(const TreeArgs& a, cudaStream_t s);
 // The tensor-core kernel (sa_tree_tc.cu): bf16 queries and K/V.
 cudaError_t launch_tree_tc(TreeArgs a, cudaStream_t s);
 
-// The EXT form (sa_tree_ext64.cu, sa_tree_ext128.cu) for units of about `rows` query rows.
+// The EXT form (sa_tree_ext64.cu, sa_tree_ext128.cu, sa_tree_tc_ext.cu) for units of about `rows` query rows.
 cudaError_t launch_tree_ext64(TreeArgs& a, bool kv_bf16, int rows, cudaStream_t s);
 cudaError_t launch_tree_ext128(TreeArgs& a, bool kv_bf16, int rows, cudaStream_t s);
-inline cudaError_t launch_tree_ext(TreeArgs& a, bool kv_bf16, int rows, cudaStream_t s)
+cudaError_t launch_tree_tc_ext(TreeArgs& a, int rows, cudaStream_t s);
+// `tiles`: of 64 tokens that the launch has for 16 rows each, about.
+inline cudaError_t launch_tree_ext(TreeArgs& a, bool kv_bf16, int rows, long long tiles, cudaStream_t s)
 {
+    if (kv_bf16 && a.q_bf16 && rows > 16 && tiles > (long long)kTreeSmallWork * num_sms()) return launch_tree_tc_ext(a, rows, s);
     return a.D == 128 ? launch_tree_ext128(a, kv_bf16, rows, s) : launch_tree_ext64(a, kv_bf16, rows, s);
 }
 

@@ -96,7 +96,7 @@ cudaError_t launch_weigh(const Geometry& g, const TreeCall& c, float* weights, c
     a.scores = reinterpret_cast<float*>(ws + L.scores);
     a.score_stride = L.stride;
     float2* stats = reinterpret_cast<float2*>(ws + L.stats);
-    cudaError_t e = launch_tree_ext(a, g.kv_bf16, a.R, s);
+    cudaError_t e = launch_tree_ext(a, g.kv_bf16, a.R, 0, s);
     if (e == cudaSuccess) e = launch_tree_join(a, nullptr, stats, s);
     if (e != cudaSuccess) return e;
     long long chunks = ((long long)g.N + g.Q + kWgTokens - 1) / kWgTokens;

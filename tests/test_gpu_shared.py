@@ -101,9 +101,77 @@ CASES = {
 }
 
 
+def big(batch, **kw):
+    """Enough tiles for the tensor-core kernel."""
+    lens = tuple(2500 + 3 * (i % 30) for i in range(batch))
+    return Case(**{**dict(batch=batch, drafts=1, lens=lens, context=2600, hq=32, hkv=8, block=64), **kw})
+
+
+TENSOR = {
+    "rows_20": (big(5), [0, 5], [2500]),
+    "rows_32": (big(8), [0, 8], [2499]),
+    "rows_64": (big(16), [0, 16], [2433]),
+    "rows_132": (big(33), [0, 33], [2500]),
+    "rows_64_dim_64": (big(8, hkv=4, dim=64), [0, 8], [2300]),
+    "rows_80_dim_64_block_16": (big(20, dim=64, block=16), [0, 20], [2391]),
+    "rows_24_dim_64_block_8": (big(6, dim=64, block=8), [0, 6], [2391]),
+    "rows_36_block_128": (big(9, block=128), [0, 9], [2391]),
+    "groups": (big(40), [0, 20, 21, 39], [2500, 77, 1000]),
+    "groups_of_one": (big(40, hkv=8, hq=64, drafts=3), list(range(41)), [2300 - 50 * i for i in range(40)]),
+    "own_rows_36": (big(5, drafts=9), [0, 5], [1200]),
+    "own_rows_72": (big(5, drafts=18, hq=16, hkv=4), [0, 3, 5], [200, 2480]),
+    "own_rows_160_dim_64": (big(5, drafts=40, hq=16, hkv=4, dim=64, block=32), [0, 3, 5], [200, 2480]),
+    "inactive": (big(12, lens=(-1, 2500, 2510, -1) * 3), [0, 9, 12], [2500, 100]),
+}
+
+
 @pytest.mark.parametrize("name", CASES)
 def test_against_64_bits(name):
     run(*CASES[name])
+
+
+@pytest.mark.parametrize("name", TENSOR)
+def test_tensor_cores_against_64_bits(name):
+    run(*TENSOR[name])
+
+
+@pytest.mark.parametrize("name", ["own_rows_36", "own_rows_72", "own_rows_160_dim_64", "groups_of_one"])
+def test_tensor_core_trees(name):
+    c, cuts, prefixes = TENSOR[name]
+    see = random_tree(c)
+    see[:, 0, :] = False
+    run(c, cuts, prefixes, see)
+
+
+@pytest.mark.parametrize("name", ["samples", "rows_32", "rows_64", "rows_132", "own_rows_36"])
+@pytest.mark.parametrize("scale", [2.0 ** 20, 2.0 ** 26, 1.9 * 2.0 ** 27, 2.0 ** 40])
+def test_large_scores(name, scale):
+    """Whole-numbered scores, exact in every order: softmax over them times a large factor is the mean of the
+    values at the largest one, whichever launch has met it.  The mean of n values: n additions of U of the sum of
+    their magnitudes and a division, or with weights equal but for exp2's 2^-21, that."""
+    c, cuts, prefixes = {**CASES, **TENSOR}[name]
+    own_table = c.block_table()
+    pools = c.fill(c.pools(), own_table)
+    g = c.gen("whole")
+    pools = (torch.where(pools[0].isnan(), pools[0], torch.randint(-1, 2, pools[0].shape, generator=g).to(c.kv)), pools[1])
+    table = share(c, own_table, pools, cuts, prefixes)
+    q = torch.randint(-1, 2, (c.batch, c.drafts, c.hq, c.dim), generator=g).to(c.dtype)
+    p = c.params(softmax_scale=scale)
+    ws = workspace(B.sparse_attn_shared_workspace_size(p, len(prefixes)))
+    out = torch.empty(c.batch, c.drafts, c.hq, c.dim, device="cuda")
+    B.sparse_attn_shared_decode(p, q.cuda(), pools[0].cuda(), pools[1].cuda(), table.cuda(), int32(cuts), int32(prefixes), out,
+                                ws, seq_lens=int32(c.all_lens))
+    got = out.cpu().double()
+    for b, n in enumerate(c.all_lens):
+        for i in range(c.drafts):
+            t = torch.arange(n + i + 1)
+            page, off = place(c, table, b, t)
+            for h in range(c.hq):
+                kvh = h // (c.hq // c.hkv)
+                score = pools[0][page, kvh, off].double() @ q[b, i, h].double()
+                v = pools[1][page, kvh, off].double()[score == score.max()]
+                bound = (len(v) * 2.0 ** -24 + 2.0 ** -20) * v.abs().mean(0)
+                assert ((got[b, i, h] - v.mean(0)).abs() <= bound).all(), (b, i, h)
 
 
 @pytest.mark.parametrize("name", ["drafts", "groups", "wide", "fp32_64", "dim_64"])
