@@ -825,11 +825,19 @@ int sparse_attn_shared_decode(const sparse_attn_params* p, const void* q, const 
                                    reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// tree_geometry, with query rows numbered in 32 bits.
+static int weigh_geometry(const sparse_attn_params* p, Geometry* g)
+{
+    const int st = tree_geometry(p, g);
+    if (st) return st;
+    return (long long)g->B * g->Q * g->Hq > INT32_MAX / 2 ? SPARSE_ATTN_UNSUPPORTED : SPARSE_ATTN_OK;
+}
+
 int sparse_attn_weigh_workspace_size(const sparse_attn_params* p, size_t* bytes)
 {
     if (!bytes) return SPARSE_ATTN_INVALID_ARG;
     Geometry g;
-    const int st = tree_geometry(p, &g);
+    const int st = weigh_geometry(p, &g);
     if (st) return st;
     const long long most = (long long)g.N + g.Q, cap = capacity_of(p);
     *bytes = weigh_workspace(g, cap > most ? cap : most);
@@ -841,7 +849,7 @@ int sparse_attn_weigh_decode(const sparse_attn_params* p, const void* q, const v
                              size_t ws_bytes, sparse_attn_stream stream)
 {
     Geometry g;
-    int st = tree_geometry(p, &g);
+    int st = weigh_geometry(p, &g);
     if (st) return st;
     if (!ws || !aligned(ws, 256) || ws_bytes < weigh_workspace(g, (long long)g.N + g.Q)) return SPARSE_ATTN_INVALID_ARG;
     st = attention_args(p, g, q, k_pages, v_pages, block_table, seq_lens, out);

@@ -6,7 +6,7 @@
 // keys of the same order, 32 bits, in shared memory; three histograms of 11, 11 and 10 bits, added up
 // over the cluster, narrow the key of the last kept token down; tokens above it stay, of those equal to
 // it as many as there is room for, lowest index first.  A kept token's place is the number of kept
-// ones before it, which two ballots a warp give.  The second launch moves rows: K and V of 64 kept
+// ones before it, which a scan over each warp's tokens gives.  The second launch moves rows: K and V of 64 kept
 // tokens a CTA, every load on its way before the first store, with their weights and their blocks' box.
 // Bytes: 4 a cached token, then each kept row once in and once out.
 #include "sa_common.cuh"
@@ -15,9 +15,9 @@
 namespace sa {
 namespace {
 
-constexpr int kEvThreads = 512;
-constexpr int kEvWarps = kEvThreads / 32;
-constexpr int kEvCache = 45056;            // keys of a CTA in shared memory; the rest is read again
+constexpr int kEvThreads = 1024;
+constexpr int kEvWarps = kEvThreads / 32;   // a lane for each
+constexpr int kEvCache = 49152;            // keys of a CTA in shared memory; the rest is read again
 constexpr int kEvMaxCluster = 8;
 constexpr int kEvRun = 64;                 // kept tokens of a moving CTA when blocks are smaller
 
@@ -47,16 +47,23 @@ __device__ __forceinline__ bool evict_counts(const EvictArgs& a, int b, int& len
     return true;
 }
 
+// Tokens of each of C CTAs: four to a lane and whole warps.
+__host__ __device__ __forceinline__ int ev_slice(int n, int C)
+{
+    const int unit = 4 * kEvThreads;
+    return ((n + C - 1) / C + unit - 1) / unit * unit;
+}
+
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr)
 {
     uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr));
     return v;
 }
 
 __global__ void __launch_bounds__(kEvThreads, 1) evict_select_kernel(EvictArgs a)
 {
-    extern __shared__ uint32_t s_key[];
+    extern __shared__ __align__(16) uint32_t s_key[];
     __shared__ uint32_t s_hist[3][2048];
     __shared__ int s_warp[2][kEvWarps];
     __shared__ uint32_t s_total[2];        // kept for sure and equal to the last key, of this CTA
@@ -73,7 +80,7 @@ __global__ void __launch_bounds__(kEvThreads, 1) evict_select_kernel(EvictArgs a
     const float* w = a.weights + u * a.w_stride;
     int32_t* ids = a.kept_ids + (long long)u * a.keep;
     float* vals = a.kept_weights + (long long)u * a.keep;
-    const int per = ((n + C - 1) / C + kEvThreads - 1) / kEvThreads * kEvThreads;   // tokens of a CTA
+    const int per = ev_slice(n, C);                            // tokens of a CTA
     const int i0 = min(n, rank * per), i1 = min(n, i0 + per);
     if (kept == n) {                                           // all of them
         for (int i = i0 + tid; i < i1; i += kEvThreads) {
@@ -84,18 +91,61 @@ __global__ void __launch_bounds__(kEvThreads, 1) evict_select_kernel(EvictArgs a
     }
     if (kept == 0) return;
     // Keys in the order of the weights; tokens that stay in any case are above all others.
-    auto make_key = [&](int i) -> uint32_t {
+    auto make_key = [&](int i, float x) -> uint32_t {
         if (i < a.sinks || i >= n - a.recent) return 0xffffffffu;
-        return min(order_key(w[i] + 0.f), 0xfffffffeu);        // + 0: no negative zero
+        return min(order_key(x + 0.f), 0xfffffffeu);           // + 0: no negative zero
     };
-    auto key = [&](int i) { return i - i0 < a.cache ? s_key[i - i0] : make_key(i); };
+    // Calls f(first index, its four keys) for this thread's tokens, four consecutive ones at a time (behind
+    // i1: 0, below every key); the first time from memory into shared memory.
+    auto each4 = [&](int from, int to, int stride, auto f) {
+        for (int i = from; i < to; i += stride) {
+            uint4 k;
+            if (i - i0 + 4 <= a.cache) {
+                k = *reinterpret_cast<const uint4*>(s_key + (i - i0));
+            } else {
+                const float4 x = *reinterpret_cast<const float4*>(w + i);
+                k.x = make_key(i, x.x);
+                k.y = i + 1 < i1 ? make_key(i + 1, x.y) : 0u;
+                k.z = i + 2 < i1 ? make_key(i + 2, x.z) : 0u;
+                k.w = i + 3 < i1 ? make_key(i + 3, x.w) : 0u;
+            }
+            f(i, k);
+        }
+    };
+    // Counts one more of a digit; a warp's lanes that have its first lane's are counted together, so that many
+    // equal weights (zeros) do not queue up.
+    auto count = [&](uint32_t* hist, bool have, uint32_t digit) {
+        const uint32_t live = __ballot_sync(kFullMask, have);
+        if (live == 0u) return;
+        const int lead = __ffs(live) - 1;
+        const uint32_t first = __shfl_sync(kFullMask, digit, lead);
+        const uint32_t same = __ballot_sync(kFullMask, have && digit == first);
+        if (lane == lead) atomicAdd(&hist[first], uint32_t(__popc(same)));
+        else if (have && digit != first) atomicAdd(&hist[digit], 1u);
+    };
 
     for (int i = tid; i < 3 * 2048; i += kEvThreads) (&s_hist[0][0])[i] = 0u;
     __syncthreads();
-    for (int i = i0 + tid; i < i1; i += kEvThreads) {
-        const uint32_t k = make_key(i);
-        if (i - i0 < a.cache) s_key[i - i0] = k;
-        atomicAdd(&s_hist[0][k >> 21], 1u);
+    constexpr int LOADS = 4;                                   // 16-byte loads a thread has on their way
+    for (int base = i0; base < i1; base += 4 * kEvThreads * LOADS) {
+        float4 x[LOADS];
+#pragma unroll
+        for (int y = 0; y < LOADS; ++y) {
+            const int i = base + 4 * (y * kEvThreads + tid);
+            if (i < i1) x[y] = *reinterpret_cast<const float4*>(w + i);      // the row goes on to a multiple of 8
+        }
+#pragma unroll
+        for (int y = 0; y < LOADS; ++y) {
+            const int i = base + 4 * (y * kEvThreads + tid);
+            const float e[4] = {x[y].x, x[y].y, x[y].z, x[y].w};
+            uint32_t k[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+                k[z] = i + z < i1 ? make_key(i + z, e[z]) : 0u;
+                count(s_hist[0], i + z < i1, k[z] >> 21);
+            }
+            if (i < i1 && i - i0 + 4 <= a.cache) *reinterpret_cast<uint4*>(s_key + (i - i0)) = make_uint4(k[0], k[1], k[2], k[3]);
+        }
     }
     uint32_t prefix = 0u;                                      // the last kept key's bits so far
     uint32_t room = uint32_t(kept);                            // tokens to take among those with these bits
@@ -104,34 +154,43 @@ __global__ void __launch_bounds__(kEvThreads, 1) evict_select_kernel(EvictArgs a
         const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
         if (pass > 0) {
             const int above = pass == 1 ? 21 : 10;
-            for (int i = i0 + tid; i < i1; i += kEvThreads) {
-                const uint32_t k = key(i);
-                if ((k >> above) == (prefix >> above)) atomicAdd(&s_hist[pass][(k >> shift) & (pass == 1 ? 2047u : 1023u)], 1u);
-            }
+            each4(i0 + 4 * tid, i1, 4 * kEvThreads, [&](int i, uint4 k) {
+                const uint32_t e[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+                for (int z = 0; z < 4; ++z)
+                    if (i + z < i1 && (e[z] >> above) == (prefix >> above))
+                        atomicAdd(&s_hist[pass][(e[z] >> shift) & (pass == 1 ? 2047u : 1023u)], 1u);
+            });
         }
         if (C > 1) cluster_sync_all();
         else __syncthreads();
-        // from the largest digit down, four to a thread
-        uint32_t h[4], sum = 0u;
+        // from the largest digit down, two to a thread
+        uint32_t h[2], sum = 0u;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const int bin = 2047 - 4 * tid - x;
+        for (int x = 0; x < 2; ++x) {
+            const int bin = 2047 - 2 * tid - x;
             h[x] = 0u;
-            if (C == 1) h[x] = s_hist[pass][bin];
-            else
-                for (int r = 0; r < C; ++r) h[x] += ld_cluster_u32(cluster_map(smem_u32(&s_hist[pass][bin]), uint32_t(r)));
+            if (C == 1) {
+                h[x] = s_hist[pass][bin];
+            } else {                                           // all ranks' loads on their way at once
+                uint32_t of[kEvMaxCluster];
+#pragma unroll
+                for (int r = 0; r < kEvMaxCluster; ++r) of[r] = ld_cluster_u32(cluster_map(smem_u32(&s_hist[pass][bin]), uint32_t(r < C ? r : rank)));
+#pragma unroll
+                for (int r = 0; r < kEvMaxCluster; ++r) h[x] += r < C ? of[r] : 0u;
+            }
             sum += h[x];
         }
         const uint32_t incl = uint32_t(warp_inclusive_scan(int(sum), lane));
         if (lane == 31) s_warp[0][warp] = int(incl);
         __syncthreads();
-        uint32_t at = incl - sum;
-        for (int x = 0; x < warp; ++x) at += uint32_t(s_warp[0][x]);
+        const uint32_t at_warp = __reduce_add_sync(kFullMask, lane < warp ? uint32_t(s_warp[0][lane]) : 0u);
+        uint32_t at = at_warp + incl - sum;
         if (at < room && room <= at + sum) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
+            for (int x = 0; x < 2; ++x) {
                 if (at < room && room <= at + h[x]) {
-                    s_found[0] = uint32_t(2047 - 4 * tid - x);
+                    s_found[0] = uint32_t(2047 - 2 * tid - x);
                     s_found[1] = room - at;
                 }
                 at += h[x];
@@ -145,11 +204,14 @@ __global__ void __launch_bounds__(kEvThreads, 1) evict_select_kernel(EvictArgs a
     // tokens with a key above `prefix` stay, and the first `room` of those equal to it
     const int seg = per / kEvWarps, w0 = min(i1, i0 + warp * seg), w1 = min(i1, w0 + seg);
     int gt = 0, eq = 0;
-    for (int i = w0 + lane; i < w1; i += 32) {
-        const uint32_t k = key(i);
-        gt += k > prefix;
-        eq += k == prefix;
-    }
+    each4(w0 + 4 * lane, w1, 128, [&](int i, uint4 k) {
+        const uint32_t e[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+            gt += i + z < w1 && e[z] > prefix;
+            eq += i + z < w1 && e[z] == prefix;
+        }
+    });
     gt = __reduce_add_sync(kFullMask, gt);
     eq = __reduce_add_sync(kFullMask, eq);
     if (lane == 0) {
@@ -157,35 +219,48 @@ __global__ void __launch_bounds__(kEvThreads, 1) evict_select_kernel(EvictArgs a
         s_warp[1][warp] = eq;
     }
     __syncthreads();
-    if (tid < 2) {
-        uint32_t all = 0u;
-        for (int x = 0; x < kEvWarps; ++x) all += uint32_t(s_warp[tid][x]);
-        s_total[tid] = all;
+    if (warp < 2) {
+        const uint32_t all = __reduce_add_sync(kFullMask, uint32_t(s_warp[warp][lane]));
+        if (lane == 0) s_total[warp] = all;
     }
     if (C > 1) cluster_sync_all();
     else __syncthreads();
-    uint32_t gt_at = 0u, eq_at = 0u;
-    for (int r = 0; r < rank; ++r) {
-        gt_at += ld_cluster_u32(cluster_map(smem_u32(&s_total[0]), uint32_t(r)));
-        eq_at += ld_cluster_u32(cluster_map(smem_u32(&s_total[1]), uint32_t(r)));
+    uint32_t gt_at = lane < warp ? uint32_t(s_warp[0][lane]) : 0u, eq_at = lane < warp ? uint32_t(s_warp[1][lane]) : 0u;
+    if (lane < rank) {                                         // the CTAs before this one
+        gt_at += ld_cluster_u32(cluster_map(smem_u32(&s_total[0]), uint32_t(lane)));
+        eq_at += ld_cluster_u32(cluster_map(smem_u32(&s_total[1]), uint32_t(lane)));
     }
-    for (int x = 0; x < warp; ++x) {
-        gt_at += uint32_t(s_warp[0][x]);
-        eq_at += uint32_t(s_warp[1][x]);
-    }
-    for (int base = w0; base < w1; base += 32) {
-        const int i = base + lane;
-        const uint32_t k = i < w1 ? key(i) : 0u;
-        const bool is_gt = i < w1 && k > prefix, is_eq = i < w1 && k == prefix;
-        const uint32_t bg = __ballot_sync(kFullMask, is_gt), be = __ballot_sync(kFullMask, is_eq);
-        const uint32_t g = gt_at + __popc(bg & lanemask_lt()), e = eq_at + __popc(be & lanemask_lt());
-        if (is_gt || (is_eq && e < room)) {
-            const uint32_t pos = g + min(e, room);
-            ids[pos] = i;
-            vals[pos] = w[i];
+    gt_at = __reduce_add_sync(kFullMask, gt_at);
+    eq_at = __reduce_add_sync(kFullMask, eq_at);
+    for (int base = w0; base < w1; base += 128) {              // four consecutive tokens a lane
+        uint4 k4 = make_uint4(0u, 0u, 0u, 0u);
+        const int i = base + 4 * lane;
+        each4(i, min(w1, i + 1), 4, [&](int, uint4 k) { k4 = k; });
+        const uint32_t e[4] = {k4.x, k4.y, k4.z, k4.w};
+        int more = 0, equal = 0;
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+            more += i + z < w1 && e[z] > prefix;
+            equal += i + z < w1 && e[z] == prefix;
         }
-        gt_at += __popc(bg);
-        eq_at += __popc(be);
+        const int both = warp_inclusive_scan(more << 16 | equal, lane);
+        const int all = __shfl_sync(kFullMask, both, 31);
+        uint32_t g = gt_at + (both >> 16) - more, q = eq_at + (both & 0xffff) - equal;
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+            if (i + z >= w1) break;
+            const bool is_gt = e[z] > prefix, is_eq = e[z] == prefix;
+            if (is_gt || (is_eq && q < room)) {
+                const uint32_t pos = g + min(q, room);
+                ids[pos] = i + z;
+                // the weight, from its key; of those that stay in any case from memory
+                vals[pos] = e[z] == 0xffffffffu ? w[i + z] : __uint_as_float((e[z] & 0x80000000u) ? e[z] ^ 0x80000000u : ~e[z]);
+            }
+            g += is_gt;
+            q += is_eq;
+        }
+        gt_at += uint32_t(all >> 16);
+        eq_at += uint32_t(all & 0xffff);
     }
     if (C > 1) cluster_sync_all();                             // others may still read this CTA's totals
 }
@@ -329,7 +404,7 @@ cudaError_t launch_evict(const Geometry& g, const EvictCall& c, char* ws, cudaSt
     // CTAs of a unit: as many as the SMs allow, each with some thousand tokens
     a.cluster = 1;
     while (a.cluster < kEvMaxCluster && 2LL * a.cluster * g.units() <= num_sms() && g.N / (2 * a.cluster) >= 2048) a.cluster *= 2;
-    const int per = ((g.N + a.cluster - 1) / a.cluster + kEvThreads - 1) / kEvThreads * kEvThreads;
+    const int per = ev_slice(g.N, a.cluster);
     a.cache = per < kEvCache ? per : kEvCache;
     static std::atomic<unsigned long long> configured{0};   // devices set up
     const cudaError_t cfg = once_per_device(configured, [&]() -> cudaError_t {

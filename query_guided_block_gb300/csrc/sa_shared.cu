@@ -11,13 +11,15 @@
 namespace sa {
 namespace {
 
+constexpr int kJoinWarps = 4;
+constexpr int kJoinThreads = 32 * kJoinWarps;
+
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// One row's shares of a launch.
+// One row's shares of a launch: rows of (m, l, o), the first one's and how many.
 struct Shares {
-    const float *m, *l, *o;        // of the first one
-    long long step;                // rows from the second slot of a CTA to the first one of the next
-    int n;
+    const float *m, *l, *o;
+    int step, n;                   // step: rows of a slot
 };
 
 __device__ __forceinline__ Shares shares_of(const TreeArgs& a, int2 parts, int rr, long long out_row)
@@ -27,31 +29,37 @@ __device__ __forceinline__ Shares shares_of(const TreeArgs& a, int2 parts, int r
     const long long at = (2LL * parts.x + 1) * a.item_rows + rr;
     return Shares{a.part_m + at, a.part_l + at, a.part_o + at * a.D, a.item_rows, parts.y};
 }
+__device__ __forceinline__ long long share_row(int step, int c) { return c == 0 ? 0 : (2LL * c - 1) * step; }
+
 // The weight of a share with maximum m and total l beside one whose maximum is M, unscaled both, and to which
 // M itself is the reference.  Shares of the warp-level kernel are relative to m * scale exactly, those of
 // the tensor-core one to the rounded product, which the difference takes into account; past 2^29 (in base-2
 // logits) they are relative to m itself again, and so are the weights here.
-__device__ __forceinline__ float share_weight(const TreeArgs& a, float m, float M, float l, float scale)
+__device__ __forceinline__ float share_weight(bool tensor, float m, float M, float l, float scale)
 {
     if (m == -INFINITY && l == 0.f) return 0.f;
     const float rounded = __fmul_rn(m, scale);
-    if (a.tensor && fabsf(rounded) < 536870912.f) return fast_exp2(-fmaf(M, scale, -rounded));
+    if (tensor && fabsf(rounded) < 536870912.f) return fast_exp2(-fmaf(M, scale, -rounded));
     return fast_exp2((m - M) * scale);
 }
-__device__ __forceinline__ long long share_row(const Shares& x, int c) { return c == 0 ? 0 : (2LL * c - 1) * x.step; }
 
-// A warp per output row.  The chain of dependent loads (the sequence's group, notes, maxima, shares) is
-// what a small call waits for.
+// CTA = an output row: each warp has all the shares' maxima and totals (lane = share) and adds up every
+// fourth share, whose loads are all on their way at once; the warps' sums go through shared memory.  A small
+// call waits for the chain of dependent loads (the sequence's group, notes, maxima, shares).
 template <int D>
-__global__ void __launch_bounds__(128) tree_join_kernel(TreeArgs own, TreeArgs pre, int with_prefix, float2* stats)
+__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ TreeArgs own,
+                                                                 const __grid_constant__ TreeArgs pre, int with_prefix,
+                                                                 float2* stats)
 {
+    __shared__ float4 s_num[kJoinWarps][D / 4];
     allow_dependents_early();
     grid_dependency_wait();   // the shares come from the previous kernels
-    const int lane = threadIdx.x & 31;
-    const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (row >= (long long)own.seqs * own.Q * own.Hq) return;
-    const int h = int(row % own.Hq), bt = int(row / own.Hq), b = bt / own.Q, t = bt - b * own.Q;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int row = int(blockIdx.x);
+    const int h = row % own.Hq, bt = row / own.Hq, b = bt / own.Q, t = bt - b * own.Q;
     const int kvh = h / own.G, r = t * own.G + h - kvh * own.G;
+    const int rg = r / own.item_rows;
+    const int2 own_parts = own.item_parts[kvh * tree_notes_per_head(own, own.item_rows) + (long long)b * own.row_groups + rg];
     int from = 0, group = 0;
     if (with_prefix) {
         from = own.seq_prefix[b];
@@ -61,75 +69,89 @@ __global__ void __launch_bounds__(128) tree_join_kernel(TreeArgs own, TreeArgs p
         const int len = own.seq_lens != nullptr ? own.seq_lens[b] : own.N;
         if (len < 0 || len > own.N) return;
     }
-    Shares x[2];
-    const int rg = r / own.item_rows;
-    x[0] = shares_of(own, own.item_parts[kvh * tree_notes_per_head(own, own.item_rows) + (long long)b * own.row_groups + rg],
-                     r - rg * own.item_rows, row);
-    x[1].n = 0;
+    const Shares x0 = shares_of(own, own_parts, r - rg * own.item_rows, row);
+    Shares x1 = x0;
+    x1.n = 0;
     if (from > 0) {
         const int b0 = pre.cu_seqs[group];
         const int rp = (b - b0) * pre.R + r, rgp = rp / pre.item_rows;
         const long long note = kvh * tree_notes_per_head(pre, pre.item_rows) + (long long)b0 * pre.R / pre.item_rows + group + rgp;
-        x[1] = shares_of(pre, pre.item_parts[note], rp - rgp * pre.item_rows, row);
+        x1 = shares_of(pre, pre.item_parts[note], rp - rgp * pre.item_rows, row);
     }
     const float scale = own.scale_log2;
-    float M = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-        for (int c = lane; c < x[k].n; c += 32) M = fmaxf(M, __ldcg(x[k].m + share_row(x[k], c)));
+    const int n = x0.n + x1.n;
+    auto share_m = [&](int c) {
+        return __ldcg(c < x0.n ? x0.m + share_row(x0.step, c) : x1.m + share_row(x1.step, c - x0.n));
+    };
+    auto share_l = [&](int c) {
+        return __ldcg(c < x0.n ? x0.l + share_row(x0.step, c) : x1.l + share_row(x1.step, c - x0.n));
+    };
+    float M = -INFINITY, m = -INFINITY, l = 0.f;              // m, l: of share `lane`
+    if (lane < n) {
+        m = share_m(lane);
+        l = share_l(lane);
+        M = m;
+    }
+    for (int c = 32 + lane; c < n; c += 32) M = fmaxf(M, share_m(c));
 #pragma unroll
     for (int i = 16; i > 0; i >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, i));
     float den = 0.f;
     float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        for (int c0 = 0; c0 < x[k].n; c0 += 32) {
-            float w = 0.f;
-            if (c0 + lane < x[k].n) {
-                const float m = __ldcg(x[k].m + share_row(x[k], c0 + lane));
-                const float l = __ldcg(x[k].l + share_row(x[k], c0 + lane));
-                w = share_weight(k == 0 ? own : pre, m, M, l, scale);
-                den = fmaf(w, l, den);
+    for (int c0 = 0; c0 < n; c0 += 32) {
+        float w = 0.f;
+        if (c0 + lane < n) {
+            if (c0 > 0) {
+                m = share_m(c0 + lane);
+                l = share_l(c0 + lane);
             }
-            const int n = min(32, x[k].n - c0);
-            for (int c = 0; c < n; c += 8) {
-                float4 o[8];
-                float wc[8];
+            w = share_weight(c0 + lane < x0.n ? own.tensor != 0 : pre.tensor != 0, m, M, l, scale);
+            den = fmaf(w, l, den);
+        }
+        float4 o[32 / kJoinWarps];
 #pragma unroll
-                for (int y = 0; y < 8; ++y) {
-                    wc[y] = __shfl_sync(kFullMask, w, (c + y) & 31);
-                    o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (c + y < n && lane < D / 4)
-                        o[y] = __ldcg(reinterpret_cast<const float4*>(x[k].o + share_row(x[k], c0 + c + y) * D) + lane);
-                }
+        for (int y = 0; y < 32 / kJoinWarps; ++y) {
+            const int c = c0 + y * kJoinWarps + warp;
+            o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (c < n && lane < D / 4)                        // without a weight too: it may hold infinities
+                o[y] = __ldcg(reinterpret_cast<const float4*>(c < x0.n ? x0.o + share_row(x0.step, c) * D
+                                                                       : x1.o + share_row(x1.step, c - x0.n) * D) + lane);
+        }
 #pragma unroll
-                for (int y = 0; y < 8; ++y) {
-                    const float wx = c + y < n ? wc[y] : 0.f;
-                    num.x = fmaf(o[y].x, wx, num.x);
-                    num.y = fmaf(o[y].y, wx, num.y);
-                    num.z = fmaf(o[y].z, wx, num.z);
-                    num.w = fmaf(o[y].w, wx, num.w);
-                }
-            }
+        for (int y = 0; y < 32 / kJoinWarps; ++y) {
+            const float wc = __shfl_sync(kFullMask, w, y * kJoinWarps + warp);
+            if (c0 + y * kJoinWarps >= n) break;
+            num.x = fmaf(o[y].x, wc, num.x);
+            num.y = fmaf(o[y].y, wc, num.y);
+            num.z = fmaf(o[y].z, wc, num.z);
+            num.w = fmaf(o[y].w, wc, num.w);
         }
     }
 #pragma unroll
     for (int i = 16; i > 0; i >>= 1) den += __shfl_xor_sync(kFullMask, den, i);
+    if (lane < D / 4) s_num[warp][lane] = num;
+    __syncthreads();
     const float inv = den == 0.f ? 0.f : 1.f / den;
-    if (lane < D / 4)
-        reinterpret_cast<float4*>(own.out + row * D)[lane] = make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
-    if (stats != nullptr && lane == 0) stats[row] = make_float2(M, inv);
+    if (threadIdx.x < D / 4) {
+#pragma unroll
+        for (int x = 1; x < kJoinWarps; ++x) {
+            const float4 y = s_num[x][lane];
+            num = make_float4(num.x + y.x, num.y + y.y, num.z + y.z, num.w + y.w);
+        }
+        reinterpret_cast<float4*>(own.out + (long long)row * D)[lane] =
+            make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
+    }
+    if (stats != nullptr && threadIdx.x == 0) stats[row] = make_float2(M, inv);
 }
 
 }  // namespace
 
 cudaError_t launch_tree_join(const TreeArgs& own, const TreeArgs* prefix, float2* stats, cudaStream_t s)
 {
-    const unsigned grid = unsigned(((long long)own.seqs * own.Q * own.Hq + 3) / 4);
+    const unsigned grid = unsigned((long long)own.seqs * own.Q * own.Hq);
     const TreeArgs& pre = prefix != nullptr ? *prefix : own;
     return own.D == 128
-               ? launch_after_previous(tree_join_kernel<128>, dim3(grid), dim3(128), 0, s, own, pre, int(prefix != nullptr), stats)
-               : launch_after_previous(tree_join_kernel<64>, dim3(grid), dim3(128), 0, s, own, pre, int(prefix != nullptr), stats);
+               ? launch_after_previous(tree_join_kernel<128>, dim3(grid), dim3(kJoinThreads), 0, s, own, pre, int(prefix != nullptr), stats)
+               : launch_after_previous(tree_join_kernel<64>, dim3(grid), dim3(kJoinThreads), 0, s, own, pre, int(prefix != nullptr), stats);
 }
 
 TreeExtLayout tree_ext_layout(const Geometry& g, size_t at, int groups)

@@ -632,12 +632,17 @@ cudaError_t launch_tree_tc(TreeArgs a, cudaStream_t s);
 cudaError_t launch_tree_ext64(TreeArgs& a, bool kv_bf16, int rows, cudaStream_t s);
 cudaError_t launch_tree_ext128(TreeArgs& a, bool kv_bf16, int rows, cudaStream_t s);
 cudaError_t launch_tree_tc_ext(TreeArgs& a, int rows, cudaStream_t s);
-// `tiles`: of 64 tokens that the launch has for 16 rows each, about.
+// Whether the tensor-core kernel takes a launch with about so many rows a unit and `tiles` tiles of 64 tokens
+// x 16 rows: kTreeSmallWork's rule, for 152 SMs.
+inline bool tree_ext_tensor(bool bf16, int rows, long long tiles) { return bf16 && rows > 16 && tiles > kTreeSmallWork * 152; }
 inline cudaError_t launch_tree_ext(TreeArgs& a, bool kv_bf16, int rows, long long tiles, cudaStream_t s)
 {
-    if (kv_bf16 && a.q_bf16 && rows > 16 && tiles > (long long)kTreeSmallWork * num_sms()) return launch_tree_tc_ext(a, rows, s);
+    if (tree_ext_tensor(kv_bf16 && a.q_bf16, rows, tiles)) return launch_tree_tc_ext(a, rows, s);
     return a.D == 128 ? launch_tree_ext128(a, kv_bf16, rows, s) : launch_tree_ext64(a, kv_bf16, rows, s);
 }
+
+// The sums of weights with the scores computed again (sa_weigh_tc.cu).
+cudaError_t launch_weigh_tc(TreeArgs a, const float2* stats, float* weights, long long w_stride, cudaStream_t s);
 
 // Joins the shares that EXT launches left and writes the output rows; `prefix` (null: none) has the group's
 // tokens.  `stats`: [seqs * Q * Hq] (maximum, 1 / total), null: not wanted.

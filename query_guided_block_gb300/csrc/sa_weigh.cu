@@ -4,7 +4,8 @@
 // A weight is known once its row's total is, after all keys.  The attention launch therefore leaves its
 // scores (4 bytes a row and token, beside 2 D bytes of keys and as many of values), the joining launch
 // every row's maximum and total, and a third launch turns the scores into weights: a thread has four
-// tokens and adds up the rows in their order, so the sums do not depend on timing.
+// tokens and adds up the rows in their order, so the sums do not depend on timing.  With many rows of
+// bf16 the scores are computed again instead (sa_weigh_tc.cu).
 #include "sa_tree.cuh"
 
 namespace sa {
@@ -73,6 +74,18 @@ struct WeighLayout {
     long long stride;
 };
 
+// Tiles of 64 tokens x 16 rows.
+long long weigh_tiles(const Geometry& g, long long tokens)
+{
+    return (long long)g.units() * ((g.Q * g.G + 15) / 16) * ((tokens + kTreeLeastTile - 1) / kTreeLeastTile);
+}
+
+// Scores are kept where the tensor-core kernels do not run.
+bool weigh_tensor(const Geometry& g, long long tokens)
+{
+    return tree_ext_tensor(g.kv_bf16 && g.q_bf16, g.Q * g.G, weigh_tiles(g, tokens));
+}
+
 WeighLayout weigh_layout(const Geometry& g, long long tokens)
 {
     WeighLayout L{};
@@ -80,7 +93,10 @@ WeighLayout weigh_layout(const Geometry& g, long long tokens)
     L.stride = (tokens + kTreeLeastTile - 1) / kTreeLeastTile * kTreeLeastTile;   // whole tiles are written
     L.stats = L.own.end;
     L.scores = align256(L.stats + size_t(g.B) * g.Q * g.Hq * sizeof(float2));
-    L.end = align256(L.scores + size_t(g.units()) * g.Q * g.G * size_t(L.stride) * sizeof(float));
+    size_t kept = size_t(g.units()) * g.Q * g.G * size_t(L.stride);
+    // with more tokens than these tiles hold none are kept: then room for any fewer
+    if (weigh_tensor(g, tokens)) kept = size_t(kTreeSmallWork) * 152 * kTreeLeastTile * 16;
+    L.end = align256(L.scores + kept * sizeof(float));
     return L;
 }
 
@@ -93,17 +109,22 @@ cudaError_t launch_weigh(const Geometry& g, const TreeCall& c, float* weights, c
     const WeighLayout L = weigh_layout(g, (long long)g.N + g.Q);
     TreeArgs a = tree_ext_args(g, c, ws, L.own);
     a.pass = kTreeAll;
-    a.scores = reinterpret_cast<float*>(ws + L.scores);
-    a.score_stride = L.stride;
     float2* stats = reinterpret_cast<float2*>(ws + L.stats);
-    cudaError_t e = launch_tree_ext(a, g.kv_bf16, a.R, 0, s);
+    const long long tokens = (long long)g.N + g.Q, w_stride = (long long)g.nb_cap * g.bs;
+    const bool tensor = weigh_tensor(g, tokens);
+    if (!tensor) {
+        a.scores = reinterpret_cast<float*>(ws + L.scores);
+        a.score_stride = L.stride;
+    }
+    cudaError_t e = launch_tree_ext(a, g.kv_bf16, a.R, weigh_tiles(g, tokens), s);
     if (e == cudaSuccess) e = launch_tree_join(a, nullptr, stats, s);
     if (e != cudaSuccess) return e;
-    long long chunks = ((long long)g.N + g.Q + kWgTokens - 1) / kWgTokens;
+    if (tensor) return launch_weigh_tc(a, stats, weights, w_stride, s);
+    long long chunks = (tokens + kWgTokens - 1) / kWgTokens;
     const long long most = (8LL * num_sms() + g.units() - 1) / g.units() * 4;   // more would only start and end
     if (chunks > most) chunks = most;
     return launch_after_previous(weigh_kernel, dim3(unsigned(chunks * g.units())), dim3(kWgThreads), 0, s, a,
-                                 (const float2*)stats, weights, (long long)g.nb_cap * g.bs, int(chunks));
+                                 (const float2*)stats, weights, w_stride, int(chunks));
 }
 
 }  // namespace sa

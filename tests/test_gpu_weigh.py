@@ -84,10 +84,36 @@ CASES = {
     "many_units": Case(batch=50, drafts=1, lens=tuple(7 * i for i in range(50)), context=400, hq=16, hkv=8, dim=64),
 }
 
+# enough query rows and tiles for the tensor-core kernels
+TENSOR = {
+    "rows_20": Case(batch=4, drafts=5, hq=32, hkv=8, lens=(700, 650, 640, 701), context=701, block=64),
+    "rows_32": Case(batch=4, drafts=8, hq=32, hkv=8, lens=(700, 0, 640, 1), context=700),
+    "rows_128": Case(batch=2, drafts=32, hq=32, hkv=8, lens=(400, 383), context=400, block=128),
+    "rows_264": Case(batch=3, drafts=33, hq=16, hkv=2, lens=(400, 127, 128), context=400, block=64),
+    "rows_560": Case(batch=4, drafts=70, hq=8, hkv=1, lens=(400, -1, 3, 256), context=400, block=16),
+    "dim_64": Case(batch=4, drafts=9, hq=32, hkv=8, lens=(700, 650, 640, 701), context=701, dim=64, block=8),
+    "dim_64_rows_160": Case(batch=4, drafts=20, hq=32, hkv=4, lens=(400, 383, 0, 200), context=400, dim=64, block=128),
+    "units": Case(batch=40, drafts=5, hq=32, hkv=8, lens=tuple(3 * i for i in range(40)), context=130, block=32),
+}
+
 
 @pytest.mark.parametrize("name", CASES)
 def test_against_64_bits(name):
     run(CASES[name])
+
+
+@pytest.mark.parametrize("name", TENSOR)
+def test_tensor_cores_against_64_bits(name):
+    run(TENSOR[name], old=0.1)
+
+
+def test_one_workspace_as_the_context_grows():
+    """Its size, of the capacity, serves every length: short contexts keep their scores, long ones do not."""
+    for n in (10, 300, 700, 1500):
+        c = Case(batch=4, drafts=8, hq=32, hkv=8, context=n, room=1600 - n)
+        small = B.sparse_attn_weigh_workspace_size(c.params(capacity_tokens=n + 8))
+        assert small <= B.sparse_attn_weigh_workspace_size(c.params())
+    run(Case(batch=4, drafts=8, hq=32, hkv=8, context=250, room=1000))
 
 
 def test_weights_add_up():
@@ -105,9 +131,26 @@ def test_every_length_the_same():
 
 
 @pytest.mark.parametrize("scale", [0.02, 3.0, 1e4])
-@pytest.mark.parametrize("name", ["batch", "window"])
+@pytest.mark.parametrize("name", ["batch", "window", "rows_20"])
 def test_scales(name, scale):
-    run(CASES[name], scale=scale)
+    run({**CASES, **TENSOR}[name], scale=scale)
+
+
+@pytest.mark.parametrize("name", ["window", "rows_32"])
+def test_pages_out_of_range_are_reported_and_weigh_nothing(name):
+    c = {**CASES, **TENSOR}[name]
+    table = c.block_table()
+    pools = [x.cuda() for x in c.fill(c.pools(empty=0.0), table)]
+    q = c.normal("q", c.batch, c.drafts, c.hq, c.dim).cuda()
+    p = c.params()
+    table[0, 1], table[2, 0] = c.pages, -1
+    ws = workspace(B.sparse_attn_weigh_workspace_size(p))
+    out = torch.zeros(c.batch, c.drafts, c.hq, c.dim, device="cuda")
+    w = torch.zeros(c.batch, c.hkv, c.nb_cap * c.block, device="cuda")
+    B.sparse_attn_weigh_decode(p, q, *pools, table.cuda(), w, out, ws, seq_lens=int32(c.all_lens))
+    assert B.sparse_attn_get_device_error(ws) == B.ERR_PAGE
+    assert (w[0, :, c.block:2 * c.block] == 0).all() and (w[2, :, :c.block] == 0).all() and (w[0, :, :c.block] > 0).all()
+    assert out.isfinite().all() and w.isfinite().all()
 
 
 def test_bad_lengths_are_reported():
