@@ -43,32 +43,38 @@ __device__ __forceinline__ float share_weight(bool tensor, float m, float M, flo
     return fast_exp2((m - M) * scale);
 }
 
-// CTA = an output row: each warp has all the shares' maxima and totals (lane = share) and adds up every
-// fourth share, whose loads are all on their way at once; the warps' sums go through shared memory.  A small
-// call waits for the chain of dependent loads (the sequence's group, notes, maxima, shares).
-template <int D>
+// WPR warps to an output row: each has all the shares' maxima and totals (lane = share) and adds up every
+// WPR-th share, eight loads on their way at once; their sums go through shared memory.  A small call waits
+// for the chain of dependent loads (the sequence's group, notes, maxima, shares) and takes four warps a row,
+// which leaves one round of shares; with many rows one warp has a row to itself.  (2048 rows of about 12
+// shares 7.0 us, four warps a row 10.6; 65536 rows of one share 50 and 145.)
+template <int D, int WPR>
 __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ TreeArgs own,
                                                                  const __grid_constant__ TreeArgs pre, int with_prefix,
                                                                  float2* stats)
 {
-    __shared__ float4 s_num[kJoinWarps][D / 4];
+    __shared__ float4 s_num[WPR > 1 ? kJoinWarps : 1][D / 4];
     allow_dependents_early();
     grid_dependency_wait();   // the shares come from the previous kernels
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int row = int(blockIdx.x);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % WPR;
+    const int row = int(blockIdx.x) * (kJoinWarps / WPR) + warp / WPR;
+    if (row >= own.seqs * own.Q * own.Hq) return;              // whole warps, and whole CTAs with WPR = 4
     const int h = row % own.Hq, bt = row / own.Hq, b = bt / own.Q, t = bt - b * own.Q;
     const int kvh = h / own.G, r = t * own.G + h - kvh * own.G;
     const int rg = r / own.item_rows;
     const int2 own_parts = own.item_parts[kvh * tree_notes_per_head(own, own.item_rows) + (long long)b * own.row_groups + rg];
+    float4* out = reinterpret_cast<float4*>(own.out + (long long)row * D) + lane;
     int from = 0, group = 0;
+    bool active;
     if (with_prefix) {
         from = own.seq_prefix[b];
         group = own.seq_group[b];
-        if (from < 0) return;                                 // inactive: no output
+        active = from >= 0;
     } else {
         const int len = own.seq_lens != nullptr ? own.seq_lens[b] : own.N;
-        if (len < 0 || len > own.N) return;
+        active = len >= 0 && len <= own.N;
     }
+    if (!active) return;                                      // no output; the same for all warps of a row
     const Shares x0 = shares_of(own, own_parts, r - rg * own.item_rows, row);
     Shares x1 = x0;
     x1.n = 0;
@@ -86,6 +92,19 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
     auto share_l = [&](int c) {
         return __ldcg(c < x0.n ? x0.l + share_row(x0.step, c) : x1.l + share_row(x1.step, c - x0.n));
     };
+    constexpr int LOADS = 8;
+    float4 o[LOADS];
+    auto load = [&](int c0) {                                 // this warp's shares of c0 .. c0 + LOADS * WPR - 1
+#pragma unroll
+        for (int y = 0; y < LOADS; ++y) {
+            const int c = c0 + y * WPR + sub;
+            o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (c < n && lane < D / 4)                        // without a weight too: it may hold infinities
+                o[y] = __ldcg(reinterpret_cast<const float4*>(c < x0.n ? x0.o + share_row(x0.step, c) * D
+                                                                       : x1.o + share_row(x1.step, c - x0.n) * D) + lane);
+        }
+    };
+    load(0);                                                  // on their way beside the maxima
     float M = -INFINITY, m = -INFINITY, l = 0.f;              // m, l: of share `lane`
     if (lane < n) {
         m = share_m(lane);
@@ -107,51 +126,53 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
             w = share_weight(c0 + lane < x0.n ? own.tensor != 0 : pre.tensor != 0, m, M, l, scale);
             den = fmaf(w, l, den);
         }
-        float4 o[32 / kJoinWarps];
+        for (int c = c0; c < min(n, c0 + 32); c += LOADS * WPR) {
+            if (c > 0) load(c);
 #pragma unroll
-        for (int y = 0; y < 32 / kJoinWarps; ++y) {
-            const int c = c0 + y * kJoinWarps + warp;
-            o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (c < n && lane < D / 4)                        // without a weight too: it may hold infinities
-                o[y] = __ldcg(reinterpret_cast<const float4*>(c < x0.n ? x0.o + share_row(x0.step, c) * D
-                                                                       : x1.o + share_row(x1.step, c - x0.n) * D) + lane);
-        }
-#pragma unroll
-        for (int y = 0; y < 32 / kJoinWarps; ++y) {
-            const float wc = __shfl_sync(kFullMask, w, y * kJoinWarps + warp);
-            if (c0 + y * kJoinWarps >= n) break;
-            num.x = fmaf(o[y].x, wc, num.x);
-            num.y = fmaf(o[y].y, wc, num.y);
-            num.z = fmaf(o[y].z, wc, num.z);
-            num.w = fmaf(o[y].w, wc, num.w);
+            for (int y = 0; y < LOADS; ++y) {
+                const float wc = __shfl_sync(kFullMask, w, (c + y * WPR + sub) & 31);
+                if (c + y * WPR + sub >= n) continue;
+                num.x = fmaf(o[y].x, wc, num.x);
+                num.y = fmaf(o[y].y, wc, num.y);
+                num.z = fmaf(o[y].z, wc, num.z);
+                num.w = fmaf(o[y].w, wc, num.w);
+            }
         }
     }
 #pragma unroll
     for (int i = 16; i > 0; i >>= 1) den += __shfl_xor_sync(kFullMask, den, i);
-    if (lane < D / 4) s_num[warp][lane] = num;
-    __syncthreads();
     const float inv = den == 0.f ? 0.f : 1.f / den;
-    if (threadIdx.x < D / 4) {
+    if constexpr (WPR > 1) {
+        if (lane < D / 4) s_num[warp][lane] = num;
+        __syncthreads();
+        if (sub == 0 && lane < D / 4) {
 #pragma unroll
-        for (int x = 1; x < kJoinWarps; ++x) {
-            const float4 y = s_num[x][lane];
-            num = make_float4(num.x + y.x, num.y + y.y, num.z + y.z, num.w + y.w);
+            for (int x = 1; x < WPR; ++x) {
+                const float4 y = s_num[warp + x][lane];
+                num = make_float4(num.x + y.x, num.y + y.y, num.z + y.z, num.w + y.w);
+            }
         }
-        reinterpret_cast<float4*>(own.out + (long long)row * D)[lane] =
-            make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
     }
-    if (stats != nullptr && threadIdx.x == 0) stats[row] = make_float2(M, inv);
+    if (sub == 0 && lane < D / 4) *out = make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
+    if (stats != nullptr && sub == 0 && lane == 0) stats[row] = make_float2(M, inv);
+}
+
+template <int D, int WPR>
+cudaError_t launch_join_t(const TreeArgs& own, const TreeArgs* prefix, float2* stats, cudaStream_t s)
+{
+    static_assert(WPR == 1 || WPR == kJoinWarps, "a CTA is one row or a row a warp");
+    const long long rows = (long long)own.seqs * own.Q * own.Hq, per = kJoinWarps / WPR;
+    return launch_after_previous(tree_join_kernel<D, WPR>, dim3(unsigned((rows + per - 1) / per)), dim3(kJoinThreads), 0, s, own,
+                                 prefix != nullptr ? *prefix : own, int(prefix != nullptr), stats);
 }
 
 }  // namespace
 
 cudaError_t launch_tree_join(const TreeArgs& own, const TreeArgs* prefix, float2* stats, cudaStream_t s)
 {
-    const unsigned grid = unsigned((long long)own.seqs * own.Q * own.Hq);
-    const TreeArgs& pre = prefix != nullptr ? *prefix : own;
-    return own.D == 128
-               ? launch_after_previous(tree_join_kernel<128>, dim3(grid), dim3(kJoinThreads), 0, s, own, pre, int(prefix != nullptr), stats)
-               : launch_after_previous(tree_join_kernel<64>, dim3(grid), dim3(kJoinThreads), 0, s, own, pre, int(prefix != nullptr), stats);
+    const bool few = (long long)own.seqs * own.Q * own.Hq <= 4LL * num_sms();
+    if (own.D == 128) return few ? launch_join_t<128, kJoinWarps>(own, prefix, stats, s) : launch_join_t<128, 1>(own, prefix, stats, s);
+    return few ? launch_join_t<64, kJoinWarps>(own, prefix, stats, s) : launch_join_t<64, 1>(own, prefix, stats, s);
 }
 
 TreeExtLayout tree_ext_layout(const Geometry& g, size_t at, int groups)

@@ -633,11 +633,16 @@ cudaError_t launch_tree_ext64(TreeArgs& a, bool kv_bf16, int rows, cudaStream_t 
 cudaError_t launch_tree_ext128(TreeArgs& a, bool kv_bf16, int rows, cudaStream_t s);
 cudaError_t launch_tree_tc_ext(TreeArgs& a, int rows, cudaStream_t s);
 // Whether the tensor-core kernel takes a launch with about so many rows a unit and `tiles` tiles of 64 tokens
-// x 16 rows: kTreeSmallWork's rule, for 152 SMs.
-inline bool tree_ext_tensor(bool bf16, int rows, long long tiles) { return bf16 && rows > 16 && tiles > kTreeSmallWork * 152; }
+// x 16 rows: kTreeSmallWork's rule, for 152 SMs.  Up to 32 rows it is for the long lists of prefixes:
+// sequences' own tokens are fewer, and where scores are kept the warp-level kernel leaves them (20 rows over
+// 4 x 32K tokens weighed in 155 us against 166, over 64 x 1000 in 102 against 156).
+inline bool tree_ext_tensor(int pass, bool bf16, int rows, long long tiles)
+{
+    return bf16 && rows > (pass == kTreePrefix ? 16 : 32) && tiles > kTreeSmallWork * 152;
+}
 inline cudaError_t launch_tree_ext(TreeArgs& a, bool kv_bf16, int rows, long long tiles, cudaStream_t s)
 {
-    if (tree_ext_tensor(kv_bf16 && a.q_bf16, rows, tiles)) return launch_tree_tc_ext(a, rows, s);
+    if (tree_ext_tensor(a.pass, kv_bf16 && a.q_bf16, rows, tiles)) return launch_tree_tc_ext(a, rows, s);
     return a.D == 128 ? launch_tree_ext128(a, kv_bf16, rows, s) : launch_tree_ext64(a, kv_bf16, rows, s);
 }
 

@@ -595,13 +595,16 @@ cudaError_t launch_tree_ext_t(TreeArgs& a, cudaStream_t s)
     return launch_after_previous(tree_kernel<D, KB, NQ, RW, true>, dim3(unsigned(ctas)), dim3(kTrThreads), smem, s, a);
 }
 
-// `rows`: query rows that a unit has, about.
+// `rows`: query rows that a unit has, about.  bf16 has an item of 32 rows too, two warps to each half of a
+// tile's tokens: 20 rows of 48 sequences with about 1500 tokens each 92 us, with 16-row items, which read
+// everything twice, 132, with 64-row items, half of them empty, 133 (the tensor-core kernel 126).
 template <int D>
 cudaError_t launch_tree_ext_d(TreeArgs& a, bool kv_bf16, int rows, cudaStream_t s)
 {
     const bool few = rows <= 16;
     if (!kv_bf16) return few ? launch_tree_ext_t<D, false, 1, 1>(a, s) : launch_tree_ext_t<D, false, 1, 4>(a, s);
     if (!a.q_bf16) return few ? launch_tree_ext_t<D, true, 3, 1>(a, s) : launch_tree_ext_t<D, true, 3, 4>(a, s);
+    if (!few && rows <= 32) return launch_tree_ext_t<D, true, 1, 2>(a, s);
     return few ? launch_tree_ext_t<D, true, 1, 1>(a, s) : launch_tree_ext_t<D, true, 1, 4>(a, s);
 }
 

@@ -83,7 +83,7 @@ long long weigh_tiles(const Geometry& g, long long tokens)
 // Scores are kept where the tensor-core kernels do not run.
 bool weigh_tensor(const Geometry& g, long long tokens)
 {
-    return tree_ext_tensor(g.kv_bf16 && g.q_bf16, g.Q * g.G, weigh_tiles(g, tokens));
+    return tree_ext_tensor(kTreeAll, g.kv_bf16 && g.q_bf16, g.Q * g.G, weigh_tiles(g, tokens));
 }
 
 WeighLayout weigh_layout(const Geometry& g, long long tokens)
