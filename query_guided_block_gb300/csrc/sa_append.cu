@@ -38,6 +38,8 @@ constexpr int kAppWarps = kAppThreads / 32;
 constexpr int kAppRun = 64;          // tokens of a run when blocks are smaller
 constexpr int kAppSlots = 4;         // items of a thread on their way from memory
 constexpr int kAppMaxBlocks = 8;     // blocks of a run
+constexpr int kAppMaxRun = 128;      // tokens of a run at most
+constexpr int kAppMaxAxes = 8;
 
 struct AppendArgs {
     const int32_t *cu_rows, *seq_lens, *positions, *block_table;
@@ -212,39 +214,111 @@ __device__ __forceinline__ void rotate16(float (&f)[16], const float4* cs_row, i
     }
 }
 
-// The norm of a head row, 16 channels at `f` of each of the CH (4 or 8) neighbouring lanes that hold it,
-// which come here together.  A sum of squares past fp32 (values from 2^60 on) is taken of smaller
-// values; eps is nothing beside it.
-__device__ __forceinline__ void norm16(float (&f)[16], const float* weight, int ea, int eb, int CH, int lane, float eps)
+// 16 channels as pairs of neighbours, for two operations an instruction.
+__device__ __forceinline__ void pair16(const float (&f)[16], F2 (&x)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = make_f2(f[2 * i], f[2 * i + 1]);
+}
+
+// What a head row's norm multiplies its channels by, 1 / sqrt(mean + eps); 16 channels are at `x` of each of the
+// CH (4 or 8) neighbouring lanes that hold the row, which come here together.  A sum of squares past fp32
+// (values from 2^60 on) is taken of smaller values; eps is nothing beside it.
+__device__ __forceinline__ float norm_factor(const F2 (&x)[8], int CH, int lane, float eps)
 {
     const unsigned seg = ((1u << CH) - 1u) << (lane & ~(CH - 1));
-    auto sum_squares = [&](float by) {
-        float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-            s0 = fmaf(f[i] * by, f[i] * by, s0);
-            s1 = fmaf(f[i + 1] * by, f[i + 1] * by, s1);
-        }
-        s0 += s1;
-        for (int m = 1; m < CH; m <<= 1) s0 += __shfl_xor_sync(seg, s0, m);
-        return s0;
+    auto over_row = [&](F2 s) {
+        float v = s.f.x + s.f.y;
+        for (int m = 1; m < CH; m <<= 1) v += __shfl_xor_sync(seg, v, m);
+        return v;
     };
     const float inv_n = CH == 8 ? 1.f / 128.f : 1.f / 64.f;
-    float by = 1.f, ss = sum_squares(1.f);
+    F2 s = mul2(x[0], x[0]);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) s = fma2(x[i], x[i], s);
+    const float ss = over_row(s);
     if (ss == INFINITY) {
-        by = 8.470329472543003e-22f;                          // 2^-70
-        ss = sum_squares(by);
-        eps = 0.f;
+        constexpr float by = 8.470329472543003e-22f;          // 2^-70
+        s = make_f2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const F2 y = mul2(x[i], make_f2(by, by));
+            s = fma2(y, y, s);
+        }
+        return by / sqrtf(over_row(s) * inv_n);
     }
-    const float r = 1.f / sqrtf(fmaf(ss, inv_n, eps));
-    const float4 w[4] = {*reinterpret_cast<const float4*>(weight + ea), *reinterpret_cast<const float4*>(weight + ea + 4),
-                         *reinterpret_cast<const float4*>(weight + eb), *reinterpret_cast<const float4*>(weight + eb + 4)};
+    return 1.f / sqrtf(fmaf(ss, inv_n, eps));
+}
+
+__device__ __forceinline__ void load_weights16(const float* weight, int ea, int eb, F2 (&w)[8])
+{
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        f[4 * i] = f[4 * i] * by * r * w[i].x;
-        f[4 * i + 1] = f[4 * i + 1] * by * r * w[i].y;
-        f[4 * i + 2] = f[4 * i + 2] * by * r * w[i].z;
-        f[4 * i + 3] = f[4 * i + 3] * by * r * w[i].w;
+        const float4 v = *reinterpret_cast<const float4*>(weight + (i < 2 ? ea + 4 * i : eb + 4 * (i - 2)));
+        w[2 * i] = make_f2(v.x, v.y);
+        w[2 * i + 1] = make_f2(v.z, v.w);
+    }
+}
+
+__device__ __forceinline__ void norm16(float (&f)[16], const float* weight, int ea, int eb, int CH, int lane, float eps)
+{
+    F2 x[8], w[8];
+    pair16(f, x);
+    const float r = norm_factor(x, CH, lane, eps);
+    load_weights16(weight, ea, eb, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const F2 y = mul2(mul2(x[i], make_f2(r, r)), w[i]);
+        f[2 * i] = y.f.x;
+        f[2 * i + 1] = y.f.y;
+    }
+}
+
+// A row's turn of a chunk's 8 pairs (a, b), the norm's weights in it: a' = a wa cos - b wb sin,
+// b' = b wb cos + a wa sin, as sums u x + v (x's partners).  Pairs are the channels p and p + 8 of the chunk, or
+// 2 p and 2 p + 1 (PAIRS).
+struct Turn16 {
+    F2 u[8], v[8];
+};
+
+template <bool PAIRS>
+__device__ __forceinline__ void make_turn16(Turn16& t, const float4* cs_row, int c, int chunks, const F2 (&w)[8])
+{
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {                             // pairs 2 q and 2 q + 1
+        float4 cs = make_float4(1.f, 0.f, 1.f, 0.f);          // behind the rotated channels: the weights alone
+        if (c < chunks) cs = cs_row[q * chunks + c];
+        if (PAIRS) {
+            const F2 w0 = w[2 * q], w1 = w[2 * q + 1];
+            t.u[2 * q] = make_f2(w0.f.x * cs.x, w0.f.y * cs.x);
+            t.v[2 * q] = make_f2(-w0.f.y * cs.y, w0.f.x * cs.y);
+            t.u[2 * q + 1] = make_f2(w1.f.x * cs.z, w1.f.y * cs.z);
+            t.v[2 * q + 1] = make_f2(-w1.f.y * cs.w, w1.f.x * cs.w);
+        } else {
+            const F2 wa = w[q], wb = w[q + 4];
+            t.u[q] = make_f2(wa.f.x * cs.x, wa.f.y * cs.z);
+            t.v[q] = make_f2(-wb.f.x * cs.y, -wb.f.y * cs.w);
+            t.u[q + 4] = make_f2(wb.f.x * cs.x, wb.f.y * cs.z);
+            t.v[q + 4] = make_f2(wa.f.x * cs.y, wa.f.y * cs.w);
+        }
+    }
+}
+
+template <bool PAIRS>
+__device__ __forceinline__ void turn16(F2 (&x)[8], const Turn16& t, float r)
+{
+    const F2 r2 = make_f2(r, r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = mul2(x[i], r2);
+#pragma unroll
+    for (int i = 0; i < (PAIRS ? 8 : 4); ++i) {
+        if (PAIRS) {
+            x[i] = fma2(x[i], t.u[i], mul2(make_f2(x[i].f.y, x[i].f.x), t.v[i]));
+        } else {
+            const F2 a = x[i], b = x[i + 4];
+            x[i] = fma2(a, t.u[i], mul2(b, t.v[i]));
+            x[i + 4] = fma2(b, t.u[i + 4], mul2(a, t.v[i + 4]));
+        }
     }
 }
 
@@ -271,13 +345,15 @@ __device__ __forceinline__ int sequence_rows(const AppendArgs& a, int b, int& ro
 
 __device__ __forceinline__ int runs_of(int n, int len, int run) { return n > 0 ? (len + n - 1) / run - len / run + 1 : 0; }
 
-template <bool QB, bool KB, bool EXT>
+// EXT: 0 the plain append, 1 queries normed with the same weights for all heads, 2 any other norm or axes.
+template <bool QB, bool KB, int EXT>
 __global__ void __launch_bounds__(kAppThreads, 2) append_kernel(AppendArgs a)
 {
     extern __shared__ __align__(16) float4 s_cs[];            // [rows of the run][rotary / 4]
     __shared__ unsigned long long s_freq[64];
     __shared__ int s_warp[kAppWarps], s_find[2], s_page[kAppMaxBlocks];
-    __shared__ int s_axis[EXT ? 64 : 1];
+    __shared__ int s_axis[EXT != 0 ? 64 : 1];
+    __shared__ int s_pos[EXT != 0 ? kAppMaxAxes : 1][EXT != 0 ? kAppMaxRun : 1];
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     allow_dependents_early();
@@ -287,7 +363,7 @@ __global__ void __launch_bounds__(kAppThreads, 2) append_kernel(AppendArgs a)
         double f = a.inv_freq[tid] * 0.15915494309189533577;   // turns per position
         f -= floor(f);
         s_freq[tid] = __double2ull_rn(f * 18446744073709551616.0);
-        if constexpr (EXT) {
+        if constexpr (EXT != 0) {
             int axis = a.axis_of != nullptr ? a.axis_of[tid] : 0;
             if (axis < 0 || axis >= a.num_axes) {
                 raise_error(a.err, SPARSE_ATTN_ERR_LENGTH);
@@ -349,14 +425,21 @@ __global__ void __launch_bounds__(kAppThreads, 2) append_kernel(AppendArgs a)
         if (!ok) raise_error(a.err, SPARSE_ATTN_ERR_PAGE);
         s_page[tid] = ok ? page : -1;
     }
-    __syncthreads();          // s_freq, s_page
+    if constexpr (EXT != 0) {
+        if (a.positions != nullptr && a.rotary > 0)
+            for (int i = tid; i < a.num_axes * kAppMaxRun; i += kAppThreads)
+                if (i % kAppMaxRun < n)
+                    s_pos[i / kAppMaxRun][i % kAppMaxRun] = a.positions[(long long)(i / kAppMaxRun) * a.num_rows + r0 + i % kAppMaxRun];
+    }
+    __syncthreads();          // s_freq, s_page, s_axis, s_pos
 
     // ---- cosines and sines of the run's rows --------------------------------------
     const int half = a.rotary / 2, rchunks = a.rotary / 16;
     for (int e = tid; e < n * half; e += kAppThreads) {
         const int r = e / half, i = e - r * half;
-        const long long first = EXT ? (long long)s_axis[EXT ? i : 0] * a.num_rows : 0;
-        const long long pos = a.positions != nullptr ? a.positions[first + r0 + r] : t0 + r;
+        long long pos;
+        if constexpr (EXT != 0) pos = a.positions != nullptr ? s_pos[s_axis[i]][r] : t0 + r;
+        else pos = a.positions != nullptr ? a.positions[r0 + r] : t0 + r;
         const unsigned long long phase = (unsigned long long)pos * s_freq[i];
         const unsigned quarter = (unsigned(phase >> 32) + 0x20000000u) >> 30;           // the nearest one
         const long long rest = (long long)(phase - ((unsigned long long)quarter << 62));
@@ -423,7 +506,7 @@ __global__ void __launch_bounds__(kAppThreads, 2) append_kernel(AppendArgs a)
                     ring.wait();
                     float f[16];
                     widen16<QB>(ring.item(slot), f);
-                    if constexpr (EXT) {
+                    if constexpr (EXT != 0) {
                         if (a.k_weight != nullptr) norm16(f, a.k_weight + kvh * a.k_wstride, ea, eb, CH, lane, a.eps);
                     }
                     if (c < rchunks) rotate16(f, s_cs + size_t(r) * (a.rotary / 4), c, rchunks, a.pairs);
@@ -465,6 +548,87 @@ __global__ void __launch_bounds__(kAppThreads, 2) append_kernel(AppendArgs a)
     {
         const int per_row = (qn + kvn) * CH;
         if (per_row == 0) return;                             // without queries, more shares than heads
+        // 16 channels of a value on their way to token t0 + row.
+        auto store_value = [&](const Raw16<QB>& raw, int row, int kvh, int c) {
+            const int t = t0 + row, page = s_page[t / a.bs - blk0];
+            if (page < 0) return;
+            void* dst = const_cast<char*>(at_elem<KB>(
+                a.v_pages, (((long long)page * a.Hkv + kvh) * a.bs + t % a.bs) * a.D));
+            if constexpr (QB == KB) {                         // same type: the bits as they are
+                uint4* p = reinterpret_cast<uint4*>(const_cast<char*>(at_elem<KB>(dst, 16 * c)));
+#pragma unroll
+                for (int i = 0; i < (KB ? 2 : 4); ++i) p[i] = raw.v[i];
+            } else {
+                float f[16];
+                widen16<QB>(raw, f);
+                store16<KB>(dst, 16 * c, 16 * c + 8, f);
+            }
+        };
+        if constexpr (EXT == 1) {
+            // A thread keeps a row's turn, weights in it, in registers and goes through heads: with cosines, sines
+            // and weights from shared memory and L1 for every item these were what the SM read most of (48K
+            // rows with positions of three axes 257 us, so 230; without any norm 202).
+            int rl = 1;                                       // rows side by side
+            while (rl < 16 && 2 * rl <= n) rl *= 2;
+            const int c = tid & (CH - 1), place = tid >> ch_shift, heads = qn + kvn;
+            const int h0 = place / rl, h_step = kAppThreads / (CH * rl);
+            const int ea = elem_a(c), eb = elem_b(c);
+            auto fetch = [&](int row, int head, int slot) {
+                if (row < n) {
+                    if (head < qn)
+                        ring.fetch(slot, at_elem<QB>(a.q_new, (r0 + row) * a.q_stride + (q0 + head) * a.D), ea, eb);
+                    else
+                        ring.fetch(slot, at_elem<QB>(a.v_new, (r0 + row) * a.v_stride + (kv0 + head - qn) * a.D), 16 * c, 16 * c + 8);
+                }
+                ring.close();
+            };
+            auto step = [&](int& row, int& head) {
+                head += h_step;
+                if (head >= heads) {
+                    head = h0;
+                    row += rl;
+                }
+            };
+            int row = h0 < heads ? place & (rl - 1) : n, head = h0, row_ahead = row, head_ahead = head, row_turn = -1;
+#pragma unroll
+            for (int s = 0; s < kAppSlots - 1; ++s) {
+                fetch(row_ahead, head_ahead, s);
+                step(row_ahead, head_ahead);
+            }
+            Turn16 turn;
+            for (int slot = 0; row < n; step(row, head), slot = (slot + 1) % kAppSlots) {
+                fetch(row_ahead, head_ahead, (slot + kAppSlots - 1) % kAppSlots);
+                step(row_ahead, head_ahead);
+                if (row != row_turn) {
+                    row_turn = row;
+                    F2 w[8];
+                    load_weights16(a.q_weight, ea, eb, w);
+                    const float4* cs = s_cs + size_t(row) * (a.rotary / 4);
+                    if (a.pairs) make_turn16<true>(turn, cs, c, rchunks, w);
+                    else make_turn16<false>(turn, cs, c, rchunks, w);
+                }
+                ring.wait();
+                const Raw16<QB> raw = ring.item(slot);
+                if (head >= qn) {
+                    store_value(raw, row, kv0 + head - qn, c);
+                    continue;
+                }
+                float f[16];
+                widen16<QB>(raw, f);
+                F2 x[8];
+                pair16(f, x);
+                const float r = norm_factor(x, CH, lane, a.eps);
+                if (a.pairs) turn16<true>(x, turn, r);
+                else turn16<false>(x, turn, r);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    f[2 * i] = x[i].f.x;
+                    f[2 * i + 1] = x[i].f.y;
+                }
+                store16<QB>(const_cast<char*>(at_elem<QB>(a.q_out, ((long long)(r0 + row) * a.Hq + q0 + head) * a.D)), ea, eb, f);
+            }
+            return;
+        }
         struct Cursor {
             int row, rest;                                    // rest: channel chunk fastest, then head
         };
@@ -503,7 +667,7 @@ __global__ void __launch_bounds__(kAppThreads, 2) append_kernel(AppendArgs a)
             if (head < qn) {
                 float f[16];
                 widen16<QB>(raw, f);
-                if constexpr (EXT) {
+                if constexpr (EXT != 0) {
                     if (a.q_weight != nullptr)
                         norm16(f, a.q_weight + (q0 + head) * a.q_wstride, elem_a(c), elem_b(c), CH, lane, a.eps);
                 }
@@ -512,24 +676,12 @@ __global__ void __launch_bounds__(kAppThreads, 2) append_kernel(AppendArgs a)
                             elem_a(c), elem_b(c), f);
                 continue;
             }
-            const int t = t0 + at.row, page = s_page[t / a.bs - blk0];
-            if (page < 0) continue;
-            void* dst = const_cast<char*>(at_elem<KB>(
-                a.v_pages, (((long long)page * a.Hkv + kv0 + head - qn) * a.bs + t % a.bs) * a.D));
-            if constexpr (QB == KB) {                         // same type: the bits as they are
-                uint4* p = reinterpret_cast<uint4*>(const_cast<char*>(at_elem<KB>(dst, 16 * c)));
-#pragma unroll
-                for (int i = 0; i < (KB ? 2 : 4); ++i) p[i] = raw.v[i];
-            } else {
-                float f[16];
-                widen16<QB>(raw, f);
-                store16<KB>(dst, 16 * c, 16 * c + 8, f);
-            }
+            store_value(raw, at.row, kv0 + head - qn, c);
         }
     }
 }
 
-template <bool QB, bool KB, bool EXT>
+template <bool QB, bool KB, int EXT>
 cudaError_t launch_append_t(const AppendArgs& a, dim3 grid, cudaStream_t s)
 {
     static std::atomic<unsigned long long> configured{0};   // devices set up
@@ -540,6 +692,13 @@ cudaError_t launch_append_t(const AppendArgs& a, dim3 grid, cudaStream_t s)
     if (cfg != cudaSuccess) return cfg;
     return launch_after_previous(append_kernel<QB, KB, EXT>, grid, dim3(kAppThreads),
                                  16 * size_t(a.cs_words) + kAppThreads * kAppSlots * (QB ? 32 : 64), s, a);
+}
+
+template <int EXT>
+cudaError_t launch_append_ext(const Geometry& g, const AppendArgs& a, dim3 grid, cudaStream_t s)
+{
+    if (g.q_bf16) return g.kv_bf16 ? launch_append_t<true, true, EXT>(a, grid, s) : launch_append_t<true, false, EXT>(a, grid, s);
+    return g.kv_bf16 ? launch_append_t<false, true, EXT>(a, grid, s) : launch_append_t<false, false, EXT>(a, grid, s);
 }
 
 // ------------------------------------------------------------------ commit ---
@@ -724,14 +883,8 @@ cudaError_t launch_append(const Geometry& g, const AppendCall& c, uint32_t* err,
     while (Y < 8 && runs * Y < num_sms() && items / Y > 2 * kAppThreads) Y *= 2;
     a.cs_words = (rows < a.run && !c.cu_rows ? rows : a.run) * (c.rotary_dim / 4);
     const dim3 grid{unsigned(runs), Y, 1};
-    if (c.q_weight == nullptr && c.k_weight == nullptr && c.axis_of == nullptr) {
-        if (g.q_bf16)
-            return g.kv_bf16 ? launch_append_t<true, true, false>(a, grid, s) : launch_append_t<true, false, false>(a, grid, s);
-        return g.kv_bf16 ? launch_append_t<false, true, false>(a, grid, s) : launch_append_t<false, false, false>(a, grid, s);
-    }
-    if (g.q_bf16)
-        return g.kv_bf16 ? launch_append_t<true, true, true>(a, grid, s) : launch_append_t<true, false, true>(a, grid, s);
-    return g.kv_bf16 ? launch_append_t<false, true, true>(a, grid, s) : launch_append_t<false, false, true>(a, grid, s);
+    if (c.q_weight == nullptr && c.k_weight == nullptr && c.axis_of == nullptr) return launch_append_ext<0>(g, a, grid, s);
+    return c.q_weight != nullptr && c.q_wstride == 0 ? launch_append_ext<1>(g, a, grid, s) : launch_append_ext<2>(g, a, grid, s);
 }
 
 cudaError_t launch_commit(const Geometry& g, const int32_t* seq_lens, const int32_t* path, int path_stride,

@@ -478,6 +478,42 @@ __device__ __forceinline__ void finish_step(uint32_t* err, uint32_t step_value)
     }
 }
 
+// Two fp32 operations in one instruction (each rounded as usual).
+union F2 {
+    unsigned long long u;
+    float2 f;
+};
+__device__ __forceinline__ F2 make_f2(float x, float y)
+{
+    F2 r;
+    r.f = make_float2(x, y);
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
+{
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.u) : "l"(a.u), "l"(b.u), "l"(c.u));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b)
+{
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(a.u), "l"(b.u));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b)
+{
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(a.u), "l"(b.u));
+    return r;
+}
+__device__ __forceinline__ F2 sub2(F2 a, F2 b)
+{
+    F2 r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(a.u), "l"(b.u));
+    return r;
+}
+
 // exp2 on the special-function unit (PTX ex2.approx.ftz.f32; about 2 ulp).
 __device__ __forceinline__ float fast_exp2(float x)
 {

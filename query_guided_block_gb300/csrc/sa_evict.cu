@@ -9,6 +9,11 @@
 // ones before it, which a scan over each warp's tokens gives.  The second launch moves rows: K and V of 64 kept
 // tokens a CTA, every load on its way before the first store, with their weights and their blocks' box.
 // Bytes: 4 a cached token, then each kept row once in and once out.
+//
+// 16 contexts of up to 32K tokens down to 8K, 8 heads of 128 (1.1 GB): 213 us, 5.2 TB/s; the first launch 26 us
+// of it (loads 7, digits 6, places 6), the second 179 of 162 for its bytes.  8 units of 128K tokens: 49 us, 26 in
+// the first launch, which the chain of its barriers bounds.  (Rows brought in by bulk copies of 256 bytes: 908 us,
+// 65 ns a copy.)
 #include "sa_common.cuh"
 #include "sa_internal.h"
 
@@ -17,7 +22,7 @@ namespace {
 
 constexpr int kEvThreads = 1024;
 constexpr int kEvWarps = kEvThreads / 32;   // a lane for each
-constexpr int kEvCache = 49152;            // keys of a CTA in shared memory; the rest is read again
+constexpr int kEvCache = 47104;            // keys of a CTA in shared memory; the rest is read again
 constexpr int kEvMaxCluster = 8;
 constexpr int kEvRun = 64;                 // kept tokens of a moving CTA when blocks are smaller
 
@@ -64,7 +69,7 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr)
 __global__ void __launch_bounds__(kEvThreads, 1) evict_select_kernel(EvictArgs a)
 {
     extern __shared__ __align__(16) uint32_t s_key[];
-    __shared__ uint32_t s_hist[3][2048];
+    __shared__ uint32_t s_hist[3][2048], s_sum[2048];         // of this CTA, of the cluster
     __shared__ int s_warp[2][kEvWarps];
     __shared__ uint32_t s_total[2];        // kept for sure and equal to the last key, of this CTA
     __shared__ uint32_t s_found[2];
@@ -164,21 +169,27 @@ __global__ void __launch_bounds__(kEvThreads, 1) evict_select_kernel(EvictArgs a
         }
         if (C > 1) cluster_sync_all();
         else __syncthreads();
+        const uint32_t* totals = s_hist[pass];
+        if (C > 1) {                                           // every CTA adds up its share of the bins and tells the others
+            const int share = 2048 / C;
+            for (int x = tid; x < share; x += kEvThreads) {
+                const int bin = rank * share + x;
+                const uint32_t at = smem_u32(&s_hist[pass][bin]), to = smem_u32(&s_sum[bin]);
+                uint32_t of[kEvMaxCluster], all = 0u;
+#pragma unroll
+                for (int r = 0; r < kEvMaxCluster; ++r) of[r] = ld_cluster_u32(cluster_map(at, uint32_t(r < C ? r : rank)));
+#pragma unroll
+                for (int r = 0; r < kEvMaxCluster; ++r) all += r < C ? of[r] : 0u;
+                for (int r = 0; r < C; ++r) st_cluster_u32(cluster_map(to, uint32_t(r)), all);
+            }
+            cluster_sync_all();
+            totals = s_sum;                                    // read before the next pass's first barrier
+        }
         // from the largest digit down, two to a thread
         uint32_t h[2], sum = 0u;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            const int bin = 2047 - 2 * tid - x;
-            h[x] = 0u;
-            if (C == 1) {
-                h[x] = s_hist[pass][bin];
-            } else {                                           // all ranks' loads on their way at once
-                uint32_t of[kEvMaxCluster];
-#pragma unroll
-                for (int r = 0; r < kEvMaxCluster; ++r) of[r] = ld_cluster_u32(cluster_map(smem_u32(&s_hist[pass][bin]), uint32_t(r < C ? r : rank)));
-#pragma unroll
-                for (int r = 0; r < kEvMaxCluster; ++r) h[x] += r < C ? of[r] : 0u;
-            }
+            h[x] = totals[2047 - 2 * tid - x];
             sum += h[x];
         }
         const uint32_t incl = uint32_t(warp_inclusive_scan(int(sum), lane));
@@ -265,6 +276,42 @@ __global__ void __launch_bounds__(kEvThreads, 1) evict_select_kernel(EvictArgs a
     if (C > 1) cluster_sync_all();                             // others may still read this CTA's totals
 }
 
+// The minimum and maximum of 16 bytes of channels over rows.
+template <bool KB>
+struct Box {
+    static constexpr int N = KB ? 8 : 4;
+    float lo[N], hi[N];
+    __device__ __forceinline__ Box()
+    {
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            lo[e] = INFINITY;
+            hi[e] = -INFINITY;
+        }
+    }
+    __device__ __forceinline__ void join(const uint4& low, const uint4& high)
+    {
+        float f[N], g[N];
+        unpack16<KB>(low, f);
+        unpack16<KB>(high, g);
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            lo[e] = fminf(lo[e], f[e]);
+            hi[e] = fmaxf(hi[e], g[e]);
+        }
+    }
+    __device__ __forceinline__ void join(const uint4& v) { join(v, v); }
+    static __device__ __forceinline__ uint4 stored(const float (&f)[N])
+    {
+        if constexpr (KB)
+            return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+        else
+            return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    }
+    __device__ __forceinline__ uint4 low() const { return stored(lo); }
+    __device__ __forceinline__ uint4 high() const { return stored(hi); }
+};
+
 // CTA = (unit, run of kept tokens): whole blocks of the new pages.
 constexpr int kMvThreads = 256;
 constexpr int kMvBatch = 4;                // rows of K and of V a thread has on their way
@@ -319,40 +366,27 @@ __global__ void __launch_bounds__(kMvThreads) evict_move_kernel(EvictArgs a)
         }
     }
     if (a.kmin == nullptr) return;
+    // The box: of eight rows a thread, then of a block's eights.  (A thread for all 64 rows of a block: 205 us
+    // for 16 x 8K tokens of 8 heads, so 179, 162 without a box.)
     __syncthreads();
-    constexpr int EPL = KB ? 8 : 4;
+    uint4* s_part = s_rows + (a.run << c_shift);               // [eight][chunk][lowest, highest]
+    for (int it = tid; it < (n + 7) / 8 * CPR; it += kMvThreads) {
+        const int ra = (it >> c_shift) * 8, rb = min(n, ra + 8);
+        Box<KB> box;
+        for (int r = ra; r < rb; ++r)
+            if (s_src[r] >= 0) box.join(s_rows[(r << c_shift) + (it & (CPR - 1))]);
+        s_part[2 * it] = box.low();
+        s_part[2 * it + 1] = box.high();
+    }
+    __syncthreads();
     const int blks = (n + a.bs - 1) / a.bs, blk0 = t0 / a.bs;
     for (int it = tid; it < blks * CPR; it += kMvThreads) {
-        const int j = it >> c_shift, cc = it & (CPR - 1), ra = j * a.bs, rb = min(n, ra + a.bs);
-        float lo[EPL], hi[EPL];
-#pragma unroll
-        for (int e = 0; e < EPL; ++e) {
-            lo[e] = INFINITY;
-            hi[e] = -INFINITY;
-        }
-#pragma unroll 4
-        for (int r = ra; r < rb; ++r) {
-            if (s_src[r] < 0) continue;
-            float f[EPL];
-            unpack16<KB>(s_rows[(r << c_shift) + cc], f);
-#pragma unroll
-            for (int e = 0; e < EPL; ++e) {
-                lo[e] = fminf(lo[e], f[e]);
-                hi[e] = fmaxf(hi[e], f[e]);
-            }
-        }
-        const long long box = (((long long)b * a.Hkv + kvh) * a.nb_cap + blk0 + j) * a.row_bytes + cc * 16;
-        uint4* pmin = reinterpret_cast<uint4*>(a.kmin + box);
-        uint4* pmax = reinterpret_cast<uint4*>(a.kmax + box);
-        if constexpr (KB) {
-            *pmin = make_uint4(pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]), pack_bf16x2(lo[4], lo[5]),
-                               pack_bf16x2(lo[6], lo[7]));
-            *pmax = make_uint4(pack_bf16x2(hi[0], hi[1]), pack_bf16x2(hi[2], hi[3]), pack_bf16x2(hi[4], hi[5]),
-                               pack_bf16x2(hi[6], hi[7]));
-        } else {
-            *pmin = make_uint4(__float_as_uint(lo[0]), __float_as_uint(lo[1]), __float_as_uint(lo[2]), __float_as_uint(lo[3]));
-            *pmax = make_uint4(__float_as_uint(hi[0]), __float_as_uint(hi[1]), __float_as_uint(hi[2]), __float_as_uint(hi[3]));
-        }
+        const int j = it >> c_shift, cc = it & (CPR - 1), ea = j * a.bs / 8, eb = (min(n, (j + 1) * a.bs) + 7) / 8;
+        Box<KB> box;
+        for (int e = ea; e < eb; ++e) box.join(s_part[2 * ((e << c_shift) + cc)], s_part[2 * ((e << c_shift) + cc) + 1]);
+        const long long at = ((long long)u * a.nb_cap + blk0 + j) * a.row_bytes + cc * 16;
+        *reinterpret_cast<uint4*>(a.kmin + at) = box.low();
+        *reinterpret_cast<uint4*>(a.kmax + at) = box.high();
     }
 }
 
@@ -361,11 +395,11 @@ cudaError_t launch_move(const EvictArgs& a, unsigned grid, cudaStream_t s)
 {
     static std::atomic<unsigned long long> configured{0};   // devices set up
     const cudaError_t cfg = once_per_device(configured, [&]() -> cudaError_t {
-        return cudaFuncSetAttribute(evict_move_kernel<KB>, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 512);
+        return cudaFuncSetAttribute(evict_move_kernel<KB>, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 512 * 5 / 4);
     });
     if (cfg != cudaSuccess) return cfg;
     return launch_after_previous(evict_move_kernel<KB>, dim3(grid), dim3(kMvThreads),
-                                 a.kmin != nullptr ? size_t(a.run) * a.row_bytes : 0, s, a);
+                                 a.kmin != nullptr ? size_t(a.run) * a.row_bytes * 5 / 4 : 0, s, a);
 }
 
 }  // namespace

@@ -414,42 +414,6 @@ __device__ TreePart tree_part(const TreeArgs& a, int* s)
     return r;
 }
 
-// Two fp32 operations in one instruction (each rounded as usual).
-union F2 {
-    unsigned long long u;
-    float2 f;
-};
-__device__ __forceinline__ F2 make_f2(float x, float y)
-{
-    F2 r;
-    r.f = make_float2(x, y);
-    return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
-{
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.u) : "l"(a.u), "l"(b.u), "l"(c.u));
-    return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b)
-{
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(a.u), "l"(b.u));
-    return r;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b)
-{
-    F2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(a.u), "l"(b.u));
-    return r;
-}
-__device__ __forceinline__ F2 sub2(F2 a, F2 b)
-{
-    F2 r;
-    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(a.u), "l"(b.u));
-    return r;
-}
-
 // The output row of an item's query row r (query r / G, head r % G of the KV head's group).
 __device__ __forceinline__ long long tree_out_row(const TreeArgs& a, int b, int kvh, int r)
 {

@@ -110,6 +110,9 @@ CASES = {
     "block_128": (Case(batch=2, lens=(700, 299), context=700, block=128), 277, dict(sinks=3)),
     "dim_64": (Case(batch=2, lens=(300, 299), dim=64, block=16), 77, dict(sinks=3)),
     "fp32": (Case(batch=2, lens=(300, 299), dtype=F32, kv=F32), 130, dict(sinks=3)),
+    "fp32_block_128": (Case(batch=2, lens=(300, 299), dtype=F32, kv=F32, block=128), 130, dict(sinks=3)),
+    "fp32_block_64": (Case(batch=2, lens=(300, 299), dtype=F32, kv=F32, block=64), 130, dict(sinks=3)),
+    "long_rows_of_runs": (Case(batch=3, lens=(4000, 3900, 4000), context=4000, hq=16, hkv=16, dim=64, block=64), 3500, {}),
     "fp32_64_block_128": (Case(batch=2, lens=(300, 299), dtype=F32, kv=F32, dim=64, block=128), 130, dict(sinks=3)),
     "no_box": (Case(batch=2, lens=(300, 299)), 77, dict(box=False)),
     "heads": (Case(batch=3, lens=(300, 299, 280), hq=8, hkv=8, dim=64), 77, {}),
@@ -176,6 +179,27 @@ def test_bad_pages_are_reported():
         (t if which == "table" else n)[1, 0] = value
         flags, _, lens = call(c, p, t, pools, n)
         assert flags == B.ERR_PAGE and lens == [100, 100]
+
+
+def test_rows_of_good_pages_move_past_a_bad_one():
+    c, p, table, pools, new = small()
+    host = [torch.randn(x.shape, generator=c.gen("rows")).to(BF) for x in pools]
+    pools = [x.cuda() for x in host]
+    bad = table.clone()
+    bad[0, 2], bad[1, 0] = c.pages + 100, -5
+    flags, ids, lens = call(c, p, bad, pools, new)
+    assert flags == B.ERR_PAGE and lens == [100, 100]
+    for b in range(2):
+        for h in range(c.hkv):
+            t = ids[b, h].cpu().long()
+            good = (bad[b].long()[t // c.block] >= 0) & (bad[b].long()[t // c.block] < c.pages)
+            assert good.any() and not good.all()
+            i = torch.arange(100)
+            for pool, before in zip(pools, host):
+                want = before[bad[b].long()[t[good] // c.block], h, t[good] % c.block]
+                assert torch.equal(pool.cpu()[new[b].long()[i[good] // c.block], h, i[good] % c.block], want)
+                old = before[new[b].long()[i[~good] // c.block], h, i[~good] % c.block]
+                assert torch.equal(pool.cpu()[new[b].long()[i[~good] // c.block], h, i[~good] % c.block], old)
 
 
 def test_bad_lengths_are_reported_and_leave_the_sequence_alone():
