@@ -243,3 +243,82 @@ class DraftDecoder:
     def device_error(self, stream=None) -> int:
         with torch.cuda.device(self.device):         # whose current stream is the default
             return B.sparse_attn_get_device_error(self.ws, stream)
+
+
+class LongContextDecoder(DraftDecoder):
+    """A DraftDecoder for long contexts: queries and keys normed on their way into the cache and turned by
+    positions of several axes, attention for groups of sequences that share a prefix, attention weights added
+    up token by token, and eviction by them.  Owns what DraftDecoder owns, the weights and the kept tokens'
+    numbers besides.
+
+    ``num_groups`` groups at most share prefixes (0: ``decode_shared`` is not used); with ``keep_tokens``
+    contexts are cut down to that many tokens (0: ``decode_weighed`` and ``evict`` are not used).  The weights
+    start at zero."""
+
+    def __init__(self, params: B.sparse_attn_params, seq_lens: torch.Tensor, num_groups: int = 0, keep_tokens: int = 0):
+        super().__init__(params, seq_lens)
+        p, dev = params, self.device
+        self.num_groups, self.keep_tokens = num_groups, keep_tokens
+        self.weights = self.kept_ids = None
+        size = self.ws.numel()
+        with torch.cuda.device(dev):
+            if num_groups > 0:
+                size = max(size, B.sparse_attn_shared_workspace_size(p, num_groups))
+            if keep_tokens > 0:
+                size = max(size, B.sparse_attn_weigh_workspace_size(p), B.sparse_attn_evict_workspace_size(p, keep_tokens))
+                nb_cap = -(-max(p.capacity_tokens, p.n_tokens) // p.block_size)
+                self.weights = torch.zeros(p.batch, p.num_kv_heads, nb_cap * p.block_size, device=dev)
+                self.kept_ids = torch.full((p.batch, p.num_kv_heads, keep_tokens), -1, dtype=torch.int32, device=dev)
+            if size > self.ws.numel():
+                self.ws = torch.empty(size, dtype=torch.uint8, device=dev)
+                B.sparse_attn_workspace_init(self.ws)
+
+    def append_norm(self, q_new, k_new, v_new, q_weight, k_weight, eps, inv_freq, q_out, k_pages, v_pages, block_table,
+                    cu_rows=None, positions=None, axis_of=None, pairing=B.ROTATE_HALVES, kmin=None, kmax=None, stream=None):
+        """``append`` with head norms (weights or None) and positions of several axes.  Once a sequence has
+        been evicted from, a token's index is not its position any more: ``positions`` says it."""
+        B.sparse_attn_append_kv_norm(self.p, q_new, k_new, v_new, q_weight, k_weight, eps, inv_freq, q_out, k_pages,
+                                     v_pages, block_table, self.ws, cu_rows, self.seq_lens, positions, axis_of, pairing,
+                                     kmin, kmax, stream)
+
+    def decode_shared(self, q, k_pages, v_pages, block_table, cu_seqs, prefix_lens, tree_mask=None, stream=None):
+        """``decode`` for groups of sequences that hold the same first tokens; returns the output tensor."""
+        if prefix_lens.numel() > self.num_groups:
+            raise ValueError(f"prefix_lens: {prefix_lens.numel()} groups, room for {self.num_groups}")
+        B.sparse_attn_shared_decode(self.p, q, k_pages, v_pages, block_table, cu_seqs, prefix_lens, self.out.view(q.shape),
+                                    self.ws, self.seq_lens, tree_mask, stream)
+        return self.out
+
+    def decode_weighed(self, q, k_pages, v_pages, block_table, stream=None):
+        """Attention of a chain of new tokens that adds to ``weights``; returns the output tensor."""
+        B.sparse_attn_weigh_decode(self.p, q, k_pages, v_pages, block_table, self.weights, self.out.view(q.shape), self.ws,
+                                   self.seq_lens, stream)
+        return self.out
+
+    def accept(self, stream=None):
+        """The new tokens of every active sequence join its context."""
+        with torch.cuda.stream(self._stream(stream)):
+            self.seq_lens.add_((self.seq_lens >= 0).to(torch.int32), alpha=self.Q)
+
+    def evict(self, sink_tokens, recent_tokens, k_pages, v_pages, block_table, new_table, keep_lens=None, kmin=None,
+              kmax=None, stream=None):
+        """Cut the contexts down to ``keep_tokens`` (or ``keep_lens``) tokens in the pages of ``new_table``
+        [B, ceil(keep_tokens / block_size)], which must be free ones; ``kept_ids`` says which tokens they were.
+        ``seq_lens`` holds the new lengths after it, and the rows of ``block_table`` begin with the new
+        pages; the pages that were in it are the caller's again."""
+        B.sparse_attn_evict_tokens(self.p, self.keep_tokens, sink_tokens, recent_tokens, self.weights, k_pages, v_pages,
+                                   block_table, new_table, self.kept_ids, self.new_lens, self.ws, self.seq_lens, keep_lens,
+                                   kmin, kmax, stream)
+        with torch.cuda.stream(self._stream(stream)):
+            # what the call leaves alone keeps its pages: inactive, no budget, or numbers out of range
+            moved = (self.seq_lens >= 0) & (self.seq_lens <= self.p.n_tokens)
+            if keep_lens is not None:
+                moved &= (keep_lens >= sink_tokens + recent_tokens) & (keep_lens <= self.keep_tokens)
+            head = block_table[:, : new_table.shape[1]]
+            head.copy_(torch.where(moved[:, None], new_table, head))
+            self.seq_lens.copy_(self.new_lens)
+
+    def _stream(self, stream):
+        if stream is None:
+            return torch.cuda.current_stream(self.device)
+        return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=self.device)
