@@ -31,34 +31,49 @@ __device__ __forceinline__ Shares shares_of(const TreeArgs& a, int2 parts, int r
 }
 __device__ __forceinline__ long long share_row(int step, int c) { return c == 0 ? 0 : (2LL * c - 1) * step; }
 
-// The weight of a share with maximum m and total l beside one whose maximum is M, unscaled both, and to which
-// M itself is the reference.  Shares of the warp-level kernel are relative to m * scale exactly, those of
-// the tensor-core one to the rounded product, which the difference takes into account; past 2^29 (in base-2
-// logits) they are relative to m itself again, and so are the weights here.
-__device__ __forceinline__ float share_weight(bool tensor, float m, float M, float l, float scale)
-{
-    if (m == -INFINITY && l == 0.f) return 0.f;
-    const float rounded = __fmul_rn(m, scale);
-    if (tensor && fabsf(rounded) < 536870912.f) return fast_exp2(-fmaf(M, scale, -rounded));
-    return fast_exp2((m - M) * scale);
-}
-
 // WPR warps to an output row: each has all the shares' maxima and totals (lane = share) and adds up every
 // WPR-th share, eight loads on their way at once; their sums go through shared memory.  A small call waits
 // for the chain of dependent loads (the sequence's group, notes, maxima, shares) and takes four warps a row,
-// which leaves one round of shares; with many rows one warp has a row to itself.  (2048 rows of about 12
-// shares 7.0 us, four warps a row 10.6; 65536 rows of one share 50 and 145.)
+// which leaves one round of shares; with many rows one warp has a row to itself (2048 rows of about 12
+// shares 7.0 us, four warps a row 10.6).  Where the attention has finished the rows in one part, a warp looks
+// eight rows' notes up and joins those that are left: from many rows on, since it joins them one by one (131072 rows,
+// none left: 5 us, 97 with a warp a row; 16384 rows in split items 15 with a warp a row, 36 with one for 32).
+template <int D, int WPR>
+__device__ __forceinline__ void join_row(const TreeArgs& own, const TreeArgs& pre, int with_prefix, float2* stats, int row);
+
+constexpr int kJoinMany = 8;               // rows of a warp that looks for what is left
+
 template <int D, int WPR>
 __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ TreeArgs own,
                                                                  const __grid_constant__ TreeArgs pre, int with_prefix,
-                                                                 float2* stats)
+                                                                 float2* stats, int many)
 {
-    __shared__ float4 s_num[WPR > 1 ? kJoinWarps : 1][D / 4];
     allow_dependents_early();
     grid_dependency_wait();   // the shares come from the previous kernels
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % WPR;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rows = own.seqs * own.Q * own.Hq;
+    if (WPR == 1 && many) {
+        const int first = (int(blockIdx.x) * kJoinWarps + warp) * kJoinMany, row = first + lane;
+        bool left = false;
+        if (lane < kJoinMany && row < rows) {
+            const int h = row % own.Hq, bt = row / own.Hq, b = bt / own.Q, kvh = h / own.G;
+            const int rg = ((bt - b * own.Q) * own.G + h - kvh * own.G) / own.item_rows;
+            const int len = own.seq_lens != nullptr ? own.seq_lens[b] : own.N;
+            if (len >= 0 && len <= own.N)
+                left = own.item_parts[kvh * tree_notes_per_head(own, own.item_rows) + (long long)b * own.row_groups + rg].y > 1;
+        }
+        for (uint32_t todo = __ballot_sync(kFullMask, left); todo != 0u; todo &= todo - 1)
+            join_row<D, WPR>(own, pre, with_prefix, stats, first + __ffs(todo) - 1);
+        return;
+    }
     const int row = int(blockIdx.x) * (kJoinWarps / WPR) + warp / WPR;
-    if (row >= own.seqs * own.Q * own.Hq) return;              // whole warps, and whole CTAs with WPR = 4
+    if (row < rows) join_row<D, WPR>(own, pre, with_prefix, stats, row);       // whole warps, and whole CTAs with WPR = 4
+}
+
+template <int D, int WPR>
+__device__ __forceinline__ void join_row(const TreeArgs& own, const TreeArgs& pre, int with_prefix, float2* stats, int row)
+{
+    __shared__ float4 s_num[WPR > 1 ? kJoinWarps : 1][D / 4];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % WPR;
     const int h = row % own.Hq, bt = row / own.Hq, b = bt / own.Q, t = bt - b * own.Q;
     const int kvh = h / own.G, r = t * own.G + h - kvh * own.G;
     const int rg = r / own.item_rows;
@@ -74,7 +89,8 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
         const int len = own.seq_lens != nullptr ? own.seq_lens[b] : own.N;
         active = len >= 0 && len <= own.N;
     }
-    if (!active) return;                                      // no output; the same for all warps of a row
+    // no output, or done already; the same for all warps of a row
+    if (!active || (own.pass == kTreeAll && own_parts.y <= 1)) return;
     const Shares x0 = shares_of(own, own_parts, r - rg * own.item_rows, row);
     Shares x1 = x0;
     x1.n = 0;
@@ -161,9 +177,11 @@ template <int D, int WPR>
 cudaError_t launch_join_t(const TreeArgs& own, const TreeArgs* prefix, float2* stats, cudaStream_t s)
 {
     static_assert(WPR == 1 || WPR == kJoinWarps, "a CTA is one row or a row a warp");
-    const long long rows = (long long)own.seqs * own.Q * own.Hq, per = kJoinWarps / WPR;
+    const long long rows = (long long)own.seqs * own.Q * own.Hq;
+    const bool many = WPR == 1 && own.pass == kTreeAll && rows >= 256LL * num_sms();
+    const long long per = kJoinWarps / WPR * (many ? kJoinMany : 1);
     return launch_after_previous(tree_join_kernel<D, WPR>, dim3(unsigned((rows + per - 1) / per)), dim3(kJoinThreads), 0, s, own,
-                                 prefix != nullptr ? *prefix : own, int(prefix != nullptr), stats);
+                                 prefix != nullptr ? *prefix : own, int(prefix != nullptr), stats, int(many));
 }
 
 }  // namespace

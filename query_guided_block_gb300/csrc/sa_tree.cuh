@@ -56,14 +56,16 @@ struct TreeArgs {
     uint32_t* counters;        // [CTA] arrivals of the item that goes on behind this CTA's part; zero between calls
     uint32_t* err;
 
-    // The kernels' EXT form (sa_shared.cu, sa_weigh.cu): a launch of its own always joins the shares, so
-    // (m, l, o) are left as they are, those of items in one part in row_m, row_l and `out`.
+    // The kernels' EXT form (sa_shared.cu, sa_weigh.cu): a launch of its own joins the shares, so (m, l, o) are
+    // left as they are, those of items in one part in row_m, row_l and `out`.  Only a kTreeAll item in one
+    // part is done with.
     int pass;                  // kTreeAll, kTreePrefix or kTreeOwn
     int tensor;                // the tensor-core kernel's shares: relative to the rounded product of maximum and scale
     int seqs;                  // sequences of the batch (B: units / Hkv, groups in the prefix pass)
     const int32_t *cu_seqs, *prefix_lens;
     int32_t *seq_prefix, *seq_group;     // [seqs]: shared tokens (-1: inactive) and group, by the prefix pass
-    float *row_m, *row_l;      // [seqs * Q * Hq]: unscaled maximum and sum
+    float *row_m, *row_l;      // [seqs * Q * Hq]: unscaled maximum and sum of rows in one part
+    float2* stats;             // [seqs * Q * Hq]: kTreeAll: maximum and 1 / total of rows that are done
     float* scores;             // [unit][R][score_stride] unscaled scores, null: not kept
     long long score_stride;
 };
@@ -443,6 +445,17 @@ __device__ __forceinline__ void tree_note_parts(const TreeArgs& a, int item, int
     a.item_parts[item] = make_int2(c0, (start + tiles - 1) / per - c0 + 1);
 }
 
+// An EXT row of an item in one part.
+__device__ __forceinline__ void tree_note_row(const TreeArgs& a, long long row, bool done, float m, float l, float inv)
+{
+    if (done) {
+        a.stats[row] = make_float2(m, inv);
+    } else {
+        a.row_m[row] = m;
+        a.row_l[row] = l;
+    }
+}
+
 // The first part of an item and how many it has.
 __device__ __forceinline__ int2 tree_parts(int start, int tiles, int per)
 {
@@ -493,6 +506,18 @@ __device__ __forceinline__ void tree_note_sequences(const TreeArgs& a, int threa
         a.seq_prefix[b] = bad || len < 0 ? -1 : n;
         a.seq_group[b] = lo;
     }
+}
+
+// The weight of a share with maximum m and total l beside one whose maximum is M, unscaled both, and to which
+// M itself is the reference.  Shares of the warp-level kernel are relative to m * scale exactly, those of
+// the tensor-core one to the rounded product, which the difference takes into account; past 2^29 (in base-2
+// logits) they are relative to m itself again, and so are the weights here.
+__device__ __forceinline__ float share_weight(bool tensor, float m, float M, float l, float scale)
+{
+    if (m == -INFINITY && l == 0.f) return 0.f;
+    const float rounded = __fmul_rn(m, scale);
+    if (tensor && fabsf(rounded) < 536870912.f) return fast_exp2(-fmaf(M, scale, -rounded));
+    return fast_exp2((m - M) * scale);
 }
 
 // Called by the CTA's first NT threads once its (m, l, o) of a shared item is written: counts the

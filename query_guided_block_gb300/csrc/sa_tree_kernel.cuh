@@ -486,14 +486,14 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
             l_run[h] += __shfl_xor_sync(kFullMask, l_run[h], 1);
             l_run[h] += __shfl_xor_sync(kFullMask, l_run[h], 2);
         }
-        const bool complete = t0 == 0 && t1 == tiles;
+        const bool complete = t0 == 0 && t1 == tiles, done = complete && (!EXT || a.pass == kTreeAll);
         const long long slot = (long long)tree_slot(blockIdx.x, part.per, start) * a.item_rows;
         if constexpr (TW == 1) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int r = h ? r_hi : r_lo, rr = r - row0;
                 if (r >= R) continue;
-                const float inv = complete && !EXT ? (l_run[h] == 0.f ? 0.f : 1.f / l_run[h]) : 1.f;
+                const float inv = done ? (l_run[h] == 0.f ? 0.f : 1.f / l_run[h]) : 1.f;
                 float* dst = (complete ? a.out + tree_out_row(a, b, kvh, r) * D : a.part_o + (slot + rr) * D) + 2 * t4;
 #pragma unroll
                 for (int j = 0; j < DT; ++j)
@@ -502,10 +502,7 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
                     a.part_m[slot + rr] = m_run[h];
                     a.part_l[slot + rr] = l_run[h];
                 }
-                if (EXT && complete && t4 == 0) {
-                    a.row_m[tree_out_row(a, b, kvh, r)] = m_run[h];
-                    a.row_l[tree_out_row(a, b, kvh, r)] = l_run[h];
-                }
+                if (EXT && complete && t4 == 0) tree_note_row(a, tree_out_row(a, b, kvh, r), done, m_run[h], l_run[h], inv);
             }
         } else {
             // the warps' token shares of the same rows, through the freed stages
@@ -544,17 +541,14 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
                     num.z = fmaf(o.z, wgt, num.z);
                     num.w = fmaf(o.w, wgt, num.w);
                 }
-                const float inv = complete && !EXT ? (den == 0.f ? 0.f : 1.f / den) : 1.f;
+                const float inv = done ? (den == 0.f ? 0.f : 1.f / den) : 1.f;
                 float* dst = complete ? a.out + tree_out_row(a, b, kvh, row0 + rr) * D : a.part_o + (slot + rr) * D;
                 *reinterpret_cast<float4*>(dst + d) = make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
                 if (!complete && d == 0) {
                     a.part_m[slot + rr] = M;
                     a.part_l[slot + rr] = den;
                 }
-                if (EXT && complete && d == 0) {
-                    a.row_m[tree_out_row(a, b, kvh, row0 + rr)] = M;
-                    a.row_l[tree_out_row(a, b, kvh, row0 + rr)] = den;
-                }
+                if (EXT && complete && d == 0) tree_note_row(a, tree_out_row(a, b, kvh, row0 + rr), done, M, den, inv);
             }
         }
         if constexpr (EXT) {

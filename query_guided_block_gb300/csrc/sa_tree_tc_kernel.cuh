@@ -511,12 +511,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const bool complete = g.t0 == 0 && g.t1 == g.tiles;
             tree_sync<kTcWork>();                                  // the softmax threads' sums are there
             const float l = x_l[row % COPY] + x_l[128 + row % COPY];
-            const float w = EXT || !complete ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+            const bool done = complete && (!EXT || a.pass == kTreeAll);
+            const float w = !done ? 1.f : (l == 0.f ? 0.f : 1.f / l);
             if (EXT && row < COPY && r_unit < g.rows) {            // the joining launch scales the maximum itself
-                const long long slot = (long long)tree_slot(blockIdx.x, part.per, g.start) * a.item_rows + row;
-                const long long at = tree_out_row(a, g.b, g.kvh, r_unit);
-                *(complete ? a.row_m + at : a.part_m + slot) = m_acc;
-                *(complete ? a.row_l + at : a.part_l + slot) = l;
+                if (complete) {
+                    // 1 / total relative to the maximum itself, as the weights are computed from it
+                    const float exact = share_weight(true, m_acc, m_acc, l, a.scale_log2);
+                    tree_note_row(a, tree_out_row(a, g.b, g.kvh, r_unit), done, m_acc, l, exact == 0.f ? 0.f : w / exact);
+                } else {
+                    const long long slot = (long long)tree_slot(blockIdx.x, part.per, g.start) * a.item_rows + row;
+                    a.part_m[slot] = m_acc;
+                    a.part_l[slot] = l;
+                }
             } else if (!EXT && !complete && row < COPY && r_unit < a.R) {
                 const long long slot = (long long)tree_slot(blockIdx.x, part.per, g.start) * a.item_rows + row;
                 a.part_m[slot] = m_acc * a.scale_log2;

@@ -110,6 +110,7 @@ cudaError_t launch_weigh(const Geometry& g, const TreeCall& c, float* weights, c
     TreeArgs a = tree_ext_args(g, c, ws, L.own);
     a.pass = kTreeAll;
     float2* stats = reinterpret_cast<float2*>(ws + L.stats);
+    a.stats = stats;
     const long long tokens = (long long)g.N + g.Q, w_stride = (long long)g.nb_cap * g.bs;
     const bool tensor = weigh_tensor(g, tokens);
     if (!tensor) {

@@ -4,17 +4,18 @@
 //
 // Per tile of 128 tokens: S^T = K Q^T (tcgen05.mma, M = the tile's tokens, N = up to 256 query rows), so that a
 // thread owns a token and adds up exp2((s - m_r) scale) / l_r over the rows r in registers, the rows' maxima and
-// reciprocal totals being broadcast from shared memory.  Two groups of four warps take half of the rows each;
-// their sums meet in shared memory.  Rows past 256 are further passes over the same tiles.
+// reciprocal totals being broadcast from shared memory.  Four groups of four warps take a quarter of the rows
+// each; their sums meet in shared memory.  Rows past 256 are further passes over the same tiles.
 //
-// Roles: warps 0-7 the sums, warp 8 resolves pages and brings K by TMA into a ring, warp 9 issues the
+// Roles: warps 0-15 the sums, warp 16 resolves pages and brings K by TMA into a ring, warp 17 issues the
 // products into one of two score tiles in tensor memory.  No wait is without a limit.
 #include "sa_tree_tc_kernel.cuh"
 
 namespace sa {
 namespace {
 
-constexpr int kWtSum = 256;
+constexpr int kWtGroups = 4;             // of four warps, each with a quarter of the rows
+constexpr int kWtSum = 128 * kWtGroups;
 constexpr int kWtThreads = kWtSum + 64;
 constexpr int kWtRows = 256;               // query rows of a pass
 
@@ -37,7 +38,7 @@ template <int D>
 struct WtShared {
     uint64_t full[WtShape<D>::STAGES], empty[WtShape<D>::STAGES], s_full[2], s_read[2];
     float m[kWtRows], inv[kWtRows];             // of the pass's rows
-    float half[2][kTcTile];                     // sums of the second group, tile mod 2
+    float part[2][kWtGroups - 1][kTcTile];      // sums of the groups behind the first, tile mod 2
     int scan[kTreeScan<kWtThreads>];
     uint32_t pages[WtShape<D>::INFO];           // entries of a tile that have a page
     uint32_t tmem;
@@ -100,12 +101,12 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         }
     };
     // columns of a pass: its rows, whole 16s for each group of warps
-    auto columns = [&](int pass) { return (min(kWtRows, a.R - pass * kWtRows) + 31) / 32 * 32; };
+    auto columns = [&](int pass) { return (min(kWtRows, a.R - pass * kWtRows) + 16 * kWtGroups - 1) / (16 * kWtGroups) * (16 * kWtGroups); };
 
     while (tc_next<true>(a, part, lo, start, item, g)) {
         const int ntl = g.t1 - g.t0;
         for (int pass = 0; pass < passes; ++pass, tile0 += ntl) {
-            if (warp == 8) {
+            if (warp == kWtSum / 32) {
                 // ---- producer -----------------------------------------------------------------
                 const int n_e = a.bs >= kTcTile ? 1 : kTcTile >> a.bs_shift;   // entries of a tile
                 const int per_batch = 32 / n_e;                    // tiles whose entries one batch holds
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                         for (int h = 0; h < SH::HALVES; ++h) tma_load_3d(dst + h * SH::HALF, &kmap, h * 64, 0, page, &sh.full[st]);
                     }
                 }
-            } else if (warp == 9) {
+            } else if (warp == kWtSum / 32 + 1) {
                 // ---- scores -------------------------------------------------------------------
                 bar_sync(1, kWtSum + 32);                          // queries staged
                 if (lane == 0) {
@@ -160,7 +161,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 }
                 __syncwarp();
             } else {
-                // ---- the sums: thread = token, group = half of the rows -----------------------------
+                // ---- the sums: thread = token, group = a quarter of the rows -----------------------------
                 const int cols = columns(pass), rows = min(kWtRows, a.R - pass * kWtRows);
                 {
                     constexpr int CPR = D / 8;                     // 16-byte chunks of a row
@@ -183,7 +184,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 }
                 bar_sync(1, kWtSum + 32);
                 const int h = warp >> 2, token = 32 * (warp & 3) + lane;
-                const int c0 = h * (cols / 2), c1 = c0 + cols / 2;
+                const int c0 = h * (cols / kWtGroups), c1 = c0 + cols / kWtGroups;
                 const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
                 const F2 scale2 = make_f2(a.scale_log2, a.scale_log2);
                 for (int i = 0; i < ntl; ++i) {
@@ -226,9 +227,13 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                     mbar_arrive(&sh.s_read[s]);
                     const F2 sum2 = add2(sum_a, sum_b);
                     float sum = sum2.f.x + sum2.f.y;
-                    if (h == 1) sh.half[s][token] = sum;
+                    if (h > 0) sh.part[s][h - 1][token] = sum;
                     bar_sync(2, kWtSum);
-                    if (h == 0 && t < g.un.len + a.Q) *w = old + (sum + sh.half[s][token]);
+                    if (h == 0 && t < g.un.len + a.Q) {
+#pragma unroll
+                        for (int x = 0; x < kWtGroups - 1; ++x) sum += sh.part[s][x][token];
+                        *w = old + sum;
+                    }
                 }
             }
         }
