@@ -22,6 +22,13 @@
  *                             it or a selection) and over the drafts each query may see.
  *   sparse_attn_commit_drafts the accepted drafts' K/V moved to the end of the context.
  *
+ * Long contexts:
+ *
+ *   sparse_attn_append_kv_norm  the append, with head norms and positions of several axes.
+ *   sparse_attn_shared_decode   attention of a batch whose sequences share prefixes.
+ *   sparse_attn_weigh_decode    attention that adds up every cached token's weight.
+ *   sparse_attn_evict_tokens    the tokens with the largest weights kept, in new pages.
+ *
  * Conventions shared by every call
  * --------------------------------
  *  * All tensor pointers are DEVICE pointers into memory the caller owns.  The library

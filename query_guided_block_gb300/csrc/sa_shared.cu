@@ -37,7 +37,7 @@ __device__ __forceinline__ long long share_row(int step, int c) { return c == 0 
 // which leaves one round of shares; with many rows one warp has a row to itself (2048 rows of about 12
 // shares 7.0 us, four warps a row 10.6).  Where the attention has finished the rows in one part, a warp looks
 // eight rows' notes up and joins those that are left: from many rows on, since it joins them one by one (131072 rows,
-// none left: 5 us, 97 with a warp a row; 16384 rows in split items 15 with a warp a row, 36 with one for 32).
+// none left: 6.5 us, 97 with a warp a row; 16384 rows in split items 15 with a warp a row, 36 with one for 32).
 template <int D, int WPR>
 __device__ __forceinline__ void join_row(const TreeArgs& own, const TreeArgs& pre, int with_prefix, float2* stats, int row);
 

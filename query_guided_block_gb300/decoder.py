@@ -258,6 +258,8 @@ class LongContextDecoder(DraftDecoder):
     def __init__(self, params: B.sparse_attn_params, seq_lens: torch.Tensor, num_groups: int = 0, keep_tokens: int = 0):
         super().__init__(params, seq_lens)
         p, dev = params, self.device
+        if keep_tokens > max(p.capacity_tokens, p.n_tokens):
+            raise ValueError(f"keep_tokens: {keep_tokens}, a sequence has pages for {max(p.capacity_tokens, p.n_tokens)}")
         self.num_groups, self.keep_tokens = num_groups, keep_tokens
         self.weights = self.kept_ids = None
         size = self.ws.numel()

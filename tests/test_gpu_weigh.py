@@ -84,7 +84,7 @@ CASES = {
     "many_units": Case(batch=50, drafts=1, lens=tuple(7 * i for i in range(50)), context=400, hq=16, hkv=8, dim=64),
 }
 
-# enough query rows and tiles for the tensor-core kernels
+# many tiles, with more than 32 query rows for the tensor-core kernels
 TENSOR = {
     "rows_20": Case(batch=4, drafts=5, hq=32, hkv=8, lens=(700, 650, 640, 701), context=701, block=64),
     "rows_32": Case(batch=4, drafts=8, hq=32, hkv=8, lens=(700, 0, 640, 1), context=700),
@@ -103,7 +103,7 @@ def test_against_64_bits(name):
 
 
 @pytest.mark.parametrize("name", TENSOR)
-def test_tensor_cores_against_64_bits(name):
+def test_many_rows_against_64_bits(name):
     run(TENSOR[name], old=0.1)
 
 
@@ -131,12 +131,12 @@ def test_every_length_the_same():
 
 
 @pytest.mark.parametrize("scale", [0.02, 3.0, 1e4])
-@pytest.mark.parametrize("name", ["batch", "window", "rows_20"])
+@pytest.mark.parametrize("name", ["batch", "window", "rows_20", "rows_128"])
 def test_scales(name, scale):
     run({**CASES, **TENSOR}[name], scale=scale)
 
 
-@pytest.mark.parametrize("name", ["window", "rows_32"])
+@pytest.mark.parametrize("name", ["window", "rows_32", "rows_264"])
 def test_pages_out_of_range_are_reported_and_weigh_nothing(name):
     c = {**CASES, **TENSOR}[name]
     table = c.block_table()
