@@ -229,7 +229,9 @@ __device__ __forceinline__ float norm_factor(const F2 (&x)[8], int CH, int lane,
     const unsigned seg = ((1u << CH) - 1u) << (lane & ~(CH - 1));
     auto over_row = [&](F2 s) {
         float v = s.f.x + s.f.y;
-        for (int m = 1; m < CH; m <<= 1) v += __shfl_xor_sync(seg, v, m);
+        v += __shfl_xor_sync(seg, v, 1);
+        v += __shfl_xor_sync(seg, v, 2);
+        if (CH == 8) v += __shfl_xor_sync(seg, v, 4);
         return v;
     };
     const float inv_n = CH == 8 ? 1.f / 128.f : 1.f / 64.f;
@@ -247,7 +249,7 @@ __device__ __forceinline__ float norm_factor(const F2 (&x)[8], int CH, int lane,
         }
         return by / sqrtf(over_row(s) * inv_n);
     }
-    return 1.f / sqrtf(fmaf(ss, inv_n, eps));
+    return rsqrtf(fmaf(ss, inv_n, eps));                      // 2 units in the last place
 }
 
 __device__ __forceinline__ void load_weights16(const float* weight, int ea, int eb, F2 (&w)[8])
@@ -548,12 +550,8 @@ __global__ void __launch_bounds__(kAppThreads, 2) append_kernel(AppendArgs a)
     {
         const int per_row = (qn + kvn) * CH;
         if (per_row == 0) return;                             // without queries, more shares than heads
-        // 16 channels of a value on their way to token t0 + row.
-        auto store_value = [&](const Raw16<QB>& raw, int row, int kvh, int c) {
-            const int t = t0 + row, page = s_page[t / a.bs - blk0];
-            if (page < 0) return;
-            void* dst = const_cast<char*>(at_elem<KB>(
-                a.v_pages, (((long long)page * a.Hkv + kvh) * a.bs + t % a.bs) * a.D));
+        // 16 channels of a value on their way to its row in the pages; to token t0 + row's.
+        auto store_raw = [&](const Raw16<QB>& raw, void* dst, int c) {
             if constexpr (QB == KB) {                         // same type: the bits as they are
                 uint4* p = reinterpret_cast<uint4*>(const_cast<char*>(at_elem<KB>(dst, 16 * c)));
 #pragma unroll
@@ -564,53 +562,70 @@ __global__ void __launch_bounds__(kAppThreads, 2) append_kernel(AppendArgs a)
                 store16<KB>(dst, 16 * c, 16 * c + 8, f);
             }
         };
+        auto store_value = [&](const Raw16<QB>& raw, int row, int kvh, int c) {
+            const int t = t0 + row, page = s_page[t / a.bs - blk0];
+            if (page < 0) return;
+            store_raw(raw, const_cast<char*>(at_elem<KB>(a.v_pages, (((long long)page * a.Hkv + kvh) * a.bs + t % a.bs) * a.D)), c);
+        };
         if constexpr (EXT == 1) {
             // A thread keeps a row's turn, weights in it, in registers and goes through heads: with cosines, sines
             // and weights from shared memory and L1 for every item these were what the SM read most of (48K
-            // rows with positions of three axes 257 us, so 230; without any norm 202).
+            // rows with positions of three axes 257 us, so 221; without any norm 202).
             int rl = 1;                                       // rows side by side
             while (rl < 16 && 2 * rl <= n) rl *= 2;
             const int c = tid & (CH - 1), place = tid >> ch_shift, heads = qn + kvn;
             const int h0 = place / rl, h_step = kAppThreads / (CH * rl);
             const int ea = elem_a(c), eb = elem_b(c);
-            auto fetch = [&](int row, int head, int slot) {
-                if (row < n) {
-                    if (head < qn)
-                        ring.fetch(slot, at_elem<QB>(a.q_new, (r0 + row) * a.q_stride + (q0 + head) * a.D), ea, eb);
-                    else
-                        ring.fetch(slot, at_elem<QB>(a.v_new, (r0 + row) * a.v_stride + (kv0 + head - qn) * a.D), 16 * c, 16 * c + 8);
-                }
-                ring.close();
+            // Places in memory are worked out once a row (a.bs is a power of two, but a divisor here).
+            const char *q_ahead = nullptr, *v_ahead = nullptr;
+            char *q_to = nullptr, *v_to = nullptr;            // v_to null: no page
+            auto rows_ahead = [&](int row) {
+                q_ahead = at_elem<QB>(a.q_new, (r0 + row) * a.q_stride + q0 * a.D);
+                v_ahead = at_elem<QB>(a.v_new, (r0 + row) * a.v_stride + kv0 * a.D);
             };
             auto step = [&](int& row, int& head) {
                 head += h_step;
-                if (head >= heads) {
+                const bool wraps = head >= heads;
+                if (wraps) {
                     head = h0;
                     row += rl;
                 }
+                return wraps;
             };
-            int row = h0 < heads ? place & (rl - 1) : n, head = h0, row_ahead = row, head_ahead = head, row_turn = -1;
+            int row = h0 < heads ? place & (rl - 1) : n, head = h0, row_ahead = row, head_ahead = head, slot_ahead = 0;
+            rows_ahead(min(row_ahead, n - 1));
+            auto fetch_ahead = [&]() {
+                if (row_ahead < n) {
+                    if (head_ahead < qn) ring.fetch(slot_ahead, at_elem<QB>(q_ahead, head_ahead * a.D), ea, eb);
+                    else ring.fetch(slot_ahead, at_elem<QB>(v_ahead, (head_ahead - qn) * a.D), 16 * c, 16 * c + 8);
+                }
+                ring.close();
+                slot_ahead = (slot_ahead + 1) % kAppSlots;
+                if (step(row_ahead, head_ahead) && row_ahead < n) rows_ahead(row_ahead);
+            };
 #pragma unroll
-            for (int s = 0; s < kAppSlots - 1; ++s) {
-                fetch(row_ahead, head_ahead, s);
-                step(row_ahead, head_ahead);
-            }
+            for (int s = 0; s < kAppSlots - 1; ++s) fetch_ahead();
             Turn16 turn;
-            for (int slot = 0; row < n; step(row, head), slot = (slot + 1) % kAppSlots) {
-                fetch(row_ahead, head_ahead, (slot + kAppSlots - 1) % kAppSlots);
-                step(row_ahead, head_ahead);
-                if (row != row_turn) {
-                    row_turn = row;
+            bool new_row = true;
+            for (int slot = 0; row < n; new_row = step(row, head), slot = (slot + 1) % kAppSlots) {
+                fetch_ahead();
+                if (new_row) {
                     F2 w[8];
                     load_weights16(a.q_weight, ea, eb, w);
                     const float4* cs = s_cs + size_t(row) * (a.rotary / 4);
                     if (a.pairs) make_turn16<true>(turn, cs, c, rchunks, w);
                     else make_turn16<false>(turn, cs, c, rchunks, w);
+                    q_to = const_cast<char*>(at_elem<QB>(a.q_out, ((long long)(r0 + row) * a.Hq + q0) * a.D));
+                    const int t = t0 + row, blk = t / a.bs, page = s_page[blk - blk0];
+                    v_to = page < 0 ? nullptr
+                                    : const_cast<char*>(at_elem<KB>(
+                                          a.v_pages, (((long long)page * a.Hkv + kv0) * a.bs + t - blk * a.bs) * a.D));
                 }
                 ring.wait();
                 const Raw16<QB> raw = ring.item(slot);
                 if (head >= qn) {
-                    store_value(raw, row, kv0 + head - qn, c);
+                    if (v_to != nullptr)
+                        store_raw(raw, const_cast<char*>(at_elem<KB>(v_to, (long long)(head - qn) * a.bs * a.D)), c);
                     continue;
                 }
                 float f[16];
@@ -625,7 +640,7 @@ __global__ void __launch_bounds__(kAppThreads, 2) append_kernel(AppendArgs a)
                     f[2 * i] = x[i].f.x;
                     f[2 * i + 1] = x[i].f.y;
                 }
-                store16<QB>(const_cast<char*>(at_elem<QB>(a.q_out, ((long long)(r0 + row) * a.Hq + q0 + head) * a.D)), ea, eb, f);
+                store16<QB>(const_cast<char*>(at_elem<QB>(q_to, head * a.D)), ea, eb, f);
             }
             return;
         }

@@ -33,10 +33,11 @@ def rotate_axes(x, angle, pairing):
 
 def norm_bound(exact, mag, dtype):
     """A sum of squares is two chains of 8 products, one addition and at most three exchanges: 12
-    roundings, U each of a sum of positive terms, which the root halves; the mean, eps, the root and
-    the reciprocal add a rounding each, then two products: 12 / 2 + 4 + 2 = 12 U of a normed
-    channel.  The rotation adds 5 U of |x_a| + |x_b| (draft_reference.rotation_bound); 20 U cover both
-    with their products.  Then the rounding to the stored type."""
+    roundings, U each of a sum of positive terms, which the root halves; the mean and eps add a rounding
+    each, the reciprocal root two units in the last place, 4 U, then come two products:
+    12 / 2 + 2 + 4 + 2 = 14 U of a normed channel.  The rotation adds 5 U of |x_a| + |x_b|
+    (draft_reference.rotation_bound); 20 U cover both with their products.  Then the rounding to the
+    stored type."""
     delta = 20 * U * mag
     return delta + half_step(dtype) * (exact.abs() + delta)
 
