@@ -59,22 +59,26 @@ struct TreeArgs {
     // The kernels' EXT form (sa_shared.cu, sa_weigh.cu): a launch of its own joins the shares, so (m, l, o) are
     // left as they are, those of items in one part in row_m, row_l and `out`.  Only a kTreeAll item in one
     // part is done with.
-    int pass;                  // kTreeAll, kTreePrefix or kTreeOwn
+    int pass;                  // kTreeAll, kTreePrefix, kTreeOwn or kTreeBoth
     int tensor;                // the tensor-core kernel's shares: relative to the rounded product of maximum and scale
-    int seqs;                  // sequences of the batch (B: units / Hkv, groups in the prefix pass)
+    int seqs, groups;          // sequences of the batch, groups that share prefixes (B: units / Hkv)
     const int32_t *cu_seqs, *prefix_lens;
     int32_t *seq_prefix, *seq_group;     // [seqs]: shared tokens (-1: inactive) and group, by the prefix pass
     float *row_m, *row_l;      // [seqs * Q * Hq]: unscaled maximum and sum of rows in one part
     float2* stats;             // [seqs * Q * Hq]: kTreeAll: maximum and 1 / total of rows that are done
     float* scores;             // [unit][R][score_stride] unscaled scores, null: not kept
     long long score_stride;
+    // kTreeBoth: where the own tokens' items go (the prefixes' to out, row_m, row_l, item_parts)
+    float *own_out, *own_row_m, *own_row_l;
+    int2* own_item_parts;
 };
 
 // What the units of an EXT launch are.
 enum {
     kTreeAll = 0,              // (sequence, KV head): its whole context and its drafts
     kTreePrefix = 1,           // (group, KV head): the group's shared tokens, all its members' rows
-    kTreeOwn = 2               // (sequence, KV head): the context behind the shared tokens, and the drafts
+    kTreeOwn = 2,              // (sequence, KV head): the context behind the shared tokens, and the drafts
+    kTreeBoth = 3              // the units of both, groups first
 };
 
 // The list of a unit.
@@ -90,20 +94,41 @@ struct TreeUnit {
     int from;         // tokens below it are not the unit's
     int first_blk;    // block of entry 0
     int drafts;       // drafts behind the context
+    bool prefix;      // a group's shared tokens
 };
+
+// Shared tokens (-1: inactive) and group of sequence b.
+__device__ __forceinline__ int2 tree_sequence(const TreeArgs& a, int b)
+{
+    int lo = 0, hi = a.groups;                               // the last group that begins at b or before
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.cu_seqs[mid] <= b) lo = mid;
+        else hi = mid;
+    }
+    const int b0 = a.cu_seqs[lo], b1 = a.cu_seqs[lo + 1];
+    const int len = a.seq_lens != nullptr ? a.seq_lens[b] : a.N;
+    const int n = b >= b0 && b < b1 ? a.prefix_lens[lo] : 0;
+    bool bad = len < -1 || len > a.N;
+    if (b >= b0 && b < b1) bad = bad || b0 < 0 || b1 > a.seqs || n < 0 || (len >= 0 && n > len);
+    if (bad) raise_error(a.err, SPARSE_ATTN_ERR_LENGTH);
+    return make_int2(bad || len < 0 ? -1 : n, lo);
+}
 
 // The unit of a launch that EXT gives other units, from the arrays that say so.
 __device__ __forceinline__ TreeUnit tree_unit_ext(const TreeArgs& a, int u)
 {
     TreeUnit t;
-    const int x = u / a.Hkv;
+    int x = u / a.Hkv;
     t.len = -1;
     t.n_ctx = t.n_entries = t.draft_blk = 0;
+    t.prefix = a.pass == kTreePrefix || (a.pass == kTreeBoth && x < a.groups);
+    if (a.pass == kTreeBoth && !t.prefix) x -= a.groups;
     t.b0 = t.table_row = x;
     t.rows = a.R;
     t.from = t.first_blk = 0;
     t.drafts = a.Q;
-    if (a.pass == kTreePrefix) {
+    if (t.prefix) {
         const int b0 = a.cu_seqs[x], b1 = a.cu_seqs[x + 1], n = a.prefix_lens[x];
         if (b0 < 0 || b1 < b0 || b1 > a.seqs || n < 0 || n > a.N) {
             raise_error(a.err, SPARSE_ATTN_ERR_LENGTH);
@@ -124,9 +149,9 @@ __device__ __forceinline__ TreeUnit tree_unit_ext(const TreeArgs& a, int u)
         return t;
     }
     const int len = a.seq_lens != nullptr ? a.seq_lens[x] : a.N;
-    if (a.pass == kTreeOwn) {
-        const int p = a.seq_prefix[x];
-        if (p < 0) return t;                                 // the prefix pass has said why
+    if (a.pass != kTreeAll) {
+        const int p = a.pass == kTreeOwn ? a.seq_prefix[x] : tree_sequence(a, x).x;
+        if (p < 0) return t;                                 // reported where it was found
         t.from = p;
         t.first_blk = p >> a.bs_shift;
     } else if (len < 0 || len > a.N) {
@@ -451,13 +476,15 @@ __device__ __forceinline__ void tree_note_parts(const TreeArgs& a, int item, int
 }
 
 // An EXT row of an item in one part.
-__device__ __forceinline__ void tree_note_row(const TreeArgs& a, long long row, bool done, float m, float l, float inv)
+__device__ __forceinline__ void tree_note_row(const TreeArgs& a, const TreeUnit& un, long long row, bool done, float m,
+                                              float l, float inv)
 {
     if (done) {
         a.stats[row] = make_float2(m, inv);
     } else {
-        a.row_m[row] = m;
-        a.row_l[row] = l;
+        const bool own = a.pass == kTreeBoth && !un.prefix;
+        (own ? a.own_row_m : a.row_m)[row] = m;
+        (own ? a.own_row_l : a.row_l)[row] = l;
     }
 }
 
@@ -470,17 +497,18 @@ __device__ __forceinline__ int2 tree_parts(int start, int tiles, int per)
 
 // Where the parts of row group rg of an EXT unit are noted: row groups of one KV head in the order of
 // their rows, a group of sequences beginning with one of its own.
-__host__ __device__ __forceinline__ long long tree_notes_per_head(const TreeArgs& a, int item_rows)
+__host__ __device__ __forceinline__ long long tree_notes_per_head(const TreeArgs& a, bool prefix, int item_rows)
 {
-    return a.pass == kTreePrefix ? (long long)a.seqs * a.R / item_rows + a.B + 1
-                                 : (long long)a.seqs * ((a.R + item_rows - 1) / item_rows);
+    return prefix ? (long long)a.seqs * a.R / item_rows + a.groups + 1
+                  : (long long)a.seqs * ((a.R + item_rows - 1) / item_rows);
 }
-__device__ __forceinline__ long long tree_note_at(const TreeArgs& a, int u, const TreeUnit& un, int rg)
+__device__ __forceinline__ int2& tree_note(const TreeArgs& a, int u, const TreeUnit& un, int rg)
 {
     const int x = u / a.Hkv, kvh = u - x * a.Hkv;
-    const long long first = a.pass == kTreePrefix ? (long long)un.b0 * a.R / a.item_rows + x
-                                                  : (long long)x * a.row_groups;
-    return kvh * tree_notes_per_head(a, a.item_rows) + first + rg;
+    const long long first = un.prefix ? (long long)un.b0 * a.R / a.item_rows + x
+                                      : (long long)un.b0 * ((a.R + a.item_rows - 1) / a.item_rows);
+    int2* notes = a.pass == kTreeBoth && !un.prefix ? a.own_item_parts : a.item_parts;
+    return notes[kvh * tree_notes_per_head(a, un.prefix, a.item_rows) + first + rg];
 }
 
 // The weight of a share with maximum m and total l among shares whose largest maximum is M.  One that saw
@@ -494,22 +522,11 @@ __device__ __forceinline__ float tree_share(float m, float M, float l, float sca
 // -1 where it is inactive.  By the last CTAs, which have the least to do when work is short.
 __device__ __forceinline__ void tree_note_sequences(const TreeArgs& a, int threads)
 {
-    if (a.pass != kTreePrefix) return;
+    if (a.pass != kTreePrefix && a.pass != kTreeBoth) return;
     for (int b = (gridDim.x - 1 - blockIdx.x) * threads + threadIdx.x; b < a.seqs; b += gridDim.x * threads) {
-        int lo = 0, hi = a.B;                                // the last group that begins at b or before
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (a.cu_seqs[mid] <= b) lo = mid;
-            else hi = mid;
-        }
-        const int b0 = a.cu_seqs[lo], b1 = a.cu_seqs[lo + 1];
-        const int len = a.seq_lens != nullptr ? a.seq_lens[b] : a.N;
-        int n = b >= b0 && b < b1 ? a.prefix_lens[lo] : 0;
-        bool bad = len < -1 || len > a.N;
-        if (b >= b0 && b < b1) bad = bad || b0 < 0 || b1 > a.seqs || n < 0 || (len >= 0 && n > len);
-        if (bad) raise_error(a.err, SPARSE_ATTN_ERR_LENGTH);
-        a.seq_prefix[b] = bad || len < 0 ? -1 : n;
-        a.seq_group[b] = lo;
+        const int2 of = tree_sequence(a, b);
+        a.seq_prefix[b] = of.x;
+        a.seq_group[b] = of.y;
     }
 }
 
@@ -634,6 +651,8 @@ inline bool tree_ext_tensor(int pass, bool bf16, int rows, long long tiles)
 {
     return bf16 && rows > (pass == kTreePrefix ? 16 : 32) && tiles > kTreeSmallWork * 152;
 }
+// Query rows of its items otherwise.
+inline int tree_ext_item_rows(bool bf16, int rows) { return rows <= 16 ? 16 : (bf16 && rows <= 32 ? 32 : 64); }
 inline cudaError_t launch_tree_ext(TreeArgs& a, bool kv_bf16, int rows, long long tiles, cudaStream_t s)
 {
     if (tree_ext_tensor(a.pass, kv_bf16 && a.q_bf16, rows, tiles)) return launch_tree_tc_ext(a, rows, s);

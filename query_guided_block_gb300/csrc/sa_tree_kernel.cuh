@@ -486,6 +486,7 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
             l_run[h] += __shfl_xor_sync(kFullMask, l_run[h], 1);
             l_run[h] += __shfl_xor_sync(kFullMask, l_run[h], 2);
         }
+        float* out = EXT && a.pass == kTreeBoth && !un.prefix ? a.own_out : a.out;
         const bool complete = t0 == 0 && t1 == tiles, done = complete && (!EXT || a.pass == kTreeAll);
         const long long slot = (long long)tree_slot(blockIdx.x, part.per, start) * a.item_rows;
         if constexpr (TW == 1) {
@@ -494,7 +495,7 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
                 const int r = h ? r_hi : r_lo, rr = r - row0;
                 if (r >= R) continue;
                 const float inv = done ? (l_run[h] == 0.f ? 0.f : 1.f / l_run[h]) : 1.f;
-                float* dst = (complete ? a.out + tree_out_row(a, b, kvh, r) * D : a.part_o + (slot + rr) * D) + 2 * t4;
+                float* dst = (complete ? out + tree_out_row(a, b, kvh, r) * D : a.part_o + (slot + rr) * D) + 2 * t4;
 #pragma unroll
                 for (int j = 0; j < DT; ++j)
                     *reinterpret_cast<float2*>(dst + j * 8) = make_float2(acc[j][2 * h] * inv, acc[j][2 * h + 1] * inv);
@@ -502,7 +503,7 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
                     a.part_m[slot + rr] = m_run[h];
                     a.part_l[slot + rr] = l_run[h];
                 }
-                if (EXT && complete && t4 == 0) tree_note_row(a, tree_out_row(a, b, kvh, r), done, m_run[h], l_run[h], inv);
+                if (EXT && complete && t4 == 0) tree_note_row(a, un, tree_out_row(a, b, kvh, r), done, m_run[h], l_run[h], inv);
             }
         } else {
             // the warps' token shares of the same rows, through the freed stages
@@ -542,17 +543,17 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
                     num.w = fmaf(o.w, wgt, num.w);
                 }
                 const float inv = done ? (den == 0.f ? 0.f : 1.f / den) : 1.f;
-                float* dst = complete ? a.out + tree_out_row(a, b, kvh, row0 + rr) * D : a.part_o + (slot + rr) * D;
+                float* dst = complete ? out + tree_out_row(a, b, kvh, row0 + rr) * D : a.part_o + (slot + rr) * D;
                 *reinterpret_cast<float4*>(dst + d) = make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
                 if (!complete && d == 0) {
                     a.part_m[slot + rr] = M;
                     a.part_l[slot + rr] = den;
                 }
-                if (EXT && complete && d == 0) tree_note_row(a, tree_out_row(a, b, kvh, row0 + rr), done, M, den, inv);
+                if (EXT && complete && d == 0) tree_note_row(a, un, tree_out_row(a, b, kvh, row0 + rr), done, M, den, inv);
             }
         }
         if constexpr (EXT) {
-            if (tid == 0 && t0 == 0) a.item_parts[tree_note_at(a, u, un, rg)] = tree_parts(start, tiles, part.per);
+            if (tid == 0 && t0 == 0) tree_note(a, u, un, rg) = tree_parts(start, tiles, part.per);
         } else if (a.combine) {
             if (tid == 0 && t0 == 0) tree_note_parts(a, item, start, tiles, part.per);
         } else if (!complete) {
@@ -583,7 +584,8 @@ cudaError_t launch_tree_ext_t(TreeArgs& a, cudaStream_t s)
     a.item_rows = 16 * RW;
     a.min_per = 2;
     a.half_slack = 4;
-    a.row_groups = int(((a.pass == kTreePrefix ? a.seqs : 1LL) * a.R + a.item_rows - 1) / a.item_rows);
+    const bool prefixes = a.pass == kTreePrefix || a.pass == kTreeBoth;
+    a.row_groups = int(((prefixes ? a.seqs : 1LL) * a.R + a.item_rows - 1) / a.item_rows);
     int ctas = num_sms() * (2 * (smem + 10 * 1024) <= size_t(kSmemPerSm) ? 2 : 1);
     if (ctas > kTreeMaxCtas) ctas = kTreeMaxCtas;
     return launch_after_previous(tree_kernel<D, KB, NQ, RW, true>, dim3(unsigned(ctas)), dim3(kTrThreads), smem, s, a);

@@ -251,7 +251,7 @@ __device__ __forceinline__ void tc_store_rows(const TreeArgs& a, const TreePart&
     }
     if constexpr (EXT) {
         if (tid == 0 && g.t0 == 0)
-            a.item_parts[tree_note_at(a, g.u, g.un, g.row0 / a.item_rows)] = tree_parts(g.start, g.tiles, part.per);
+            tree_note(a, g.u, g.un, g.row0 / a.item_rows) = tree_parts(g.start, g.tiles, part.per);
     } else if (a.combine) {
         if (tid == 0 && g.t0 == 0) tree_note_parts(a, g.item, g.start, g.tiles, part.per);
     } else if (!complete) {
@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (complete) {
                     // 1 / total relative to the maximum itself, as the weights are computed from it
                     const float exact = share_weight(true, m_acc, m_acc, l, a.scale_log2);
-                    tree_note_row(a, tree_out_row(a, g.b, g.kvh, r_unit), done, m_acc, l, exact == 0.f ? 0.f : w / exact);
+                    tree_note_row(a, g.un, tree_out_row(a, g.b, g.kvh, r_unit), done, m_acc, l, exact == 0.f ? 0.f : w / exact);
                 } else {
                     const long long slot = (long long)tree_slot(blockIdx.x, part.per, g.start) * a.item_rows + row;
                     a.part_m[slot] = m_acc;
