@@ -4,6 +4,7 @@
 // over the prefix, the sequence's own context and the drafts it sees.  Sums over parts of the tokens
 // add up once they are relative to one maximum, so the prefix is one launch, in which all the
 // members' query rows are rows of one item, the own tokens are another, and a third joins the shares (m, l, o).
+// Where neither needs the tensor-core kernel, prefixes and own tokens are one launch.
 //
 // The launches are the EXT form of the draft-tree kernels (sa_tree_kernel.cuh).
 #include "sa_tree_join.cuh"

@@ -116,7 +116,10 @@ CASES = {
     "fp32_64_block_128": (Case(batch=2, lens=(300, 299), dtype=F32, kv=F32, dim=64, block=128), 130, dict(sinks=3)),
     "no_box": (Case(batch=2, lens=(300, 299)), 77, dict(box=False)),
     "heads": (Case(batch=3, lens=(300, 299, 280), hq=8, hkv=8, dim=64), 77, {}),
-    "two_ctas": (Case(batch=1, lens=(5001,), context=5001, hq=1, hkv=1, dim=64), 1500, dict(sinks=4, recent=64)),
+    "one_cta": (Case(batch=1, lens=(5001,), context=5001, hq=1, hkv=1, dim=64), 1500, dict(sinks=4, recent=64)),
+    "two_ctas": (Case(batch=60, lens=(17001,) + (-1,) * 59, context=17001, hq=1, hkv=1, dim=64, block=128), 1500,
+                 dict(sinks=4, recent=64)),
+    "four_ctas": (Case(batch=1, lens=(17001,), context=17001, hq=1, hkv=1, dim=64, block=64), 1500, dict(kind="ties")),
     "eight_ctas": (Case(batch=1, lens=(40001,), context=40001, hq=1, hkv=1, dim=64, block=64), 5000, dict(kind="ties")),
     "eight_ctas_short": (Case(batch=2, lens=(40000, 700), context=40001, hq=1, hkv=1, dim=64, block=64), 500, {}),
     "many_units": (Case(batch=90, lens=tuple(200 + 3 * i for i in range(90)), context=500, hq=2, hkv=2, dim=64), 150, {}),
