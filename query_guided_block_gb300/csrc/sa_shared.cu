@@ -164,8 +164,9 @@ cudaError_t launch_shared(const Geometry& g, const TreeCall& c, int groups, cons
     const int pre_rows = int(rows < 1024 ? rows : 1024);
     const long long pre_tiles = tiles * groups * g.Hkv * ((rows + 15) / 16), own_tiles = tiles * g.units() * ((own.R + 15) / 16);
     const bool bf16 = g.kv_bf16 && g.q_bf16;
-    if (!tree_ext_tensor(kTreePrefix, bf16, pre_rows, pre_tiles) && !tree_ext_tensor(kTreeOwn, bf16, own.R, own_tiles) &&
-        (bf16 || tree_ext_item_rows(bf16, pre_rows) == tree_ext_item_rows(bf16, own.R))) {
+    const bool pre_tensor = tree_ext_tensor(kTreePrefix, bf16, pre_rows, pre_tiles);
+    const bool own_tensor = tree_ext_tensor(kTreeOwn, bf16, own.R, own_tiles);
+    if (!pre_tensor && !own_tensor && (bf16 || tree_ext_item_rows(bf16, pre_rows) == tree_ext_item_rows(bf16, own.R))) {
         // Both kinds on one line of work, in items of the own rows' size (more rows of bf16 are then few tiles):
         // 4 samples of a 777-token prompt 16.3 us, two launches 25.
         pre.pass = kTreeBoth;
@@ -174,7 +175,7 @@ cudaError_t launch_shared(const Geometry& g, const TreeCall& c, int groups, cons
         pre.own_row_m = own.row_m;
         pre.own_row_l = own.row_l;
         pre.own_item_parts = own.item_parts;
-        const cudaError_t e = launch_tree_ext(pre, g.kv_bf16, own.R, 0, s);
+        const cudaError_t e = launch_tree_ext(pre, g.kv_bf16, own.R, false, s);
         if (e != cudaSuccess) return e;
         own.part_m = pre.part_m;
         own.part_l = pre.part_l;
@@ -183,8 +184,8 @@ cudaError_t launch_shared(const Geometry& g, const TreeCall& c, int groups, cons
         own.row_groups = (own.R + own.item_rows - 1) / own.item_rows;
         return launch_tree_join(own, &pre, nullptr, s);
     }
-    cudaError_t e = launch_tree_ext(pre, g.kv_bf16, pre_rows, pre_tiles, s);
-    if (e == cudaSuccess) e = launch_tree_ext(own, g.kv_bf16, own.R, own_tiles, s);
+    cudaError_t e = launch_tree_ext(pre, g.kv_bf16, pre_rows, pre_tensor, s);
+    if (e == cudaSuccess) e = launch_tree_ext(own, g.kv_bf16, own.R, own_tensor, s);
     return e == cudaSuccess ? launch_tree_join(own, &pre, nullptr, s) : e;
 }
 

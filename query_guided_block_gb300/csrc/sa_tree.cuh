@@ -653,9 +653,9 @@ inline bool tree_ext_tensor(int pass, bool bf16, int rows, long long tiles)
 }
 // Query rows of its items otherwise.
 inline int tree_ext_item_rows(bool bf16, int rows) { return rows <= 16 ? 16 : (bf16 && rows <= 32 ? 32 : 64); }
-inline cudaError_t launch_tree_ext(TreeArgs& a, bool kv_bf16, int rows, long long tiles, cudaStream_t s)
+inline cudaError_t launch_tree_ext(TreeArgs& a, bool kv_bf16, int rows, bool tensor, cudaStream_t s)
 {
-    if (tree_ext_tensor(a.pass, kv_bf16 && a.q_bf16, rows, tiles)) return launch_tree_tc_ext(a, rows, s);
+    if (tensor) return launch_tree_tc_ext(a, rows, s);
     return a.D == 128 ? launch_tree_ext128(a, kv_bf16, rows, s) : launch_tree_ext64(a, kv_bf16, rows, s);
 }
 

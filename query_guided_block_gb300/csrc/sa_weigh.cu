@@ -154,10 +154,20 @@ long long weigh_tiles(const Geometry& g, long long tokens)
     return (long long)g.units() * ((g.Q * g.G + 15) / 16) * ((tokens + kTreeLeastTile - 1) / kTreeLeastTile);
 }
 
-// Scores are kept where the tensor-core kernels do not run.
+size_t weigh_scores(const Geometry& g, long long tokens)     // bytes
+{
+    return size_t(g.units()) * g.Q * g.G * size_t((tokens + kTreeLeastTile - 1) / kTreeLeastTile * kTreeLeastTile) * sizeof(float);
+}
+
+// Scores are kept where the tensor-core kernels do not run.  Those also take 17 to 32 rows of bf16 whose scores
+// would be more than this, which costs a few percent (see tree_ext_tensor).
+constexpr size_t kWgMostScores = size_t(256) << 20;
 bool weigh_tensor(const Geometry& g, long long tokens)
 {
-    return tree_ext_tensor(kTreeAll, g.kv_bf16 && g.q_bf16, g.Q * g.G, weigh_tiles(g, tokens));
+    const bool bf16 = g.kv_bf16 && g.q_bf16;
+    const int rows = g.Q * g.G;
+    return tree_ext_tensor(kTreeAll, bf16, rows, weigh_tiles(g, tokens)) ||
+           (bf16 && rows > 16 && rows <= 32 && weigh_scores(g, tokens) > kWgMostScores);
 }
 
 WeighLayout weigh_layout(const Geometry& g, long long tokens)
@@ -167,10 +177,10 @@ WeighLayout weigh_layout(const Geometry& g, long long tokens)
     L.stride = (tokens + kTreeLeastTile - 1) / kTreeLeastTile * kTreeLeastTile;   // whole tiles are written
     L.stats = L.own.end;
     L.scores = align256(L.stats + size_t(g.B) * g.Q * g.Hq * sizeof(float2));
-    size_t kept = size_t(g.units()) * g.Q * g.G * size_t(L.stride);
-    // with more tokens than these tiles hold none are kept: then room for any fewer
-    if (weigh_tensor(g, tokens)) kept = size_t(kTreeSmallWork) * 152 * kTreeLeastTile * 16;
-    L.end = align256(L.scores + kept * sizeof(float));
+    size_t kept = weigh_scores(g, tokens);
+    // with more tokens than that none are kept: then room for any fewer
+    if (weigh_tensor(g, tokens)) kept = g.Q * g.G <= 32 ? kWgMostScores : size_t(kTreeSmallWork) * 152 * kTreeLeastTile * 16 * sizeof(float);
+    L.end = align256(L.scores + kept);
     return L;
 }
 
@@ -191,7 +201,7 @@ cudaError_t launch_weigh(const Geometry& g, const TreeCall& c, float* weights, c
         a.scores = reinterpret_cast<float*>(ws + L.scores);
         a.score_stride = L.stride;
     }
-    cudaError_t e = launch_tree_ext(a, g.kv_bf16, a.R, weigh_tiles(g, tokens), s);
+    cudaError_t e = launch_tree_ext(a, g.kv_bf16, a.R, tensor, s);
     if (e != cudaSuccess) return e;
     long long chunks = (tokens + kWgTokens - 1) / kWgTokens;
     const long long most = (8LL * num_sms() + g.units() - 1) / g.units() * 4;   // more would only start and end

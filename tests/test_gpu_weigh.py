@@ -164,3 +164,32 @@ def test_bad_lengths_are_reported():
     B.sparse_attn_weigh_decode(p, q, *pools, table.cuda(), w, out, ws, seq_lens=int32([150, 171, -7]))
     assert B.sparse_attn_get_device_error(ws) == B.ERR_LENGTH
     assert (out[1:] == 5.0).all() and (w[1:] == 0).all() and (w[0] != 0).any()
+
+
+def test_long_contexts_of_some_rows_keep_no_scores():
+    """32 rows over so many tokens that their scores would be over 256 MB are computed again; the rows' weights add up
+    to one, and sampled units agree with 64 bits."""
+    c = Case(batch=9, drafts=8, hq=32, hkv=8, context=33001, block=128)
+    p = c.params(num_pages=c.batch * c.nb_cap)
+    size = B.sparse_attn_weigh_workspace_size(p)
+    assert 256 << 20 < size < 400 << 20
+    assert size >= B.sparse_attn_weigh_workspace_size(c.params(n_tokens=2000, capacity_tokens=2008))
+    g = torch.Generator(device="cuda").manual_seed(1)
+    pools = [torch.randn(c.batch * c.nb_cap, c.hkv, c.block, c.dim, generator=g, device="cuda", dtype=BF) for _ in range(2)]
+    table = torch.randperm(c.batch * c.nb_cap, generator=g, device="cuda").to(torch.int32).view(c.batch, -1)
+    q = torch.randn(c.batch, c.drafts, c.hq, c.dim, generator=g, device="cuda", dtype=BF)
+    ws = workspace(size)
+    w, out = torch.zeros(c.batch, c.hkv, c.nb_cap * c.block, device="cuda"), torch.empty(q.shape, device="cuda")
+    B.sparse_attn_weigh_decode(p, q, *pools, table, w, out, ws)
+    assert B.sparse_attn_get_device_error(ws) == 0
+    assert ((w.double().sum(-1) - 32).abs() < 1e-3).all()
+    n = c.context + c.drafts
+    for b, h in ((0, 0), (4, 7), (8, 3)):
+        k, v = (x[table[b].long(), h].reshape(-1, c.dim)[:n].double() for x in pools)
+        s = q[b, :, 4 * h:4 * h + 4].double() @ k.t() * c.dim ** -0.5                    # [Q, G, tokens]
+        late = torch.arange(n, device="cuda") > c.context + torch.arange(c.drafts, device="cuda")[:, None]
+        prob = torch.softmax(s.masked_fill(late[:, None], -float("inf")), -1)
+        # score errors of 2^-18 (chains of 8 steps of magnitudes up to 40), twice, and the totals' chain
+        assert ((w[b, h, :n].double() - prob.sum((0, 1))).abs() <= 2.0 ** -15 * prob.sum((0, 1))).all()
+        err = (out[b, :, 4 * h:4 * h + 4].double() - prob @ v).abs()
+        assert (err <= 2.0 ** -15 * (prob @ v.abs())).all()
