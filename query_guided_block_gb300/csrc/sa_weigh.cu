@@ -80,8 +80,9 @@ __global__ void __launch_bounds__(kWgThreads) weigh_kernel(TreeArgs a, const flo
 
 // With few rows the join and the sums are one launch: the first CTAs are those of weigh_kernel, and find the
 // rows' maxima and totals from the shares by themselves (a warp a row, lane = share), the others join rows.
-// One token over 4096: 16.5 us, 18.8 in three launches.
-constexpr int kWgFew = 32;
+// One token over 4096: 16.5 us, 18.8 in three launches;
+// 32 rows over 32K tokens 87, 65 in three.
+constexpr int kWgFew = 8;
 
 template <int D, int WPR>
 __global__ void __launch_bounds__(kJoinThreads) weigh_join_kernel(const __grid_constant__ TreeArgs a, float* weights,
