@@ -339,7 +339,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 auto load = [&](uint32_t n, const void* map, int tile_index, uint32_t entries) {
                     const uint32_t st = n % SH::UNITS;
                     if (n >= SH::UNITS) wait(&sh.empty[st], (n / SH::UNITS - 1) & 1u);
-                    if (*reinterpret_cast<volatile int*>(&sh.dead) != 0) return;      // start no more copies
+                    // start no more copies; the warp decides together
+                    if (__any_sync(kFullMask, *reinterpret_cast<volatile int*>(&sh.dead) != 0)) return;
                     if (lane == 0) mbar_arrive_expect_tx(&sh.full[st], entries * uint32_t(a.bs * 128 * SH::HALVES));
                     __syncwarp();
                     if (lane < n_e && tile_index >= 0) {

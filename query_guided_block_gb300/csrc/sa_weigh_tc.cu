@@ -126,7 +126,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                     const uint32_t ok = __ballot_sync(kFullMask, lane < n_e && page >= 0);
                     const uint32_t n = tile0 + i, st = n % SH::STAGES;
                     if (n >= SH::STAGES) wait(&sh.empty[st], (n / SH::STAGES - 1) & 1u);
-                    if (*reinterpret_cast<volatile int*>(&sh.dead) != 0) continue;    // start no more copies
+                    // start no more copies; the warp decides together
+                    if (__any_sync(kFullMask, *reinterpret_cast<volatile int*>(&sh.dead) != 0)) continue;
                     if (lane == 0) {
                         sh.pages[n % SH::INFO] = ok;               // before the arrival that the sums wait for, through the product
                         mbar_arrive_expect_tx(&sh.full[st], __popc(ok) * uint32_t(a.bs * 128 * SH::HALVES));

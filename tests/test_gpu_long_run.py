@@ -216,3 +216,37 @@ def test_captured_steps_replay_as_the_contexts_grow(side):
     assert torch.equal(a.dec.weights, b.dec.weights) and torch.equal(a.dec.seq_lens, b.dec.seq_lens)
     assert torch.equal(a.k, b.k) and torch.equal(a.table, b.table) and torch.equal(a.dec.kept_ids, b.dec.kept_ids)
     assert a.dec.device_error() == 0 and b.dec.device_error() == 0
+
+
+def test_two_streams_at_once():
+    """Two caches, each with a workspace of its own, on two streams: the bits of one after the other."""
+    def work(w, rows, pos, new, stream):
+        outs = []
+        for _ in range(6):
+            q = w.append([Q] * BATCH, pos, rows=rows, stream=stream).view(BATCH, Q, HQ, D)
+            with torch.cuda.stream(stream):
+                outs.append(w.dec.decode_weighed(q, w.k, w.v, w.table, stream=stream).clone())
+                outs.append(w.dec.decode_shared(q, w.k, w.v, w.table, cuts, prefix, stream=stream).clone())
+        w.dec.evict(SINKS, RECENT, w.k, w.v, w.table, new, stream=stream)
+        return outs
+
+    cuts, prefix = int32([0, 1, 2, 3]), int32([40, 45, 3])
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for together in (False, True):
+        worlds = [World(seed=11, groups=3), World(seed=12, groups=3)]
+        made = []
+        for w in worlds:
+            w.k.normal_(generator=torch.Generator(device="cuda").manual_seed(8))
+            w.v.normal_(generator=torch.Generator(device="cuda").manual_seed(9))
+            made.append((w, w.rows(Q * BATCH), positions(LENS, [Q] * BATCH), w.pages(2)))
+        torch.cuda.synchronize()
+        outs = []
+        for m, s in zip(made, streams if together else [streams[0]] * 2):
+            outs.append(work(*m, s))
+            if not together:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        got.append([x for o in outs for x in o] + [y for w in worlds for y in (w.dec.weights, w.k, w.v, w.dec.kept_ids, w.table)])
+        assert all(w.dec.device_error() == 0 for w in worlds)
+    assert all(torch.equal(x, y) for x, y in zip(*got))
