@@ -25,6 +25,7 @@
  * Long contexts:
  *
  *   sparse_attn_append_kv_norm  the append, with head norms and positions of several axes.
+ *   sparse_attn_append_kv_weights  that, and the new tokens' attention weights set to 0.
  *   sparse_attn_shared_decode   attention of a batch whose sequences share prefixes.
  *   sparse_attn_weigh_decode    attention that adds up every cached token's weight.
  *   sparse_attn_evict_tokens    the tokens with the largest weights kept, in new pages.
@@ -448,6 +449,21 @@ int sparse_attn_append_kv_norm(const sparse_attn_params* p, int32_t num_rows, co
                                void* q_out, void* k_pages, void* v_pages, const int32_t* block_table,
                                void* kmin, void* kmax, void* ws, size_t ws_bytes, sparse_attn_stream stream);
 
+/* sparse_attn_append_kv_norm that also sets the new tokens' entries of `weights` (device float
+ * [B, Hkv, nb_cap * block_size], 16-byte aligned: what sparse_attn_weigh_decode adds to) to 0, in the
+ * same launch.  Entries hold the sums of whatever tokens were at their index before (evicted, taken
+ * back, of another request): a token that comes in without being weighed has to start at 0.  NULL: no
+ * entry is written. */
+int sparse_attn_append_kv_weights(const sparse_attn_params* p, int32_t num_rows, const int32_t* cu_rows,
+                                  const int32_t* seq_lens, const int32_t* positions, int32_t num_axes,
+                                  const int32_t* axis_of, int32_t rotary_dim, int32_t pairing, const double* inv_freq,
+                                  const float* q_weight, int64_t q_weight_stride, const float* k_weight,
+                                  int64_t k_weight_stride, float eps, const void* q_new, int64_t q_stride,
+                                  const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,
+                                  void* q_out, void* k_pages, void* v_pages, const int32_t* block_table,
+                                  void* kmin, void* kmax, float* weights, void* ws, size_t ws_bytes,
+                                  sparse_attn_stream stream);
+
 /* Workspace of sparse_attn_tree_decode for this problem (it also serves
  * sparse_attn_append_kv and sparse_attn_commit_drafts, which use its first 256 bytes);
  * independent of n_tokens, so one workspace serves a growing context.  A workspace large
@@ -528,7 +544,7 @@ int sparse_attn_weigh_workspace_size(const sparse_attn_params* p, size_t* bytes)
  * of every token: weights, device float [B, Hkv, nb_cap * block_size], 16-byte aligned,
  *   weights[b][kvh][t] += sum over the Q x G query rows of the KV head of softmax_t  for t < seq_lens[b];
  * the Q new tokens' entries are set to that sum (whatever they held), entries behind them are left
- * alone.  With Q = 1 a decode step; with the last Q tokens of a prompt as queries the weights by which
+ * alone.  Tokens that were never weighed start at the caller's 0 (sparse_attn_append_kv_weights).  With Q = 1 a decode step; with the last Q tokens of a prompt as queries the weights by which
  * its first eviction may go.  All tokens must be finite.  The sums do not depend on timing. */
 int sparse_attn_weigh_decode(const sparse_attn_params* p, const void* q, const void* k_pages, const void* v_pages,
                              const int32_t* block_table, const int32_t* seq_lens, float* weights, float* out, void* ws,
@@ -545,8 +561,9 @@ int sparse_attn_evict_workspace_size(const sparse_attn_params* p, int32_t keep_t
  *   among equals.
  *   Kept tokens stay in their order: the i-th one's K and V go to page new_table[b][i / block_size]
  *   (device int32 [B, ceil(keep_tokens / block_size)]) at i % block_size, its weight to
- *   weights[b][kvh][i], its index to kept_ids[b][kvh][i] (device int32 [B, Hkv, keep_tokens]; entries
- *   behind the kept ones are left alone).  new_lens[b] = the number kept (an inactive sequence keeps
+ *   weights[b][kvh][i], its index to kept_ids[b][kvh][i] (device int32 [B, Hkv, keep_tokens]).  Entries
+ *   behind the kept ones are left alone in both: those of `weights` still hold the sums of tokens that
+ *   are gone, and the tokens that come in at their indexes have to start at 0.  new_lens[b] = the number kept (an inactive sequence keeps
  *   -1, one left alone its length); new_lens must not overlap seq_lens or keep_lens.
  *   The new pages must not be pages that any sequence of the call reads, and belong to one sequence.
  *   kmin / kmax: both or neither; the rows of the new blocks become the box of their tokens.

@@ -115,6 +115,8 @@ def lib():
                                        vp, vp, vp, sz, vp], C.c_int),
             "sparse_attn_append_kv_norm": ([P, i32, vp, vp, vp, i32, vp, i32, i32, vp, vp, i64, vp, i64, C.c_float, vp, i64,
                                             vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, sz, vp], C.c_int),
+            "sparse_attn_append_kv_weights": ([P, i32, vp, vp, vp, i32, vp, i32, i32, vp, vp, i64, vp, i64, C.c_float, vp, i64,
+                                               vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp], C.c_int),
             "sparse_attn_tree_workspace_size": ([P, C.POINTER(C.c_size_t)], C.c_int),
             "sparse_attn_tree_decode": ([P, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp], C.c_int),
             "sparse_attn_commit_drafts": ([P, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp], C.c_int),
@@ -144,7 +146,7 @@ def exported_symbols():
             "sparse_attn_select_noalloc_device_error", "sparse_attn_workspace_set_wait_limit",
             "sparse_attn_decode_slots_io", "sparse_attn_diff_slots", "sparse_attn_append_kv",
             "sparse_attn_tree_workspace_size", "sparse_attn_tree_decode", "sparse_attn_commit_drafts",
-            "sparse_attn_append_kv_norm", "sparse_attn_shared_workspace_size", "sparse_attn_shared_decode",
+            "sparse_attn_append_kv_norm", "sparse_attn_append_kv_weights", "sparse_attn_shared_workspace_size", "sparse_attn_shared_decode",
             "sparse_attn_weigh_workspace_size", "sparse_attn_weigh_decode", "sparse_attn_evict_workspace_size",
             "sparse_attn_evict_tokens"]
 
@@ -501,10 +503,11 @@ def _norm_weight(t, device: int, what: str, heads: int, dim: int):
 
 def sparse_attn_append_kv_norm(p, q_new, k_new, v_new, q_weight, k_weight, eps, inv_freq, q_out, k_pages, v_pages,
                                block_table, ws, cu_rows=None, seq_lens=None, positions=None, axis_of=None,
-                               pairing=ROTATE_HALVES, kmin=None, kmax=None, stream=None) -> None:
+                               pairing=ROTATE_HALVES, kmin=None, kmax=None, stream=None, weights=None) -> None:
     """sparse_attn_append_kv with a norm of each head's queries and keys (q_weight, k_weight: float32
     [D] or [heads, D], or None for no norm) and positions of several axes: positions int32
-    [axes, rows] with axis_of int32 [rotary_dim / 2], or [rows] (or None) without it."""
+    [axes, rows] with axis_of int32 [rotary_dim / 2], or [rows] (or None) without it.  The new tokens'
+    entries of weights (as sparse_attn_weigh_decode has them), when given, become 0."""
     g, dev, rows = _shapes(p), _device_of(k_new, "k_new"), k_new.shape[0]
     kv_rows, q_rows, qt, kvt = (rows, g.kv_heads, g.dim), (rows, g.q_heads, g.dim), g.q_dtype, g.kv_dtype
     k, ks = _rows_ptr(k_new, dev, "k_new", kv_rows, qt)
@@ -524,7 +527,10 @@ def sparse_attn_append_kv_norm(p, q_new, k_new, v_new, q_weight, k_weight, eps, 
     if positions is not None:
         pos = _tensor_ptr(positions, dev, "positions", (rows,) if axis_of is None else (axes, rows), _I32)
     w, n = _workspace(ws, dev)
-    _launch_on(dev, "sparse_attn_append_kv_norm", stream, C.byref(p), rows,
+    name, tail = "sparse_attn_append_kv_norm", (w, n)
+    if weights is not None:
+        name, tail = "sparse_attn_append_kv_weights", (_tensor_ptr(weights, dev, "weights", g.weights, torch.float32), w, n)
+    _launch_on(dev, name, stream, C.byref(p), rows,
                None if cu_rows is None else _tensor_ptr(cu_rows, dev, "cu_rows", g.ends, _I32),
                None if seq_lens is None else _tensor_ptr(seq_lens, dev, "seq_lens", g.per_seq, _I32),
                pos, axes, axis, rotary, pairing, freq, qw, qws, kw, kws, eps, q, qs, k, ks, v, vs,
@@ -532,7 +538,7 @@ def sparse_attn_append_kv_norm(p, q_new, k_new, v_new, q_weight, k_weight, eps, 
                _tensor_ptr(k_pages, dev, "k_pages", g.pool, kvt), _tensor_ptr(v_pages, dev, "v_pages", g.pool, kvt),
                _tensor_ptr(block_table, dev, "block_table", g.table, _I32),
                None if kmin is None else _tensor_ptr(kmin, dev, "kmin", g.box, kvt),
-               None if kmax is None else _tensor_ptr(kmax, dev, "kmax", g.box, kvt), w, n)
+               None if kmax is None else _tensor_ptr(kmax, dev, "kmax", g.box, kvt), *tail)
 
 
 def sparse_attn_tree_workspace_size(p: sparse_attn_params) -> int:

@@ -600,7 +600,7 @@ static long long capacity_of(const sparse_attn_params* p)
     return p->capacity_tokens > 0 ? p->capacity_tokens : p->n_tokens;
 }
 
-// What sparse_attn_append_kv_norm has beyond sparse_attn_append_kv.
+// What sparse_attn_append_kv_weights has beyond sparse_attn_append_kv.
 struct AppendNorm {
     int32_t num_axes;
     const int32_t* axis_of;
@@ -609,6 +609,7 @@ struct AppendNorm {
     const float* k_weight;
     int64_t k_wstride;
     float eps;
+    float* weights;
 };
 
 static int append_common(const sparse_attn_params* p, int32_t num_rows, const int32_t* cu_rows,
@@ -635,7 +636,8 @@ static int append_common(const sparse_attn_params* p, int32_t num_rows, const in
     if ((x.q_weight || x.k_weight) && !(x.eps > 0.f && !isinf(x.eps))) return SPARSE_ATTN_INVALID_ARG;
     if (x.q_weight && !q_new) return SPARSE_ATTN_INVALID_ARG;
     if ((x.q_wstride != 0 && x.q_wstride != g.D) || (x.k_wstride != 0 && x.k_wstride != g.D)) return SPARSE_ATTN_INVALID_ARG;
-    if (!aligned(x.axis_of, 4) || !aligned(x.q_weight, 16) || !aligned(x.k_weight, 16)) return SPARSE_ATTN_INVALID_ARG;
+    if (!aligned(x.axis_of, 4) || !aligned(x.q_weight, 16) || !aligned(x.k_weight, 16) || !aligned(x.weights, 16))
+        return SPARSE_ATTN_INVALID_ARG;
     if (g.B == 0 || num_rows == 0) return SPARSE_ATTN_OK;
     const int per_seq = num_rows / g.B;
     if (!cu_rows && num_rows % g.B != 0) return SPARSE_ATTN_INVALID_ARG;
@@ -680,6 +682,7 @@ static int append_common(const sparse_attn_params* p, int32_t num_rows, const in
     c.eps = x.eps;
     c.num_axes = x.num_axes;
     c.axis_of = x.num_axes > 1 ? x.axis_of : nullptr;   // with one axis there is nothing to look up
+    c.weights = x.weights;
     return status_of(launch_append(g, c, static_cast<uint32_t*>(ws), reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -692,7 +695,7 @@ int sparse_attn_append_kv(const sparse_attn_params* p, int32_t num_rows, const i
 {
     return append_common(p, num_rows, cu_rows, seq_lens, positions, rotary_dim, pairing, inv_freq, q_new, q_stride, k_new,
                          k_stride, v_new, v_stride, q_out, k_pages, v_pages, block_table, kmin, kmax, ws, ws_bytes, stream,
-                         AppendNorm{1, nullptr, nullptr, 0, nullptr, 0, 0.f});
+                         AppendNorm{1, nullptr, nullptr, 0, nullptr, 0, 0.f, nullptr});
 }
 
 int sparse_attn_append_kv_norm(const sparse_attn_params* p, int32_t num_rows, const int32_t* cu_rows,
@@ -706,7 +709,22 @@ int sparse_attn_append_kv_norm(const sparse_attn_params* p, int32_t num_rows, co
 {
     return append_common(p, num_rows, cu_rows, seq_lens, positions, rotary_dim, pairing, inv_freq, q_new, q_stride, k_new,
                          k_stride, v_new, v_stride, q_out, k_pages, v_pages, block_table, kmin, kmax, ws, ws_bytes, stream,
-                         AppendNorm{num_axes, axis_of, q_weight, q_weight_stride, k_weight, k_weight_stride, eps});
+                         AppendNorm{num_axes, axis_of, q_weight, q_weight_stride, k_weight, k_weight_stride, eps, nullptr});
+}
+
+int sparse_attn_append_kv_weights(const sparse_attn_params* p, int32_t num_rows, const int32_t* cu_rows,
+                                  const int32_t* seq_lens, const int32_t* positions, int32_t num_axes,
+                                  const int32_t* axis_of, int32_t rotary_dim, int32_t pairing, const double* inv_freq,
+                                  const float* q_weight, int64_t q_weight_stride, const float* k_weight,
+                                  int64_t k_weight_stride, float eps, const void* q_new, int64_t q_stride,
+                                  const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,
+                                  void* q_out, void* k_pages, void* v_pages, const int32_t* block_table,
+                                  void* kmin, void* kmax, float* weights, void* ws, size_t ws_bytes,
+                                  sparse_attn_stream stream)
+{
+    return append_common(p, num_rows, cu_rows, seq_lens, positions, rotary_dim, pairing, inv_freq, q_new, q_stride, k_new,
+                         k_stride, v_new, v_stride, q_out, k_pages, v_pages, block_table, kmin, kmax, ws, ws_bytes, stream,
+                         AppendNorm{num_axes, axis_of, q_weight, q_weight_stride, k_weight, k_weight_stride, eps, weights});
 }
 
 int sparse_attn_tree_workspace_size(const sparse_attn_params* p, size_t* bytes)

@@ -60,6 +60,7 @@ struct AppendArgs {
     float eps;
     const int32_t* axis_of;              // [rotary / 2], null: one axis
     int num_axes;
+    float* weights;                      // [B, Hkv, nb_cap * bs], null: not written
 };
 
 // 16 channels of a row as fp32: 8 at `a`, 8 at `b` (16-byte aligned both).
@@ -421,6 +422,10 @@ __global__ void __launch_bounds__(kAppThreads, 2) append_kernel(AppendArgs a)
     const int n = t1 - t0;                                    // tokens [t0, t1)
     const int r0 = row0 + (t0 - len);                         // their first row
     const int blk0 = t0 / a.bs, blks = (t1 - 1) / a.bs - blk0 + 1;
+    if (a.weights != nullptr && blockIdx.y == 0) {            // a share of the heads has all heads' entries
+        float* w = a.weights + (long long)b * a.Hkv * a.nb_cap * a.bs + t0;
+        for (int i = tid; i < n * a.Hkv; i += kAppThreads) w[(long long)(i / n) * a.nb_cap * a.bs + i % n] = 0.f;
+    }
     if (tid < blks) {
         const int page = a.block_table[(long long)b * a.nb_cap + blk0 + tid];
         const bool ok = page >= 0 && page < a.num_pages;
@@ -886,6 +891,7 @@ cudaError_t launch_append(const Geometry& g, const AppendCall& c, uint32_t* err,
     a.eps = c.eps;
     a.axis_of = c.axis_of;
     a.num_axes = c.num_axes;
+    a.weights = c.weights;
     a.rotary = c.rotary_dim;
     a.pairs = c.pairing == SPARSE_ATTN_ROTATE_PAIRS;
     // n > 0 tokens touch at most (n - 2 + run) / run + 1 aligned runs

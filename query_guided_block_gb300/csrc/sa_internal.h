@@ -169,6 +169,7 @@ struct AppendCall {
     float eps;
     int num_axes;
     const int32_t* axis_of;
+    float* weights;              // the new tokens' entries become 0; null: not written
 };
 cudaError_t launch_append(const Geometry& g, const AppendCall& c, uint32_t* err, cudaStream_t s);
 cudaError_t launch_commit(const Geometry& g, const int32_t* seq_lens, const int32_t* path, int path_stride,

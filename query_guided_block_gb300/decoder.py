@@ -252,8 +252,9 @@ class LongContextDecoder(DraftDecoder):
     numbers besides.
 
     ``num_groups`` groups at most share prefixes (0: ``decode_shared`` is not used); with ``keep_tokens``
-    contexts are cut down to that many tokens (0: ``decode_weighed`` and ``evict`` are not used).  The weights
-    start at zero."""
+    contexts are cut down to that many tokens (0: ``decode_weighed`` and ``evict`` are not used).  Every token
+    that ``append`` or ``append_norm`` brings in has the weight zero until ``decode_weighed`` adds to it,
+    whatever was at its index before: an evicted token, a rejected draft, another request."""
 
     def __init__(self, params: B.sparse_attn_params, seq_lens: torch.Tensor, num_groups: int = 0, keep_tokens: int = 0):
         super().__init__(params, seq_lens)
@@ -271,9 +272,15 @@ class LongContextDecoder(DraftDecoder):
                 nb_cap = -(-max(p.capacity_tokens, p.n_tokens) // p.block_size)
                 self.weights = torch.zeros(p.batch, p.num_kv_heads, nb_cap * p.block_size, device=dev)
                 self.kept_ids = torch.full((p.batch, p.num_kv_heads, keep_tokens), -1, dtype=torch.int32, device=dev)
+                self._index = torch.arange(nb_cap * p.block_size, device=dev)
             if size > self.ws.numel():
                 self.ws = torch.empty(size, dtype=torch.uint8, device=dev)
                 B.sparse_attn_workspace_init(self.ws)
+
+    def append(self, q_new, k_new, v_new, inv_freq, q_out, k_pages, v_pages, block_table, cu_rows=None,
+               positions=None, pairing=B.ROTATE_HALVES, kmin=None, kmax=None, stream=None):
+        self.append_norm(q_new, k_new, v_new, None, None, 0.0, inv_freq, q_out, k_pages, v_pages, block_table, cu_rows,
+                         positions, None, pairing, kmin, kmax, stream)
 
     def append_norm(self, q_new, k_new, v_new, q_weight, k_weight, eps, inv_freq, q_out, k_pages, v_pages, block_table,
                     cu_rows=None, positions=None, axis_of=None, pairing=B.ROTATE_HALVES, kmin=None, kmax=None, stream=None):
@@ -281,7 +288,7 @@ class LongContextDecoder(DraftDecoder):
         been evicted from, a token's index is not its position any more: ``positions`` says it."""
         B.sparse_attn_append_kv_norm(self.p, q_new, k_new, v_new, q_weight, k_weight, eps, inv_freq, q_out, k_pages,
                                      v_pages, block_table, self.ws, cu_rows, self.seq_lens, positions, axis_of, pairing,
-                                     kmin, kmax, stream)
+                                     kmin, kmax, stream, self.weights)
 
     def decode_shared(self, q, k_pages, v_pages, block_table, cu_seqs, prefix_lens, tree_mask=None, stream=None):
         """``decode`` for groups of sequences that hold the same first tokens; returns the output tensor."""
@@ -292,7 +299,8 @@ class LongContextDecoder(DraftDecoder):
         return self.out
 
     def decode_weighed(self, q, k_pages, v_pages, block_table, stream=None):
-        """Attention of a chain of new tokens that adds to ``weights``; returns the output tensor."""
+        """Attention of a chain of new tokens that adds to ``weights``; returns the output tensor.  Of a chain the
+        first tokens are accepted: all by ``accept``, some by ``commit`` with a path 0, 1, 2, ..."""
         B.sparse_attn_weigh_decode(self.p, q, k_pages, v_pages, block_table, self.weights, self.out.view(q.shape), self.ws,
                                    self.seq_lens, stream)
         return self.out
@@ -318,6 +326,8 @@ class LongContextDecoder(DraftDecoder):
                 moved &= (keep_lens >= sink_tokens + recent_tokens) & (keep_lens <= self.keep_tokens)
             head = block_table[:, : new_table.shape[1]]
             head.copy_(torch.where(moved[:, None], new_table, head))
+            gone = moved[:, None] & (self._index >= self.new_lens[:, None])
+            self.weights.masked_fill_(gone[:, None], 0.0)        # the sums of tokens that are not there any more
             self.seq_lens.copy_(self.new_lens)
 
     def _stream(self, stream):
