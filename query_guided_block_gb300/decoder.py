@@ -273,6 +273,7 @@ class LongContextDecoder(DraftDecoder):
                 self.weights = torch.zeros(p.batch, p.num_kv_heads, nb_cap * p.block_size, device=dev)
                 self.kept_ids = torch.full((p.batch, p.num_kv_heads, keep_tokens), -1, dtype=torch.int32, device=dev)
                 self._index = torch.arange(nb_cap * p.block_size, device=dev)
+                self._column = torch.arange(nb_cap, device=dev)
             if size > self.ws.numel():
                 self.ws = torch.empty(size, dtype=torch.uint8, device=dev)
                 B.sparse_attn_workspace_init(self.ws)
@@ -313,18 +314,40 @@ class LongContextDecoder(DraftDecoder):
     def evict(self, sink_tokens, recent_tokens, k_pages, v_pages, block_table, new_table, keep_lens=None, kmin=None,
               kmax=None, stream=None):
         """Cut the contexts down to ``keep_tokens`` (or ``keep_lens``) tokens in the pages of ``new_table``
-        [B, ceil(keep_tokens / block_size)], which must be free ones; ``kept_ids`` says which tokens they were.
-        ``seq_lens`` holds the new lengths after it, and the rows of ``block_table`` begin with the new
-        pages; the pages that were in it are the caller's again."""
+        [B, n], n >= ceil(keep_tokens / block_size), which must be free ones; ``kept_ids`` says which tokens they
+        were.  ``seq_lens`` holds the new lengths after it.
+
+        The rows of ``block_table`` of the sequences that moved begin with their n new pages.  Of the entries
+        behind them, those whose page another sequence's context reads (a shared prefix) become -1: an ``append``
+        that gets there reports ``ERR_PAGE`` until the caller names a page.  The others stay, and with them their
+        pages, which the sequence grows into next.  So the caller's again are the pages of a moved row's first n
+        entries and of those that became -1, unless another row holds them.  What somebody outside of the
+        batch or an inactive sequence reads is not looked for: where that may be, ``new_table`` as wide as
+        ``block_table`` replaces the whole rows (-1: no page yet)."""
+        width, blocks = new_table.shape[1], -(-self.keep_tokens // self.p.block_size)
+        if width > block_table.shape[1]:
+            raise ValueError(f"new_table: {width} pages a sequence, block_table has {block_table.shape[1]}")
+        with torch.cuda.stream(self._stream(stream)):
+            kept_in = new_table if width <= blocks else new_table[:, :blocks].contiguous()
         B.sparse_attn_evict_tokens(self.p, self.keep_tokens, sink_tokens, recent_tokens, self.weights, k_pages, v_pages,
-                                   block_table, new_table, self.kept_ids, self.new_lens, self.ws, self.seq_lens, keep_lens,
+                                   block_table, kept_in, self.kept_ids, self.new_lens, self.ws, self.seq_lens, keep_lens,
                                    kmin, kmax, stream)
         with torch.cuda.stream(self._stream(stream)):
             # what the call leaves alone keeps its pages: inactive, no budget, or numbers out of range
-            moved = (self.seq_lens >= 0) & (self.seq_lens <= self.p.n_tokens)
+            active = (self.seq_lens >= 0) & (self.seq_lens <= self.p.n_tokens)
+            moved = active
             if keep_lens is not None:
-                moved &= (keep_lens >= sink_tokens + recent_tokens) & (keep_lens <= self.keep_tokens)
-            head = block_table[:, : new_table.shape[1]]
+                moved = active & (keep_lens >= sink_tokens + recent_tokens) & (keep_lens <= self.keep_tokens)
+            if width < block_table.shape[1]:
+                # entries that a context reads, and how many others read the same page
+                read = (active[:, None] & (self._column * self.p.block_size < self.seq_lens[:, None]) &
+                        (block_table >= 0) & (block_table < self.p.num_pages)).to(torch.int32)
+                page = block_table.clamp(0, self.p.num_pages - 1).long()
+                readers = torch.zeros(self.p.num_pages, dtype=torch.int32, device=self.device)
+                readers.scatter_add_(0, page.flatten(), read.flatten())
+                shared = moved[:, None] & (self._column >= width) & (readers[page] > read)
+                block_table.masked_fill_(shared, -1)
+            head = block_table[:, :width]
             head.copy_(torch.where(moved[:, None], new_table, head))
             gone = moved[:, None] & (self._index >= self.new_lens[:, None])
             self.weights.masked_fill_(gone[:, None], 0.0)        # the sums of tokens that are not there any more
