@@ -567,6 +567,8 @@ int sparse_attn_evict_workspace_size(const sparse_attn_params* p, int32_t keep_t
  *   -1, one left alone its length); new_lens must not overlap seq_lens or keep_lens.
  *   The new pages must not be pages that any sequence of the call reads, and belong to one sequence.
  *   kmin / kmax: both or neither; the rows of the new blocks become the box of their tokens.
+ * The call needs no room behind a context: one past n_tokens (its pages reach the capacity) is evicted from
+ * with parameters whose n_tokens is the capacity.
  * Afterwards new_table's row is the sequence's page table.  A token's index no longer tells its position:
  * later tokens are appended with `positions`.  keep_tokens >= 1. */
 int sparse_attn_evict_tokens(const sparse_attn_params* p, const int32_t* seq_lens, int32_t keep_tokens,

@@ -315,7 +315,8 @@ class LongContextDecoder(DraftDecoder):
               kmax=None, stream=None):
         """Cut the contexts down to ``keep_tokens`` (or ``keep_lens``) tokens in the pages of ``new_table``
         [B, n], n >= ceil(keep_tokens / block_size), which must be free ones; ``kept_ids`` says which tokens they
-        were.  ``seq_lens`` holds the new lengths after it.
+        were.  ``seq_lens`` holds the new lengths after it.  Contexts of any length that has pages are cut, also
+        those that an ``accept``, a ``commit`` or a prompt has carried past ``p.n_tokens``.
 
         The rows of ``block_table`` of the sequences that moved begin with their n new pages.  Of the entries
         behind them, those whose page another sequence's context reads (a shared prefix) become -1: an ``append``
@@ -327,23 +328,25 @@ class LongContextDecoder(DraftDecoder):
         width, blocks = new_table.shape[1], -(-self.keep_tokens // self.p.block_size)
         if width > block_table.shape[1]:
             raise ValueError(f"new_table: {width} pages a sequence, block_table has {block_table.shape[1]}")
+        p = B.sparse_attn_params.from_buffer_copy(self.p)
+        p.n_tokens = max(p.capacity_tokens, p.n_tokens)              # needs no room for drafts behind a context
         with torch.cuda.stream(self._stream(stream)):
             kept_in = new_table if width <= blocks else new_table[:, :blocks].contiguous()
-        B.sparse_attn_evict_tokens(self.p, self.keep_tokens, sink_tokens, recent_tokens, self.weights, k_pages, v_pages,
+        B.sparse_attn_evict_tokens(p, self.keep_tokens, sink_tokens, recent_tokens, self.weights, k_pages, v_pages,
                                    block_table, kept_in, self.kept_ids, self.new_lens, self.ws, self.seq_lens, keep_lens,
                                    kmin, kmax, stream)
         with torch.cuda.stream(self._stream(stream)):
             # what the call leaves alone keeps its pages: inactive, no budget, or numbers out of range
-            active = (self.seq_lens >= 0) & (self.seq_lens <= self.p.n_tokens)
+            active = (self.seq_lens >= 0) & (self.seq_lens <= p.n_tokens)
             moved = active
             if keep_lens is not None:
                 moved = active & (keep_lens >= sink_tokens + recent_tokens) & (keep_lens <= self.keep_tokens)
             if width < block_table.shape[1]:
                 # entries that a context reads, and how many others read the same page
-                read = (active[:, None] & (self._column * self.p.block_size < self.seq_lens[:, None]) &
-                        (block_table >= 0) & (block_table < self.p.num_pages)).to(torch.int32)
-                page = block_table.clamp(0, self.p.num_pages - 1).long()
-                readers = torch.zeros(self.p.num_pages, dtype=torch.int32, device=self.device)
+                read = (active[:, None] & (self._column * p.block_size < self.seq_lens[:, None]) &
+                        (block_table >= 0) & (block_table < p.num_pages)).to(torch.int32)
+                page = block_table.clamp(0, p.num_pages - 1).long()
+                readers = torch.zeros(p.num_pages, dtype=torch.int32, device=self.device)
                 readers.scatter_add_(0, page.flatten(), read.flatten())
                 shared = moved[:, None] & (self._column >= width) & (readers[page] > read)
                 block_table.masked_fill_(shared, -1)
