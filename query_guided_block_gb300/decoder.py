@@ -307,9 +307,11 @@ class LongContextDecoder(DraftDecoder):
         return self.out
 
     def accept(self, stream=None):
-        """The new tokens of every active sequence join its context."""
+        """The new tokens of every active sequence join its context.  A sequence whose context no attention has taken
+        (out of range, or longer than ``p.n_tokens``) stays as it is."""
         with torch.cuda.stream(self._stream(stream)):
-            self.seq_lens.add_((self.seq_lens >= 0).to(torch.int32), alpha=self.Q)
+            taken = (self.seq_lens >= 0) & (self.seq_lens <= self.p.n_tokens)
+            self.seq_lens.add_(taken.to(torch.int32), alpha=self.Q)
 
     def evict(self, sink_tokens, recent_tokens, k_pages, v_pages, block_table, new_table, keep_lens=None, kmin=None,
               kmax=None, stream=None):

@@ -57,6 +57,24 @@ def test_a_full_context_is_evicted(n_tokens, capacity):
     assert dec.device_error() == 0
 
 
+def test_a_context_that_no_attention_took_does_not_grow():
+    """The attention leaves contexts past n_tokens alone; so does accept, until there are parameters for them."""
+    dec, k, v, table, _ = world([10, 100, 101, -1, 0], 100, 160)
+    q = torch.randn(BATCH, Q, HQ, D, device="cuda").to(BF)
+    rows = [torch.randn(BATCH * Q, HKV, D, device="cuda").to(BF) for _ in range(2)]
+    dec.append(None, *rows, None, None, k, v, table)
+    dec.decode_weighed(q, k, v, table)
+    assert dec.device_error() == B.ERR_LENGTH
+    dec.accept()
+    assert dec.seq_lens.tolist() == [14, 104, 101, -1, 4]
+    dec.p = B.make_params(BATCH, HQ, HKV, D, 156, BS, dec.p.num_pages, 0, 1, num_queries=Q, capacity_tokens=160)
+    dec.append(None, *rows, None, None, k, v, table)
+    dec.decode_weighed(q, k, v, table)
+    assert dec.device_error() == 0
+    dec.accept()
+    assert dec.seq_lens.tolist() == [18, 108, 105, -1, 8]
+
+
 def test_lengths_past_the_pages_are_reported():
     dec, k, v, table, new = world([161, -2, 160, 20, 0], 156, 160)
     before = table.clone()
