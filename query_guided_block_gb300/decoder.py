@@ -302,6 +302,7 @@ class LongContextDecoder(DraftDecoder):
     def decode_weighed(self, q, k_pages, v_pages, block_table, stream=None):
         """Attention of a chain of new tokens that adds to ``weights``; returns the output tensor.  Of a chain the
         first tokens are accepted: all by ``accept``, some by ``commit`` with a path 0, 1, 2, ..."""
+        self._budget()
         B.sparse_attn_weigh_decode(self.p, q, k_pages, v_pages, block_table, self.weights, self.out.view(q.shape), self.ws,
                                    self.seq_lens, stream)
         return self.out
@@ -327,6 +328,7 @@ class LongContextDecoder(DraftDecoder):
         entries and of those that became -1, unless another row holds them.  What somebody outside of the
         batch or an inactive sequence reads is not looked for: where that may be, ``new_table`` as wide as
         ``block_table`` replaces the whole rows (-1: no page yet)."""
+        self._budget()
         width, blocks = new_table.shape[1], -(-self.keep_tokens // self.p.block_size)
         if width > block_table.shape[1]:
             raise ValueError(f"new_table: {width} pages a sequence, block_table has {block_table.shape[1]}")
@@ -357,6 +359,10 @@ class LongContextDecoder(DraftDecoder):
             gone = moved[:, None] & (self._index >= self.new_lens[:, None])
             self.weights.masked_fill_(gone[:, None], 0.0)        # the sums of tokens that are not there any more
             self.seq_lens.copy_(self.new_lens)
+
+    def _budget(self):
+        if self.weights is None:
+            raise ValueError("keep_tokens: 0, so there are no weights to add to or to evict by")
 
     def _stream(self, stream):
         if stream is None:
