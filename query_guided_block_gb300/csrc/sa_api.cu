@@ -809,7 +809,8 @@ static int shared_geometry(const sparse_attn_params* p, int32_t num_groups, Geom
     const long long rows = (long long)g->B * g->Q * g->Hq;
     const long long groups = ((long long)g->B * g->Q * g->G + 15) / 16 + num_groups;      // row groups of a KV head at most
     const long long tiles = (long long)g->nb_cap * g->bs / kTreeLeastTile + 1;
-    if (rows > INT32_MAX / 2 || tiles * groups * g->Hkv > INT32_MAX / 2 ||
+    const long long own = (long long)g->units() * ((g->Q * g->G + 15) / 16);              // and of the own tokens
+    if (rows > INT32_MAX / 2 || tiles * groups * g->Hkv > INT32_MAX / 2 || tiles * (groups * g->Hkv + own) > INT32_MAX - 1024 ||
         ((long long)num_groups + g->B) * g->Hkv * (((long long)g->B * g->Q * g->G + 15) / 16) > INT32_MAX / 2)
         return SPARSE_ATTN_UNSUPPORTED;
     return SPARSE_ATTN_OK;
