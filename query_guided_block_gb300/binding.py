@@ -527,18 +527,20 @@ def sparse_attn_append_kv_norm(p, q_new, k_new, v_new, q_weight, k_weight, eps, 
     if positions is not None:
         pos = _tensor_ptr(positions, dev, "positions", (rows,) if axis_of is None else (axes, rows), _I32)
     w, n = _workspace(ws, dev)
-    name, tail = "sparse_attn_append_kv_norm", (w, n)
-    if weights is not None:
-        name, tail = "sparse_attn_append_kv_weights", (_tensor_ptr(weights, dev, "weights", g.weights, torch.float32), w, n)
-    _launch_on(dev, name, stream, C.byref(p), rows,
-               None if cu_rows is None else _tensor_ptr(cu_rows, dev, "cu_rows", g.ends, _I32),
-               None if seq_lens is None else _tensor_ptr(seq_lens, dev, "seq_lens", g.per_seq, _I32),
-               pos, axes, axis, rotary, pairing, freq, qw, qws, kw, kws, eps, q, qs, k, ks, v, vs,
-               None if q_out is None else _tensor_ptr(q_out, dev, "q_out", q_rows, qt),
-               _tensor_ptr(k_pages, dev, "k_pages", g.pool, kvt), _tensor_ptr(v_pages, dev, "v_pages", g.pool, kvt),
-               _tensor_ptr(block_table, dev, "block_table", g.table, _I32),
-               None if kmin is None else _tensor_ptr(kmin, dev, "kmin", g.box, kvt),
-               None if kmax is None else _tensor_ptr(kmax, dev, "kmax", g.box, kvt), *tail)
+    cu = None if cu_rows is None else _tensor_ptr(cu_rows, dev, "cu_rows", g.ends, _I32)
+    lens = None if seq_lens is None else _tensor_ptr(seq_lens, dev, "seq_lens", g.per_seq, _I32)
+    qo = None if q_out is None else _tensor_ptr(q_out, dev, "q_out", q_rows, qt)
+    kp, vp = _tensor_ptr(k_pages, dev, "k_pages", g.pool, kvt), _tensor_ptr(v_pages, dev, "v_pages", g.pool, kvt)
+    table = _tensor_ptr(block_table, dev, "block_table", g.table, _I32)
+    lo = None if kmin is None else _tensor_ptr(kmin, dev, "kmin", g.box, kvt)
+    hi = None if kmax is None else _tensor_ptr(kmax, dev, "kmax", g.box, kvt)
+    if weights is None:
+        _launch_on(dev, "sparse_attn_append_kv_norm", stream, C.byref(p), rows, cu, lens, pos, axes, axis, rotary, pairing,
+                   freq, qw, qws, kw, kws, eps, q, qs, k, ks, v, vs, qo, kp, vp, table, lo, hi, w, n)
+    else:
+        _launch_on(dev, "sparse_attn_append_kv_weights", stream, C.byref(p), rows, cu, lens, pos, axes, axis, rotary, pairing,
+                   freq, qw, qws, kw, kws, eps, q, qs, k, ks, v, vs, qo, kp, vp, table, lo, hi,
+                   _tensor_ptr(weights, dev, "weights", g.weights, torch.float32), w, n)
 
 
 def sparse_attn_tree_workspace_size(p: sparse_attn_params) -> int:

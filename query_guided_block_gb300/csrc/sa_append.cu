@@ -422,9 +422,10 @@ __global__ void __launch_bounds__(kAppThreads, 2) append_kernel(AppendArgs a)
     const int n = t1 - t0;                                    // tokens [t0, t1)
     const int r0 = row0 + (t0 - len);                         // their first row
     const int blk0 = t0 / a.bs, blks = (t1 - 1) / a.bs - blk0 + 1;
-    if (a.weights != nullptr && blockIdx.y == 0) {            // a share of the heads has all heads' entries
-        float* w = a.weights + (long long)b * a.Hkv * a.nb_cap * a.bs + t0;
-        for (int i = tid; i < n * a.Hkv; i += kAppThreads) w[(long long)(i / n) * a.nb_cap * a.bs + i % n] = 0.f;
+    if (a.weights != nullptr && blockIdx.y == 0 && tid < n) {  // one share of the heads has all heads' entries
+        float* w = a.weights + (long long)b * a.Hkv * (a.nb_cap * a.bs) + t0 + tid;
+#pragma unroll 1
+        for (int h = a.Hkv; h > 0; --h, w += a.nb_cap * a.bs) *w = 0.f;
     }
     if (tid < blks) {
         const int page = a.block_table[(long long)b * a.nb_cap + blk0 + tid];

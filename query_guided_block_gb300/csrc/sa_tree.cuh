@@ -33,7 +33,7 @@ inline int tree_item_rows(int R) { return R <= 16 ? 16 : (R <= 64 ? 64 : kTreeMa
 
 // Words of shared memory that tree_part needs.
 template <int NT>
-constexpr int kTreeScan = 7 * (NT / 32) + 3;
+constexpr int kTreeScan = 6 * (NT / 32) + 3;
 
 struct TreeArgs {
     const void* q;
@@ -312,7 +312,6 @@ struct TreePart {
     int item;
     int per;          // tiles of a part
     bool whole;       // the items that begin in the part belong to it to their ends
-    bool overlap;     // EXT: groups hold more sequences than there are; no part has any work
 };
 
 // Found by all threads (NT of them): as many warps as the units need count tiles, the others
@@ -330,54 +329,32 @@ __device__ TreePart tree_part(const TreeArgs& a, int* s)
     const int u0 = warp < warps ? min(units, tid * ch) : units, u1 = min(units, u0 + ch);
     struct Count {
         int tiles, groups;            // of an item, row groups (EXT: of all KV heads)
-        int shared;                   // query rows of a prefix
     };
     auto count = [&](int u) {
         const TreeUnit un = tree_unit<EXT>(a, EXT ? u * a.Hkv : u);
-        const int tiles = tree_tiles<EXT>(a, un);
-        return Count{tiles, tree_row_groups<EXT>(a, un) * (EXT ? a.Hkv : 1), EXT && un.prefix && tiles > 0 ? un.rows : 0};
+        return Count{tree_tiles<EXT>(a, un), tree_row_groups<EXT>(a, un) * (EXT ? a.Hkv : 1)};
     };
-    const Count t_first = u0 < u1 ? count(u0) : Count{0, a.row_groups, 0};
+    const Count t_first = u0 < u1 ? count(u0) : Count{0, a.row_groups};
     auto tiles_of = [&](int u) { return u == u0 ? t_first : count(u); };
     int* s_sum = s;                   // [W] tiles
     int* s_parts = s + W;             // [3][W] parts at three lengths
     int* s_line = s + 4 * W;          // [W] stretches of the line
     int* s_longest = s + 5 * W;       // [W] tiles of the longest item
-    int* s_rows = s + 6 * W;          // [W] EXT: query rows of prefixes, cut off above all the batch's
-    int* s_found = s + 7 * W;         // item, start, end
+    int* s_found = s + 6 * W;         // item, start, end
 
-    // The tiles fit into 32 bits because the groups are parts of the batch.  Groups that overlap (cu_seqs out of
-    // order) may have any number: then nothing is done.  Their sums below are unsigned, which may wrap.
-    const bool grouped = EXT && (a.pass == kTreePrefix || a.pass == kTreeBoth);
-    const int most_rows = grouped ? a.seqs * a.R : 0;          // below 2^30
-    unsigned tile_sum = 0u;
-    long long rows = 0;
+    int tiles = 0;
     for (int u = u0; u < u1; ++u) {
         const Count n = tiles_of(u);
-        tile_sum += EXT ? unsigned(n.tiles) * unsigned(n.groups) : unsigned(n.tiles);
-        if constexpr (EXT) rows += n.shared;
+        tiles += EXT ? n.tiles * n.groups : n.tiles;
     }
-    int tiles = int(tile_sum);
     if (!EXT) tiles *= a.row_groups;
     if (warp < warps) {
         const int sum = __reduce_add_sync(kFullMask, tiles);
         if (lane == 0) s_sum[warp] = sum;
-        if (grouped) {
-            const unsigned mine_rows = unsigned(min(rows, most_rows + 1LL));
-            const unsigned high = __reduce_add_sync(kFullMask, mine_rows >> 16);
-            const unsigned low = __reduce_add_sync(kFullMask, mine_rows & 0xffffu);
-            if (lane == 0) s_rows[warp] = int(min(((long long)high << 16) + low, most_rows + 1LL));
-        }
     }
     __syncthreads();
     int total = 0;
-    long long all_rows = 0;
-    for (int w = 0; w < warps; ++w) {
-        total = int(unsigned(total) + unsigned(s_sum[w]));
-        if (grouped) all_rows += s_rows[w];
-    }
-    const bool overlap = all_rows > most_rows;
-    if (overlap) total = 0;
+    for (int w = 0; w < warps; ++w) total += s_sum[w];
     int per = max(a.min_per, (total + ctas - 1) / ctas);
     // Items may begin with a part if the parts then suffice: at no cost, with half of the slack
     // added to a part, or with all of it.  Where items are too many for that and none is longer
@@ -431,9 +408,8 @@ __device__ TreePart tree_part(const TreeArgs& a, int* s)
     TreePart r;
     r.per = per;
     r.whole = !aligned && longest <= 2 * a.half_slack;
-    r.overlap = overlap;
-    r.lo = overlap ? 0 : int(min((long long)total, (long long)blockIdx.x * per));
-    r.hi = overlap ? 0 : int(min((long long)total, (long long)r.lo + per));
+    r.lo = int(min((long long)total, (long long)blockIdx.x * per));
+    r.hi = int(min((long long)total, (long long)r.lo + per));
     if (r.lo < r.hi && mine > 0) {
         int at = incl - mine;
         for (int w = 0; w < warp; ++w) at += s_line[w];
@@ -543,15 +519,13 @@ __device__ __forceinline__ float tree_share(float m, float M, float l, float sca
 }
 
 // The prefix pass: which group and how many shared tokens every sequence has, for the launches behind it;
-// -1 where it is inactive, and everywhere when groups overlap.  By the last CTAs, which have the least to do when
-// work is short.
-__device__ __forceinline__ void tree_note_sequences(const TreeArgs& a, int threads, bool overlap)
+// -1 where it is inactive.  By the last CTAs, which have the least to do when work is short.
+__device__ __forceinline__ void tree_note_sequences(const TreeArgs& a, int threads)
 {
     if (a.pass != kTreePrefix && a.pass != kTreeBoth) return;
-    if (overlap && blockIdx.x == 0 && threadIdx.x == 0) raise_error(a.err, SPARSE_ATTN_ERR_LENGTH);
     for (int b = (gridDim.x - 1 - blockIdx.x) * threads + threadIdx.x; b < a.seqs; b += gridDim.x * threads) {
         const int2 of = tree_sequence(a, b);
-        a.seq_prefix[b] = overlap ? -1 : of.x;
+        a.seq_prefix[b] = of.x;
         a.seq_group[b] = of.y;
     }
 }

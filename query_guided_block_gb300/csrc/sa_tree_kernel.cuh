@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kTrThreads, 2) tree_kernel(TreeArgs a)
                               // so nothing of them is read through the read-only cache
 
     const TreePart part = tree_part<kTrThreads, EXT>(a, s_scan);
-    if constexpr (EXT) tree_note_sequences(a, kTrThreads, part.overlap);
+    if constexpr (EXT) tree_note_sequences(a, kTrThreads);
     const bool dense = EXT || a.sel_ids == nullptr;
     int lo = part.lo, start = part.start, item = part.item;
 

@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc_fence_after_sync();
     const uint32_t tmem = sh.tmem;
     const bool dense = EXT || a.sel_ids == nullptr;
-    if constexpr (EXT) tree_note_sequences(a, kTcThreads, part.overlap);
+    if constexpr (EXT) tree_note_sequences(a, kTcThreads);
     int lo = part.lo, start = part.start, item = part.item;
     TcSegment g;
 
