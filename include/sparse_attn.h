@@ -530,8 +530,7 @@ int sparse_attn_shared_workspace_size(const sparse_attn_params* p, int32_t num_g
  *   no group (which share nothing) are allowed.
  *   A sequence with fewer tokens than its group's prefix, cu_seqs that are not ascending numbers in
  *   0 .. B and prefix_lens out of range set SPARSE_ATTN_ERR_LENGTH; the sequences concerned are then
- *   treated as inactive or, with cu_seqs out of order, their rows are unspecified.  Groups that overlap so far
- *   that they have more sequences between them than the batch has make all sequences inactive.
+ *   treated as inactive or, with cu_seqs out of order, their rows are unspecified.
  * num_groups >= 1.  q, out, tree_mask and what may be NULL or infinite as in sparse_attn_tree_decode. */
 int sparse_attn_shared_decode(const sparse_attn_params* p, const void* q, const void* k_pages, const void* v_pages,
                               const int32_t* block_table, const int32_t* seq_lens, int32_t num_groups,

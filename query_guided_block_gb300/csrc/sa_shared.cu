@@ -122,7 +122,7 @@ TreeArgs tree_ext_args(const Geometry& g, const TreeCall& c, char* ws, const Tre
 namespace {
 
 struct SharedLayout {
-    size_t seq_prefix, seq_group, prior;
+    size_t seq_prefix, seq_group, cu_seqs, prior;
     TreeExtLayout prefix, own;
 };
 
@@ -131,10 +131,36 @@ SharedLayout shared_layout(const Geometry& g, int groups)
     SharedLayout L{};
     L.seq_prefix = kTreeWsFree;
     L.seq_group = align256(L.seq_prefix + size_t(g.B) * sizeof(int32_t));
-    L.prior = align256(L.seq_group + size_t(g.B) * sizeof(int32_t));
+    L.cu_seqs = align256(L.seq_group + size_t(g.B) * sizeof(int32_t));
+    L.prior = align256(L.cu_seqs + (size_t(groups) + 1) * sizeof(int32_t));
     L.prefix = tree_ext_layout(g, align256(L.prior + size_t(g.B) * g.Q * g.Hq * g.D * sizeof(float)), groups);
     L.own = tree_ext_layout(g, L.prefix.end, 0);
     return L;
+}
+
+// Groups out of order may overlap, up to every group being the whole batch.  The launches number the tiles of their
+// items in 32 bits, which hold them as long as every sequence is in one group at most.  Whether they also hold the
+// most that any cu_seqs can name:
+bool any_groups_fit(const Geometry& g, int groups)
+{
+    const long long tiles = (long long)g.nb_cap * g.bs / kTreeLeastTile + 1, R = g.Q * g.G;
+    const long long rows = ((long long)g.B * R + 15) / 16 * g.Hkv, own = (R + 15) / 16 * g.units();
+    return double(tiles) * (double(groups) * double(rows) + double(own)) < double(INT32_MAX / 2);
+}
+
+// Where they do not, cu_seqs is looked over first, by one CTA: `to` becomes a copy or, with groups out of order,
+// all 0, which leaves every sequence to itself.
+constexpr int kOrderThreads = 1024;
+
+__global__ void __launch_bounds__(kOrderThreads) order_kernel(const int32_t* cu_seqs, int groups, int32_t* to, uint32_t* err)
+{
+    allow_dependents_early();
+    grid_dependency_wait();   // the groups may come from the previous kernel
+    int bad = 0;
+    for (int i = threadIdx.x; i < groups; i += kOrderThreads) bad |= cu_seqs[i] > cu_seqs[i + 1];
+    bad = __syncthreads_or(bad);
+    if (bad && threadIdx.x == 0) raise_error(err, SPARSE_ATTN_ERR_LENGTH);
+    for (int i = threadIdx.x; i <= groups; i += kOrderThreads) to[i] = bad ? 0 : cu_seqs[i];
 }
 
 }  // namespace
@@ -145,6 +171,13 @@ cudaError_t launch_shared(const Geometry& g, const TreeCall& c, int groups, cons
                           char* ws, cudaStream_t s)
 {
     const SharedLayout L = shared_layout(g, groups);
+    if (!any_groups_fit(g, groups)) {
+        int32_t* to = reinterpret_cast<int32_t*>(ws + L.cu_seqs);
+        const cudaError_t e = launch_after_previous(order_kernel, dim3(1), dim3(kOrderThreads), 0, s, cu_seqs, groups, to,
+                                                    reinterpret_cast<uint32_t*>(ws));
+        if (e != cudaSuccess) return e;
+        cu_seqs = to;
+    }
     TreeArgs pre = tree_ext_args(g, c, ws, L.prefix);
     pre.pass = kTreePrefix;
     pre.B = pre.groups = groups;
