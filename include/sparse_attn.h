@@ -537,7 +537,11 @@ int sparse_attn_shared_decode(const sparse_attn_params* p, const void* q, const 
                               const int32_t* cu_seqs, const int32_t* prefix_lens, const uint32_t* tree_mask, float* out,
                               void* ws, size_t ws_bytes, sparse_attn_stream stream);
 
-/* Workspace of sparse_attn_weigh_decode for contexts up to the capacity. */
+/* Workspace of sparse_attn_weigh_decode for contexts up to the capacity.  Besides a fixed part it has room for
+ * scores, 4 bytes for every query row and token: 4 * B * Q * Hq * capacity (rounded up to 64 tokens) for up
+ * to 16 rows a KV head (Q * Hq / Hkv) and, whatever the rows, for fp32 queries or an fp32 cache.  That has no
+ * bound: 4 sequences of 32K tokens with 32 fp32 queries of 32 heads take 0.54 GB, with 256 queries 4.3 GB; a call
+ * over parts of the batch takes its part.  bf16 with 17 to 32 rows keeps 256 MB at most, with more 2.5 MB. */
 int sparse_attn_weigh_workspace_size(const sparse_attn_params* p, size_t* bytes);
 
 /* sparse_attn_tree_decode of a chain (no selection, tree_mask NULL) that also adds up the attention weight

@@ -254,7 +254,10 @@ class LongContextDecoder(DraftDecoder):
     ``num_groups`` groups at most share prefixes (0: ``decode_shared`` is not used); with ``keep_tokens``
     contexts are cut down to that many tokens (0: ``decode_weighed`` and ``evict`` are not used).  Every token
     that ``append`` or ``append_norm`` brings in has the weight zero until ``decode_weighed`` adds to it,
-    whatever was at its index before: an evicted token, a rejected draft, another request."""
+    whatever was at its index before: an evicted token, a rejected draft, another request.
+
+    The workspace grows with the scores that ``decode_weighed`` keeps: 4 bytes for each of the B Q Hq query rows and
+    each token of the capacity with up to 16 rows a KV head, or with fp32 queries or K/V."""
 
     def __init__(self, params: B.sparse_attn_params, seq_lens: torch.Tensor, num_groups: int = 0, keep_tokens: int = 0):
         super().__init__(params, seq_lens)
