@@ -433,7 +433,8 @@ int sparse_attn_append_kv(const sparse_attn_params* p, int32_t num_rows, const i
  *   Norm: x[d] / sqrt(mean over the head's D channels of x^2 + eps) * weight[d], of queries when
  *   q_weight is given and of keys when k_weight is; values are not normed.  Weights are device
  *   floats, 16-byte aligned: [D] for all heads (stride 0) or [heads, D] (stride D).  eps > 0 when
- *   there is a weight.  Norm and rotation are fp32; each result is rounded once.
+ *   there is a weight.  Norm and rotation are fp32; each result is rounded once.  One set of query weights for
+ *   all heads is the faster form (48K rows of 32 + 2 x 8 heads 221 us, with weights for each head 261 us).
  *   Axes: with num_axes = A > 1 (at most 8), positions is device int32 [A, num_rows] and
  *   axis_of device int32 [rotary_dim / 2] says which axis turns pair i:
  *   angle_i = positions[axis_of[i]][row] * inv_freq[i].  An axis outside [0, A) sets

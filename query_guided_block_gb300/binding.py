@@ -543,6 +543,11 @@ def sparse_attn_append_kv_norm(p, q_new, k_new, v_new, q_weight, k_weight, eps, 
                    _tensor_ptr(weights, dev, "weights", g.weights, torch.float32), w, n)
 
 
+def sparse_attn_append_kv_weights(*args, weights, **kw) -> None:
+    """sparse_attn_append_kv_norm, with weights."""
+    sparse_attn_append_kv_norm(*args, weights=weights, **kw)
+
+
 def sparse_attn_tree_workspace_size(p: sparse_attn_params) -> int:
     n = C.c_size_t(0)
     _check("sparse_attn_tree_workspace_size", lib().sparse_attn_tree_workspace_size(C.byref(p), C.byref(n)))

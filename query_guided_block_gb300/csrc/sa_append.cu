@@ -348,7 +348,8 @@ __device__ __forceinline__ int sequence_rows(const AppendArgs& a, int b, int& ro
 
 __device__ __forceinline__ int runs_of(int n, int len, int run) { return n > 0 ? (len + n - 1) / run - len / run + 1 : 0; }
 
-// EXT: 0 the plain append, 1 queries normed with the same weights for all heads, 2 any other norm or axes.
+// EXT: 0 the plain append, 1 queries normed with the same weights for all heads, 2 any other norm or axes (48K rows with
+// a weight for each head 261 us, 221 with EXT 1).
 template <bool QB, bool KB, int EXT>
 __global__ void __launch_bounds__(kAppThreads, 2) append_kernel(AppendArgs a)
 {

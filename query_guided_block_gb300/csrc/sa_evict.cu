@@ -10,9 +10,11 @@
 // tokens a CTA, every load on its way before the first store, with their weights and their blocks' box.
 // Bytes: 4 a cached token, then each kept row once in and once out.
 //
-// 16 contexts of up to 32K tokens down to 8K, 8 heads of 128 (1.1 GB): 213 us, 5.2 TB/s; the first launch 26 us
-// of it (loads 7, digits 6, places 6), the second 179 of 162 for its bytes.  8 units of 128K tokens: 49 us, 26 in
-// the first launch, which the chain of its barriers bounds.  (Rows brought in by bulk copies of 256 bytes: 908 us,
+// 16 contexts of up to 32K tokens down to 8K, 8 heads of 128 (1.1 GB): 207 us, 5.3 TB/s; the first launch 26 us
+// of it (loads with the first counts 10, digits 5, places 8), the second 179 of 162 for its bytes.  8 units of 128K
+// tokens: 49 us, 26 in the first launch, by clusters of 8 (loads and first counts 6, digits 8: two barriers of
+// the cluster and a round of remote reads each; places 6).  8 units of 8K tokens: 13.6 us, 10 in the first launch, a
+// CTA a unit (lengths 1, loads and first counts 3, digits 3, places 3).  (Rows brought in by bulk copies of 256 bytes: 908 us,
 // 65 ns a copy.)
 #include "sa_common.cuh"
 #include "sa_internal.h"
