@@ -29,6 +29,7 @@
  *   sparse_attn_shared_decode   attention of a batch whose sequences share prefixes.
  *   sparse_attn_weigh_decode    attention that adds up every cached token's weight.
  *   sparse_attn_evict_tokens    the tokens with the largest weights kept, in new pages.
+ *   sparse_attn_evict_adopt     page table, lengths and weights brought in line with that.
  *
  * Conventions shared by every call
  * --------------------------------
@@ -555,7 +556,7 @@ int sparse_attn_weigh_decode(const sparse_attn_params* p, const void* q, const v
                              const int32_t* block_table, const int32_t* seq_lens, float* weights, float* out, void* ws,
                              size_t ws_bytes, sparse_attn_stream stream);
 
-/* Workspace of sparse_attn_evict_tokens. */
+/* Workspace of sparse_attn_evict_tokens and sparse_attn_evict_adopt. */
 int sparse_attn_evict_workspace_size(const sparse_attn_params* p, int32_t keep_tokens, size_t* bytes);
 
 /* Keep the tokens with the largest weights and drop the others, for each KV head by itself.
@@ -581,6 +582,21 @@ int sparse_attn_evict_tokens(const sparse_attn_params* p, const int32_t* seq_len
                              void* k_pages, void* v_pages, const int32_t* block_table, const int32_t* new_table,
                              void* kmin, void* kmax, int32_t* kept_ids, int32_t* new_lens, void* ws, size_t ws_bytes,
                              sparse_attn_stream stream);
+
+/* Behind sparse_attn_evict_tokens, with the same parameters, keep_tokens, keep_lens, sink_tokens, recent_tokens and
+ * (old) lengths, for a program that goes on in place.  For every sequence b that was moved:
+ *   - block_table[b] (read and written) begins with the new_width entries of new_table[b] (device int32
+ *     [B, new_width], ceil(keep_tokens / block_size) <= new_width <= nb_cap; the eviction's new_table is its first
+ *     columns).  Of the entries behind them those whose page the context of another active sequence
+ *     reads (a shared prefix) become -1, so that an append there reports SPARSE_ATTN_ERR_PAGE; the others stay,
+ *     and the sequence grows into their pages.
+ *   - weights[b][kvh][t] (layout of sparse_attn_weigh_decode; NULL: left alone) becomes 0 for t >= new_lens[b].
+ *   - seq_lens[b] becomes new_lens[b].
+ * Everything of the other sequences stays.  Reports nothing: what is out of range was reported by the eviction. */
+int sparse_attn_evict_adopt(const sparse_attn_params* p, int32_t* seq_lens, int32_t keep_tokens, const int32_t* keep_lens,
+                            int32_t sink_tokens, int32_t recent_tokens, const int32_t* new_lens, int32_t* block_table,
+                            const int32_t* new_table, int32_t new_width, float* weights, void* ws, size_t ws_bytes,
+                            sparse_attn_stream stream);
 
 /* Synchronise `stream`, copy the device error word to *flags (SPARSE_ATTN_ERR_* bits)
  * and clear it.  Returns SPARSE_ATTN_DEVICE_BOUNDS when any bit was set. */

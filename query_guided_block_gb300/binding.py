@@ -126,6 +126,7 @@ def lib():
             "sparse_attn_weigh_decode": ([P, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp], C.c_int),
             "sparse_attn_evict_workspace_size": ([P, i32, C.POINTER(C.c_size_t)], C.c_int),
             "sparse_attn_evict_tokens": ([P, vp, i32, vp, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp], C.c_int),
+            "sparse_attn_evict_adopt": ([P, vp, i32, vp, i32, i32, vp, vp, vp, i32, vp, vp, sz, vp], C.c_int),
         }
         for name, (args, res) in sigs.items():
             fn = getattr(L, name)
@@ -148,7 +149,7 @@ def exported_symbols():
             "sparse_attn_tree_workspace_size", "sparse_attn_tree_decode", "sparse_attn_commit_drafts",
             "sparse_attn_append_kv_norm", "sparse_attn_append_kv_weights", "sparse_attn_shared_workspace_size", "sparse_attn_shared_decode",
             "sparse_attn_weigh_workspace_size", "sparse_attn_weigh_decode", "sparse_attn_evict_workspace_size",
-            "sparse_attn_evict_tokens"]
+            "sparse_attn_evict_tokens", "sparse_attn_evict_adopt"]
 
 
 def _status_string(status: int) -> str:
@@ -467,10 +468,11 @@ def _launch_on(device: int, name: str, stream, *args) -> None:
 
 def sparse_attn_append_kv(p, q_new, k_new, v_new, inv_freq, q_out, k_pages, v_pages, block_table, ws,
                           cu_rows=None, seq_lens=None, positions=None, pairing=ROTATE_HALVES, kmin=None,
-                          kmax=None, stream=None) -> None:
+                          kmax=None, stream=None, weights=None) -> None:
     """Append rows of new tokens to the cache: q_new [rows, Hq, D] (or None), k_new and v_new
     [rows, Hkv, D], rows possibly strided (slices of one projection); inv_freq float64
-    [rotary_dim / 2] or None for no rotation; q_out [rows, Hq, D]."""
+    [rotary_dim / 2] or None for no rotation; q_out [rows, Hq, D].  The new tokens' entries of
+    weights (as sparse_attn_weigh_decode has them), when given, become 0."""
     g, dev, rows = _shapes(p), _device_of(k_new, "k_new"), k_new.shape[0]
     kv_rows, q_rows, qt, kvt = (rows, g.kv_heads, g.dim), (rows, g.q_heads, g.dim), g.q_dtype, g.kv_dtype
     k, ks = _rows_ptr(k_new, dev, "k_new", kv_rows, qt)
@@ -481,16 +483,21 @@ def sparse_attn_append_kv(p, q_new, k_new, v_new, inv_freq, q_out, k_pages, v_pa
         rotary = 2 * inv_freq.numel()
         freq = _tensor_ptr(inv_freq, dev, "inv_freq", (rotary // 2,), torch.float64)
     w, n = _workspace(ws, dev)
-    _launch_on(dev, "sparse_attn_append_kv", stream, C.byref(p), rows,
-               None if cu_rows is None else _tensor_ptr(cu_rows, dev, "cu_rows", g.ends, _I32),
-               None if seq_lens is None else _tensor_ptr(seq_lens, dev, "seq_lens", g.per_seq, _I32),
-               None if positions is None else _tensor_ptr(positions, dev, "positions", (rows,), _I32),
-               rotary, pairing, freq, q, qs, k, ks, v, vs,
-               None if q_out is None else _tensor_ptr(q_out, dev, "q_out", q_rows, qt),
-               _tensor_ptr(k_pages, dev, "k_pages", g.pool, kvt), _tensor_ptr(v_pages, dev, "v_pages", g.pool, kvt),
-               _tensor_ptr(block_table, dev, "block_table", g.table, _I32),
-               None if kmin is None else _tensor_ptr(kmin, dev, "kmin", g.box, kvt),
-               None if kmax is None else _tensor_ptr(kmax, dev, "kmax", g.box, kvt), w, n)
+    cu = None if cu_rows is None else _tensor_ptr(cu_rows, dev, "cu_rows", g.ends, _I32)
+    lens = None if seq_lens is None else _tensor_ptr(seq_lens, dev, "seq_lens", g.per_seq, _I32)
+    pos = None if positions is None else _tensor_ptr(positions, dev, "positions", (rows,), _I32)
+    qo = None if q_out is None else _tensor_ptr(q_out, dev, "q_out", q_rows, qt)
+    kp, vp = _tensor_ptr(k_pages, dev, "k_pages", g.pool, kvt), _tensor_ptr(v_pages, dev, "v_pages", g.pool, kvt)
+    table = _tensor_ptr(block_table, dev, "block_table", g.table, _I32)
+    lo = None if kmin is None else _tensor_ptr(kmin, dev, "kmin", g.box, kvt)
+    hi = None if kmax is None else _tensor_ptr(kmax, dev, "kmax", g.box, kvt)
+    if weights is None:
+        _launch_on(dev, "sparse_attn_append_kv", stream, C.byref(p), rows, cu, lens, pos, rotary, pairing, freq, q, qs, k, ks,
+                   v, vs, qo, kp, vp, table, lo, hi, w, n)
+    else:
+        _launch_on(dev, "sparse_attn_append_kv_weights", stream, C.byref(p), rows, cu, lens, pos, 1, None, rotary, pairing,
+                   freq, None, 0, None, 0, 0.0, q, qs, k, ks, v, vs, qo, kp, vp, table, lo, hi,
+                   _tensor_ptr(weights, dev, "weights", g.weights, torch.float32), w, n)
 
 
 def _norm_weight(t, device: int, what: str, heads: int, dim: int):
@@ -677,3 +684,19 @@ def sparse_attn_evict_tokens(p, keep_tokens, sink_tokens, recent_tokens, weights
                None if kmax is None else _tensor_ptr(kmax, dev, "kmax", g.box, kvt),
                _tensor_ptr(kept_ids, dev, "kept_ids", g.per_unit + (keep,), _I32),
                _tensor_ptr(new_lens, dev, "new_lens", g.per_seq, _I32), w, n)
+
+
+def sparse_attn_evict_adopt(p, keep_tokens, sink_tokens, recent_tokens, seq_lens, new_lens, block_table, new_table, ws,
+                            keep_lens=None, weights=None, stream=None) -> None:
+    """Behind sparse_attn_evict_tokens of the same sequences: block_table's rows begin with those of new_table [B, n],
+    n >= ceil(keep_tokens / block_size), entries behind them that another context reads become -1, the
+    weights behind the kept tokens 0, and seq_lens new_lens."""
+    g, dev = _shapes(p), _device_of(seq_lens, "seq_lens")
+    width = new_table.shape[1] if new_table.dim() == 2 else -1
+    w, n = _workspace(ws, dev)
+    _launch_on(dev, "sparse_attn_evict_adopt", stream, C.byref(p), _tensor_ptr(seq_lens, dev, "seq_lens", g.per_seq, _I32),
+               int(keep_tokens), None if keep_lens is None else _tensor_ptr(keep_lens, dev, "keep_lens", g.per_seq, _I32),
+               int(sink_tokens), int(recent_tokens), _tensor_ptr(new_lens, dev, "new_lens", g.per_seq, _I32),
+               _tensor_ptr(block_table, dev, "block_table", g.table, _I32),
+               _tensor_ptr(new_table, dev, "new_table", g.per_seq + (width,), _I32), width,
+               None if weights is None else _tensor_ptr(weights, dev, "weights", g.weights, torch.float32), w, n)

@@ -924,6 +924,34 @@ int sparse_attn_evict_tokens(const sparse_attn_params* p, const int32_t* seq_len
     return status_of(launch_evict(g, c, static_cast<char*>(ws), reinterpret_cast<cudaStream_t>(stream)));
 }
 
+int sparse_attn_evict_adopt(const sparse_attn_params* p, int32_t* seq_lens, int32_t keep_tokens, const int32_t* keep_lens,
+                            int32_t sink_tokens, int32_t recent_tokens, const int32_t* new_lens, int32_t* block_table,
+                            const int32_t* new_table, int32_t new_width, float* weights, void* ws, size_t ws_bytes,
+                            sparse_attn_stream stream)
+{
+    Geometry g;
+    const int st = evict_geometry(p, keep_tokens, &g);
+    if (st) return st;
+    if (!ws || !aligned(ws, 256) || ws_bytes < evict_workspace(g, keep_tokens)) return SPARSE_ATTN_INVALID_ARG;
+    if (sink_tokens < 0 || recent_tokens < 0 || (long long)sink_tokens + recent_tokens > keep_tokens) return SPARSE_ATTN_INVALID_ARG;
+    if ((long long)g.B * g.nb_cap > INT32_MAX / 4) return SPARSE_ATTN_UNSUPPORTED;       // twice the entries, numbered in 32 bits
+    if (new_width < (keep_tokens - 1) / g.bs + 1 || new_width > g.nb_cap) return SPARSE_ATTN_INVALID_ARG;
+    if (g.B == 0) return SPARSE_ATTN_OK;
+    if (g.num_pages < 1 || !seq_lens || !new_lens || !block_table || !new_table) return SPARSE_ATTN_INVALID_ARG;
+    if (!aligned(weights, 16) || !aligned(seq_lens, 4) || !aligned(keep_lens, 4) || !aligned(new_lens, 4) ||
+        !aligned(block_table, 4) || !aligned(new_table, 4))
+        return SPARSE_ATTN_INVALID_ARG;
+    // what is written must not be what is read
+    auto apart = [](const int32_t* x, size_t n, const int32_t* y, size_t m) { return !x || !y || x + n <= y || y + m <= x; };
+    const size_t B = size_t(g.B), table = B * size_t(g.nb_cap), fresh = B * size_t(new_width);
+    if (!apart(seq_lens, B, new_lens, B) || !apart(seq_lens, B, keep_lens, B) || !apart(block_table, table, new_table, fresh) ||
+        !apart(block_table, table, new_lens, B) || !apart(block_table, table, seq_lens, B))
+        return SPARSE_ATTN_INVALID_ARG;
+    const AdoptCall c{seq_lens, keep_lens, new_lens, new_table, keep_tokens, sink_tokens, recent_tokens, new_width, block_table,
+                      weights};
+    return status_of(launch_adopt(g, c, static_cast<char*>(ws), reinterpret_cast<cudaStream_t>(stream)));
+}
+
 // ---- selection for callers that cannot allocate device memory ---------------
 // The scratch lives in this file-scope array; host code needs its device address,
 // looked up once per device (cudaGetSymbolAddress) with that device current.

@@ -404,9 +404,145 @@ cudaError_t launch_move(const EvictArgs& a, unsigned grid, cudaStream_t s)
                                  a.kmin != nullptr ? size_t(a.run) * a.row_bytes * 5 / 4 : 0, s, a);
 }
 
+// Behind an eviction: the page table, the lengths and the weights of the sequences that moved.  The first launch counts
+// for each page the contexts that read it and writes down which sequences moved, from the old lengths; the
+// second overwrites them.  The counts are in a hash table, whose size goes by the page table's and not by the
+// pool's, with open addressing: it is half empty at least, so a search ends.  Bytes: the page table twice, the hash
+// table, the weights behind the kept tokens once.
+constexpr int kAdThreads = 256;
+
+struct Reader {
+    int page;              // -1: free
+    int count;             // contexts that read it, less one
+};
+
+struct AdoptArgs {
+    AdoptCall c;
+    Reader* readers;                       // [2^readers_log2], all bits set before
+    int32_t *was, *moved;                  // [B] old length (-1: no context), [B]
+    long long w_stride;
+    int B, Hkv, N, bs, nb_cap, num_pages, table_ctas, readers_log2;
+};
+
+__device__ __forceinline__ unsigned reader_place(const AdoptArgs& a, int page)
+{
+    return (unsigned(page) * 2654435769u) >> (32 - a.readers_log2);        // 2^32 over the golden ratio
+}
+
+__global__ void __launch_bounds__(kAdThreads) adopt_count_kernel(AdoptArgs a)
+{
+    allow_dependents_early();
+    grid_dependency_wait();   // lengths and pages may come from the previous kernel
+    const long long entries = (long long)a.B * a.nb_cap, step = (long long)gridDim.x * kAdThreads;
+    for (long long i = (long long)blockIdx.x * kAdThreads + threadIdx.x; i < entries; i += step) {
+        const int b = int(i / a.nb_cap), j = int(i - (long long)b * a.nb_cap), len = a.c.seq_lens[b];
+        const bool active = len >= 0 && len <= a.N;
+        if (j == 0) {
+            const int k = a.c.keep_lens != nullptr ? a.c.keep_lens[b] : a.c.keep;
+            a.was[b] = active ? len : -1;
+            a.moved[b] = active && k >= a.c.sinks + a.c.recent && k <= a.c.keep;
+        }
+        if (!active || (long long)j * a.bs >= len) continue;
+        const int page = a.c.block_table[i];
+        if (page < 0 || page >= a.num_pages) continue;
+        const unsigned size = 1u << a.readers_log2;
+        unsigned at = reader_place(a, page);
+        for (unsigned n = 0; n < size; ++n, at = (at + 1) & (size - 1)) {
+            const int there = atomicCAS(&a.readers[at].page, -1, page);
+            if (there != -1 && there != page) continue;
+            atomicAdd(&a.readers[at].count, 1);
+            break;
+        }
+    }
+}
+
+// The first table_ctas CTAs write the table and the lengths, the others the weights.
+__global__ void __launch_bounds__(kAdThreads) adopt_kernel(AdoptArgs a)
+{
+    allow_dependents_early();
+    grid_dependency_wait();   // counts and old lengths come from the previous kernel
+    const int tid = threadIdx.x;
+    if (int(blockIdx.x) >= a.table_ctas) {
+        const int first = int(blockIdx.x) - a.table_ctas, ctas = int(gridDim.x) - a.table_ctas;
+        for (int u = first; u < a.B * a.Hkv; u += ctas) {
+            const int b = u / a.Hkv;
+            if (a.moved[b] == 0) continue;
+            float* w = a.c.weights + u * a.w_stride;           // a row is whole 16 bytes
+            const int from = a.c.new_lens[b], up = min((from + 3) & ~3, int(a.w_stride));
+            if (tid < up - from) w[from + tid] = 0.f;
+            for (int t = up + 4 * tid; t < int(a.w_stride); t += 4 * kAdThreads) *reinterpret_cast<float4*>(w + t) = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        return;
+    }
+    auto readers = [&](int page) {
+        const unsigned size = 1u << a.readers_log2;
+        unsigned at = reader_place(a, page);
+        for (unsigned n = 0; n < size && a.readers[at].page != -1; ++n, at = (at + 1) & (size - 1))
+            if (a.readers[at].page == page) return a.readers[at].count + 1;
+        return 0;
+    };
+    const long long entries = (long long)a.B * a.nb_cap, step = (long long)a.table_ctas * kAdThreads;
+    for (long long i = (long long)blockIdx.x * kAdThreads + tid; i < entries; i += step) {
+        const int b = int(i / a.nb_cap), j = int(i - (long long)b * a.nb_cap);
+        if (a.moved[b] == 0) continue;
+        if (j == 0) a.c.seq_lens[b] = a.c.new_lens[b];
+        if (j < a.c.new_width) {
+            a.c.block_table[i] = a.c.new_table[(long long)b * a.c.new_width + j];
+        } else {
+            const int page = a.c.block_table[i], own = (long long)j * a.bs < a.was[b];
+            if (page >= 0 && page < a.num_pages && readers(page) > own) a.c.block_table[i] = -1;
+        }
+    }
+}
+
+struct EvictLayout {
+    size_t kept_weights, readers, was, moved, end;
+    int readers_log2;
+};
+
+EvictLayout evict_layout(const Geometry& g, int keep)
+{
+    auto align256 = [](size_t x) { return (x + 255) & ~size_t(255); };
+    EvictLayout L{};
+    L.kept_weights = kTreeWsFree;
+    L.readers = align256(L.kept_weights + size_t(g.units()) * keep * sizeof(float));
+    L.readers_log2 = 1;
+    while ((1LL << L.readers_log2) < 2LL * g.B * g.nb_cap) ++L.readers_log2;
+    L.was = L.readers + align256((sizeof(Reader)) << L.readers_log2);
+    L.moved = L.was + align256(size_t(g.B) * sizeof(int32_t));
+    L.end = L.moved + align256(size_t(g.B) * sizeof(int32_t));
+    return L;
+}
+
 }  // namespace
 
-size_t evict_workspace(const Geometry& g, int keep) { return kTreeWsFree + size_t(g.units()) * keep * sizeof(float); }
+size_t evict_workspace(const Geometry& g, int keep) { return evict_layout(g, keep).end; }
+
+cudaError_t launch_adopt(const Geometry& g, const AdoptCall& c, char* ws, cudaStream_t s)
+{
+    const EvictLayout L = evict_layout(g, c.keep);
+    AdoptArgs a{};
+    a.c = c;
+    a.readers = reinterpret_cast<Reader*>(ws + L.readers);
+    a.readers_log2 = L.readers_log2;
+    a.was = reinterpret_cast<int32_t*>(ws + L.was);
+    a.moved = reinterpret_cast<int32_t*>(ws + L.moved);
+    a.w_stride = (long long)g.nb_cap * g.bs;
+    a.B = g.B;
+    a.Hkv = g.Hkv;
+    a.N = g.N;
+    a.bs = g.bs;
+    a.nb_cap = g.nb_cap;
+    a.num_pages = g.num_pages;
+    const long long entries = (long long)g.B * g.nb_cap, ctas = (entries + kAdThreads - 1) / kAdThreads, most = 4LL * num_sms();
+    a.table_ctas = int(ctas < most ? ctas : most);
+    const int weight_ctas = c.weights == nullptr ? 0 : int(g.units() < most ? g.units() : most);
+    cudaError_t e = cudaMemsetAsync(a.readers, 0xff, sizeof(Reader) << L.readers_log2, s);
+    if (e != cudaSuccess) return e;
+    e = launch_after_previous(adopt_count_kernel, dim3(unsigned(a.table_ctas)), dim3(kAdThreads), 0, s, a);
+    if (e != cudaSuccess) return e;
+    return launch_after_previous(adopt_kernel, dim3(unsigned(a.table_ctas + weight_ctas)), dim3(kAdThreads), 0, s, a);
+}
 
 cudaError_t launch_evict(const Geometry& g, const EvictCall& c, char* ws, cudaStream_t s)
 {
@@ -416,7 +552,7 @@ cudaError_t launch_evict(const Geometry& g, const EvictCall& c, char* ws, cudaSt
     a.block_table = c.block_table;
     a.new_table = c.new_table;
     a.weights = c.weights;
-    a.kept_weights = reinterpret_cast<float*>(ws + kTreeWsFree);
+    a.kept_weights = reinterpret_cast<float*>(ws + evict_layout(g, c.keep).kept_weights);
     a.kept_ids = c.kept_ids;
     a.new_lens = c.new_lens;
     a.k_pages = static_cast<char*>(c.k_pages);

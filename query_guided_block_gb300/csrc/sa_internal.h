@@ -216,6 +216,15 @@ struct EvictCall {
 };
 size_t evict_workspace(const Geometry& g, int keep);
 cudaError_t launch_evict(const Geometry& g, const EvictCall& c, char* ws, cudaStream_t s);
+// Page table, lengths and weights behind it.
+struct AdoptCall {
+    int32_t* seq_lens;
+    const int32_t *keep_lens, *new_lens, *new_table;
+    int keep, sinks, recent, new_width;
+    int32_t* block_table;
+    float* weights;              // null: left alone
+};
+cudaError_t launch_adopt(const Geometry& g, const AdoptCall& c, char* ws, cudaStream_t s);
 
 cudaError_t launch_diff(const Geometry& g, int step, const int32_t* sel_ids,
                         const int32_t* sel_count, const int32_t* prev_ids,

@@ -275,16 +275,14 @@ class LongContextDecoder(DraftDecoder):
                 nb_cap = -(-max(p.capacity_tokens, p.n_tokens) // p.block_size)
                 self.weights = torch.zeros(p.batch, p.num_kv_heads, nb_cap * p.block_size, device=dev)
                 self.kept_ids = torch.full((p.batch, p.num_kv_heads, keep_tokens), -1, dtype=torch.int32, device=dev)
-                self._index = torch.arange(nb_cap * p.block_size, device=dev)
-                self._column = torch.arange(nb_cap, device=dev)
             if size > self.ws.numel():
                 self.ws = torch.empty(size, dtype=torch.uint8, device=dev)
                 B.sparse_attn_workspace_init(self.ws)
 
     def append(self, q_new, k_new, v_new, inv_freq, q_out, k_pages, v_pages, block_table, cu_rows=None,
                positions=None, pairing=B.ROTATE_HALVES, kmin=None, kmax=None, stream=None):
-        self.append_norm(q_new, k_new, v_new, None, None, 0.0, inv_freq, q_out, k_pages, v_pages, block_table, cu_rows,
-                         positions, None, pairing, kmin, kmax, stream)
+        B.sparse_attn_append_kv(self.p, q_new, k_new, v_new, inv_freq, q_out, k_pages, v_pages, block_table, self.ws,
+                                cu_rows, self.seq_lens, positions, pairing, kmin, kmax, stream, self.weights)
 
     def append_norm(self, q_new, k_new, v_new, q_weight, k_weight, eps, inv_freq, q_out, k_pages, v_pages, block_table,
                     cu_rows=None, positions=None, axis_of=None, pairing=B.ROTATE_HALVES, kmin=None, kmax=None, stream=None):
@@ -337,31 +335,15 @@ class LongContextDecoder(DraftDecoder):
             raise ValueError(f"new_table: {width} pages a sequence, block_table has {block_table.shape[1]}")
         p = B.sparse_attn_params.from_buffer_copy(self.p)
         p.n_tokens = max(p.capacity_tokens, p.n_tokens)              # needs no room for drafts behind a context
-        with torch.cuda.stream(self._stream(stream)):
-            kept_in = new_table if width <= blocks else new_table[:, :blocks].contiguous()
+        kept_in = new_table
+        if width > blocks:
+            with torch.cuda.stream(self._stream(stream)):
+                kept_in = new_table[:, :blocks].contiguous()
         B.sparse_attn_evict_tokens(p, self.keep_tokens, sink_tokens, recent_tokens, self.weights, k_pages, v_pages,
                                    block_table, kept_in, self.kept_ids, self.new_lens, self.ws, self.seq_lens, keep_lens,
                                    kmin, kmax, stream)
-        with torch.cuda.stream(self._stream(stream)):
-            # what the call leaves alone keeps its pages: inactive, no budget, or numbers out of range
-            active = (self.seq_lens >= 0) & (self.seq_lens <= p.n_tokens)
-            moved = active
-            if keep_lens is not None:
-                moved = active & (keep_lens >= sink_tokens + recent_tokens) & (keep_lens <= self.keep_tokens)
-            if width < block_table.shape[1]:
-                # entries that a context reads, and how many others read the same page
-                read = (active[:, None] & (self._column * p.block_size < self.seq_lens[:, None]) &
-                        (block_table >= 0) & (block_table < p.num_pages)).to(torch.int32)
-                page = block_table.clamp(0, p.num_pages - 1).long()
-                readers = torch.zeros(p.num_pages, dtype=torch.int32, device=self.device)
-                readers.scatter_add_(0, page.flatten(), read.flatten())
-                shared = moved[:, None] & (self._column >= width) & (readers[page] > read)
-                block_table.masked_fill_(shared, -1)
-            head = block_table[:, :width]
-            head.copy_(torch.where(moved[:, None], new_table, head))
-            gone = moved[:, None] & (self._index >= self.new_lens[:, None])
-            self.weights.masked_fill_(gone[:, None], 0.0)        # the sums of tokens that are not there any more
-            self.seq_lens.copy_(self.new_lens)
+        B.sparse_attn_evict_adopt(p, self.keep_tokens, sink_tokens, recent_tokens, self.seq_lens, self.new_lens, block_table,
+                                  new_table, self.ws, keep_lens, self.weights, stream)
 
     def _budget(self):
         if self.weights is None:
