@@ -408,8 +408,11 @@ cudaError_t launch_move(const EvictArgs& a, unsigned grid, cudaStream_t s)
 // for each page the contexts that read it and writes down which sequences moved, from the old lengths; the
 // second overwrites them.  The counts are in a hash table, whose size goes by the page table's and not by the
 // pool's, with open addressing: it is half empty at least, so a search ends.  Bytes: the page table twice, the hash
-// table, the weights behind the kept tokens once.
+// table, the weights behind the kept tokens once.  Up to 64 contexts 5 to 8 us, which are the three steps' starts; 256 x
+// 32K tokens of 8 heads (235 MB of zeros) 46 us, the zeros' time (a CTA a row of weights: one context of 128K 11.7 us
+// for 5.2).
 constexpr int kAdThreads = 256;
+constexpr int kAdRun = 4096;               // weights of a CTA at a time
 
 struct Reader {
     int page;              // -1: free
@@ -421,7 +424,7 @@ struct AdoptArgs {
     Reader* readers;                       // [2^readers_log2], all bits set before
     int32_t *was, *moved;                  // [B] old length (-1: no context), [B]
     long long w_stride;
-    int B, Hkv, N, bs, nb_cap, num_pages, table_ctas, readers_log2;
+    int B, Hkv, N, bs, nb_cap, num_pages, table_ctas, w_runs, readers_log2;
 };
 
 __device__ __forceinline__ unsigned reader_place(const AdoptArgs& a, int page)
@@ -464,13 +467,13 @@ __global__ void __launch_bounds__(kAdThreads) adopt_kernel(AdoptArgs a)
     const int tid = threadIdx.x;
     if (int(blockIdx.x) >= a.table_ctas) {
         const int first = int(blockIdx.x) - a.table_ctas, ctas = int(gridDim.x) - a.table_ctas;
-        for (int u = first; u < a.B * a.Hkv; u += ctas) {
-            const int b = u / a.Hkv;
+        for (long long it = first; it < (long long)a.B * a.Hkv * a.w_runs; it += ctas) {
+            const int u = int(it / a.w_runs), t0 = int(it - (long long)u * a.w_runs) * kAdRun, b = u / a.Hkv;
             if (a.moved[b] == 0) continue;
             float* w = a.c.weights + u * a.w_stride;           // a row is whole 16 bytes
-            const int from = a.c.new_lens[b], up = min((from + 3) & ~3, int(a.w_stride));
+            const int from = max(t0, a.c.new_lens[b]), to = min(int(a.w_stride), t0 + kAdRun), up = min((from + 3) & ~3, to);
             if (tid < up - from) w[from + tid] = 0.f;
-            for (int t = up + 4 * tid; t < int(a.w_stride); t += 4 * kAdThreads) *reinterpret_cast<float4*>(w + t) = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int t = up + 4 * tid; t < to; t += 4 * kAdThreads) *reinterpret_cast<float4*>(w + t) = make_float4(0.f, 0.f, 0.f, 0.f);
         }
         return;
     }
@@ -536,7 +539,9 @@ cudaError_t launch_adopt(const Geometry& g, const AdoptCall& c, char* ws, cudaSt
     a.num_pages = g.num_pages;
     const long long entries = (long long)g.B * g.nb_cap, ctas = (entries + kAdThreads - 1) / kAdThreads, most = 4LL * num_sms();
     a.table_ctas = int(ctas < most ? ctas : most);
-    const int weight_ctas = c.weights == nullptr ? 0 : int(g.units() < most ? g.units() : most);
+    a.w_runs = int((a.w_stride + kAdRun - 1) / kAdRun);
+    const long long runs = (long long)g.units() * a.w_runs;
+    const int weight_ctas = c.weights == nullptr ? 0 : int(runs < most ? runs : most);
     cudaError_t e = cudaMemsetAsync(a.readers, 0xff, sizeof(Reader) << L.readers_log2, s);
     if (e != cudaSuccess) return e;
     e = launch_after_previous(adopt_count_kernel, dim3(unsigned(a.table_ctas)), dim3(kAdThreads), 0, s, a);

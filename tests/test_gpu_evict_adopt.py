@@ -85,6 +85,7 @@ CASES = {
                         pages=60),
     "pages_far_apart": dict(batch=50, nb=40, bs=8, keep=64, width=8, n_tokens=320, capacity=320, lens=[(37 * i) % 321 for i in range(50)],
                             pages=900, spread=1 << 16),
+    "long_kept": dict(batch=3, nb=1300, bs=8, keep=5002, width=626, n_tokens=10400, capacity=10400, lens=[10397, 4096, 4097], pages=3500),
     "long_rows": dict(batch=3, nb=1000, bs=8, keep=500, width=63, n_tokens=8000, capacity=8000, lens=[8000, 7001, 600], pages=2500,
                       hkv=8),
 }
