@@ -550,7 +550,8 @@ int sparse_attn_weigh_workspace_size(const sparse_attn_params* p, size_t* bytes)
  * of every token: weights, device float [B, Hkv, nb_cap * block_size], 16-byte aligned,
  *   weights[b][kvh][t] += sum over the Q x G query rows of the KV head of softmax_t  for t < seq_lens[b];
  * the Q new tokens' entries are set to that sum (whatever they held), entries behind them are left
- * alone.  Tokens that were never weighed start at the caller's 0 (sparse_attn_append_kv_weights).  With Q = 1 a decode step; with the last Q tokens of a prompt as queries the weights by which
+ * alone.  Tokens that were never weighed start at the caller's 0 (sparse_attn_append_kv_weights).
+ * With Q = 1 a decode step; with the last Q tokens of a prompt as queries the weights by which
  * its first eviction may go.  All tokens must be finite.  The sums do not depend on timing. */
 int sparse_attn_weigh_decode(const sparse_attn_params* p, const void* q, const void* k_pages, const void* v_pages,
                              const int32_t* block_table, const int32_t* seq_lens, float* weights, float* out, void* ws,
@@ -569,8 +570,8 @@ int sparse_attn_evict_workspace_size(const sparse_attn_params* p, int32_t keep_t
  *   (device int32 [B, ceil(keep_tokens / block_size)]) at i % block_size, its weight to
  *   weights[b][kvh][i], its index to kept_ids[b][kvh][i] (device int32 [B, Hkv, keep_tokens]).  Entries
  *   behind the kept ones are left alone in both: those of `weights` still hold the sums of tokens that
- *   are gone, and the tokens that come in at their indexes have to start at 0.  new_lens[b] = the number kept (an inactive sequence keeps
- *   -1, one left alone its length); new_lens must not overlap seq_lens or keep_lens.
+ *   are gone, and the tokens that come in at their indexes have to start at 0 (sparse_attn_evict_adopt).
+ *   new_lens[b] = the number kept (an inactive sequence keeps -1, one left alone its length); new_lens must not overlap seq_lens or keep_lens.
  *   The new pages must not be pages that any sequence of the call reads, and belong to one sequence.
  *   kmin / kmax: both or neither; the rows of the new blocks become the box of their tokens.
  * The call needs no room behind a context: one past n_tokens (its pages reach the capacity) is evicted from
