@@ -571,7 +571,8 @@ int sparse_attn_evict_workspace_size(const sparse_attn_params* p, int32_t keep_t
  *   weights[b][kvh][i], its index to kept_ids[b][kvh][i] (device int32 [B, Hkv, keep_tokens]).  Entries
  *   behind the kept ones are left alone in both: those of `weights` still hold the sums of tokens that
  *   are gone, and the tokens that come in at their indexes have to start at 0 (sparse_attn_evict_adopt).
- *   new_lens[b] = the number kept (an inactive sequence keeps -1, one left alone its length); new_lens must not overlap seq_lens or keep_lens.
+ *   new_lens[b] = the number kept (an inactive sequence keeps -1, one left alone its length); new_lens
+ *   must not overlap seq_lens or keep_lens.
  *   The new pages must not be pages that any sequence of the call reads, and belong to one sequence.
  *   kmin / kmax: both or neither; the rows of the new blocks become the box of their tokens.
  * The call needs no room behind a context: one past n_tokens (its pages reach the capacity) is evicted from
